@@ -244,6 +244,120 @@ fw_status fw_moe_route_noalloc(const void *x, int32_t T, int32_t H, const float 
  * an all-zero block stores zeros. */
 fw_status fw_q8_0_quantize(const float *w, int64_t rows, int64_t K, uint8_t *blocks, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The attention side of the same layer (the Flyweight README, §Features:
+ * attention with tensor-core prefill, sliding window; §Quantization:
+ * KV-cache codecs; the pages print no formula or layout, and the readings
+ * below are this library's own): the step's plan, the norms and rotation of
+ * queries and keys, and attention over a paged key/value cache held in 4 bits.
+ * These calls need no handle: the caller owns every buffer, the cache among
+ * them. They never synchronise and allocate nothing, so they capture into
+ * CUDA graphs. Bad values that only the device sees (a slot or position out of
+ * range) are skipped and reported as FW_KV_* bits in a caller's status word.
+ *
+ * Page format. A page holds P positions (16, 32, 64 or 128) of one request for
+ * every key/value head; the cache is n_pages x n_kv blocks of P * D * 9 / 8
+ * bytes, 16-byte aligned, D = 64 or 128 dims a head, NB = D / 32:
+ *   K codes  [P][4 q][NB b] 32-bit words: dims 32 b + 8 q + i; nibbles 0..3
+ *            hold i = 0, 2, 4, 6 and nibbles 4..7 hold i = 1, 3, 5, 7
+ *   K scales [P][NB] bf16
+ *   V codes  [P / 2][8 g][NB b] 32-bit words: dims 32 b + 4 g + i; nibbles
+ *            0..3 hold i = 0..3 of the even position, 4..7 of the odd one
+ *   V scales [P / 2][NB][2] bf16: the even position's, the odd position's
+ * The value of a code c in 0..15 is d * (c - 8). A block of 32 values x takes
+ * d = its element of largest magnitude (of a tie the positive one) / -8 and
+ * c = round-half-even(x / d) + 8 clamped to 0..15 (d = 0: c = 8); d is exact in
+ * bf16 for the bf16 keys and values stored here. A block holding an infinity
+ * or NaN stands for non-finite values. A slot is page * P + place in the page. */
+enum {
+  FW_KV_POOL_EMPTY = 1,   /* the plan ran out of free pages */
+  FW_KV_TABLE_FULL = 2,   /* a request needs more than max_blocks pages */
+  FW_KV_TOKENS_FULL = 4,  /* more new tokens than T_cap */
+  FW_KV_BAD_LENGTH = 8,   /* a negative length, or one above 2^30 (taken as 0) */
+  FW_KV_BAD_SLOT = 16,    /* a slot or page id outside the cache */
+  FW_KV_BAD_POSITION = 32 /* a position outside the cos_sin table */
+};
+
+/* The plan of a step, made on the GPU from the requests' lengths: all DEVICE
+ * int32. Request r has cached_lens[r] positions in the cache and brings
+ * new_lens[r] more (0 is allowed for both). Its pages are block_table[r][0 ..];
+ * the first ceil(cached / page) entries are read, the entries of the pages its
+ * new positions open are WRITTEN, taken from free_pages in request order,
+ * starting at entry *free_used (NULL: 0). Outputs: q_start [R + 1], the
+ * exclusive sum of new_lens; seq_lens [R] = cached + new; for each of T_cap
+ * token places requests, positions and slots (-1 past the last token); counts
+ * [3] = {tokens, free-list entries used, *free_used included, FW_KV_* bits}.
+ * Without a page for it a token's slot, and its table entry, is -1; tokens past
+ * T_cap are not placed and the entries of pages they open not written. The next
+ * step may pass this call's counts + 1 as free_used, with other counts. */
+fw_status fw_kv_plan(const int32_t *cached_lens, const int32_t *new_lens, int32_t R, int32_t page,
+                     int32_t *block_table, int32_t max_blocks, const int32_t *free_pages, int32_t n_free,
+                     const int32_t *free_used, int32_t T_cap, int32_t *q_start, int32_t *seq_lens,
+                     int32_t *requests, int32_t *positions, int32_t *slots, int32_t *counts, void *stream);
+
+/* Norms of queries and keys for each head with the position rotation in the
+ * same pass, and the store into the cache: per head row x of D bf16 values
+ *   y = x / sqrt(mean(x^2) + eps) * norm           (norm NULL: y = x)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)       over rot dims, the rest as is
+ * in fp32, rounded once to bf16. The pairs (a, b) are dims (i, i + rot / 2), or
+ * (2 i, 2 i + 1) when interleaved. cos_sin [n_pos][rot] fp32 holds a position's
+ * rot / 2 cosines, then its sines. With a cache, the rotated keys (as rounded
+ * to bf16) and the values v are quantised into the tokens' slots; a slot of -1
+ * stores nothing, and a position of -1 (padding) is rotated as position 0.
+ * Two tokens of a call may not share a slot. Outputs may be their inputs. */
+typedef struct {
+  int32_t T, n_q, n_kv, D;   /* tokens, query heads, key/value heads, dims a head (64 or 128) */
+  int32_t rot;               /* dims rotated: a multiple of 16, 0..D */
+  int32_t interleaved;       /* 0 or 1 */
+  float eps;
+  int32_t n_pos;             /* rows of cos_sin */
+  const void *q, *k, *v;     /* DEVICE bf16 [T][heads][D]; v read only with a cache */
+  int64_t q_stride, k_stride, v_stride; /* elements between tokens; multiples of 8 */
+  const float *q_norm, *k_norm;         /* DEVICE fp32 [D] or NULL */
+  const float *cos_sin;      /* DEVICE fp32 [n_pos][rot] */
+  const int32_t *positions;  /* DEVICE [T] */
+  void *q_out, *k_out;       /* DEVICE bf16; k_out may be NULL with a cache */
+  int64_t q_out_stride, k_out_stride;
+  void *cache;               /* DEVICE, or NULL */
+  const int32_t *slots;      /* DEVICE [T], with a cache */
+  int32_t page, n_pages;
+  int32_t *status;           /* DEVICE, FW_KV_* bits are OR-ed in; or NULL */
+} fw_qk_norm_rope_args;
+fw_status fw_qk_norm_rope(const fw_qk_norm_rope_args *args, void *stream);
+
+/* The keys and values that slots hold, as bf16 [T][n_kv][D] (d * (c - 8)
+ * rounded; zeros for a slot of -1): for tests and for moving a cache. */
+fw_status fw_kv_export(const void *cache, int32_t n_pages, int32_t n_kv, int32_t D, int32_t page,
+                       const int32_t *slots, int32_t T, void *k, void *v, int32_t *status, void *stream);
+
+/* Causal attention of a step's new tokens over the cache, which already holds
+ * their own keys and values. Tokens q_start[r] .. q_start[r + 1] - 1 belong to
+ * request r and are its last positions: the i-th of n stands at
+ * p = seq_lens[r] - n + i and sees position j when
+ *   j <= p and (window == 0 or j > p - window or j < sinks)
+ * Query head h reads key/value head h / (n_q / n_kv). A row that sees nothing
+ * gives zeros; what is masked is never part of a result, whatever it holds.
+ * Softmax statistics and sums are fp32; probabilities and 4-bit values enter
+ * the tensor cores in bf16. max_q is the largest number of new tokens of a
+ * request, or more. Rows of q past q_start[R] are neither read nor written.
+ * workspace: DEVICE, 16-byte aligned, at least fw_attn_q4_workspace bytes; its
+ * contents mean nothing between calls, and calls that may overlap need one each. */
+typedef struct {
+  int32_t R, T, max_q;       /* requests, rows of q, most new tokens of a request */
+  int32_t n_q, n_kv, D;
+  int32_t page, n_pages, max_blocks; /* max_blocks: entries of a block_table row */
+  int32_t window, sinks;
+  float scale;               /* > 0; usually 1 / sqrt(D) */
+  const void *q;             /* DEVICE bf16 [T][n_q][D] */
+  void *out;                 /* DEVICE bf16 [T][n_q][D] */
+  int64_t q_stride, out_stride; /* elements between tokens; multiples of 8 */
+  const void *cache;         /* DEVICE */
+  const int32_t *block_table, *q_start, *seq_lens; /* DEVICE [R][max_blocks], [R + 1], [R] */
+  int32_t *status;           /* DEVICE, FW_KV_BAD_SLOT is OR-ed in; or NULL */
+} fw_attn_q4_args;
+fw_status fw_attn_q4_workspace(const fw_attn_q4_args *args, int64_t *bytes);
+fw_status fw_attn_q4(const fw_attn_q4_args *args, void *workspace, int64_t bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,8 @@ fw_moe_export_q8_0, fw_moe_status, fw_moe_free, fw_moe_last_error,
 fw_q8_0_quantize), taking raw pointers and ints.
 
 High level: `MoELayer` (one handle = one layer) and `quantize_q8_0`, taking
-torch tensors.
+torch tensors, and the attention side of a layer: `kv_cache`, `kv_plan`,
+`qk_norm_rope`, `kv_export`, `attn_q4` (attention.py).
 """
 from __future__ import annotations
 
@@ -52,7 +53,8 @@ _lib = None
 EXPORTED = ("fw_moe_init", "fw_moe_route", "fw_moe_ffn", "fw_moe_forward", "fw_moe_forward_host",
             "fw_moe_get_permutation", "fw_moe_export_q8_0", "fw_moe_status", "fw_moe_free", "fw_moe_last_error",
             "fw_q8_0_quantize", "fw_moe_profile_begin", "fw_moe_profile_end", "fw_moe_route_noalloc",
-            "fw_moe_graph_create", "fw_moe_graph_launch", "fw_moe_graph_destroy")
+            "fw_moe_graph_create", "fw_moe_graph_launch", "fw_moe_graph_destroy", "fw_kv_plan", "fw_qk_norm_rope",
+            "fw_kv_export", "fw_attn_q4_workspace", "fw_attn_q4")
 
 KERNEL_KINDS = ("route_decode", "route_tiles", "route_scan", "route_scatter", "decode_experts", "reserved",
                 "prefill_gateup", "prefill_down", "prefill_combine", "prefill_gather", "prefill_gateup_small",
@@ -85,6 +87,11 @@ def lib():
             "fw_moe_graph_create": [vp, i32, i32, vp, vp, vp, ctypes.POINTER(vp)],
             "fw_moe_graph_launch": [vp, vp],
             "fw_moe_graph_destroy": [vp],
+            "fw_kv_plan": [vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp],
+            "fw_qk_norm_rope": [vp, vp],
+            "fw_kv_export": [vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp],
+            "fw_attn_q4_workspace": [vp, vp],
+            "fw_attn_q4": [vp, vp, i64, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -315,3 +322,18 @@ class MoELayer:
             self.close()
         except Exception:
             pass
+
+
+# The attention side's torch-level calls import torch at their top; the names
+# are looked up on first use so that this module itself does not.
+_ATTENTION = ("KVPlan", "kv_cache", "kv_plan", "qk_norm_rope", "kv_export", "attn_q4", "FwQkNormRopeArgs", "FwAttnQ4Args",
+              "KV_POOL_EMPTY", "KV_TABLE_FULL", "KV_TOKENS_FULL", "KV_BAD_LENGTH", "KV_BAD_SLOT", "KV_BAD_POSITION")
+
+
+def __getattr__(name):
+    if name in _ATTENTION:
+        from . import attention
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,486 @@
+// The attention side of a layer around its cache: the step's plan (block
+// tables, slots, positions), the norms and rotation of queries and keys with
+// the store into the 4-bit cache, and the read-back.
+#include <algorithm>
+#include <initializer_list>
+
+#include "kvcache.cuh"
+
+namespace fw {
+namespace {
+
+using namespace dev;
+
+// ------------------------------------------------------------- the plan
+// Two running sums over the requests decide everything: of the new tokens
+// (which request a token belongs to) and of the fresh pages (which entry of
+// the free list a block takes). Every CTA makes both sums for itself -- R
+// lengths are a few KB from L2 -- so one launch without any wait between CTAs
+// is enough; it then fills its own kPlanTokens tokens. The thread of the token
+// that opens a fresh page also writes that page's block-table entry, so a
+// request of any length is spread over the grid. What bounds it is latency:
+// one launch, two dependent loads and a scan of the lengths.
+constexpr int kPlanThreads = 512, kPlanItems = 4, kPlanChunk = kPlanThreads * kPlanItems;
+constexpr int kPlanTokens = 1024;  // tokens per CTA
+constexpr int kMaxLen = 1 << 30;
+
+struct PlanArgs {
+  const int32_t *ctx, *fresh, *free_pages, *free_used;
+  int32_t* table;
+  int R, max_blocks, n_free, page_shift, T_cap;
+  int32_t *q_start, *seq_lens, *req, *pos, *slot, *counts;
+};
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
+  __shared__ int s_start[kPlanChunk + 1];  // first new token of each request of the chunk (clamped to kMaxLen)
+  __shared__ int s_ctx[kPlanChunk];
+  __shared__ int s_page[kPlanChunk];       // free-list index of its first fresh page
+  __shared__ longlong2 s_warp[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t0 = blockIdx.x * kPlanTokens, t1 = ::min(a.T_cap, t0 + kPlanTokens);
+  const int P = 1 << a.page_shift;
+  const bool first_cta = blockIdx.x == 0;
+  // 64-bit sums: no lengths that pass the check below overflow them
+  long long tokens = 0, pages = a.free_used ? ::max(0, *a.free_used) : 0;
+  int bits = 0;
+  for (int r0 = 0; r0 < a.R; r0 += kPlanChunk) {
+    if (!first_cta && tokens >= t1) return;  // all of this CTA's tokens are done
+    int c[kPlanItems], n_new[kPlanItems], n_pages[kPlanItems];
+    long long sum_t = 0, sum_p = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+      const int r = r0 + tid * kPlanItems + i;
+      int n = 0;
+      c[i] = 0;
+      if (r < a.R) {
+        c[i] = a.ctx[r];
+        n = a.fresh[r];
+        if (c[i] < 0 || n < 0 || c[i] > kMaxLen || n > kMaxLen - c[i]) {
+          bits |= FW_KV_BAD_LENGTH;
+          c[i] = n = 0;
+        }
+        if ((c[i] + n + P - 1) >> a.page_shift > a.max_blocks) bits |= FW_KV_TABLE_FULL;
+      }
+      n_new[i] = n;
+      n_pages[i] = ((c[i] + n + P - 1) >> a.page_shift) - ((c[i] + P - 1) >> a.page_shift);
+      sum_t += n;
+      sum_p += n_pages[i];
+    }
+    longlong2 inc = make_longlong2(sum_t, sum_p);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long ut = __shfl_up_sync(0xFFFFFFFFu, inc.x, o), up = __shfl_up_sync(0xFFFFFFFFu, inc.y, o);
+      if (lane >= o) {
+        inc.x += ut;
+        inc.y += up;
+      }
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    long long before_t = tokens + inc.x - sum_t, before_p = pages + inc.y - sum_p;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      const longlong2 u = s_warp[w];
+      if (w < warp) {
+        before_t += u.x;
+        before_p += u.y;
+      }
+      tokens += u.x;
+      pages += u.y;
+    }
+    const int n_here = ::min(kPlanChunk, a.R - r0);
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+      const int k = tid * kPlanItems + i;
+      const int start = (int)::min(before_t, (long long)kMaxLen);
+      s_start[k] = start;
+      s_ctx[k] = c[i];
+      s_page[k] = (int)::min(before_p, (long long)kMaxLen);
+      if (first_cta && k < n_here) {
+        a.q_start[r0 + k] = start;
+        a.seq_lens[r0 + k] = c[i] + n_new[i];
+      }
+      before_t += n_new[i];
+      before_p += n_pages[i];
+    }
+    const int end = (int)::min(tokens, (long long)kMaxLen);
+    if (tid == 0) s_start[n_here] = end;
+    __syncthreads();
+    const int lo = ::max(t0, s_start[0]), hi = ::min(t1, end);
+    for (int t = lo + tid; t < hi; t += kPlanThreads) {
+      int l = 0, h = n_here;  // the last request that starts at or before t
+      while (h - l > 1) {
+        const int m = (l + h) >> 1;
+        if (s_start[m] <= t) l = m; else h = m;
+      }
+      const int r = r0 + l, pos = s_ctx[l] + t - s_start[l];
+      const int blk = pos >> a.page_shift, have = (s_ctx[l] + P - 1) >> a.page_shift;
+      int page = -1;
+      if (blk < a.max_blocks) {
+        int32_t* entry = a.table + (int64_t)r * a.max_blocks + blk;
+        if (blk < have) {
+          page = *entry;
+        } else {
+          const int f = s_page[l] + blk - have;
+          if (f < a.n_free) page = a.free_pages[f];
+          if ((pos & (P - 1)) == 0) *entry = page;
+        }
+      }
+      a.req[t] = r;
+      a.pos[t] = pos;
+      a.slot[t] = page < 0 ? -1 : (page << a.page_shift) + (pos & (P - 1));
+    }
+    __syncthreads();
+  }
+  const int total = (int)::min(tokens, (long long)kMaxLen);
+  for (int t = ::max(t0, total) + tid; t < t1; t += kPlanThreads) a.req[t] = a.pos[t] = a.slot[t] = -1;
+  if (first_cta) {
+    const int used = (int)::min(pages, (long long)kMaxLen);
+    if (used > a.n_free) bits |= FW_KV_POOL_EMPTY;
+    if (total > a.T_cap) bits |= FW_KV_TOKENS_FULL;
+    bits = __syncthreads_or(bits & FW_KV_BAD_LENGTH) ? bits | FW_KV_BAD_LENGTH : bits;
+    bits = __syncthreads_or(bits & FW_KV_TABLE_FULL) ? bits | FW_KV_TABLE_FULL : bits;
+    if (tid == 0) {
+      a.q_start[a.R] = total;
+      a.counts[0] = total;
+      a.counts[1] = used;
+      a.counts[2] = bits;
+    }
+  }
+}
+
+// ------------------------------------------------------------- norms, rotation, store
+// A head's row of D values lies in D / 8 lanes, 16 bytes each, so its sum of
+// squares, its rotation partners and a 4-bit block's extreme are a few
+// shuffles away. A warp takes kRows rows per lane group of ONE token (its
+// queries, then keys, then values, as one row index), so the token's cosines
+// and sines are loaded once for all of them and every row's 16-byte load is
+// in flight before the first sum. Bound by HBM at many tokens; at few, by the
+// chain of loads (position -> table row) of one warp.
+constexpr int kRopeWarps = 4, kRopeRows = 4;
+
+struct RopeArgs {
+  fw_qk_norm_rope_args u;
+  int rows;    // n_q + n_kv, + n_kv when storing
+  int tasks;   // warps a token takes
+};
+
+// One row's 4-bit block halves: the scale of the 4 lanes' 32 values (already
+// bf16) and this lane's 8 codes, x / d rounded half to even. The scale is the
+// element of largest magnitude (the positive one of a tie) over -8: exact in
+// bf16 for bf16 values.
+__device__ __forceinline__ float quantise8(const float (&x)[8], int (&code)[8]) {
+  float hi = x[0], lo = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    hi = max_nan(hi, x[i]);
+    lo = min_nan(lo, x[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    hi = max_nan(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    lo = min_nan(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+  }
+  const float d = (hi >= -lo ? hi : lo) * -0.125f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    code[i] = d != 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(x[i], d)) + 8.f, 0.f), 15.f) : 8;
+  return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs a) {
+  constexpr int L = D / 8, Groups = 32 / L, NB = D / kKvBlock;  // lanes of a row, rows side by side in a warp
+  const fw_qk_norm_rope_args& u = a.u;
+  const int lane = threadIdx.x & 31, grp = lane / L, l = lane % L;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t task = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const int64_t t = task / a.tasks;
+  if (t >= u.T) return;  // a whole warp
+  const int row0 = (int)(task % a.tasks) * (Groups * kRopeRows) + grp;
+  const int half = u.rot / 2;
+
+  uint4 raw[kRopeRows];
+#pragma unroll
+  for (int i = 0; i < kRopeRows; ++i) {
+    const int r = row0 + i * Groups;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (r < a.rows) {
+      const __nv_bfloat16* src = r < u.n_q ? (const __nv_bfloat16*)u.q + t * u.q_stride + r * D
+                                 : r < u.n_q + u.n_kv ? (const __nv_bfloat16*)u.k + t * u.k_stride + (r - u.n_q) * D
+                                                      : (const __nv_bfloat16*)u.v + t * u.v_stride + (r - u.n_q - u.n_kv) * D;
+      raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
+    }
+  }
+  // the rotation of this lane's 8 dims: y' = y * cs + partner * sn (sn signed)
+  float cs[8], sn[8];
+  const bool turns = 8 * l < u.rot;
+  if (turns) {
+    int pos = u.positions[t];
+    if (pos < 0 || pos >= u.n_pos) {
+      // a padding row (-1) keeps position 0's rotation: nothing reads it
+      if (pos != -1 && l == 0 && row0 == 0) raise(u.status, FW_KV_BAD_POSITION);
+      pos = 0;
+    }
+    const float* row = u.cos_sin + (int64_t)pos * u.rot;
+    if (u.interleaved) {
+      const float4 c = *reinterpret_cast<const float4*>(row + 4 * l), s = *reinterpret_cast<const float4*>(row + half + 4 * l);
+      cs[0] = cs[1] = c.x; cs[2] = cs[3] = c.y; cs[4] = cs[5] = c.z; cs[6] = cs[7] = c.w;
+      sn[1] = s.x; sn[3] = s.y; sn[5] = s.z; sn[7] = s.w;
+      sn[0] = -s.x; sn[2] = -s.y; sn[4] = -s.z; sn[6] = -s.w;
+    } else {
+      const bool low = 8 * l < half;
+      const int at = low ? 8 * l : 8 * l - half;
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(row + at + j), s = *reinterpret_cast<const float4*>(row + half + at + j);
+        cs[j] = c.x; cs[j + 1] = c.y; cs[j + 2] = c.z; cs[j + 3] = c.w;
+        sn[j] = low ? -s.x : s.x; sn[j + 1] = low ? -s.y : s.y; sn[j + 2] = low ? -s.z : s.z; sn[j + 3] = low ? -s.w : s.w;
+      }
+    }
+  }
+  int64_t block = -1;  // byte offset of the token's page block of head 0, and its place in the page
+  int at = 0;
+  if (u.cache) {
+    const int slot = u.slots[t];
+    if (slot >= 0 && slot / u.page < u.n_pages) {
+      block = (int64_t)(slot / u.page) * u.n_kv * kv_head_bytes(u.page, D);
+      at = slot % u.page;
+    } else if (slot != -1 && l == 0 && row0 == 0) {
+      raise(u.status, FW_KV_BAD_SLOT);
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < kRopeRows; ++i) {
+    const int r = row0 + i * Groups;
+    float x[8];
+    bf16x2_to_f32(raw[i].x, x[0], x[1]);
+    bf16x2_to_f32(raw[i].y, x[2], x[3]);
+    bf16x2_to_f32(raw[i].z, x[4], x[5]);
+    bf16x2_to_f32(raw[i].w, x[6], x[7]);
+    const bool is_q = r < u.n_q, is_v = r >= u.n_q + u.n_kv;
+    const float* w = is_v ? nullptr : is_q ? u.q_norm : u.k_norm;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += x[j] * x[j];
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (w) {
+      const float inv = __fdiv_rn(1.f, __fsqrt_rn(sum * (1.f / D) + u.eps));
+      const float4 w0 = *reinterpret_cast<const float4*>(w + 8 * l), w1 = *reinterpret_cast<const float4*>(w + 8 * l + 4);
+      const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], inv), ww[j]);
+    }
+    // products rounded one by one, as the definition writes them
+    float y[8];
+    if (u.interleaved) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+    } else {
+      const int other = (lane & ~(L - 1)) + (8 * l < half ? l + half / 8 : l - half / 8);  // shfl reads it mod 32
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xFFFFFFFFu, x[j], other);
+    }
+    if (turns && !is_v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(y[j], sn[j]));
+    }
+    uint4 o4;
+    o4.x = bf16x2_bits(x[0], x[1]);
+    o4.y = bf16x2_bits(x[2], x[3]);
+    o4.z = bf16x2_bits(x[4], x[5]);
+    o4.w = bf16x2_bits(x[6], x[7]);
+    if (r < a.rows && !is_v) {
+      __nv_bfloat16* dst = is_q ? (__nv_bfloat16*)u.q_out + t * u.q_out_stride + r * D
+                                : (__nv_bfloat16*)u.k_out + t * u.k_out_stride + (r - u.n_q) * D;
+      if (is_q || u.k_out) *reinterpret_cast<uint4*>(dst + 8 * l) = o4;
+    }
+    if (u.cache) {
+      bf16x2_to_f32(o4.x, x[0], x[1]);
+      bf16x2_to_f32(o4.y, x[2], x[3]);
+      bf16x2_to_f32(o4.z, x[4], x[5]);
+      bf16x2_to_f32(o4.w, x[6], x[7]);
+      int c[8];
+      const float d = quantise8(x, c);
+      if (!is_q && r < a.rows && block >= 0) {
+        const int head = is_v ? r - u.n_q - u.n_kv : r - u.n_q;
+        uint8_t* base = (uint8_t*)u.cache + block + head * kv_head_bytes(u.page, D);
+        const KvPlanes p = kv_planes(u.page, D);
+        const int b = l / 4, q = l % 4;
+        const __nv_bfloat16 db = __float2bfloat16_rn(d);
+        if (!is_v) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) word |= (uint32_t)c[j] << (4 * (j / 2) + 16 * (j % 2));
+          reinterpret_cast<uint32_t*>(base + at * (D / 2))[q * NB + b] = word;
+          if (q == 0) reinterpret_cast<__nv_bfloat16*>(base + p.ks)[at * NB + b] = db;
+        } else {
+          uint16_t* codes = reinterpret_cast<uint16_t*>(base + p.vc + (at / 2) * D);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            codes[2 * ((2 * q + k) * NB + b) + (at & 1)] =
+                (uint16_t)(c[4 * k] | c[4 * k + 1] << 4 | c[4 * k + 2] << 8 | c[4 * k + 3] << 12);
+          if (q == 0) reinterpret_cast<__nv_bfloat16*>(base + p.vs)[2 * ((at / 2) * NB + b) + (at & 1)] = db;
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- read-back
+// D / 8 lanes per (token, head), one 8-dim word of K and two half words of V
+// each. Bound by the bf16 values it writes.
+template <int D>
+__global__ void __launch_bounds__(256)
+    kv_export_kernel(const uint8_t* cache, int n_pages, int n_kv, int page, const int32_t* slots, int64_t rows,
+                     __nv_bfloat16* k, __nv_bfloat16* v, int32_t* status) {
+  constexpr int L = D / 8, NB = D / kKvBlock;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, row = i / L;
+  const int l = (int)(i % L), b = l / 4, q = l % 4;
+  if (row >= rows) return;
+  const int head = (int)(row % n_kv), slot = slots[row / n_kv];
+  uint4 ko = make_uint4(0, 0, 0, 0), vo = ko;
+  if (slot >= 0 && slot / page < n_pages) {
+    const uint8_t* base = cache + ((int64_t)(slot / page) * n_kv + head) * kv_head_bytes(page, D);
+    const KvPlanes p = kv_planes(page, D);
+    const int at = slot % page;
+    const uint32_t kw = reinterpret_cast<const uint32_t*>(base + at * (D / 2))[q * NB + b];
+    const float kd = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base + p.ks)[at * NB + b]);
+    const uint16_t* vc = reinterpret_cast<const uint16_t*>(base + p.vc + (at / 2) * D);
+    const uint32_t vw = vc[2 * ((2 * q) * NB + b) + (at & 1)] | (uint32_t)vc[2 * ((2 * q + 1) * NB + b) + (at & 1)] << 16;
+    const float vd = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base + p.vs)[2 * ((at / 2) * NB + b) + (at & 1)]);
+    auto pair = [](uint32_t w, int n0, int n1, float d) {
+      return bf16x2_bits((float)((int)(w >> (4 * n0) & 15) - 8) * d, (float)((int)(w >> (4 * n1) & 15) - 8) * d);
+    };
+    ko = make_uint4(pair(kw, 0, 4, kd), pair(kw, 1, 5, kd), pair(kw, 2, 6, kd), pair(kw, 3, 7, kd));
+    vo = make_uint4(pair(vw, 0, 1, vd), pair(vw, 2, 3, vd), pair(vw, 4, 5, vd), pair(vw, 6, 7, vd));
+  } else if (slot != -1 && l == 0 && head == 0) {
+    raise(status, FW_KV_BAD_SLOT);
+  }
+  *reinterpret_cast<uint4*>(k + row * D + 8 * l) = ko;
+  *reinterpret_cast<uint4*>(v + row * D + 8 * l) = vo;
+}
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+
+const char* kv_format_error(int n_kv, int page, int64_t n_pages) {
+  if (n_kv < 1 || n_kv > 1024) return "4-bit cache: need 1 <= n_kv <= 1024";
+  if (page != 16 && page != 32 && page != 64 && page != 128) return "4-bit cache: page must be 16, 32, 64 or 128 positions";
+  if (n_pages < 1 || n_pages * page > 0x7FFFFFFFll) return "4-bit cache: need 1 <= n_pages and n_pages * page < 2^31";
+  return nullptr;
+}
+
+// Refuses devices other than sm_103 (the only code in this library), once per device.
+fw_status check_device(const char* text) {
+  static bool ok[64] = {};
+  int dev = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_error(FW_ECUDA, text);
+  if (ok[dev]) return FW_OK;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+    return set_error(FW_ECUDA, text);
+  if (major != 10 || minor != 3) return set_error(FW_EUNSUPPORTED, text);
+  ok[dev] = true;
+  return FW_OK;
+}
+
+}  // namespace fw
+
+using namespace fw;
+
+extern "C" fw_status fw_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t R, int32_t page,
+                                int32_t* block_table, int32_t max_blocks, const int32_t* free_pages, int32_t n_free,
+                                const int32_t* free_used, int32_t T_cap, int32_t* q_start, int32_t* seq_lens,
+                                int32_t* requests, int32_t* positions, int32_t* slots, int32_t* counts, void* stream) {
+  if (R < 0 || R > (1 << 20)) return set_error(FW_EINVAL, "fw_kv_plan: need 0 <= R <= 2^20");
+  if (page != 16 && page != 32 && page != 64 && page != 128)
+    return set_error(FW_EINVAL, "fw_kv_plan: page must be 16, 32, 64 or 128 positions");
+  if (max_blocks < 1 || n_free < 0 || T_cap < 1 || T_cap > (1 << 30))
+    return set_error(FW_EINVAL, "fw_kv_plan: need max_blocks >= 1, n_free >= 0 and 1 <= T_cap <= 2^30");
+  if (!q_start || !counts || !requests || !positions || !slots ||
+      (R > 0 && (!cached_lens || !new_lens || !block_table || !seq_lens)) || (n_free > 0 && !free_pages))
+    return set_error(FW_EINVAL, "fw_kv_plan: null pointer");
+  for (const void* p : {(const void*)cached_lens, (const void*)new_lens, (const void*)block_table, (const void*)free_pages,
+                        (const void*)free_used, (const void*)q_start, (const void*)seq_lens, (const void*)requests,
+                        (const void*)positions, (const void*)slots, (const void*)counts})
+    if (!aligned(p, 4)) return set_error(FW_EINVAL, "fw_kv_plan: pointers need 4-byte alignment");
+  if (free_used && free_used >= counts && free_used < counts + 3)
+    return set_error(FW_EINVAL, "fw_kv_plan: free_used must not lie in this call's counts (use two buffers in turn)");
+  if (fw_status st = check_device("fw_kv_plan: needs an sm_103 device"); st != FW_OK) return st;
+  PlanArgs a = {cached_lens, new_lens, free_pages, free_used, block_table, R, max_blocks, n_free, 0, T_cap,
+                q_start, seq_lens, requests, positions, slots, counts};
+  while ((1 << a.page_shift) < page) ++a.page_shift;
+  if (dev::launch_dependent(plan_kernel, dim3((T_cap + kPlanTokens - 1) / kPlanTokens), dim3(kPlanThreads), 0,
+                            static_cast<cudaStream_t>(stream), a) != cudaSuccess)
+    return set_error(FW_ECUDA, "fw_kv_plan: launch failed");
+  return FW_OK;
+}
+
+extern "C" fw_status fw_qk_norm_rope(const fw_qk_norm_rope_args* u, void* stream) {
+  if (!u) return set_error(FW_EINVAL, "fw_qk_norm_rope: null argument struct");
+  if (u->D != 64 && u->D != 128) return set_error(FW_EUNSUPPORTED, "fw_qk_norm_rope: D must be 64 or 128");
+  if (u->T < 0 || u->n_q < 1 || u->n_q > 1024 || u->n_kv < 1 || u->n_kv > 1024)
+    return set_error(FW_EINVAL, "fw_qk_norm_rope: need T >= 0 and 1 <= n_q, n_kv <= 1024");
+  if (u->rot < 0 || u->rot > u->D || u->rot % 16 || (u->interleaved != 0 && u->interleaved != 1))
+    return set_error(FW_EINVAL, "fw_qk_norm_rope: rot must be a multiple of 16 in [0, D], interleaved 0 or 1");
+  if (!(u->eps >= 0.f)) return set_error(FW_EINVAL, "fw_qk_norm_rope: eps must not be negative");
+  if (u->cache) {
+    if (const char* e = kv_format_error(u->n_kv, u->page, u->n_pages)) return set_error(FW_EINVAL, e);
+  }
+  if (u->T == 0) return FW_OK;
+  if (!u->q || !u->k || !u->q_out || (!u->k_out && !u->cache) || (u->cache && (!u->v || !u->slots)))
+    return set_error(FW_EINVAL, "fw_qk_norm_rope: null pointer (k_out may be null only when a cache is given, which needs v and slots)");
+  if (u->rot && (!u->positions || !u->cos_sin || u->n_pos < 1))
+    return set_error(FW_EINVAL, "fw_qk_norm_rope: a rotation needs positions and a cos_sin table");
+  const int64_t qw = (int64_t)u->n_q * u->D, kw = (int64_t)u->n_kv * u->D;
+  if (u->q_stride < qw || u->k_stride < kw || u->q_out_stride < qw || (u->k_out && u->k_out_stride < kw) ||
+      (u->cache && u->v_stride < kw) || u->q_stride % 8 || u->k_stride % 8 || u->q_out_stride % 8 ||
+      (u->k_out && u->k_out_stride % 8) || (u->cache && u->v_stride % 8))
+    return set_error(FW_EINVAL, "fw_qk_norm_rope: token strides must cover the heads and be multiples of 8 elements");
+  for (const void* p : {u->q, u->k, u->v, (const void*)u->q_norm, (const void*)u->k_norm, (const void*)u->cos_sin,
+                        (const void*)u->q_out, (const void*)u->k_out, (const void*)u->cache})
+    if (!aligned(p, 16)) return set_error(FW_EINVAL, "fw_qk_norm_rope: tensors need 16-byte alignment");
+  if (!aligned(u->positions, 4) || !aligned(u->slots, 4) || !aligned(u->status, 4))
+    return set_error(FW_EINVAL, "fw_qk_norm_rope: positions, slots and status need 4-byte alignment");
+  if (fw_status st = check_device("fw_qk_norm_rope: needs an sm_103 device"); st != FW_OK) return st;
+  RopeArgs a;
+  a.u = *u;
+  a.rows = u->n_q + u->n_kv + (u->cache ? u->n_kv : 0);
+  const int per_warp = 32 / (u->D / 8) * kRopeRows;
+  a.tasks = (a.rows + per_warp - 1) / per_warp;
+  const int64_t ctas = ((int64_t)u->T * a.tasks + kRopeWarps - 1) / kRopeWarps;
+  if (ctas > 0x7FFFFFFF) return set_error(FW_EINVAL, "fw_qk_norm_rope: too many rows for one launch");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dev::launch_dependent(u->D == 64 ? qk_norm_rope_kernel<64> : qk_norm_rope_kernel<128>,
+                                              dim3((unsigned)ctas), dim3(kRopeWarps * 32), 0, s, a);
+  if (e != cudaSuccess) return set_error(FW_ECUDA, "fw_qk_norm_rope: launch failed");
+  return FW_OK;
+}
+
+extern "C" fw_status fw_kv_export(const void* cache, int32_t n_pages, int32_t n_kv, int32_t D, int32_t page,
+                                  const int32_t* slots, int32_t T, void* k, void* v, int32_t* status, void* stream) {
+  if (D != 64 && D != 128) return set_error(FW_EUNSUPPORTED, "fw_kv_export: D must be 64 or 128");
+  if (const char* e = kv_format_error(n_kv, page, n_pages)) return set_error(FW_EINVAL, e);
+  if (T < 0) return set_error(FW_EINVAL, "fw_kv_export: T must not be negative");
+  if (T == 0) return FW_OK;
+  if (!cache || !slots || !k || !v) return set_error(FW_EINVAL, "fw_kv_export: null pointer");
+  if (!aligned(cache, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(status, 4))
+    return set_error(FW_EINVAL, "fw_kv_export: cache, k and v need 16-byte, slots and status 4-byte alignment");
+  if (fw_status st = check_device("fw_kv_export: needs an sm_103 device"); st != FW_OK) return st;
+  const int64_t rows = (int64_t)T * n_kv, ctas = (rows * (D / 8) + 255) / 256;
+  if (ctas > 0x7FFFFFFF) return set_error(FW_EINVAL, "fw_kv_export: too many rows for one launch");
+  const cudaError_t e = dev::launch_dependent(D == 64 ? kv_export_kernel<64> : kv_export_kernel<128>, dim3((unsigned)ctas),
+                                              dim3(256), 0, static_cast<cudaStream_t>(stream), (const uint8_t*)cache,
+                                              n_pages, n_kv, page, slots, rows, (__nv_bfloat16*)k, (__nv_bfloat16*)v, status);
+  if (e != cudaSuccess) return set_error(FW_ECUDA, "fw_kv_export: launch failed");
+  return FW_OK;
+}
