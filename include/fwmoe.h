@@ -275,7 +275,8 @@ enum {
   FW_KV_TOKENS_FULL = 4,  /* more new tokens than T_cap */
   FW_KV_BAD_LENGTH = 8,   /* a negative length, or one above 2^30 (taken as 0) */
   FW_KV_BAD_SLOT = 16,    /* a slot or page id outside the cache */
-  FW_KV_BAD_POSITION = 32 /* a position outside the cos_sin table */
+  FW_KV_BAD_POSITION = 32, /* a position outside the cos_sin table */
+  FW_KV_TIMEOUT = 64      /* a kernel gave up a bounded wait; its outputs mean nothing */
 };
 
 /* The plan of a step, made on the GPU from the requests' lengths: all DEVICE

@@ -34,40 +34,52 @@ class FwAttnQ4Args(ctypes.Structure):
                 + [(n, _vp) for n in ("cache", "block_table", "q_start", "seq_lens", "status")])
 
 
-def _need(ok, text):
-    if not ok:
-        raise ValueError(text)
+_bf16, _int32, _fp32, _uint8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # not in builds of torch without CUDA
+
+# Small calls last a few microseconds, most of it here: each check is one
+# expression, and a message is only made for one that failed.
 
 
-def _int32(where, **tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            _need(t.is_cuda and t.dtype == torch.int32 and t.is_contiguous(), f"{where}: {name} must be a contiguous int32 CUDA tensor")
+def _stream(t, stream):
+    return stream if stream is not None else _raw_stream(t.get_device())
+
+
+def _ints(where, name, t):
+    if t is not None and not (t.dtype is _int32 and t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{where}: {name} must be a contiguous int32 CUDA tensor")
 
 
 def _heads(where, name, t):
-    """A bf16 [T, heads, D] tensor whose heads lie side by side; tokens may be any distance apart."""
-    _need(t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3, f"{where}: {name} must be a bf16 CUDA tensor [T, heads, D]")
+    """Elements between tokens of a bf16 [T, heads, D] tensor whose heads lie side by side."""
+    if not (t.dtype is _bf16 and t.is_cuda and t.dim() == 3):
+        raise ValueError(f"{where}: {name} must be a bf16 CUDA tensor [T, heads, D]")
+    T, heads, D = t.shape
     s = t.stride()
-    _need(t.numel() == 0 or (s[2] == 1 and (s[1] == t.shape[2] or t.shape[1] == 1)),
-          f"{where}: {name}'s heads must be contiguous within a token")
-    return s[0] if t.shape[0] > 1 and t.numel() else t.shape[1] * t.shape[2]
+    if T * heads and not (s[2] == 1 and (s[1] == D or heads == 1)):
+        raise ValueError(f"{where}: {name}'s heads must be contiguous within a token")
+    return s[0] if T > 1 and heads else heads * D
 
 
 def _cache_page(where, cache, D):
-    _need(cache.is_cuda and cache.dtype == torch.uint8 and cache.dim() == 3 and cache.is_contiguous(),
-          f"{where}: cache must be a contiguous uint8 CUDA tensor [n_pages, n_kv, page * D * 9 / 8]")
-    page, rest = divmod(cache.shape[2] * 8, D * 9)
-    _need(rest == 0, f"{where}: cache blocks of {cache.shape[2]} bytes do not hold whole positions of {D} dims")
+    if not (cache.dtype is _uint8 and cache.is_cuda and cache.dim() == 3 and cache.is_contiguous()):
+        raise ValueError(f"{where}: cache must be a contiguous uint8 CUDA tensor [n_pages, n_kv, page * D * 9 / 8]")
+    page, rest = divmod(cache.shape[2] * 8, D * 9) if D else (0, 1)
+    if rest:
+        raise ValueError(f"{where}: cache blocks of {cache.shape[2]} bytes do not hold whole positions of {D} dims")
     return page
+
+
+def _fail(text):
+    raise ValueError(text)
 
 
 def _keep(stream, *tensors):
     """Tensors made here and used on another stream than the current one stay alive until it is done with them."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(torch.cuda.ExternalStream(stream))
+    other = torch.cuda.ExternalStream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(other)
 
 
 def kv_cache(n_pages, n_kv, D, page, device="cuda"):
@@ -80,20 +92,28 @@ def kv_plan(cached_lens, new_lens, block_table, free_pages, page, T_cap, free_us
     cached_lens [R], new_lens [R], block_table [R, max_blocks] (fresh entries are
     written), free_pages [n], free_used [1] or None -> KVPlan(q_start [R + 1],
     seq_lens [R], requests, positions, slots [T_cap], counts [3])."""
-    _int32("kv_plan", cached_lens=cached_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, free_used=free_used)
+    for name, t in (("cached_lens", cached_lens), ("new_lens", new_lens), ("block_table", block_table), ("free_pages", free_pages),
+                    ("free_used", free_used)):
+        _ints("kv_plan", name, t)
     R = cached_lens.shape[0]
-    _need(new_lens.shape == (R,) and block_table.dim() == 2 and block_table.shape[0] == R,
-          "kv_plan: cached_lens [R], new_lens [R] and block_table [R, max_blocks] must agree")
-    _need(T_cap >= 1, "kv_plan: T_cap must be positive")
-    lens = torch.empty(2 * R + 4, dtype=torch.int32, device=cached_lens.device)
-    toks = torch.empty((3, T_cap), dtype=torch.int32, device=cached_lens.device)
-    _keep(stream, lens, toks)
-    at, row = lens.data_ptr(), toks.data_ptr()
-    _fw._check(_fw.lib().fw_kv_plan(cached_lens.data_ptr(), new_lens.data_ptr(), R, page, block_table.data_ptr(),
-                                    block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
-                                    _fw._ptr(free_used), T_cap, at, at + 4 * (R + 1), row, row + 4 * T_cap, row + 8 * T_cap,
-                                    at + 4 * (2 * R + 1), _fw._stream(stream)), "fw_kv_plan")
-    return KVPlan(lens[:R + 1], lens[R + 1:2 * R + 1], toks[0], toks[1], toks[2], lens[2 * R + 1:])
+    if new_lens.shape != cached_lens.shape or block_table.dim() != 2 or block_table.shape[0] != R:
+        _fail("kv_plan: cached_lens [R], new_lens [R] and block_table [R, max_blocks] must agree")
+    if T_cap < 1:
+        _fail("kv_plan: T_cap must be positive")
+    dev = cached_lens.device
+    # one buffer for all outputs; its rows are cut where the parts start
+    buf = torch.empty(3 * T_cap + 2 * R + 4, dtype=_int32, device=dev)
+    if stream is not None:
+        _keep(stream, buf)
+    at = buf.data_ptr()
+    lens = at + 12 * T_cap
+    rc = _fw.lib().fw_kv_plan(cached_lens.data_ptr(), new_lens.data_ptr(), R, page, block_table.data_ptr(), block_table.shape[1],
+                              free_pages.data_ptr(), free_pages.shape[0], _fw._ptr(free_used), T_cap, lens, lens + 4 * (R + 1),
+                              at, at + 4 * T_cap, at + 8 * T_cap, lens + 4 * (2 * R + 1), _stream(buf, stream))
+    if rc:
+        _fw._check(rc, "fw_kv_plan")
+    req, pos, slots, q_start, seq, counts = buf.split((T_cap, T_cap, T_cap, R + 1, R, 3))
+    return KVPlan(q_start, seq, req, pos, slots, counts)
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, interleaved=False, v=None, cache=None,
@@ -107,48 +127,69 @@ def qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, i
     qs, ks = _heads(w, "q", q), _heads(w, "k", k)
     T, n_q, D = q.shape
     n_kv = k.shape[1]
-    _need(k.shape == (T, n_kv, D), f"{w}: q [T, n_q, D] and k [T, n_kv, D] must agree")
-    _int32(w, positions=positions, slots=slots, status=status)
-    _need(cos_sin.is_cuda and cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
-          f"{w}: cos_sin must be a contiguous fp32 CUDA tensor [n_pos, rot]")
-    _need(positions.shape == (T,), f"{w}: positions must be [T]")
+    if k.shape[0] != T or k.shape[2] != D:
+        _fail(f"{w}: q [T, n_q, D] and k [T, n_kv, D] must agree")
+    for name, t in (("positions", positions), ("slots", slots), ("status", status)):
+        _ints(w, name, t)
+    if not (cos_sin.dtype is _fp32 and cos_sin.is_cuda and cos_sin.dim() == 2 and cos_sin.is_contiguous()):
+        _fail(f"{w}: cos_sin must be a contiguous fp32 CUDA tensor [n_pos, rot]")
+    if positions.shape[0] != T or positions.dim() != 1:
+        _fail(f"{w}: positions must be [T]")
     for t in (q_norm, k_norm):
-        _need(t is None or (t.is_cuda and t.dtype == torch.float32 and t.shape == (D,) and t.is_contiguous()),
-              f"{w}: norms must be contiguous fp32 CUDA tensors [D]")
+        if t is not None and not (t.dtype is _fp32 and t.is_cuda and t.dim() == 1 and t.shape[0] == D and t.is_contiguous()):
+            _fail(f"{w}: norms must be contiguous fp32 CUDA tensors [D]")
     page = n_pages = vs = 0
     if cache is not None:
         page, n_pages = _cache_page(w, cache, D), cache.shape[0]
-        _need(cache.shape[1] == n_kv, f"{w}: cache holds {cache.shape[1]} heads, k has {n_kv}")
-        _need(v is not None and v.shape == k.shape, f"{w}: a cache needs v [T, n_kv, D]")
-        _need(slots is not None and slots.shape == (T,), f"{w}: a cache needs slots [T]")
+        if cache.shape[1] != n_kv:
+            _fail(f"{w}: cache holds {cache.shape[1]} heads, k has {n_kv}")
+        if v is None or v.shape != k.shape:
+            _fail(f"{w}: a cache needs v [T, n_kv, D]")
+        if slots is None or slots.dim() != 1 or slots.shape[0] != T:
+            _fail(f"{w}: a cache needs slots [T]")
         vs = _heads(w, "v", v)
     if q_out is None:
-        q_out = torch.empty((T, n_q, D), dtype=torch.bfloat16, device=q.device)
-        _keep(stream, q_out)
-    if k_out is None and cache is None:
-        k_out = torch.empty((T, n_kv, D), dtype=torch.bfloat16, device=q.device)
-        _keep(stream, k_out)
-    _need(q_out.shape == q.shape and (k_out is None or k_out.shape == k.shape), f"{w}: outputs must have their inputs' shapes")
+        q_out = torch.empty((T, n_q, D), dtype=_bf16, device=q.device)
+        qos = n_q * D
+        if stream is not None:
+            _keep(stream, q_out)
+    else:
+        qos = _heads(w, "q_out", q_out)
+    kos = 0
+    if k_out is not None:
+        kos = _heads(w, "k_out", k_out)
+    elif cache is None:
+        k_out = torch.empty((T, n_kv, D), dtype=_bf16, device=q.device)
+        kos = n_kv * D
+        if stream is not None:
+            _keep(stream, k_out)
+    if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
+        _fail(f"{w}: outputs must have their inputs' shapes")
+    ptr = _fw._ptr
     args = FwQkNormRopeArgs(T, n_q, n_kv, D, cos_sin.shape[1], 1 if interleaved else 0, eps, cos_sin.shape[0], q.data_ptr(),
-                            k.data_ptr(), _fw._ptr(v), qs, ks, vs, _fw._ptr(q_norm), _fw._ptr(k_norm), cos_sin.data_ptr(),
-                            positions.data_ptr(), q_out.data_ptr(), _fw._ptr(k_out), _heads(w, "q_out", q_out),
-                            0 if k_out is None else _heads(w, "k_out", k_out), _fw._ptr(cache), _fw._ptr(slots), page, n_pages,
-                            _fw._ptr(status))
-    _fw._check(_fw.lib().fw_qk_norm_rope(ctypes.byref(args), _fw._stream(stream)), "fw_qk_norm_rope")
+                            k.data_ptr(), ptr(v), qs, ks, vs, ptr(q_norm), ptr(k_norm), cos_sin.data_ptr(), positions.data_ptr(),
+                            q_out.data_ptr(), ptr(k_out), qos, kos, ptr(cache), ptr(slots), page, n_pages, ptr(status))
+    rc = _fw.lib().fw_qk_norm_rope(ctypes.byref(args), _stream(q, stream))
+    if rc:
+        _fw._check(rc, "fw_qk_norm_rope")
     return q_out, k_out
 
 
 def kv_export(cache, slots, D, status=None, stream=None):
     """What slots (int32 [T]) of a cache hold (fw_kv_export) -> k, v bf16 [T, n_kv, D]."""
     page = _cache_page("kv_export", cache, D)
-    _int32("kv_export", slots=slots, status=status)
+    _ints("kv_export", "slots", slots)
+    _ints("kv_export", "status", status)
     T, n_kv = slots.shape[0], cache.shape[1]
-    kv = torch.empty((2, T, n_kv, D), dtype=torch.bfloat16, device=cache.device)
-    _keep(stream, kv)
-    at = kv.data_ptr()
-    _fw._check(_fw.lib().fw_kv_export(cache.data_ptr(), cache.shape[0], n_kv, D, page, slots.data_ptr(), T, at,
-                                      at + 2 * T * n_kv * D, _fw._ptr(status), _fw._stream(stream)), "fw_kv_export")
-    return kv[0], kv[1]
+    k = torch.empty((T, n_kv, D), dtype=_bf16, device=cache.device)
+    v = torch.empty((T, n_kv, D), dtype=_bf16, device=cache.device)
+    if stream is not None:
+        _keep(stream, k, v)
+    rc = _fw.lib().fw_kv_export(cache.data_ptr(), cache.shape[0], n_kv, D, page, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
+                                _fw._ptr(status), _stream(cache, stream))
+    if rc:
+        _fw._check(rc, "fw_kv_export")
+    return k, v
 
 
 def attn_q4(q, cache, block_table, q_start, seq_lens, max_q, scale=None, window=0, sinks=0, out=None, status=None, stream=None):
@@ -160,20 +201,32 @@ def attn_q4(q, cache, block_table, q_start, seq_lens, max_q, scale=None, window=
     qs = _heads(w, "q", q)
     T, n_q, D = q.shape
     page = _cache_page(w, cache, D)
-    _int32(w, block_table=block_table, q_start=q_start, seq_lens=seq_lens, status=status)
+    for name, t in (("block_table", block_table), ("q_start", q_start), ("seq_lens", seq_lens), ("status", status)):
+        _ints(w, name, t)
     R = seq_lens.shape[0]
-    _need(block_table.dim() == 2 and block_table.shape[0] == R and q_start.shape == (R + 1,),
-          f"{w}: block_table [R, max_blocks], q_start [R + 1] and seq_lens [R] must agree")
+    if block_table.dim() != 2 or block_table.shape[0] != R or q_start.dim() != 1 or q_start.shape[0] != R + 1:
+        _fail(f"{w}: block_table [R, max_blocks], q_start [R + 1] and seq_lens [R] must agree")
     if out is None:
-        out = torch.empty((T, n_q, D), dtype=torch.bfloat16, device=q.device)
-        _keep(stream, out)
-    _need(out.shape == q.shape, f"{w}: out must have q's shape")
+        out = torch.empty((T, n_q, D), dtype=_bf16, device=q.device)
+        os = n_q * D
+        if stream is not None:
+            _keep(stream, out)
+    else:
+        os = _heads(w, "out", out)
+        if out.shape != q.shape:
+            _fail(f"{w}: out must have q's shape")
     args = FwAttnQ4Args(R, T, max_q, n_q, cache.shape[1], D, page, cache.shape[0], block_table.shape[1], window, sinks,
-                        1.0 / math.sqrt(D) if scale is None else scale, q.data_ptr(), out.data_ptr(), qs, _heads(w, "out", out),
-                        cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(), seq_lens.data_ptr(), _fw._ptr(status))
-    L, ref, need = _fw.lib(), ctypes.byref(args), _i64()
-    _fw._check(L.fw_attn_q4_workspace(ref, ctypes.byref(need)), "fw_attn_q4_workspace")
-    ws = torch.empty(need.value, dtype=torch.uint8, device=q.device) if need.value else None
-    _keep(stream, ws)
-    _fw._check(L.fw_attn_q4(ref, _fw._ptr(ws), need.value, _fw._stream(stream)), "fw_attn_q4")
+                        1.0 / math.sqrt(D) if scale is None else scale, q.data_ptr(), out.data_ptr(), qs, os, cache.data_ptr(),
+                        block_table.data_ptr(), q_start.data_ptr(), seq_lens.data_ptr(), _fw._ptr(status))
+    L, ref, need, ws = _fw.lib(), ctypes.byref(args), _i64(), None
+    rc = L.fw_attn_q4_workspace(ref, ctypes.byref(need))
+    if rc:
+        _fw._check(rc, "fw_attn_q4_workspace")
+    if need.value:
+        ws = torch.empty(need.value, dtype=_uint8, device=q.device)
+        if stream is not None:
+            _keep(stream, ws)
+    rc = L.fw_attn_q4(ref, _fw._ptr(ws), need.value, _stream(q, stream))
+    if rc:
+        _fw._check(rc, "fw_attn_q4")
     return out

@@ -4,6 +4,8 @@
 //
 // for request r's i-th new token at position p = seq_len - n_new + i; key j is
 // visible when j <= p and (window == 0 or j > p - window or j < sinks).
+#include <mutex>
+
 #include "attn.cuh"
 
 namespace fw {
@@ -30,6 +32,7 @@ __global__ void __launch_bounds__(kTile) attn_rows_kernel(fw_attn_q4_args a) {
   }
   const int r = lo;
   if (t < a.q_start[r] || t >= a.q_start[r + 1]) return;
+  if ((a.q_start[r + 1] - a.q_start[r]) * (a.n_q / a.n_kv) <= kDecodeRows) return;  // the decode kernel's
   const int S = a.seq_lens[r], p = S - (a.q_start[r + 1] - t);
   for (int d = tid; d < D; d += kTile)
     s_q[d] = __bfloat162float(((const __nv_bfloat16*)a.q)[t * a.q_stride + h * D + d]) * a.scale;
@@ -113,6 +116,12 @@ static fw_status check_args(const fw_attn_q4_args* a, bool pointers) {
   if (a->R < 0 || a->R > (1 << 20) || a->T < 0 || a->max_q < 0 || a->max_q > a->T || a->max_blocks < 1)
     return set_error(FW_EINVAL, "fw_attn_q4: need 0 <= R <= 2^20, 0 <= max_q <= T and max_blocks >= 1");
   if (a->window < 0 || a->sinks < 0) return set_error(FW_EINVAL, "fw_attn_q4: window and sinks must not be negative");
+  if ((int64_t)a->max_blocks * a->page > 0x7FFFFFFFll)
+    return set_error(FW_EINVAL, "fw_attn_q4: need max_blocks * page < 2^31");
+  // a request's 128-key units over all heads are counted in 32 bits, and so is a CTA's share of all (at least 152 CTAs)
+  const int64_t units = ((int64_t)a->max_blocks * a->page / 128 + 2) * a->n_kv;
+  if (units >= 1 << 30 || units / 128 * a->R >= 1 << 30)
+    return set_error(FW_EUNSUPPORTED, "fw_attn_q4: R block-table rows of max_blocks pages are beyond any cache");
   if (!(a->scale > 0.f) || a->scale > 3e38f) return set_error(FW_EINVAL, "fw_attn_q4: scale must be positive and finite");
   if (!pointers || a->R == 0 || a->T == 0 || a->max_q == 0) return FW_OK;
   if (!a->q || !a->out || !a->cache || !a->block_table || !a->q_start || !a->seq_lens)
@@ -126,18 +135,49 @@ static fw_status check_args(const fw_attn_q4_args* a, bool pointers) {
   return FW_OK;
 }
 
+// The current device's SM count, its kernels configured once; 0: no such device.
+static int device_sms() {
+  static std::mutex mu;
+  static int sms[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> g(mu);
+  if (!sms[dev]) {
+    int n = 0;
+    if (configure_attn_kernels() != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return 0;
+    sms[dev] = n;
+  }
+  return sms[dev];
+}
+
+static bool has_decode(const fw_attn_q4_args* a) { return a->n_q / a->n_kv <= kDecodeRows; }
+
 extern "C" fw_status fw_attn_q4_workspace(const fw_attn_q4_args* a, int64_t* bytes) {
   if (!bytes) return set_error(FW_EINVAL, "fw_attn_q4_workspace: null pointer");
   *bytes = 0;
-  return check_args(a, false);
+  if (fw_status st = check_args(a, false); st != FW_OK) return st;
+  if (a->R == 0 || a->T == 0 || a->max_q == 0) return FW_OK;
+  if (fw_status st = check_device("fw_attn_q4: needs an sm_103 device"); st != FW_OK) return st;
+  const int sms = device_sms();
+  if (!sms) return set_error(FW_ECUDA, "fw_attn_q4: the device could not be set up");
+  if (has_decode(a)) *bytes = decode_workspace(*a, sms);
+  return FW_OK;
 }
 
 extern "C" fw_status fw_attn_q4(const fw_attn_q4_args* a, void* workspace, int64_t bytes, void* stream) {
   if (fw_status st = check_args(a, true); st != FW_OK) return st;
   if (a->R == 0 || a->T == 0 || a->max_q == 0) return FW_OK;
-  if (fw_status st = check_device("fw_attn_q4: needs an sm_103 device"); st != FW_OK) return st;
-  const cudaError_t e = dev::launch_dependent(a->D == 64 ? attn_rows_kernel<64> : attn_rows_kernel<128>, dim3(a->T, a->n_q),
-                                              dim3(kTile), 0, static_cast<cudaStream_t>(stream), *a);
+  int64_t need = 0;
+  if (fw_status st = fw_attn_q4_workspace(a, &need); st != FW_OK) return st;
+  if (need && (!workspace || bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16))
+    return set_error(FW_EINVAL, "fw_attn_q4: the workspace is too small (see fw_attn_q4_workspace) or not 16-byte aligned");
+  const int sms = device_sms(), G = a->n_q / a->n_kv;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (has_decode(a)) e = launch_attn_decode(*a, workspace, sms, s);
+  if (e == cudaSuccess && (int64_t)a->max_q * G > kDecodeRows)
+    e = dev::launch_dependent(a->D == 64 ? attn_rows_kernel<64> : attn_rows_kernel<128>, dim3(a->T, a->n_q), dim3(kTile), 0, s, *a);
   if (e != cudaSuccess) return set_error(FW_ECUDA, "fw_attn_q4: launch failed");
   return FW_OK;
 }

@@ -1,0 +1,705 @@
+// Attention for requests that bring few query rows (new tokens x heads that
+// share a key/value head, at most 16): single tokens and short drafts over
+// long contexts. Every key and value is used by few rows, so the kernel is
+// bound by streaming the 4-bit cache from HBM, and by the instructions that
+// unpack it.
+//
+//   s[t, n] = sum_b d_k[t, b] sum_{i in b} q[n, i] (c[t, i] - 8)
+//   o[n, i] = sum_t (p[t, n] d_v[t, b(i)]) (c'[t, i] - 8)
+//
+// The block scales are taken out of the products: what enters the tensor
+// cores as their 16-row operand are the bare codes (keys in rows for s, dims in
+// rows for o), which bf16 holds exactly, and the query rows are the 8-column
+// operand, so a group of up to 8 rows wastes nothing. A nibble becomes bf16
+// 128 + c by one AND-OR with 0x4300 (after a shift; two values at once). For the keys the
+// offset is taken back in the accumulator's start (-136 sum q, one block of 32
+// long: exact enough in fp32); the values' sums run over the whole context,
+// where the offset would cancel badly, so 136 is subtracted exactly first.
+//
+// Work: a unit is 128 keys of one (request, key/value head); the CTAs take
+// equal consecutive shares of all units, so that ragged lengths and few
+// requests both fill the GPU. A unit's pages come into a shared-memory ring by
+// one bulk copy each, which the CTA's eight warps issue in turn; each warp
+// takes 16 of the unit's keys, with a softmax state of its own that is joined
+// at the end of a segment. A pair whose units fall into several CTAs leaves
+// partial results that a second small kernel joins. (Eight warps and no ninth
+// as producer: two CTAs of eight leave each warp 128 registers, of nine 96.)
+#include <type_traits>
+
+#include "attn.cuh"
+
+namespace fw {
+namespace {
+
+using namespace dev;
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kTeam = 4;          // warps of a stage (32 keys each); two teams take the stages in turn
+constexpr int kChunk = kThreads;  // requests scanned at a time
+constexpr float kLazy = 8.f;      // a row's maximum moves only when a score passes it by 2^8
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int NB = D / kKvBlock, Rows = 8 * NT;
+  static constexpr uint32_t StageBytes = kStageKeys * D * 9 / 8;
+  static constexpr int Stages = D == 128 ? 4 : 8;
+  static constexpr int Pitch = D + 4;  // floats between rows of the join buffer: its 16-byte accesses meet no bank twice
+  static constexpr uint32_t JoinBytes = kWarps / 2 * 8 * Pitch * 4;
+  static constexpr uint32_t QBytes = NT == 1 ? 0 : Rows * D * 2;
+  static constexpr uint32_t SmemBytes = Stages * StageBytes + JoinBytes + QBytes;
+};
+
+struct DecodeArgs {
+  fw_attn_q4_args u;
+  float* o;             // [2 grid][Rows][D]
+  float2* ml;           // [2 grid][Rows] maximum (log2), sum
+  SplitRecord* rec;     // [grid]
+  float scale_log2;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// nibbles j and j + 4 of a word -> bf16 pair 128 + c, in one shift and one
+// three-input logic operation: the mask has to sit in a register the compiler
+// takes for a variable, or it makes the last step two operations with constants
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, 0x43004300, 0xEA;" : "=r"(r) : "r"(w >> (4 * j)), "r"(mask));
+  return r;
+}
+__device__ __forceinline__ uint32_t minus136(uint32_t x) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x43084308u));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+template <int N, int Offset>
+__device__ __forceinline__ Words<N> lds(uint32_t p) {
+  Words<N> r;
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(p), "n"(Offset) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2+%3];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(p), "n"(Offset) : "memory");
+  else
+    asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(r.w[0]) : "r"(p), "n"(Offset) : "memory");
+  return r;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) {
+  using C = Cfg<D, NT>;
+  constexpr int NB = C::NB, kStages = C::Stages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+  __shared__ uint32_t s_have[kStages];       // bit w: the stage's keys 16 w .. 16 w + 15 are there
+  __shared__ int s_pref[kChunk + 1];         // units before each request of the chunk, from this CTA's first one on
+  __shared__ int s_len[kChunk], s_new[kChunk], s_tok[kChunk];
+  __shared__ long long s_scan[kWarps];
+  __shared__ float2 s_ml[kWarps][C::Rows];
+  __shared__ float s_qs[C::Rows][NB];        // several row tiles: -136 x a row's sums over the blocks
+  float* join = reinterpret_cast<float*>(smem + kStages * C::StageBytes);
+  uint8_t* s_q = smem + kStages * C::StageBytes + C::JoinBytes;  // several row tiles: their query rows
+  const fw_attn_q4_args& u = a.u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int G = u.n_q / u.n_kv;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kTeam);
+    }
+    fence_mbar_init();
+    a.rec[blockIdx.x].parts = 0;
+  }
+
+  // a request's units; 0 when it has no rows or more than this kernel takes
+  auto request = [&](int r, int& S, int& n, int& q0) -> long long {
+    if (r >= u.R) return 0;
+    q0 = u.q_start[r];
+    n = u.q_start[r + 1] - q0;
+    S = u.seq_lens[r];
+    if (n < 1 || n * (long long)G > kDecodeRows || q0 < 0 || q0 > u.T - n) return 0;
+    if (S > u.max_blocks * u.page) {
+      S = u.max_blocks * u.page;
+      raise(u.status, FW_KV_BAD_SLOT);
+    }
+    // an empty context is one unit without keys: its rows are zeros
+    return (long long)::max(1, visible_stages(::max(S, 0), S - n, u.window, u.sinks).count()) * u.n_kv;
+  };
+  // sum over the CTA; also the running sum before each thread
+  auto scan = [&](long long v, long long& before) -> long long {
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    long long sum = 0;
+    before = inc - v;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_scan[w];
+      sum += s_scan[w];
+    }
+    return sum;
+  };
+  long long total = 0, before, mine = 0;
+  int S = 0, n = 0, q0 = 0;
+  for (int r0 = 0; r0 < u.R; r0 += kChunk) {
+    mine = request(r0 + tid, S, n, q0);
+    total += scan(mine, before);
+  }
+  // no more CTAs than units: the parts of a split pair are then consecutive CTAs
+  const int grid = (int)::min((long long)gridDim.x, ::max(total, 1ll)), cta = ::min((int)blockIdx.x, grid);
+  const long long u_begin = total * cta / grid;
+  const int u_end = (int)(total * (cta + 1) / grid - u_begin);
+  const KvPlanes pl = kv_planes(u.page, D);
+  const uint32_t hb = (uint32_t)kv_head_bytes(u.page, D);
+  const int page_shift = __ffs(u.page) - 1;
+  // where this lane's operands of the warp's 32 keys lie in a stage (shared
+  // addresses), and how far on those of the second 16 are
+  const int key_w = (warp % kTeam) * 32, at0 = key_w & (u.page - 1);
+  const bool apart = u.page == 16;  // the second 16 keys are another page's
+  const uint32_t blk0 = smem_u32(smem) + (key_w >> page_shift) * hb;
+  const uint32_t at_k = blk0 + (at0 + g) * (D / 2) + q * (NB * 4), at_ks = blk0 + pl.ks + (at0 + g) * (NB * 2);
+  const uint32_t at_v = blk0 + pl.vc + (at0 / 2 + q) * D + g * (NB * 4), at_vs = blk0 + pl.vs + (at0 / 2 + q) * (NB * 4);
+  const uint32_t on_k = apart ? hb : 16 * (D / 2), on_ks = apart ? hb : 16 * NB * 2;
+  const uint32_t on_v = apart ? hb : 8 * D, on_vs = apart ? hb : 8 * NB * 4;
+  uint32_t mask;
+  asm volatile("mov.u32 %0, 0x000F000F;" : "=r"(mask));
+
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // by a whole warp
+    if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity))) {
+      ok = false;
+      raise(u.status, FW_KV_TIMEOUT);
+    }
+  };
+  uint32_t it = 0, last_fill = 0;  // stages consumed; one past the last stage this warp filled
+  long long base = -u_begin;
+  for (int r0 = 0; r0 < u.R && base < u_end; r0 += kChunk) {
+    if (u.R > kChunk) mine = request(r0 + tid, S, n, q0);  // else they are still in registers
+    const long long sum = scan(mine, before);
+    // (a request's units and a CTA's share fit 32 bits: checked on the host; what lies before the CTA's share does not matter)
+    s_pref[tid] = (int)::max(base + before, -(1ll << 30));
+    s_len[tid] = S;
+    s_new[tid] = n;
+    s_tok[tid] = q0;
+    base += sum;
+    if (tid == 0) s_pref[kChunk] = (int)::max(::min(base, 1ll << 30), -(1ll << 30));
+    __syncthreads();
+    const int from = ::max(0, s_pref[0]), to = ::min(u_end, s_pref[kChunk]);
+    if (from >= to) continue;
+    int k = 0;  // the request (of the chunk) that holds unit `from`
+    for (int step = kChunk / 2; step; step >>= 1)
+      if (s_pref[k + step] <= from) k += step;
+
+    // Filling a stage takes two steps, so that the block table's latency is
+    // nobody's: look() finds unit y's pages, one to a lane (the pages without a
+    // key that some row sees are left out), several stages before issue()
+    // copies them. kf: the request at or before the next y's.
+    int kf = k, f_head = 0, f_id = 0;
+    bool f_copy = false;
+    auto look = [&](int y) {
+      f_copy = false;
+      if (y >= to) return;
+      while (s_pref[kf + 1] <= y) ++kf;
+      const int S_r = s_len[kf], first = S_r - s_new[kf];
+      const Stages v = visible_stages(::max(S_r, 0), first, u.window, u.sinks);
+      const int lo_key = u.window ? ::max(0, ::max(0, first) + 1 - u.window) : 0;
+      const int n_st = ::max(1, v.count()), rel = y - s_pref[kf];
+      f_head = rel / n_st;
+      const int key = v.block(rel - f_head * n_st) * kStageKeys + (lane << page_shift);
+      f_copy = lane < (kStageKeys >> page_shift) && key < S_r && (key + u.page > lo_key || key < u.sinks);
+      if (f_copy) f_id = u.block_table[(int64_t)(r0 + kf) * u.max_blocks + (key >> page_shift)];
+    };
+    auto issue = [&](uint32_t j) {
+      const int slot = j % kStages;
+      bool copy = f_copy;
+      if (copy && (f_id < 0 || f_id >= u.n_pages)) {
+        copy = false;
+        raise(u.status, FW_KV_BAD_SLOT);
+      }
+      const uint32_t got = __ballot_sync(0xFFFFFFFFu, copy);
+      wait(&empty[slot], ((j / kStages) & 1) ^ 1);
+      if (!ok) return;
+      if (lane == 0) {
+        uint32_t have = 0;  // a page's bit, for each 16 keys of it
+#pragma unroll
+        for (int w = 0; w < kStageKeys / 16; ++w) have |= (got >> ((w * 16) >> page_shift) & 1) << w;
+        s_have[slot] = have;
+        mbar_arrive_expect_tx(&full[slot], (uint32_t)__popc(got) * hb);
+      }
+      __syncwarp();
+      if (copy)
+        bulk_g2s(smem + slot * C::StageBytes + lane * hb, (const uint8_t*)u.cache + ((int64_t)f_id * u.n_kv + f_head) * hb, hb,
+                 &full[slot]);
+      last_fill = j + 1;
+    };
+    // the warps take turns at filling, kStages - 1 stages ahead
+    const uint32_t it0 = it - from;  // the ring's count at this CTA's first unit
+    if (warp < kStages - 1 && from + warp < to) {
+      look(from + warp);
+      issue(it + warp);
+    }
+    // the unit this warp fills next: at the end of the stage kStages - 1 before, one of its team's
+    const int turn = 2 * (warp % kTeam) + warp / kTeam;
+    int next = from + kStages - 1 + ((turn - (int)it) & (kWarps - 1));
+    look(next);
+
+    for (int x = from; x < to; ++k) {
+      const int p0 = s_pref[k], p1 = s_pref[k + 1];
+      if (p1 <= x) continue;
+      const int S_r = s_len[k], n_r = s_new[k], first = S_r - n_r, rows = n_r * G, tok0 = s_tok[k];
+      const Stages v = visible_stages(::max(S_r, 0), first, u.window, u.sinks);
+      const int n_st = ::max(1, v.count());
+      const int lo_key = u.window ? ::max(0, ::max(0, first) + 1 - u.window) : 0;  // the first key of the first row's window
+      const int lo_edge = u.window ? lo_key + n_r : 0;  // keys below are not seen by every row
+      const int stop = ::min(p1, to);
+      while (x < stop) {  // one segment: the rest of this head's stages, or of this CTA's share
+        const int head = (x - p0) / n_st, st0 = x - p0 - head * n_st;
+        const int n_here = ::min(n_st - st0, stop - x);
+        // Query rows as the 8-column operand: thread (g, q) holds row g's dims
+        // 32 b + 8 q .. + 7. One tile of rows stays in registers, two in shared
+        // memory. qs: -136 x the sums of rows 2 q and 2 q + 1 over block b.
+        auto load_q = [&](int row, int b) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (row < rows)
+            w = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)u.q + (int64_t)(tok0 + row / G) * u.q_stride +
+                                                (head * G + row % G) * D + 32 * b + 8 * q);
+          return w;
+        };
+        auto sum8 = [&](uint4 w) {
+          float s = 0.f, lo, hi;
+          for (uint32_t x : {w.x, w.y, w.z, w.w}) {
+            bf16x2_to_f32(x, lo, hi);
+            s += lo + hi;
+          }
+          s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+          s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+          return s * -136.f;
+        };
+        uint4 qf[NT == 1 ? NB : 1];
+        float qs[NT == 1 ? NB : 1][2];
+        if constexpr (NT == 1) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            qf[b] = load_q(g, b);
+            const float s = sum8(qf[b]);
+            qs[b][0] = __shfl_sync(0xFFFFFFFFu, s, 8 * q);
+            qs[b][1] = __shfl_sync(0xFFFFFFFFu, s, 8 * q + 4);
+          }
+        } else {  // (the previous segment's last barrier lies behind)
+          for (int e = warp; e < NT * NB; e += kWarps) {
+            const int t = e / NB, b = e % NB;
+            const uint4 w = load_q(8 * t + g, b);
+            const float s = sum8(w);
+            *reinterpret_cast<uint4*>(s_q + (e * 32 + lane) * 16) = w;
+            if (q == 0) s_qs[8 * t + g][b] = s;
+          }
+          __syncthreads();
+        }
+        int pos[NT][2];  // positions of rows 2 q, 2 q + 1 (rows past the last: none)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row2 = 8 * t + 2 * q + i;
+            pos[t][i] = row2 < rows ? first + row2 / G : -1;
+          }
+        // mz: a row's maximum (0 before there is one); lim: what a score may
+        // pass it by before it moves (-inf: there is none yet)
+        float o[NT][NB][2][4] = {}, mz[NT][2], lim[NT][2], l[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mz[t][0] = mz[t][1] = l[t][0] = l[t][1] = 0.f, lim[t][0] = lim[t][1] = -INFINITY;
+
+        // 16 keys of this warp, or its 32 at once (U = 2: twice the independent
+        // work). kEdge: not every row sees all of them (the last keys, the
+        // window's edge); `stage`: byte offset of their stage, `second`: the
+        // keys are the second 16.
+        auto keys = [&](auto count, auto edge, uint32_t stage, bool second, int key0) {
+          constexpr int U = decltype(count)::value;
+          constexpr bool kEdge = decltype(edge)::value;
+          const uint32_t in_k = at_k + stage + (second ? on_k : 0), in_ks = at_ks + stage + (second ? on_ks : 0);
+          const uint32_t in_v = at_v + stage + (second ? on_v : 0), in_vs = at_vs + stage + (second ? on_vs : 0);
+          float s[U][NT][4];
+#pragma unroll
+          for (int h = 0; h < U; ++h) {
+            const Words<NB> k0 = lds<NB, 0>(in_k + h * on_k), k1 = lds<NB, 8 * (D / 2)>(in_k + h * on_k);
+            const Words<NB / 2> d0 = lds<NB / 2, 0>(in_ks + h * on_ks), d1 = lds<NB / 2, 8 * NB * 2>(in_ks + h * on_ks);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const float e0 = __uint_as_float(b & 1 ? d0.w[b / 2] & 0xFFFF0000u : d0.w[b / 2] << 16);
+              const float e1 = __uint_as_float(b & 1 ? d1.w[b / 2] & 0xFFFF0000u : d1.w[b / 2] << 16);
+              uint32_t x0[4], x1[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x0[j] = code_pair(k0.w[b], j, mask), x1[j] = code_pair(k1.w[b], j, mask);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                uint4 w;
+                float z0, z1;
+                if constexpr (NT == 1) {
+                  w = qf[b], z0 = qs[b][0], z1 = qs[b][1];
+                } else {
+                  w = *reinterpret_cast<const uint4*>(s_q + ((t * NB + b) * 32 + lane) * 16);
+                  z0 = s_qs[8 * t + 2 * q][b], z1 = s_qs[8 * t + 2 * q + 1][b];
+                }
+                const float c0[4] = {z0, z1, z0, z1};
+                float c[4];
+                mma16816(c, x0[0], x1[0], x0[1], x1[1], w.x, w.y, c0);
+                mma16816(c, x0[2], x1[2], x0[3], x1[3], w.z, w.w, c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[h][t][e] = b == 0 ? c[e] * (e < 2 ? e0 : e1) : fmaf(c[e], e < 2 ? e0 : e1, s[h][t][e]);
+              }
+            }
+          }
+          // in units of log2 and less the row's maximum as last taken
+          bool moves = false;
+#pragma unroll
+          for (int h = 0; h < U; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[h][t][e] = fmaf(s[h][t][e], a.scale_log2, -mz[t][e & 1]);
+                if (kEdge && !sees(pos[t][e & 1], key0 + 16 * h + g + 8 * (e >> 1), u.window, u.sinks)) s[h][t][e] = -INFINITY;
+                moves |= s[h][t][e] > lim[t][e & 1];
+              }
+          if (__any_sync(0xFFFFFFFFu, moves)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float up = fmaxf(s[0][t][j], s[0][t][j + 2]);
+                if (U == 2) up = fmaxf(up, fmaxf(s[U - 1][t][j], s[U - 1][t][j + 2]));
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, d));
+                // a first maximum is taken as it is, a later one only moves up
+                if (lim[t][j] != -INFINITY) up = fmaxf(up, 0.f);
+                if (up == -INFINITY) continue;
+                const float keep = lim[t][j] == -INFINITY ? 0.f : exp2_fast(-up);
+                mz[t][j] += up;
+                lim[t][j] = kLazy;
+                l[t][j] *= keep;
+#pragma unroll
+                for (int h = 0; h < U; ++h) {
+                  s[h][t][j] -= up;
+                  s[h][t][j + 2] -= up;
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    o[t][b][h][j] *= keep;
+                    o[t][b][h][j + 2] *= keep;
+                  }
+              }
+          }
+          uint32_t pf[U][NT][2];  // probabilities: row g, keys 2 q, 2 q + 1 (+ 8)
+#pragma unroll
+          for (int h = 0; h < U; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              float(&x)[4] = s[h][t];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = exp2_fast(x[e]);
+              l[t][0] += x[0] + x[2];
+              l[t][1] += x[1] + x[3];
+              pf[h][t][0] = transpose8x8(bf16x2_bits(x[0], x[1]));
+              pf[h][t][1] = transpose8x8(bf16x2_bits(x[2], x[3]));
+            }
+          // which of this lane's two key pairs its row g sees, as masks of packed pairs
+          uint32_t keep[U][NT][2];
+          if constexpr (kEdge) {
+#pragma unroll
+            for (int h = 0; h < U; ++h)
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int row = 8 * t + g, p = row < rows ? first + row / G : -1, j = key0 + 16 * h + 8 * e + 2 * q;
+                  keep[h][t][e] = (sees(p, j, u.window, u.sinks) ? 0xFFFFu : 0u) | (sees(p, j + 1, u.window, u.sinks) ? 0xFFFF0000u : 0u);
+                }
+          }
+          // values
+#pragma unroll
+          for (int h = 0; h < U; ++h) {
+            const Words<NB> v0 = lds<NB, 0>(in_v + h * on_v), v1 = lds<NB, 4 * D>(in_v + h * on_v);
+            const Words<NB> f0 = lds<NB, 0>(in_vs + h * on_vs), f1 = lds<NB, 4 * NB * 4>(in_vs + h * on_vs);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              uint32_t w0[NT], w1[NT];
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                w0[t] = mul_bf16x2(pf[h][t][0], f0.w[b]);
+                w1[t] = mul_bf16x2(pf[h][t][1], f1.w[b]);
+                if constexpr (kEdge) {  // a masked key adds nothing, whatever its scale is
+                  w0[t] &= keep[h][t][0];
+                  w1[t] &= keep[h][t][1];
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t a0 = minus136(code_pair(v0.w[b], 2 * e, mask)), a1 = minus136(code_pair(v0.w[b], 2 * e + 1, mask));
+                const uint32_t a2 = minus136(code_pair(v1.w[b], 2 * e, mask)), a3 = minus136(code_pair(v1.w[b], 2 * e + 1, mask));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816(o[t][b][e], a0, a1, a2, a3, w0[t], w1[t], o[t][b][e]);
+              }
+            }
+          }
+        };
+        using one = std::integral_constant<int, 1>;
+        using two = std::integral_constant<int, 2>;
+
+        // the stages of this warp's team
+#pragma unroll 1
+        for (int i = (it ^ (warp / kTeam)) & 1; i < n_here; i += 2) {
+          const uint32_t j = it + i;
+          const int slot = j % kStages;
+          wait(&full[slot], (j / kStages) & 1);
+          const int key0 = v.block(st0 + i) * kStageKeys + key_w;
+          const uint32_t have = ok ? s_have[slot] >> (key_w / 16) & 3 : 0, stage = slot * C::StageBytes;
+          if (NT == 1 && have == 3 && key0 + 31 <= first && key0 >= lo_edge) {
+            keys(two{}, std::false_type{}, stage, false, key0);
+          } else {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              const int key_h = key0 + 16 * h;
+              if (!(have >> h & 1) || key_h >= S_r) continue;
+              if (NT > 1 && key_h + 15 <= first && key_h >= lo_edge)
+                keys(one{}, std::false_type{}, stage, h, key_h);
+              else
+                keys(one{}, std::true_type{}, stage, h, key_h);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[slot]);
+          // this warp's turn: the slot of the stage before, which the other team has left by now
+          if (x + i + kStages - 1 == next && next < to) {
+            issue(it0 + next);
+            next += kWarps;
+            look(next);
+          }
+        }
+        it += n_here;
+
+        // -------------------------------- join the eight warps, a tile of rows at a time
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[t][j] += __shfl_xor_sync(0xFFFFFFFFu, l[t][j], d);
+            const float m = lim[t][j] == -INFINITY ? -INFINITY : mz[t][j];
+            if (g == 0) s_ml[warp][8 * t + 2 * q + j] = make_float2(m, l[t][j]);
+          }
+        __syncthreads();
+        const bool whole = n_here == n_st;
+        const int part = 2 * cta + (x == 0 ? 0 : 1);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          // warps 4..7 hand over to warps 0..3, whose sums the rows' threads then add
+#pragma unroll
+          for (int half = 1; half >= 0; --half) {
+            if (warp / (kWarps / 2) == half) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int row = 8 * t + 2 * q + j;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][row].x);
+                const float f = lim[t][j] == -INFINITY ? 0.f : exp2_fast(mz[t][j] - top);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                  float4* at = reinterpret_cast<float4*>(join + ((warp % (kWarps / 2)) * 8 + 2 * q + j) * C::Pitch + 32 * b + 4 * g);
+                  float4 y = make_float4(o[t][b][0][j] * f, o[t][b][0][j + 2] * f, o[t][b][1][j] * f, o[t][b][1][j + 2] * f);
+                  if (half == 0) {
+                    const float4 z = *at;
+                    y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+                  }
+                  *at = y;
+                }
+              }
+            }
+            __syncthreads();
+          }
+          for (int e = tid; e < 8 * (D / 4); e += kThreads) {
+            const int r8 = e / (D / 4), row = 8 * t + r8, d4 = e % (D / 4);
+            if (row >= rows) break;
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][row].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const float2 ml = s_ml[w][row];
+              sum += ml.y * (ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top));
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps / 2; ++w) {
+              const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 + r8) * C::Pitch + 4 * d4);
+              acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
+            }
+            if (whole) {
+              const float inv = sum == 0.f ? 0.f : 1.f / sum;
+              __nv_bfloat16* dst = (__nv_bfloat16*)u.out + (int64_t)(tok0 + row / G) * u.out_stride + (head * G + row % G) * D + 4 * d4;
+              *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
+            } else {
+              *reinterpret_cast<float4*>(a.o + ((int64_t)part * C::Rows + row) * D + 4 * d4) = acc;
+              if (d4 == 0) a.ml[(int64_t)part * C::Rows + row] = make_float2(top, sum);
+            }
+          }
+          __syncthreads();
+        }
+        if (!whole && st0 == 0 && tid == 0) {
+          const long long last = u_begin + x + n_st - 1;  // this head's last unit, and the CTA that has it
+          SplitRecord rec;
+          rec.cta0 = cta;
+          rec.parts = (int)(((last + 1) * grid - 1) / total) - cta + 1;
+          rec.slot0 = part;
+          rec.rows = rows;
+          rec.token0 = tok0;
+          rec.head0 = head * G;
+          rec.group = G;
+          rec.pad = 0;
+          a.rec[cta] = rec;
+        }
+        x += n_here;
+      }
+    }
+  }
+  // copies in flight after an abandoned wait land before the CTA leaves: this
+  // warp's last kStages fills are the only ones that can be
+  if (!ok)
+    for (uint32_t j = last_fill > (uint32_t)kStages ? last_fill - kStages : 0; j < last_fill; ++j)
+      mbar_wait(&full[j % kStages], (j / kStages) & 1);
+}
+
+// Joins the parts of one row of one split pair: o = sum_i 2^(m_i - M) o_i over
+// sum_i 2^(m_i - M) l_i, the parts taken by eight groups of lanes.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(DecodeArgs a, int rows_max) {
+  constexpr int L = D / 4, Groups = 256 / L;
+  __shared__ float4 s_o[256];
+  __shared__ float2 s_ml[Groups];
+  pdl_wait();
+  pdl_launch_dependents();
+  const SplitRecord rec = a.rec[blockIdx.x];
+  const int row = blockIdx.y, l = threadIdx.x % L, grp = threadIdx.x / L;
+  if (rec.parts == 0 || row >= rec.rows) return;
+  float m = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = grp; i < rec.parts; i += Groups) {
+    const int64_t at = (int64_t)(i == 0 ? rec.slot0 : 2 * (rec.cta0 + i)) * rows_max + row;
+    const float2 ml = __ldcg(a.ml + at);
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.o + at * D) + l);
+    const float m2 = fmaxf(m, ml.x), keep = m == -INFINITY ? 0.f : exp2_fast(m - m2);
+    const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m2);
+    m = m2;
+    sum = sum * keep + ml.y * f;
+    acc.x = acc.x * keep + o.x * f;
+    acc.y = acc.y * keep + o.y * f;
+    acc.z = acc.z * keep + o.z * f;
+    acc.w = acc.w * keep + o.w * f;
+  }
+  s_o[threadIdx.x] = acc;
+  if (l == 0) s_ml[grp] = make_float2(m, sum);
+  __syncthreads();
+  if (grp) return;
+  float top = -INFINITY;
+  for (int i = 0; i < Groups; ++i) top = fmaxf(top, s_ml[i].x);
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  sum = 0.f;
+  for (int i = 0; i < Groups; ++i) {
+    const float f = s_ml[i].x == -INFINITY ? 0.f : exp2_fast(s_ml[i].x - top);
+    const float4 o = s_o[i * L + l];
+    sum += s_ml[i].y * f;
+    acc.x += o.x * f;
+    acc.y += o.y * f;
+    acc.z += o.z * f;
+    acc.w += o.w * f;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* dst = (__nv_bfloat16*)a.u.out + (int64_t)(rec.token0 + row / rec.group) * a.u.out_stride +
+                       (rec.head0 + row % rec.group) * D + 4 * l;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
+}
+
+int decode_tiles(const fw_attn_q4_args& a) { return (int64_t)a.max_q * (a.n_q / a.n_kv) <= 8 ? 1 : 2; }
+
+// CTAs: as many as the SMs hold, but no more than there can be units.
+int decode_grid(const fw_attn_q4_args& a, int sms) {
+  const int64_t most = (int64_t)a.R * a.n_kv * (((int64_t)a.max_blocks * a.page + kStageKeys - 1) / kStageKeys);
+  return (int)::min((int64_t)sms * 2, most < 1 ? 1 : most);
+}
+
+template <int D, int NT>
+cudaError_t launch(const DecodeArgs& d, int grid, cudaStream_t s) {
+  cudaError_t e = launch_dependent(attn_decode_kernel<D, NT>, dim3(grid), dim3(kThreads), Cfg<D, NT>::SmemBytes, s, d);
+  if (e == cudaSuccess) e = launch_dependent(attn_join_kernel<D>, dim3(grid, 8 * NT), dim3(256), 0, s, d, 8 * NT);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t configure_attn_kernels() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto* k, int bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  set(attn_decode_kernel<64, 1>, Cfg<64, 1>::SmemBytes);
+  set(attn_decode_kernel<64, 2>, Cfg<64, 2>::SmemBytes);
+  set(attn_decode_kernel<128, 1>, Cfg<128, 1>::SmemBytes);
+  set(attn_decode_kernel<128, 2>, Cfg<128, 2>::SmemBytes);
+  return e;
+}
+
+int64_t decode_workspace(const fw_attn_q4_args& a, int sms) {
+  const int64_t grid = decode_grid(a, sms), rows = 8 * decode_tiles(a);
+  return grid * sizeof(SplitRecord) + 2 * grid * rows * (a.D * 4 + 8);
+}
+
+cudaError_t launch_attn_decode(const fw_attn_q4_args& a, void* workspace, int sms, cudaStream_t s) {
+  const int nt = decode_tiles(a), grid = decode_grid(a, sms);
+  DecodeArgs d;
+  d.u = a;
+  d.rec = static_cast<SplitRecord*>(workspace);
+  d.o = reinterpret_cast<float*>(d.rec + grid);
+  d.ml = reinterpret_cast<float2*>(d.o + (int64_t)2 * grid * 8 * nt * a.D);
+  d.scale_log2 = a.scale * kLog2e;
+  if (a.D == 64) return nt == 1 ? launch<64, 1>(d, grid, s) : launch<64, 2>(d, grid, s);
+  return nt == 1 ? launch<128, 1>(d, grid, s) : launch<128, 2>(d, grid, s);
+}
+
+}  // namespace fw
