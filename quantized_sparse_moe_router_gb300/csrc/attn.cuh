@@ -29,6 +29,12 @@ __device__ __forceinline__ Stages visible_stages(int S, int first, int window, i
   return v;
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Whether the query at position p sees key j (j >= 0).
 __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
   return j <= p && (window == 0 || j > p - window || j < sinks);
@@ -36,16 +42,26 @@ __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
 
 }  // namespace dev
 
-// Partial result of one (request, key/value head) that several CTAs share:
-// row-wise softmax maximum (in units of log2) and sum, and the unnormalised
-// output. Slot 2 c + i: CTA c's first (i = 0) or a later (i = 1) segment.
-struct SplitRecord {  // of the CTA that holds the first part
-  int parts, slot0, cta0, rows;  // parts = 0: nothing to join; part i > 0 is slot 2 (cta0 + i)
-  int token0, head0, group, pad; // row n is token token0 + n / group, query head head0 + n % group
+// Partial results of one (request, key/value head, run of query rows) that
+// several CTAs share: row-wise softmax maximum (in units of log2) and sum, and
+// the unnormalised output. Part i is slot slot0 (i = 0) or slot1 + i step.
+struct SplitRecord {
+  int parts, slot0, slot1, step;  // parts = 0: nothing to join
+  int rows, row0;                 // row n of a part is row m = row0 + n of the request:
+  int token0, head0;              // token token0 + m / G, query head head0 + m % G
 };
 
-cudaError_t configure_attn_kernels();
+cudaError_t configure_decode_attn();
 int64_t decode_workspace(const fw_attn_q4_args& a, int sms);
 cudaError_t launch_attn_decode(const fw_attn_q4_args& a, void* workspace, int sms, cudaStream_t s);
+
+cudaError_t configure_prefill_attn();
+int64_t prefill_workspace(const fw_attn_q4_args& a, int sms);
+// min_rows: requests of at most so many query rows are left to the decode kernel (0: none are)
+cudaError_t launch_attn_prefill(const fw_attn_q4_args& a, int min_rows, void* workspace, int sms, cudaStream_t s);
+
+// Joins the parts of `records` records; a slot holds rows_max rows of ml and o.
+cudaError_t launch_attn_join(const fw_attn_q4_args& a, const SplitRecord* rec, const float* o, const float2* ml, int records,
+                             int rows_max, cudaStream_t s);
 
 }  // namespace fw

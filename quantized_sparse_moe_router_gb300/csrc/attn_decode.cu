@@ -88,12 +88,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 template <int N>
 struct Words {
   uint32_t w[N];
@@ -585,14 +579,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
         if (!whole && st0 == 0 && tid == 0) {
           const long long last = u_begin + x + n_st - 1;  // this head's last unit, and the CTA that has it
           SplitRecord rec;
-          rec.cta0 = cta;
           rec.parts = (int)(((last + 1) * grid - 1) / total) - cta + 1;
           rec.slot0 = part;
+          rec.slot1 = 2 * cta;
+          rec.step = 2;
           rec.rows = rows;
+          rec.row0 = 0;
           rec.token0 = tok0;
           rec.head0 = head * G;
-          rec.group = G;
-          rec.pad = 0;
           a.rec[cta] = rec;
         }
         x += n_here;
@@ -606,56 +600,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
       mbar_wait(&full[j % kStages], (j / kStages) & 1);
 }
 
-// Joins the parts of one row of one split pair: o = sum_i 2^(m_i - M) o_i over
-// sum_i 2^(m_i - M) l_i, the parts taken by eight groups of lanes.
-template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(DecodeArgs a, int rows_max) {
-  constexpr int L = D / 4, Groups = 256 / L;
-  __shared__ float4 s_o[256];
-  __shared__ float2 s_ml[Groups];
-  pdl_wait();
-  pdl_launch_dependents();
-  const SplitRecord rec = a.rec[blockIdx.x];
-  const int row = blockIdx.y, l = threadIdx.x % L, grp = threadIdx.x / L;
-  if (rec.parts == 0 || row >= rec.rows) return;
-  float m = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = grp; i < rec.parts; i += Groups) {
-    const int64_t at = (int64_t)(i == 0 ? rec.slot0 : 2 * (rec.cta0 + i)) * rows_max + row;
-    const float2 ml = __ldcg(a.ml + at);
-    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.o + at * D) + l);
-    const float m2 = fmaxf(m, ml.x), keep = m == -INFINITY ? 0.f : exp2_fast(m - m2);
-    const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m2);
-    m = m2;
-    sum = sum * keep + ml.y * f;
-    acc.x = acc.x * keep + o.x * f;
-    acc.y = acc.y * keep + o.y * f;
-    acc.z = acc.z * keep + o.z * f;
-    acc.w = acc.w * keep + o.w * f;
-  }
-  s_o[threadIdx.x] = acc;
-  if (l == 0) s_ml[grp] = make_float2(m, sum);
-  __syncthreads();
-  if (grp) return;
-  float top = -INFINITY;
-  for (int i = 0; i < Groups; ++i) top = fmaxf(top, s_ml[i].x);
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  sum = 0.f;
-  for (int i = 0; i < Groups; ++i) {
-    const float f = s_ml[i].x == -INFINITY ? 0.f : exp2_fast(s_ml[i].x - top);
-    const float4 o = s_o[i * L + l];
-    sum += s_ml[i].y * f;
-    acc.x += o.x * f;
-    acc.y += o.y * f;
-    acc.z += o.z * f;
-    acc.w += o.w * f;
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* dst = (__nv_bfloat16*)a.u.out + (int64_t)(rec.token0 + row / rec.group) * a.u.out_stride +
-                       (rec.head0 + row % rec.group) * D + 4 * l;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
-}
-
 int decode_tiles(const fw_attn_q4_args& a) { return (int64_t)a.max_q * (a.n_q / a.n_kv) <= 8 ? 1 : 2; }
 
 // CTAs: as many as the SMs hold, but no more than there can be units.
@@ -667,13 +611,13 @@ int decode_grid(const fw_attn_q4_args& a, int sms) {
 template <int D, int NT>
 cudaError_t launch(const DecodeArgs& d, int grid, cudaStream_t s) {
   cudaError_t e = launch_dependent(attn_decode_kernel<D, NT>, dim3(grid), dim3(kThreads), Cfg<D, NT>::SmemBytes, s, d);
-  if (e == cudaSuccess) e = launch_dependent(attn_join_kernel<D>, dim3(grid, 8 * NT), dim3(256), 0, s, d, 8 * NT);
+  if (e == cudaSuccess) e = launch_attn_join(d.u, d.rec, d.o, d.ml, grid, 8 * NT, s);
   return e;
 }
 
 }  // namespace
 
-cudaError_t configure_attn_kernels() {
+cudaError_t configure_decode_attn() {
   cudaError_t e = cudaSuccess;
   auto set = [&](auto* k, int bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);

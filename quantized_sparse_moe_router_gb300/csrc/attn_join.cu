@@ -1,0 +1,89 @@
+// Joins the partial results of rows whose keys several CTAs shared:
+//   o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i
+// A row's D / 4 lanes read 16 bytes each; with few rows (decode) the parts of a
+// row are shared out among the lane groups of a CTA, with many (prefill) every
+// group has a row of its own. Bound by the latency of reading the parts.
+#include "attn.cuh"
+
+namespace fw {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 256;
+
+struct JoinArgs {
+  const SplitRecord* rec;
+  const float* o;
+  const float2* ml;
+  __nv_bfloat16* out;
+  int64_t out_stride;
+  int rows_max, G;
+};
+
+template <int D, bool kShare>
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinArgs a) {
+  constexpr int L = D / 4, Groups = kThreads / L;
+  __shared__ float4 s_o[kShare ? kThreads : 1];
+  __shared__ float2 s_ml[Groups];
+  pdl_wait();
+  pdl_launch_dependents();
+  const SplitRecord rec = a.rec[blockIdx.x];
+  const int l = threadIdx.x % L, grp = threadIdx.x / L, row = kShare ? blockIdx.y : blockIdx.y * Groups + grp;
+  if (rec.parts == 0 || row >= rec.rows) return;
+  float m = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = kShare ? grp : 0; i < rec.parts; i += kShare ? Groups : 1) {
+    const int64_t at = (int64_t)(i == 0 ? rec.slot0 : rec.slot1 + i * rec.step) * a.rows_max + row;
+    const float2 ml = __ldcg(a.ml + at);
+    // a part in which the row saw nothing has no output; NaN has to go on
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.o + at * D) + l);
+    const float top = fmaxf(m, ml.x), keep = m == -INFINITY ? 0.f : exp2_fast(m - top);
+    const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+    m = top;
+    sum = sum * keep + ml.y * f;
+    acc.x = acc.x * keep + o.x * f;
+    acc.y = acc.y * keep + o.y * f;
+    acc.z = acc.z * keep + o.z * f;
+    acc.w = acc.w * keep + o.w * f;
+  }
+  if constexpr (kShare) {
+    s_o[threadIdx.x] = acc;
+    if (l == 0) s_ml[grp] = make_float2(m, sum);
+    __syncthreads();
+    if (grp) return;
+    float top = -INFINITY;
+    for (int i = 0; i < Groups; ++i) top = fmaxf(top, s_ml[i].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum = 0.f;
+    for (int i = 0; i < Groups; ++i) {
+      const float f = s_ml[i].x == -INFINITY ? 0.f : exp2_fast(s_ml[i].x - top);
+      const float4 o = s_o[i * L + l];
+      sum += s_ml[i].y * f;
+      acc.x += o.x * f;
+      acc.y += o.y * f;
+      acc.z += o.z * f;
+      acc.w += o.w * f;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int n = rec.row0 + row;
+  __nv_bfloat16* dst = a.out + (int64_t)(rec.token0 + n / a.G) * a.out_stride + (rec.head0 + n % a.G) * D + 4 * l;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
+}
+
+}  // namespace
+
+cudaError_t launch_attn_join(const fw_attn_q4_args& a, const SplitRecord* rec, const float* o, const float2* ml, int records,
+                             int rows_max, cudaStream_t s) {
+  const JoinArgs j = {rec, o, ml, (__nv_bfloat16*)a.out, a.out_stride, rows_max, a.n_q / a.n_kv};
+  const bool share = rows_max <= kDecodeRows;
+  const int groups = kThreads / (a.D / 4);
+  const dim3 grid(records, share ? rows_max : rows_max / groups);
+  if (a.D == 64) return launch_dependent(share ? attn_join_kernel<64, true> : attn_join_kernel<64, false>, grid, dim3(kThreads), 0, s, j);
+  return launch_dependent(share ? attn_join_kernel<128, true> : attn_join_kernel<128, false>, grid, dim3(kThreads), 0, s, j);
+}
+
+}  // namespace fw
