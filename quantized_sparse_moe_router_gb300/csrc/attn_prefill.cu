@@ -9,13 +9,14 @@
 // heads. A CTA owns 256 rows as two 128-row tiles, and walks the 128-key tiles
 // that they see. While one tile is in its softmax the tensor core works on the
 // other: per row tile the steps S(i) -> P(i) -> O(i) are serial, S and P share
-// tensor-memory columns, and the issue order PV(i), QK(i + 1) of one thread is
+// tensor-memory columns, and the issue order PV(i), QK(i + 1) of one warp is
 // all the ordering that needs.
 //
 // 16 warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread a row: no
 // shuffles; S in 128 registers), 8-11 unpack the 4-bit codes to 16-bit operand
 // tiles (K by keys, V transposed by dims, both K-major with the 128-byte
-// swizzle), 12 issues the MMAs, 13 copies pages (one bulk copy each). Bound by
+// swizzle), 12 issues the
+// MMAs, 13 copies pages (one bulk copy each). Bound by
 // the tensor core at head dims of 128, by the softmax's instructions at 64.
 //
 // Tensor memory: S0 | S1 | O0 | O1, 128 columns each; P (bf16) over the first
@@ -37,7 +38,7 @@ constexpr int kDeqWarp0 = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr int kPacked = 3, kTiles = 3, kHave = 8, kPoison = 4;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // of 128 a thread at launch
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLazy = 8.f;  // a row's maximum moves only when a score passes it by 2^8
+constexpr float kMost = 1048576.f;  // a row's maximum moves only when a tile's sum of p passes this
 
 template <int D>
 struct Cfg {
@@ -80,10 +81,10 @@ constexpr float kKeyScale = 1.f / 64.f;
 // nibbles 2 k + {0, 1} (and + 4) of a word, shifted to the low byte of each
 // half -> two f16 pairs (c - 8) d: the upper nibble stands for 16 c as it is,
 // and takes d / 16
-__device__ __forceinline__ void unpack_f16(uint32_t w, uint32_t mask, uint32_t d, uint32_t d16, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void unpack_f16(uint32_t w, uint32_t mask, uint32_t mask4, uint32_t d, uint32_t d16, uint32_t& lo, uint32_t& hi) {
   uint32_t x, y;
   asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(x) : "r"(w), "r"(mask));        // 1024 + c
-  asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(w), "r"(mask << 4));   // 1024 + 16 c
+  asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(w), "r"(mask4));   // 1024 + 16 c
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0x64086408u));               // - 1032
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(y), "r"(0x64806480u));               // - 1152
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(d));
@@ -102,14 +103,16 @@ __device__ __forceinline__ uint32_t unpack(uint32_t w, int shift, uint32_t mask,
 }
 __device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7F80u) != 0x7F80u; }
 
-// mbar_wait with its loop in place: where warps change their register share a
-// call would need a register split of its own.
+// A bounded wait with its loop in place (where warps change their register
+// share a call would need a register split of its own) and without a suspend
+// hint: a thread that sleeps on one wakes about 1000 cycles after the barrier
+// flips, which the chain of softmax and products would pay four times a tile.
 __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-    if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) return false;
   }
 }
 
@@ -288,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_cols = tmem + lanes + t * 128, o_cols = tmem + lanes + 256 + t * 128;
       const int p = row < rows ? S - n_new + (row0 + row) / G : -1;
-      float mz = 0.f, lim = -INFINITY, scale = 0.f;
-      f2 l2 = f2_pack(0.f, 0.f);
+      float mz = 0.f, l = 0.f, scale = 0.f;
+      bool first_max = true;  // none was taken yet
       uint32_t poison = 0;
       int key_before = 0;
       // blocks of V that are not finite in keys this row sees (the tile whose product is in O by now)
@@ -317,22 +320,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
           for (int c = 0; c < 128; ++c)
             if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
         }
-        float top = -INFINITY, top2 = -INFINITY;
+        // P and its sum against the maximum as last taken; both are exact to
+        // their rounding whatever their magnitude, so it only has to move
+        // when a tile's sum shows that some p is past kMost (or none was taken)
+        auto weights = [&]() {
+          const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
+          f2 sum = f2_pack(0.f, 0.f), sum2 = sum;
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          top = fmaxf(top, fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
-          top2 = fmaxf(top2, fmaxf(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
-        }
-        float up = fmaf(fmaxf(top, top2), scale, -mz);
-        if (__any_sync(0xFFFFFFFFu, up > lim)) {
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float x, y;
+              f2_unpack(f2_fma(f2_pack_bits(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), sc, mm), x, y);
+              x = exp2_fast(x);
+              y = exp2_fast(y);
+              if (j & 1) sum2 = f2_add(sum2, f2_pack(x, y)); else sum = f2_add(sum, f2_pack(x, y));
+              pk[j] = bf16x2_bits(x, y);
+            }
+            tmem_st16(s_cols + 16 * c, pk);
+          }
+          float x, y;
+          f2_unpack(f2_add(sum, sum2), x, y);
+          return x + y;
+        };
+        float sum = first_max ? 0.f : weights();
+        if (__any_sync(0xFFFFFFFFu, first_max || sum > kMost)) {
+          float top = -INFINITY, top2 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            top = fmaxf(top, fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+            top2 = fmaxf(top2, fmaxf(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
+          }
+          float up = fmaf(fmaxf(top, top2), scale, -mz);
           // a first maximum is taken as it is, a later one only moves up
-          if (lim != -INFINITY) up = fmaxf(up, 0.f);
+          if (!first_max) up = fmaxf(up, 0.f);
           const bool none = up == -INFINITY;
-          const float keep = lim == -INFINITY ? 0.f : exp2_fast(-up);
+          const float keep = first_max ? 0.f : exp2_fast(-up);
           if (!none) {
             mz += up;
-            l2 = f2_mul(l2, f2_pack(keep, keep));
-            lim = kLazy;
+            l *= keep;
+            first_max = false;
           }
           if (i > 0) {  // O holds the tiles before: S(i) came after their product
 #pragma unroll 1
@@ -344,31 +372,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
               tmem_st16(o_cols + c, o);
             }
           }
+          sum = weights();
         }
-        const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float x, y;
-            f2_unpack(f2_fma(f2_pack_bits(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), sc, mm), x, y);
-            x = exp2_fast(x);
-            y = exp2_fast(y);
-            l2 = f2_add(l2, f2_pack(x, y));
-            pk[j] = bf16x2_bits(x, y);
-          }
-          tmem_st16(s_cols + 16 * c, pk);
-        }
+        l += sum;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t]);
       }
       // ---------------------------------------------- out = O / l
-      float l, lb;
-      f2_unpack(l2, l, lb);
-      l += lb;
       if (n_t > 0) {
         wait(&o_full, 0);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -377,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
       }
       const int n = row0 + row;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      if (a.splits > 1 && row < rows) a.ml[part * kBlockRows + row] = make_float2(lim == -INFINITY ? -INFINITY : mz, n_t > 0 ? l : 0.f);
+      if (a.splits > 1 && row < rows) a.ml[part * kBlockRows + row] = make_float2(first_max ? -INFINITY : mz, l);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -429,15 +441,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
       {
         uint8_t* tile = sT + (seq % kTiles) * C::TileBytes;
         const uint8_t* codes = pk + blk_k + at * (D / 2);
-        uint32_t d[NB];
+        uint32_t d[NB], d16[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const float x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(pk + blk_k + pl.ks)[at * NB + b] << 16) * kKeyScale;
           d[b] = f16x2_bits(x, x);
+          d16[b] = f16x2_bits(x * 0.0625f, x * 0.0625f);
         }
+        // the 16-byte chunk 4 b + q of this key lies at ((4 (b & 1) + q) ^ (key & 7)) in panel b / 2
+        uint8_t* row = tile + key * 128;
+        const int x4 = (key & 4) << 4;
 #pragma unroll
         for (int qq = 0; qq < 4; ++qq) {
           const int q = (qq + (NB == 4 ? lane >> 1 : lane >> 2)) & 3;  // (the reads of 8 lanes fall into different banks)
+          uint8_t* at_q = row + ((q ^ (key & 3)) << 4);
           uint32_t x[NB];
           if constexpr (NB == 4) {
             const uint4 c4 = *reinterpret_cast<const uint4*>(codes + q * 16);
@@ -448,13 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
           }
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const int c = b * 4 + q;  // 8-dim chunk
-            uint32_t d16;
-            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d16) : "r"(d[b]), "r"(0x2C002C00u));  // d / 16
             uint4 o;
-            unpack_f16(x[b], mask, d[b], d16, o.x, o.y);
-            unpack_f16(x[b] >> 8, mask, d[b], d16, o.z, o.w);
-            *reinterpret_cast<uint4*>(tile + (c / 8) * (kStageKeys * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4)) = o;
+            unpack_f16(x[b], mask, mask << 4, d[b], d16[b], o.x, o.y);
+            unpack_f16(x[b] >> 8, mask, mask << 4, d[b], d16[b], o.z, o.w);
+            *reinterpret_cast<uint4*>(at_q + (b / 2) * (kStageKeys * 128) + (x4 ^ ((b & 1) << 6))) = o;
           }
         }
       }
@@ -467,10 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       {
         uint8_t* tile = sT + (seq % kTiles) * C::TileBytes;
-        auto pair_at = [&](int kp) {  // byte offset of a key pair's codes and scales within the packed tile
-          const int k2 = 2 * kp, a2 = (k2 & (u.page - 1)) / 2;
-          return make_uint2((k2 >> page_shift) * hb + pl.vc + a2 * D, (k2 >> page_shift) * hb + pl.vs + a2 * (NB * 4));
-        };
+        // byte offset of a key pair's codes and scales within the packed tile
+        auto codes_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vc + (kp & (u.page / 2 - 1)) * D; };
+        auto scales_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (u.page / 2 - 1)) * (NB * 4); };
         // scales that must not enter the product: keys past the last or of a
         // missing page (whatever is there), and what is not finite (noted for
         // the rows that see it). Half a pair's blocks to a lane.
@@ -479,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
         uint32_t bad0 = 0, bad1 = 0;  // blocks of the even and the odd key
         {
           const int kp = 16 * w + lane / 2;
-          const uint32_t at_s = pair_at(kp).y;
+          const uint32_t at_s = scales_at(kp);
 #pragma unroll
           for (int k = 0; k < NB / 2; ++k) {
             const int b = (lane & 1) * (NB / 2) + k;
@@ -509,11 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
         for (int cc = 0; cc < 4; cc += Chunks) {
           const int c = 4 * w + cc + lane / Lanes;  // chunk of 8 keys
           uint32_t x[4], d[4];
+          const uint8_t* in_x = pk + codes_at(4 * c) + word * 4;  // (a chunk's four pairs are one page's)
+          const uint8_t* in_d = pk + scales_at(4 * c) + b * 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint2 off = pair_at(4 * c + k);
-            x[k] = *reinterpret_cast<const uint32_t*>(pk + off.x + word * 4);
-            d[k] = *reinterpret_cast<const uint32_t*>(pk + off.y + b * 4);
+            x[k] = *reinterpret_cast<const uint32_t*>(in_x + k * D);
+            d[k] = *reinterpret_cast<const uint32_t*>(in_d + k * (NB * 4));
           }
           if (odd_tile) {
             const bool there = s_have[i % kHave] >> (c / 2) & 1;
@@ -524,10 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
               if (!there || j + 1 >= S || !finite_bf16(d[k] >> 16)) d[k] &= 0xFFFFu;
             }
           }
+          uint8_t* col = tile + (c / 8) * (D * 128) + (32 * b + 4 * g) * 128;
+          const int c4 = (c & 7) ^ ((g & 1) << 2);  // ((dim & 7) = 4 (g & 1) + j)
 #pragma unroll
           for (int jj = 0; jj < 4; ++jj) {
-            const int j = (jj + (NB == 4 ? b : 2 * b + (g >> 1))) & 3, dim = 32 * b + 4 * g + j;  // (the writes of 8 lanes fall into different banks)
-            *reinterpret_cast<uint4*>(tile + (c / 8) * (D * 128) + dim * 128 + (((c & 7) ^ (dim & 7)) << 4)) =
+            const int j = (jj + (NB == 4 ? b : 2 * b + (g >> 1))) & 3;  // (the writes of 8 lanes fall into different banks)
+            *reinterpret_cast<uint4*>(col + j * 128 + ((c4 ^ j) << 4)) =
                 make_uint4(unpack(x[0], 4 * j, mask, d[0]), unpack(x[1], 4 * j, mask, d[1]), unpack(x[2], 4 * j, mask, d[2]),
                            unpack(x[3], 4 * j, mask, d[3]));
           }
@@ -542,48 +558,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp) {
       // ---------------------------------------------- MMA issuer
-      const uint32_t q0 = smem_u32(sQ), t0 = smem_u32(sT);
-      auto qk = [&](int t, uint32_t seq) {
-        const uint32_t k0 = t0 + (seq % kTiles) * C::TileBytes, a0 = q0 + t * C::QBytes;
+      // The warp stays together and elects a lane for the MMAs only: their
+      // descriptors are then uniform, and their issue fast enough. One issuer
+      // and a fixed order keep the two row tiles half a period apart: with an
+      // issuer each they fall into step, and softmax and products take turns
+      // instead of overlapping.
+      // (a value shuffled from lane 0 is uniform for the compiler, too)
+      const uint32_t q0 = __shfl_sync(0xFFFFFFFFu, sw128_desc_lo(smem_u32(sQ)), 0);
+      const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, sw128_desc_lo(smem_u32(sT)), 0);
+      const uint32_t cols = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      auto qk = [&](int t, uint32_t seq, bool last_use) {
+        const uint32_t k0 = t0 + (seq % kTiles) * (C::TileBytes >> 4), a0 = q0 + t * (C::QBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + t * 128, sw128_desc(a0 + (k / 4) * (kRowTile * 128) + (k % 4) * 32),
-                 sw128_desc(k0 + (k / 4) * (kStageKeys * 128) + (k % 4) * 32), idesc_f16(kRowTile, kStageKeys), k != 0);
-        mma_commit(&s_full[t]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = ((k / 4) * (kRowTile * 128) + (k % 4) * 32) >> 4;  // (both tiles have 128 rows)
+            mma_ss_lo(cols + t * 128, a0 + at, k0 + at, idesc_f16(kRowTile, kStageKeys), k != 0);
+          }
+          mma_commit(&s_full[t]);
+          if (last_use) mma_commit(&tile_empty[seq % kTiles]);
+        }
+        __syncwarp();
       };
-      auto pv = [&](int t, uint32_t seq, bool more) {
-        const uint32_t v0 = t0 + (seq % kTiles) * C::TileBytes;
+      auto pv = [&](int t, uint32_t seq, bool more, bool last_use) {
+        const uint32_t v0 = t0 + (seq % kTiles) * (C::TileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kStageKeys / 16; ++k)
-          mma_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + k * 8, sw128_desc(v0 + (k / 4) * (D * 128) + (k % 4) * 32),
-                     idesc_bf16(kRowTile, D), more || k != 0);
+          for (int k = 0; k < kStageKeys / 16; ++k)
+            mma_ts_lo(cols + 256 + t * 128, cols + t * 128 + k * 8, v0 + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4),
+                      idesc_bf16(kRowTile, D), more || k != 0);
+          if (last_use) mma_commit(&tile_empty[seq % kTiles]);
+        }
+        __syncwarp();
       };
-      auto tile_wait = [&](uint32_t seq) { return wait(&tile_full[seq % kTiles], (seq / kTiles) & 1); };
-      if (n_t > 0 && wait(&q_full, 0) && tile_wait(0)) {
+      auto ready = [&](uint64_t* bar, uint32_t parity) {
+        wait(bar, parity);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
-        for (int t = 0; t < row_tiles; ++t) qk(t, 0);
-        mma_commit(&tile_empty[0]);
+        return ok;
+      };
+      auto tile_ready = [&](uint32_t seq) { return ready(&tile_full[seq % kTiles], (seq / kTiles) & 1); };
+      if (n_t > 0 && ready(&q_full, 0) && tile_ready(0)) {
+        for (int t = 0; t < row_tiles; ++t) qk(t, 0, t == row_tiles - 1);
         for (int i = 0; i < n_t && ok; ++i) {
-          const uint32_t seq = 2 * i + 1;
           const bool next = i + 1 < n_t;
-          if (!tile_wait(seq)) break;
-          for (int t = 0; t < row_tiles && ok; ++t) {
-            if (!wait(&p_full[t], i & 1)) break;
-            tc_fence_after();
-            pv(t, seq, i > 0);
+          if (!tile_ready(2 * i + 1)) break;
+          for (int t = 0; t < row_tiles; ++t) {
+            if (!ready(&p_full[t], i & 1)) break;
+            pv(t, 2 * i + 1, i > 0, t == row_tiles - 1);
             if (next) {
-              if (t == 0 && !tile_wait(seq + 1)) break;
-              tc_fence_after();
-              qk(t, seq + 1);
+              if (t == 0 && !tile_ready(2 * i + 2)) break;
+              qk(t, 2 * i + 2, t == row_tiles - 1);
             }
           }
-          mma_commit(&tile_empty[seq % kTiles]);
-          if (next) mma_commit(&tile_empty[(seq + 1) % kTiles]);
         }
         // every MMA issued has finished before tensor memory is read or released
-        mma_commit(&o_full);
+        if (elect_one()) mma_commit(&o_full);
+        __syncwarp();
         mbar_wait_inline(&o_full, 0);
       }
     } else if (warp == kLoadWarp) {
