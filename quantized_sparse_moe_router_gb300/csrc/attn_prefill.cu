@@ -5,23 +5,29 @@
 //   S = Q K^T,  P = 2^(scale S - m),  O = sum over key tiles of P V,  out = O / l
 //
 // The rows of a head's group are packed (row = new token x G + head in the
-// group), so a key/value head's tiles are unpacked once for all its query
-// heads. A CTA owns 256 rows as two 128-row tiles, and walks the 128-key tiles
-// that they see. While one tile is in its softmax the tensor core works on the
-// other: per row tile the steps S(i) -> P(i) -> O(i) are serial, S and P share
+// group), so a key/value head's tiles serve all its query heads. A CTA owns
+// 256 rows as two 128-row tiles, and walks the 128-key tiles that they see.
+// While one row tile is in its softmax the tensor core works on the other: per
+// row tile the steps S(i) -> P(i) -> O(i) are serial, S and P share
 // tensor-memory columns, and the issue order PV(i), QK(i + 1) of one warp is
 // all the ordering that needs.
 //
-// 16 warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread a row: no
-// shuffles; S in 128 registers), 8-11 unpack the 4-bit codes to 16-bit operand
-// tiles (K by keys, V transposed by dims, both K-major with the 128-byte
-// swizzle), 12 issues the
-// MMAs, 13 copies pages (one bulk copy each). Bound by
-// the tensor core at head dims of 128, by the softmax's instructions at 64.
+// The 4-bit tiles are unpacked to 16-bit operands (K by keys, V transposed by
+// dims, both K-major with the 128-byte swizzle) in one of two places. Where
+// many row blocks read each key tile (kReady), a kernel before this one
+// unpacks every tile once, into the workspace, as the very bytes of the shared
+// memory it will lie in, and one bulk copy brings a tile. Where few do, four
+// warps of the CTA unpack its own tiles.
+//
+// Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread a row: no
+// shuffles), then four unpacking warps (not kReady), one that issues the MMAs,
+// one that copies tiles or pages. The chain S -> P -> O -> S of a row tile
+// bounds it: 1024 cycles of products, about 900 of softmax, and four barriers
+// of about 175 from arrival to wake.
 //
 // Tensor memory: S0 | S1 | O0 | O1, 128 columns each; P (bf16) over the first
-// 64 columns of its S. Shared memory: Q, a ring of three unpacked tiles taken in
-// the order K0 V0 K1 V1 ..., a ring of three packed tiles.
+// 64 columns of its S. Shared memory: Q, a ring of operand tiles taken in the
+// order K0 V0 K1 V1 ..., and (not kReady) a ring of packed tiles.
 #include <initializer_list>
 
 #include "attn.cuh"
@@ -33,20 +39,36 @@ namespace {
 using namespace dev;
 
 constexpr int kRowTile = 128, kBlockRows = 2 * kRowTile;
-constexpr int kThreads = 512;
-constexpr int kDeqWarp0 = 8, kMmaWarp = 12, kLoadWarp = 13;
-constexpr int kPacked = 3, kTiles = 3, kHave = 8, kPoison = 4;
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // of 128 a thread at launch
+constexpr int kPacked = 3, kHave = 8;
 constexpr uint32_t kTmemCols = 512;
+// not kReady: registers of the softmax warps and of the others, of 128 a thread at launch (kReady: all have 200)
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr float kMost = 1048576.f;  // a row's maximum moves only when a tile's sum of p passes this
+
+// What goes with an unpacked tile of a head.
+struct __align__(16) TileInfo {
+  uint32_t have;                // bit g: the keys 16 g .. 16 g + 15 are there
+  uint8_t flag[4];              // per 32 keys: some scale of V is not finite
+  uint32_t pad[2];
+  uint8_t poison[kStageKeys];   // then: the key's blocks (bits) that are not
+};
 
 template <int D>
 struct Cfg {
   static constexpr int NB = D / kKvBlock;
-  static constexpr uint32_t QBytes = kRowTile * D * 2;        // one row tile: [D / 64] panels of [128 rows][128 B]
-  static constexpr uint32_t TileBytes = kStageKeys * D * 2;   // K: as Q; V: [2] panels of 64 keys, [D dims][128 B]
+  static constexpr uint32_t QBytes = kRowTile * D * 2;       // one row tile: [D / 64] panels of [128 rows][128 B]
+  static constexpr uint32_t TileBytes = kStageKeys * D * 2;  // K: as Q; V: [2] panels of 64 keys, [D dims][128 B]
   static constexpr uint32_t PackedBytes = kStageKeys * D * 9 / 8;
-  static constexpr uint32_t SmemBytes = 2 * QBytes + kTiles * TileBytes + kPacked * PackedBytes + 1024;
+  // an unpacked tile in the workspace: K, V, TileInfo
+  static constexpr int64_t ReadyBytes = 2 * TileBytes + 256;
+};
+static_assert(sizeof(TileInfo) <= 256 && sizeof(TileInfo) % 16 == 0, "TileInfo is copied in bulk");
+
+template <int D, bool kReady>
+struct Lay {
+  static constexpr int UnpackWarp0 = 8, MmaWarp = kReady ? 8 : 12, LoadWarp = MmaWarp + 1, Threads = kReady ? 320 : 512;
+  static constexpr int Tiles = kReady ? 4 : 3;  // ring of operand tiles
+  static constexpr uint32_t SmemBytes = 2 * Cfg<D>::QBytes + Tiles * Cfg<D>::TileBytes + (kReady ? 0 : kPacked * Cfg<D>::PackedBytes) + 1024;
 };
 
 struct PrefillArgs {
@@ -54,22 +76,13 @@ struct PrefillArgs {
   int splits;        // CTAs that share a block's key tiles
   int min_rows;      // requests of at most so many rows are not this kernel's
   int blocks;        // blocks of 256 rows at most (grid = blocks * n_kv * splits)
+  uint8_t* ready;    // kReady: [tiles of all requests][n_kv] unpacked tiles
   float* o;          // splits > 1: [blocks * n_kv * splits][256][D]
   float2* ml;        // [blocks * n_kv * splits][256]
   SplitRecord* rec;  // [blocks * n_kv]
   float scale_log2;
 };
 
-__device__ __forceinline__ uint32_t bf16x2_op_sub136(uint32_t x) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x43084308u));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2_op_mul(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
 // Keys go to f16, values to bf16. A key d (c - 8) has at most 8 + 3 significant
 // bits, so f16 holds it exactly (scores are then exact up to the fp32 sums,
 // however large); what f16 lacks in range is made up by powers of two: a
@@ -95,6 +108,16 @@ __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t bf16x2_op_sub136(uint32_t x) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x43084308u));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_op_mul(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 // nibbles at bit `shift` of a word's halves -> (c - 8) * d, rounded once to bf16
 __device__ __forceinline__ uint32_t unpack(uint32_t w, int shift, uint32_t mask, uint32_t d) {
   uint32_t r;
@@ -103,6 +126,244 @@ __device__ __forceinline__ uint32_t unpack(uint32_t w, int shift, uint32_t mask,
 }
 __device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7F80u) != 0x7F80u; }
 
+// A request's tokens and key tiles as far as this kernel takes it.
+__device__ __forceinline__ bool prefill_request(const PrefillArgs& a, int r, int& n, int& q0, int& S) {
+  const fw_attn_q4_args& u = a.u;
+  q0 = u.q_start[r];
+  n = u.q_start[r + 1] - q0;
+  S = ::min(u.seq_lens[r], u.max_blocks * u.page);
+  return n * (long long)(u.n_q / u.n_kv) > a.min_rows && q0 >= 0 && q0 <= u.T - n;
+}
+__device__ __forceinline__ int key_tiles(int S) { return S > 0 ? (S + kStageKeys - 1) / kStageKeys : 0; }
+
+// 32 keys of a packed tile (a lane a key) -> K operand tile.
+template <int D>
+__device__ __forceinline__ void unpack_keys(uint8_t* tile, const uint8_t* pk, int w, int lane, int page, int page_shift, uint32_t hb,
+                                            const KvPlanes& pl, uint32_t mask) {
+  constexpr int NB = Cfg<D>::NB;
+  const int key = 32 * w + lane, at = key & (page - 1);
+  const uint8_t* blk = pk + (key >> page_shift) * hb;
+  const uint8_t* codes = blk + at * (D / 2);
+  uint32_t d[NB], d16[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const float x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(blk + pl.ks)[at * NB + b] << 16) * kKeyScale;
+    d[b] = f16x2_bits(x, x);
+    d16[b] = f16x2_bits(x * 0.0625f, x * 0.0625f);
+  }
+  // the 16-byte chunk 4 b + q of this key lies at ((4 (b & 1) + q) ^ (key & 7)) in panel b / 2
+  uint8_t* row = tile + key * 128;
+  const int x4 = (key & 4) << 4;
+#pragma unroll
+  for (int qq = 0; qq < 4; ++qq) {
+    const int q = (qq + (NB == 4 ? lane >> 1 : lane >> 2)) & 3;  // (the reads of 8 lanes fall into different banks)
+    uint8_t* at_q = row + ((q ^ (key & 3)) << 4);
+    uint32_t x[NB];
+    if constexpr (NB == 4) {
+      const uint4 c4 = *reinterpret_cast<const uint4*>(codes + q * 16);
+      x[0] = c4.x; x[1] = c4.y; x[2] = c4.z; x[3] = c4.w;
+    } else {
+      const uint2 c2 = *reinterpret_cast<const uint2*>(codes + q * 8);
+      x[0] = c2.x; x[1] = c2.y;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      uint4 o;
+      unpack_f16(x[b], mask, mask << 4, d[b], d16[b], o.x, o.y);
+      unpack_f16(x[b] >> 8, mask, mask << 4, d[b], d16[b], o.z, o.w);
+      *reinterpret_cast<uint4*>(at_q + (b / 2) * (kStageKeys * 128) + (x4 ^ ((b & 1) << 6))) = o;
+    }
+  }
+}
+
+// 32 keys of a packed tile -> V operand tile, as four 8-key chunks, a lane four
+// dims of one block. key0: the tile's first key; have: its keys that are there.
+// Scales that must not enter the product -- of keys past the last or of a
+// missing page (whatever is there), and what is not finite (noted for the rows
+// that see it) -- count as zero.
+template <int D>
+__device__ __forceinline__ void unpack_values(uint8_t* tile, const uint8_t* pk, int w, int lane, int page, int page_shift, uint32_t hb,
+                                              const KvPlanes& pl, uint32_t mask, int key0, int S, uint32_t have, TileInfo* info) {
+  constexpr int NB = Cfg<D>::NB;
+  // byte offset of a key pair's codes and scales within the packed tile
+  auto codes_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vc + (kp & (page / 2 - 1)) * D; };
+  auto scales_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (page / 2 - 1)) * (NB * 4); };
+  const uint32_t mine = have >> (2 * w) & 3;
+  bool odd_tile = mine != 3 || key0 + 32 * w + 32 > S;
+  {
+    const int kp = 16 * w + lane / 2;  // half a pair's blocks to a lane
+    const uint32_t at_s = scales_at(kp);
+    uint32_t bad0 = 0, bad1 = 0;       // blocks of the even and the odd key
+#pragma unroll
+    for (int k = 0; k < NB / 2; ++k) {
+      const int b = (lane & 1) * (NB / 2) + k;
+      const uint32_t sc = *reinterpret_cast<const uint32_t*>(pk + at_s + b * 4);
+      if (!finite_bf16(sc & 0xFFFFu)) bad0 |= 1u << b;
+      if (!finite_bf16(sc >> 16)) bad1 |= 1u << b;
+    }
+    const bool there = mine >> (lane / 16) & 1;
+    if (!there || key0 + 2 * kp >= S) bad0 = 0;
+    if (!there || key0 + 2 * kp + 1 >= S) bad1 = 0;
+    const bool some = __any_sync(0xFFFFFFFFu, (bad0 | bad1) != 0);
+    if (some) {
+      bad0 |= __shfl_xor_sync(0xFFFFFFFFu, bad0, 1);
+      bad1 |= __shfl_xor_sync(0xFFFFFFFFu, bad1, 1);
+      if ((lane & 1) == 0) {
+        info->poison[2 * kp] = (uint8_t)bad0;
+        info->poison[2 * kp + 1] = (uint8_t)bad1;
+      }
+      odd_tile = true;
+    }
+    __syncwarp();
+    if (lane == 0) info->flag[w] = some;
+  }
+  constexpr int Lanes = 8 * NB, Chunks = 32 / Lanes;  // lanes of a pair's words; chunks side by side in a warp
+  const int word = lane % Lanes, b = word % NB, g = word / NB;
+#pragma unroll 1
+  for (int cc = 0; cc < 4; cc += Chunks) {
+    const int c = 4 * w + cc + lane / Lanes;  // chunk of 8 keys
+    uint32_t x[4], d[4];
+    const uint8_t* in_x = pk + codes_at(4 * c) + word * 4;  // (a chunk's four pairs are one page's)
+    const uint8_t* in_d = pk + scales_at(4 * c) + b * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[k] = *reinterpret_cast<const uint32_t*>(in_x + k * D);
+      d[k] = *reinterpret_cast<const uint32_t*>(in_d + k * (NB * 4));
+    }
+    if (odd_tile) {
+      const bool there = have >> (c / 2) & 1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = key0 + 8 * c + 2 * k;
+        if (!there || j >= S || !finite_bf16(d[k] & 0xFFFFu)) d[k] &= 0xFFFF0000u;
+        if (!there || j + 1 >= S || !finite_bf16(d[k] >> 16)) d[k] &= 0xFFFFu;
+      }
+    }
+    uint8_t* col = tile + (c / 8) * (D * 128) + (32 * b + 4 * g) * 128;
+    const int c4 = (c & 7) ^ ((g & 1) << 2);  // ((dim & 7) = 4 (g & 1) + j)
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const int j = (jj + (NB == 4 ? b : 2 * b + (g >> 1))) & 3;  // (the writes of 8 lanes fall into different banks)
+      *reinterpret_cast<uint4*>(col + j * 128 + ((c4 ^ j) << 4)) =
+          make_uint4(unpack(x[0], 4 * j, mask, d[0]), unpack(x[1], 4 * j, mask, d[1]), unpack(x[2], 4 * j, mask, d[2]),
+                     unpack(x[3], 4 * j, mask, d[3]));
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t code_mask() {  // a variable for the compiler: see unpack
+  uint32_t m;
+  asm volatile("mov.u32 %0, 0x000F000F;" : "=r"(m));
+  return m;
+}
+
+// The pages of key tile `block` of request r that some row of positions
+// first .. last sees, one to a lane (`need`), by bulk copies into `dst`.
+// have_out: the tile's keys that come (16 to a bit).
+__device__ __forceinline__ void copy_pages(uint8_t* dst, uint64_t* full, const fw_attn_q4_args& u, bool need, int id, int head,
+                                               uint32_t hb, int page_shift, int lane, uint32_t* have_out) {
+  bool copy = need;
+  if (copy && (id < 0 || id >= u.n_pages)) {
+    copy = false;
+    raise(u.status, FW_KV_BAD_SLOT);
+  }
+  const uint32_t got = __ballot_sync(0xFFFFFFFFu, copy);
+  uint32_t have = 0;  // a page's bit, for each 16 keys of it
+#pragma unroll
+  for (int k = 0; k < kStageKeys / 16; ++k) have |= (got >> ((k * 16) >> page_shift) & 1) << k;
+  if (lane == 0) {
+    *have_out = have;
+    mbar_arrive_expect_tx(full, (uint32_t)__popc(got) * hb);
+  }
+  __syncwarp();
+  if (copy) bulk_g2s(dst + lane * hb, (const uint8_t*)u.cache + ((int64_t)id * u.n_kv + head) * hb, hb, full);
+}
+
+// ------------------------------------------------------------- unpacking ahead
+// One CTA per (tile, head): pages in by bulk copies, warps 0-3 unpack K and 4-7
+// V, the operand tiles out by bulk copies. Bound by the 16-bit tiles written.
+constexpr int kAheadThreads = 256;
+template <int D>
+struct AheadSmem {
+  static constexpr uint32_t Bytes = 2 * Cfg<D>::TileBytes + 256 + Cfg<D>::PackedBytes;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAheadThreads) unpack_ahead_kernel(PrefillArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full;
+  __shared__ int s_sum[kAheadThreads / 32], s_found[2];
+  const fw_attn_q4_args& u = a.u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile = blockIdx.x / u.n_kv, head = blockIdx.x % u.n_kv;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid == 0) {
+    mbar_init(&full, 1);
+    fence_mbar_init();
+    s_found[0] = -1;
+  }
+  // the request that tile number `tile` belongs to
+  int base = 0;
+  for (int r0 = 0; r0 < u.R && base <= tile; r0 += kAheadThreads) {
+    const int r = r0 + tid;
+    int n, q0, S, t = 0;
+    if (r < u.R && prefill_request(a, r, n, q0, S)) t = key_tiles(S);
+    int inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    int before = base + inc - t;
+#pragma unroll
+    for (int w = 0; w < kAheadThreads / 32; ++w) {
+      if (w < warp) before += s_sum[w];
+      base += s_sum[w];
+    }
+    if (tile >= before && tile < before + t) {
+      s_found[0] = r;
+      s_found[1] = tile - before;
+    }
+  }
+  __syncthreads();
+  const int r = s_found[0], block = s_found[1];
+  if (r < 0) return;  // fewer tiles than the host had to allow for
+  int n, q0, S;
+  prefill_request(a, r, n, q0, S);
+  const int first = S - n, lo_key = u.window ? ::max(0, ::max(0, first) + 1 - u.window) : 0, key0 = block * kStageKeys;
+  if (key0 + kStageKeys <= lo_key && key0 >= u.sinks) return;  // no row sees it
+  const int page_shift = __ffs(u.page) - 1;
+  const uint32_t hb = (uint32_t)kv_head_bytes(u.page, D);
+  const KvPlanes pl = kv_planes(u.page, D);
+  uint8_t* pk = smem + 2 * C::TileBytes + 256;
+  TileInfo* info = reinterpret_cast<TileInfo*>(smem + 2 * C::TileBytes);
+  if (warp == 0) {
+    const int key = key0 + (lane << page_shift);
+    const bool need = lane < (kStageKeys >> page_shift) && key < S;
+    const int id = need ? u.block_table[(int64_t)r * u.max_blocks + (key >> page_shift)] : 0;
+    copy_pages(pk, &full, u, need, id, head, hb, page_shift, lane, &info->have);
+  }
+  __syncthreads();
+  if (!mbar_wait(&full, 0)) raise(u.status, FW_KV_TIMEOUT);
+  const uint32_t mask = code_mask();
+  if (warp < 4)
+    unpack_keys<D>(smem, pk, warp, lane, u.page, page_shift, hb, pl, mask);
+  else
+    unpack_values<D>(smem + C::TileBytes, pk, warp - 4, lane, u.page, page_shift, hb, pl, mask, key0, S, info->have, info);
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    bulk_s2g(a.ready + (int64_t)blockIdx.x * C::ReadyBytes, smem, 2 * C::TileBytes + (uint32_t)sizeof(TileInfo));
+    bulk_s2g_wait();
+  }
+}
+
+// ------------------------------------------------------------- the attention
 // A bounded wait with its loop in place (where warps change their register
 // share a call would need a register split of its own) and without a suspend
 // hint: a thread that sleeps on one wakes about 1000 cycles after the barrier
@@ -116,17 +377,17 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity)
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a) {
+template <int D, bool kReady>
+__global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kernel(PrefillArgs a) {
   using C = Cfg<D>;
-  constexpr int NB = C::NB;
+  using Y = Lay<D, kReady>;
+  constexpr int kThreads = Y::Threads, kTiles = Y::Tiles;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t packed_full[kPacked], packed_empty[kPacked], tile_full[kTiles], tile_empty[kTiles];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full, q_full;
-  __shared__ uint32_t s_tmem, s_have[kHave];
-  __shared__ __align__(4) uint8_t s_flag[kPoison][4];       // per unpacking warp: some scale of V is not finite
-  __shared__ uint8_t s_poison[kPoison][kStageKeys];  // then: the key's blocks (bits) that are not
-  __shared__ int s_scan[kThreads / 32], s_found[4];
+  __shared__ TileInfo s_info[kHave];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_scan[kThreads / 32], s_scan_tiles[kThreads / 32], s_found[6];
   __shared__ float s_qscale[kBlockRows];  // powers of two the query rows were divided by
   const fw_attn_q4_args& u = a.u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -135,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = base;
   uint8_t* sT = sQ + 2 * C::QBytes;
-  uint8_t* sP = sT + kTiles * C::TileBytes;
+  uint8_t* sP = sT + kTiles * C::TileBytes;  // packed tiles
   pdl_wait();
   pdl_launch_dependents();
 
@@ -143,46 +404,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
   // place, so that a prompt's later rows, which see the most keys, start first.
   int total = 0, want = -1;
   for (int pass = 0; pass < 2; ++pass) {
-    int sum = 0;
+    int sum = 0, sum_tiles = 0;
     for (int r0 = 0; r0 < u.R; r0 += kThreads) {
       const int r = r0 + tid;
-      int n = 0, q0 = 0, nb = 0;
-      if (r < u.R) {
-        q0 = u.q_start[r];
-        n = u.q_start[r + 1] - q0;
-        if (n * (long long)G > a.min_rows && q0 >= 0 && q0 <= u.T - n) nb = (int)((n * (long long)G + kBlockRows - 1) / kBlockRows);
+      int n = 0, q0 = 0, S = 0, nb = 0, nt = 0;
+      if (r < u.R && prefill_request(a, r, n, q0, S)) {
+        nb = (int)((n * (long long)G + kBlockRows - 1) / kBlockRows);
+        nt = key_tiles(S);
       }
-      int inc = nb;
+      int inc = nb, inc_tiles = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += x;
+        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, o), y = kReady ? __shfl_up_sync(0xFFFFFFFFu, inc_tiles, o) : 0;
+        if (lane >= o) {
+          inc += x;
+          inc_tiles += y;
+        }
       }
       __syncthreads();
-      if (lane == 31) s_scan[warp] = inc;
+      if (lane == 31) {
+        s_scan[warp] = inc;
+        s_scan_tiles[warp] = inc_tiles;
+      }
       __syncthreads();
-      int before = sum + inc - nb;
+      int before = sum + inc - nb, before_tiles = sum_tiles + inc_tiles - nt;
 #pragma unroll
       for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += s_scan[w];
+        if (w < warp) {
+          before += s_scan[w];
+          before_tiles += s_scan_tiles[w];
+        }
         sum += s_scan[w];
+        sum_tiles += s_scan_tiles[w];
       }
+      if (pass == 0 && r0 + kThreads >= u.R) {
+        total = sum;
+        want = total - 1 - pair / u.n_kv;
+      }
+      // (in the first pass the total, and so the block, is known in the last chunk only)
       if (want >= before && want < before + nb) {
         s_found[0] = r;
         s_found[1] = want - before;
         s_found[2] = n;
         s_found[3] = q0;
-      }
-      if (pass == 0 && r0 + kThreads >= u.R) {
-        total = sum;
-        want = total - 1 - pair / u.n_kv;
-        // one chunk holds everybody: no second pass
-        if (u.R <= kThreads && want >= before && want < before + nb) {
-          s_found[0] = r;
-          s_found[1] = want - before;
-          s_found[2] = n;
-          s_found[3] = q0;
-        }
+        s_found[4] = S;
+        s_found[5] = before_tiles;
       }
     }
     if (want < 0 || u.R <= kThreads) break;
@@ -194,11 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
   __syncthreads();
   const int r = s_found[0], row0 = s_found[1] * kBlockRows, n_new = s_found[2], tok0 = s_found[3];
   const int rows = ::min(kBlockRows, n_new * G - row0), row_tiles = rows > kRowTile ? 2 : 1;
-  int S = u.seq_lens[r];
-  if (S > u.max_blocks * u.page) {
-    S = u.max_blocks * u.page;
-    if (tid == 0) raise(u.status, FW_KV_BAD_SLOT);
-  }
+  const int S = s_found[4];
+  if (u.seq_lens[r] > S && tid == 0) raise(u.status, FW_KV_BAD_SLOT);  // more positions than the table has pages
   const int first = S - n_new + row0 / G, last = S - n_new + (row0 + rows - 1) / G;  // positions of the block's rows
   const Stages v = visible_stages(::max(last + 1, 0), first, u.window, u.sinks);
   const int lo_key = u.window ? ::max(0, ::max(0, first) + 1 - u.window) : 0;
@@ -222,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
       mbar_init(&packed_empty[i], 4);
     }
     for (int i = 0; i < kTiles; ++i) {
-      mbar_init(&tile_full[i], 4);
+      mbar_init(&tile_full[i], kReady ? 1 : 4);
       mbar_init(&tile_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -233,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
     mbar_init(&q_full, 8);
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == Y::MmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -254,13 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
     return ok;
   };
 
-  if (warp < kDeqWarp0) {
+  if (warp < Y::UnpackWarp0) {
     // ------------------------------------------------ softmax: a thread a row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if constexpr (!kReady) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = warp >> 2, row = t * kRowTile + (warp & 3) * 32 + lane;
     // this thread's share of Q into shared memory: 16 bytes a lane, rows of a
     // token side by side (all 256 rows: those past the last are zeros)
-    for (int e = tid; e < kBlockRows * (D / 8); e += kDeqWarp0 * 32) {
+    for (int e = tid; e < kBlockRows * (D / 8); e += Y::UnpackWarp0 * 32) {
       const int qr = e / (D / 8), c = e % (D / 8), n = row0 + qr;
       uint4 w = make_uint4(0, 0, 0, 0);
       if (qr < rows)
@@ -292,93 +555,92 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
       const uint32_t s_cols = tmem + lanes + t * 128, o_cols = tmem + lanes + 256 + t * 128;
       const int p = row < rows ? S - n_new + (row0 + row) / G : -1;
       float mz = 0.f, l = 0.f, scale = 0.f;
-      bool first_max = true;  // none was taken yet
+      bool unset = true;  // no maximum yet
       uint32_t poison = 0;
       int key_before = 0;
       // blocks of V that are not finite in keys this row sees (the tile whose product is in O by now)
       auto check_poison = [&](int i, int key0) {
-        const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(s_flag[i % kPoison]);
+        const TileInfo& info = s_info[i % kHave];
+        const uint32_t flags = *reinterpret_cast<const volatile uint32_t*>(info.flag);
         if (flags == 0) return;
         for (int c = 0; c < kStageKeys; ++c)
-          if ((flags >> (8 * (c / 32)) & 1) && sees(p, key0 + c, u.window, u.sinks)) poison |= s_poison[i % kPoison][c];
+          if ((flags >> (8 * (c / 32)) & 1) && sees(p, key0 + c, u.window, u.sinks)) poison |= info.poison[c];
       };
       for (int i = 0; i < n_t; ++i) {
         const int key0 = v.block(i0 + i) * kStageKeys;
+        const bool edge = key0 + kStageKeys - 1 > first || (u.window && key0 < last + 1 - u.window);
         wait(&s_full[t], i & 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
         // (the first score tells that every row of Q and its scale were written)
         if (i == 0) scale = a.scale_log2 * (1.f / kKeyScale) * s_qscale[row];
-        uint32_t s[128];
-        tmem_ld128(s_cols, s);
-        if (i > 0) check_poison(i - 1, key_before);
-        key_before = key0;
-        const uint32_t have = s_have[i % kHave];
-        if (key0 + kStageKeys - 1 > first || (u.window && key0 < last + 1 - u.window) || have != 0xFF) {
-          const int hi = p - key0, lo = u.window ? hi - u.window : -1, sk = u.sinks - key0;  // sees: c <= hi, c > lo or c < sk
+        const uint32_t have = s_info[i % kHave].have;
+        // P against the maximum as last set. P and O are exact to their
+        // rounding whatever their magnitude, so the maximum only moves (by
+        // whole powers of two) when a tile's sum shows that some p is past
+        // kMost, or when none was set yet; it is not even taken otherwise.
+        uint32_t pk[4][16];
+        float sum;
+        for (int pass = 0;; ++pass) {
+          uint32_t s[128];
+          tmem_ld128(s_cols, s);
+          if (edge || have != 0xFF) {
+            const int hi = p - key0, lo = u.window ? hi - u.window : -1, sk = u.sinks - key0;  // sees: c <= hi, c > lo or c < sk
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
-        }
-        // P and its sum against the maximum as last taken; both are exact to
-        // their rounding whatever their magnitude, so it only has to move
-        // when a tile's sum shows that some p is past kMost (or none was taken)
-        auto weights = [&]() {
-          const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
-          f2 sum = f2_pack(0.f, 0.f), sum2 = sum;
+            for (int c = 0; c < 128; ++c)
+              if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
+          }
+          if (__any_sync(0xFFFFFFFFu, pass == 1 || unset)) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float x, y;
-              f2_unpack(f2_fma(f2_pack_bits(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), sc, mm), x, y);
-              x = exp2_fast(x);
-              y = exp2_fast(y);
-              if (j & 1) sum2 = f2_add(sum2, f2_pack(x, y)); else sum = f2_add(sum, f2_pack(x, y));
-              pk[j] = bf16x2_bits(x, y);
+            for (int c = 0; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
+            float up = ceilf(fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale, -mz));
+            // a first maximum is taken as it is, a later one only moves up
+            if (!unset) up = fmaxf(up, 0.f);
+            const bool moves = up != -INFINITY;
+            const float keep = unset ? 0.f : exp2_fast(-up);
+            if (moves) {
+              mz += up;
+              l *= keep;
+              unset = false;
             }
-            tmem_st16(s_cols + 16 * c, pk);
+            if (i > 0)  // O holds the tiles before: S(i) came after their product
+#pragma unroll 1
+              for (int c = 0; c < D; c += 8) {  // 8 columns at a time: S holds 128 registers
+                uint32_t w[8];
+                tmem_ld8(o_cols + c, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (moves) w[j] = __float_as_uint(__uint_as_float(w[j]) * keep);
+                tmem_st8(o_cols + c, w);
+              }
+          }
+          const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
+          f2 sums[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            float x, y;
+            f2_unpack(f2_fma(f2_pack_bits(s[2 * c], s[2 * c + 1]), sc, mm), x, y);
+            x = exp2_fast(x);
+            y = exp2_fast(y);
+            sums[c & 1] = f2_add(sums[c & 1], f2_pack(x, y));
+            pk[c / 16][c % 16] = bf16x2_bits(x, y);
           }
           float x, y;
-          f2_unpack(f2_add(sum, sum2), x, y);
-          return x + y;
-        };
-        float sum = first_max ? 0.f : weights();
-        if (__any_sync(0xFFFFFFFFu, first_max || sum > kMost)) {
-          float top = -INFINITY, top2 = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            top = fmaxf(top, fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
-            top2 = fmaxf(top2, fmaxf(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
-          }
-          float up = fmaf(fmaxf(top, top2), scale, -mz);
-          // a first maximum is taken as it is, a later one only moves up
-          if (!first_max) up = fmaxf(up, 0.f);
-          const bool none = up == -INFINITY;
-          const float keep = first_max ? 0.f : exp2_fast(-up);
-          if (!none) {
-            mz += up;
-            l *= keep;
-            first_max = false;
-          }
-          if (i > 0) {  // O holds the tiles before: S(i) came after their product
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {  // 16 columns at a time: S holds 128 registers
-              uint32_t o[16];
-              tmem_ld16(o_cols + c, o);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = none ? o[j] : __float_as_uint(__uint_as_float(o[j]) * keep);
-              tmem_st16(o_cols + c, o);
-            }
-          }
-          sum = weights();
+          f2_unpack(f2_add(sums[0], sums[1]), x, y);
+          sum = x + y;
+          if (pass == 1 || !__any_sync(0xFFFFFFFFu, sum > kMost)) break;
         }
         l += sum;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st16(s_cols + 16 * c, pk[c]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t]);
+        // (S(i) told that tile i - 1 had been unpacked; its notes stay until this row tile's next P)
+        if (i > 0) check_poison(i - 1, key_before);
+        key_before = key0;
       }
       // ---------------------------------------------- out = O / l
       if (n_t > 0) {
@@ -389,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
       }
       const int n = row0 + row;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      if (a.splits > 1 && row < rows) a.ml[part * kBlockRows + row] = make_float2(first_max ? -INFINITY : mz, l);
+      if (a.splits > 1 && row < rows) a.ml[part * kBlockRows + row] = make_float2(unset ? -INFINITY : mz, l);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -422,143 +684,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
         }
       }
     }
-  } else if (warp < kMmaWarp) {
+  } else if (warp < Y::MmaWarp) {
     // ------------------------------------------------ unpack 4-bit codes to operand tiles
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    const int w = warp - kDeqWarp0;
-    uint32_t mask;
-    asm volatile("mov.u32 %0, 0x000F000F;" : "=r"(mask));
-    const int key = 32 * w + lane, at = key & (u.page - 1);      // K: a lane a key
-    const uint32_t blk_k = (key >> page_shift) * hb;
-    for (int i = 0; i < n_t; ++i) {
-      const int key0 = v.block(i0 + i) * kStageKeys;
-      const uint8_t* pk = sP + (i % kPacked) * C::PackedBytes;
-      wait(&packed_full[i % kPacked], (i / kPacked) & 1);
-      // ---- K
-      uint32_t seq = 2 * i;
-      wait(&tile_empty[seq % kTiles], ((seq / kTiles) & 1) ^ 1);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      {
-        uint8_t* tile = sT + (seq % kTiles) * C::TileBytes;
-        const uint8_t* codes = pk + blk_k + at * (D / 2);
-        uint32_t d[NB], d16[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const float x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(pk + blk_k + pl.ks)[at * NB + b] << 16) * kKeyScale;
-          d[b] = f16x2_bits(x, x);
-          d16[b] = f16x2_bits(x * 0.0625f, x * 0.0625f);
+    if constexpr (!kReady) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      const int w = warp - Y::UnpackWarp0;
+      const uint32_t mask = code_mask();
+      for (int i = 0; i < n_t; ++i) {
+        const uint8_t* pk = sP + (i % kPacked) * C::PackedBytes;
+        wait(&packed_full[i % kPacked], (i / kPacked) & 1);
+        uint32_t seq = 2 * i;
+        wait(&tile_empty[seq % kTiles], ((seq / kTiles) & 1) ^ 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        unpack_keys<D>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tile_full[seq % kTiles]);
+        seq = 2 * i + 1;
+        wait(&tile_empty[seq % kTiles], ((seq / kTiles) & 1) ^ 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        unpack_values<D>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask,
+                         v.block(i0 + i) * kStageKeys, S, s_info[i % kHave].have, &s_info[i % kHave]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&tile_full[seq % kTiles]);
+          mbar_arrive(&packed_empty[i % kPacked]);
         }
-        // the 16-byte chunk 4 b + q of this key lies at ((4 (b & 1) + q) ^ (key & 7)) in panel b / 2
-        uint8_t* row = tile + key * 128;
-        const int x4 = (key & 4) << 4;
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) {
-          const int q = (qq + (NB == 4 ? lane >> 1 : lane >> 2)) & 3;  // (the reads of 8 lanes fall into different banks)
-          uint8_t* at_q = row + ((q ^ (key & 3)) << 4);
-          uint32_t x[NB];
-          if constexpr (NB == 4) {
-            const uint4 c4 = *reinterpret_cast<const uint4*>(codes + q * 16);
-            x[0] = c4.x; x[1] = c4.y; x[2] = c4.z; x[3] = c4.w;
-          } else {
-            const uint2 c2 = *reinterpret_cast<const uint2*>(codes + q * 8);
-            x[0] = c2.x; x[1] = c2.y;
-          }
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            uint4 o;
-            unpack_f16(x[b], mask, mask << 4, d[b], d16[b], o.x, o.y);
-            unpack_f16(x[b] >> 8, mask, mask << 4, d[b], d16[b], o.z, o.w);
-            *reinterpret_cast<uint4*>(at_q + (b / 2) * (kStageKeys * 128) + (x4 ^ ((b & 1) << 6))) = o;
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tile_full[seq % kTiles]);
-      // ---- V: this warp's 32 keys as four 8-key chunks; a lane four dims of one block
-      seq = 2 * i + 1;
-      wait(&tile_empty[seq % kTiles], ((seq / kTiles) & 1) ^ 1);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      {
-        uint8_t* tile = sT + (seq % kTiles) * C::TileBytes;
-        // byte offset of a key pair's codes and scales within the packed tile
-        auto codes_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vc + (kp & (u.page / 2 - 1)) * D; };
-        auto scales_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (u.page / 2 - 1)) * (NB * 4); };
-        // scales that must not enter the product: keys past the last or of a
-        // missing page (whatever is there), and what is not finite (noted for
-        // the rows that see it). Half a pair's blocks to a lane.
-        const uint32_t have = s_have[i % kHave] >> (2 * w) & 3;
-        bool odd_tile = have != 3 || key0 + 32 * w + 32 > S;
-        uint32_t bad0 = 0, bad1 = 0;  // blocks of the even and the odd key
-        {
-          const int kp = 16 * w + lane / 2;
-          const uint32_t at_s = scales_at(kp);
-#pragma unroll
-          for (int k = 0; k < NB / 2; ++k) {
-            const int b = (lane & 1) * (NB / 2) + k;
-            const uint32_t sc = *reinterpret_cast<const uint32_t*>(pk + at_s + b * 4);
-            if (!finite_bf16(sc & 0xFFFFu)) bad0 |= 1u << b;
-            if (!finite_bf16(sc >> 16)) bad1 |= 1u << b;
-          }
-          const bool there = have >> (lane / 16) & 1;
-          if (!there || key0 + 2 * kp >= S) bad0 = 0;
-          if (!there || key0 + 2 * kp + 1 >= S) bad1 = 0;
-          const bool some = __any_sync(0xFFFFFFFFu, (bad0 | bad1) != 0);
-          if (some) {
-            bad0 |= __shfl_xor_sync(0xFFFFFFFFu, bad0, 1);
-            bad1 |= __shfl_xor_sync(0xFFFFFFFFu, bad1, 1);
-            if ((lane & 1) == 0) {
-              s_poison[i % kPoison][2 * kp] = (uint8_t)bad0;
-              s_poison[i % kPoison][2 * kp + 1] = (uint8_t)bad1;
-            }
-            odd_tile = true;
-          }
-          __syncwarp();
-          if (lane == 0) s_flag[i % kPoison][w] = some;
-        }
-        constexpr int Lanes = 8 * NB, Chunks = 32 / Lanes;  // lanes of a pair's words; chunks side by side in a warp
-        const int word = lane % Lanes, b = word % NB, g = word / NB;
-#pragma unroll
-        for (int cc = 0; cc < 4; cc += Chunks) {
-          const int c = 4 * w + cc + lane / Lanes;  // chunk of 8 keys
-          uint32_t x[4], d[4];
-          const uint8_t* in_x = pk + codes_at(4 * c) + word * 4;  // (a chunk's four pairs are one page's)
-          const uint8_t* in_d = pk + scales_at(4 * c) + b * 4;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[k] = *reinterpret_cast<const uint32_t*>(in_x + k * D);
-            d[k] = *reinterpret_cast<const uint32_t*>(in_d + k * (NB * 4));
-          }
-          if (odd_tile) {
-            const bool there = s_have[i % kHave] >> (c / 2) & 1;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int j = key0 + 8 * c + 2 * k;
-              if (!there || j >= S || !finite_bf16(d[k] & 0xFFFFu)) d[k] &= 0xFFFF0000u;
-              if (!there || j + 1 >= S || !finite_bf16(d[k] >> 16)) d[k] &= 0xFFFFu;
-            }
-          }
-          uint8_t* col = tile + (c / 8) * (D * 128) + (32 * b + 4 * g) * 128;
-          const int c4 = (c & 7) ^ ((g & 1) << 2);  // ((dim & 7) = 4 (g & 1) + j)
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            const int j = (jj + (NB == 4 ? b : 2 * b + (g >> 1))) & 3;  // (the writes of 8 lanes fall into different banks)
-            *reinterpret_cast<uint4*>(col + j * 128 + ((c4 ^ j) << 4)) =
-                make_uint4(unpack(x[0], 4 * j, mask, d[0]), unpack(x[1], 4 * j, mask, d[1]), unpack(x[2], 4 * j, mask, d[2]),
-                           unpack(x[3], 4 * j, mask, d[3]));
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&tile_full[seq % kTiles]);
-        mbar_arrive(&packed_empty[i % kPacked]);
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kMmaWarp) {
+    if constexpr (!kReady) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == Y::MmaWarp) {
       // ---------------------------------------------- MMA issuer
       // The warp stays together and elects a lane for the MMAs only: their
       // descriptors are then uniform, and their issue fast enough. One issuer
@@ -619,52 +776,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(PrefillArgs a
         __syncwarp();
         mbar_wait_inline(&o_full, 0);
       }
-    } else if (warp == kLoadWarp) {
-      // ---------------------------------------------- pages, one to a lane
-      int id = 0;
-      auto look = [&](int i) {
-        const int key = v.block(i0 + i) * kStageKeys + (lane << page_shift);
-        const bool need = lane < (kStageKeys >> page_shift) && key <= last && (key + u.page > lo_key || key < u.sinks);
-        if (need) id = u.block_table[(int64_t)r * u.max_blocks + (key >> page_shift)];
-        return need;
-      };
-      bool need = n_t > 0 && look(0);
-      int issued = 0;
-      for (int i = 0; i < n_t; ++i) {
-        bool copy = need;
-        if (copy && (id < 0 || id >= u.n_pages)) {
-          copy = false;
-          raise(u.status, FW_KV_BAD_SLOT);
+    } else if (warp == Y::LoadWarp) {
+      int issued = 0;  // tiles whose copies were started
+      if constexpr (kReady) {
+        // -------------------------------------------- unpacked tiles
+        const uint8_t* src = a.ready + (int64_t)s_found[5] * u.n_kv * C::ReadyBytes;
+        for (int seq = 0; seq < 2 * n_t; ++seq) {
+          const int i = seq / 2, slot = seq % kTiles;
+          wait(&tile_empty[slot], ((seq / kTiles) & 1) ^ 1);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (elect_one()) {
+            const uint8_t* tile = src + ((int64_t)v.block(i0 + i) * u.n_kv + head) * C::ReadyBytes;
+            mbar_arrive_expect_tx(&tile_full[slot], C::TileBytes + (seq & 1 ? 0 : (uint32_t)sizeof(TileInfo)));
+            bulk_g2s(sT + slot * C::TileBytes, tile + (seq & 1) * C::TileBytes, C::TileBytes, &tile_full[slot]);
+            if (!(seq & 1)) bulk_g2s(&s_info[i % kHave], tile + 2 * C::TileBytes, sizeof(TileInfo), &tile_full[slot]);
+          }
+          __syncwarp();
+          issued = seq + 1;
         }
-        const int page = id, slot = i % kPacked;
-        if (i + 1 < n_t) need = look(i + 1);  // in flight during this tile
-        const uint32_t got = __ballot_sync(0xFFFFFFFFu, copy);
-        wait(&packed_empty[slot], ((i / kPacked) & 1) ^ 1);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          uint32_t have = 0;  // a page's bit, for each 16 keys of it
-#pragma unroll
-          for (int k = 0; k < kStageKeys / 16; ++k) have |= (got >> ((k * 16) >> page_shift) & 1) << k;
-          s_have[i % kHave] = have;
-          mbar_arrive_expect_tx(&packed_full[slot], (uint32_t)__popc(got) * hb);
+        // copies still in flight after an abandoned wait land before the CTA leaves
+        if (!ok)
+          for (int j = ::max(0, issued - kTiles); j < issued; ++j) mbar_wait_inline(&tile_full[j % kTiles], (j / kTiles) & 1);
+      } else {
+        // -------------------------------------------- pages, one to a lane
+        int id = 0;
+        auto look = [&](int i) {
+          const int key = v.block(i0 + i) * kStageKeys + (lane << page_shift);
+          const bool need = lane < (kStageKeys >> page_shift) && key <= last && (key + u.page > lo_key || key < u.sinks);
+          if (need) id = u.block_table[(int64_t)r * u.max_blocks + (key >> page_shift)];
+          return need;
+        };
+        bool need = n_t > 0 && look(0);
+        for (int i = 0; i < n_t; ++i) {
+          const bool copy = need;
+          const int page = id, slot = i % kPacked;
+          if (i + 1 < n_t) need = look(i + 1);  // in flight during this tile
+          wait(&packed_empty[slot], ((i / kPacked) & 1) ^ 1);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          // (what the tile has is written before the arrival that lets others read it)
+          copy_pages(sP + slot * C::PackedBytes, &packed_full[slot], u, copy, page, head, hb, page_shift, lane, &s_info[i % kHave].have);
+          issued = i + 1;
         }
-        __syncwarp();
-        if (copy)
-          bulk_g2s(sP + slot * C::PackedBytes + lane * hb, (const uint8_t*)u.cache + ((int64_t)page * u.n_kv + head) * hb, hb,
-                   &packed_full[slot]);
-        issued = i + 1;
+        if (!ok)
+          for (int j = ::max(0, issued - kPacked); j < issued; ++j) mbar_wait_inline(&packed_full[j % kPacked], (j / kPacked) & 1);
       }
-      // copies still in flight after an abandoned wait land before the CTA leaves
-      if (!ok)
-        for (int j = ::max(0, issued - kPacked); j < issued; ++j) mbar_wait_inline(&packed_full[j % kPacked], (j / kPacked) & 1);
     }
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp)
+  if (warp == Y::MmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
@@ -681,24 +845,61 @@ int prefill_splits(const fw_attn_q4_args& a, int sms) {
   return (int)::max((int64_t)1, ::min(tiles, sms / ctas));
 }
 
-}  // namespace
+// Key tiles of all requests at most.
+int64_t most_tiles(const fw_attn_q4_args& a) {
+  return (int64_t)a.R * (((int64_t)a.max_blocks * a.page + kStageKeys - 1) / kStageKeys);
+}
+int64_t ready_bytes(const fw_attn_q4_args& a) {
+  return most_tiles(a) * a.n_kv * (a.D == 64 ? Cfg<64>::ReadyBytes : Cfg<128>::ReadyBytes);
+}
 
-cudaError_t configure_prefill_attn() {
+// Whether tiles are unpacked ahead: where a request has kReadyBlocks row blocks
+// or more to read them (on average), and the workspace for all that the block
+// tables can hold stays moderate.
+constexpr int kReadyBlocks = 4;
+constexpr int64_t kReadyMost = 1ll << 30;
+bool prefill_ready(const fw_attn_q4_args& a, int sms) {
+  return prefill_splits(a, sms) == 1 && (int64_t)a.T * (a.n_q / a.n_kv) >= (int64_t)kReadyBlocks * kBlockRows * a.R &&
+         ready_bytes(a) <= kReadyMost;
+}
+
+template <int D>
+cudaError_t configure() {
   // the warps' register shares (setmaxnreg) must fit what the launch gives
   // the CTA, or the growing ones would wait for ever
-  for (const void* k : {(const void*)attn_prefill_kernel<64>, (const void*)attn_prefill_kernel<128>}) {
-    cudaFuncAttributes f;
-    const cudaError_t e = cudaFuncGetAttributes(&f, k);
-    if (e != cudaSuccess) return e;
-    if (f.numRegs * kThreads < kSoftmaxRegs * 256 + kOtherRegs * 256) return cudaErrorInvalidDeviceFunction;
-  }
-  cudaError_t e = cudaFuncSetAttribute(attn_prefill_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<64>::SmemBytes);
+  using Y = Lay<D, false>;
+  cudaFuncAttributes f;
+  cudaError_t e = cudaFuncGetAttributes(&f, attn_prefill_kernel<D, false>);
+  if (e != cudaSuccess) return e;
+  if (f.numRegs * Y::Threads < kSoftmaxRegs * 256 + kOtherRegs * (Y::Threads - 256)) return cudaErrorInvalidDeviceFunction;
+  e = cudaFuncSetAttribute(attn_prefill_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Y::SmemBytes);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_prefill_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::SmemBytes);
+    e = cudaFuncSetAttribute(attn_prefill_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, true>::SmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(unpack_ahead_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AheadSmem<D>::Bytes);
   return e;
 }
 
+template <int D>
+cudaError_t launch(const PrefillArgs& d, int64_t ctas, cudaStream_t s) {
+  if (!d.ready)
+    return launch_dependent(attn_prefill_kernel<D, false>, dim3((unsigned)ctas), dim3(Lay<D, false>::Threads), Lay<D, false>::SmemBytes, s, d);
+  const int64_t tiles = most_tiles(d.u) * d.u.n_kv;
+  cudaError_t e = launch_dependent(unpack_ahead_kernel<D>, dim3((unsigned)tiles), dim3(kAheadThreads), AheadSmem<D>::Bytes, s, d);
+  if (e == cudaSuccess)
+    e = launch_dependent(attn_prefill_kernel<D, true>, dim3((unsigned)ctas), dim3(Lay<D, true>::Threads), Lay<D, true>::SmemBytes, s, d);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t configure_prefill_attn() {
+  const cudaError_t e = configure<64>();
+  return e == cudaSuccess ? configure<128>() : e;
+}
+
 int64_t prefill_workspace(const fw_attn_q4_args& a, int sms) {
+  if (prefill_ready(a, sms)) return ready_bytes(a);
   const int64_t pairs = (int64_t)prefill_blocks(a) * a.n_kv, splits = prefill_splits(a, sms);
   return splits == 1 ? 0 : pairs * sizeof(SplitRecord) + pairs * splits * kBlockRows * (a.D * 4 + 8);
 }
@@ -711,12 +912,12 @@ cudaError_t launch_attn_prefill(const fw_attn_q4_args& a, int min_rows, void* wo
   d.blocks = prefill_blocks(a);
   const int64_t pairs = (int64_t)d.blocks * a.n_kv;
   if (pairs * d.splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  d.ready = prefill_ready(a, sms) ? static_cast<uint8_t*>(workspace) : nullptr;
   d.rec = static_cast<SplitRecord*>(workspace);
   d.o = reinterpret_cast<float*>(d.rec + pairs);
   d.ml = reinterpret_cast<float2*>(d.o + pairs * d.splits * kBlockRows * a.D);
   d.scale_log2 = a.scale * kLog2e;
-  cudaError_t e = launch_dependent(a.D == 64 ? attn_prefill_kernel<64> : attn_prefill_kernel<128>, dim3((unsigned)(pairs * d.splits)),
-                                   dim3(kThreads), a.D == 64 ? Cfg<64>::SmemBytes : Cfg<128>::SmemBytes, s, d);
+  cudaError_t e = a.D == 64 ? launch<64>(d, pairs * d.splits, s) : launch<128>(d, pairs * d.splits, s);
   if (e == cudaSuccess && d.splits > 1) e = launch_attn_join(a, d.rec, d.o, d.ml, (int)pairs, kBlockRows, s);
   return e;
 }

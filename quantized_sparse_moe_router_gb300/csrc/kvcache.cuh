@@ -56,6 +56,14 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// One bulk asynchronous copy shared -> global (16-byte aligned, size % 16 == 0), and the wait for this thread's.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_s2g_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // Sets bits of a caller's status word (may be null).
 __device__ __forceinline__ void raise(int32_t* status, int bits) {
   if (status) atomicOr(status, bits);
