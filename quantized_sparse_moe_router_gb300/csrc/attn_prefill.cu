@@ -19,8 +19,8 @@
 // memory it will lie in, and one bulk copy brings a tile. Where few do, four
 // warps of the CTA unpack its own tiles.
 //
-// Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread a row: no
-// shuffles), then four unpacking warps (not kReady), one that issues the MMAs,
+// Warps: those of the softmax, row tile 0's first (one or two threads a row: no
+// shuffles), then four unpacking warps (not kReady), two that issue the MMAs,
 // one that copies tiles or pages. The chain S -> P -> O -> S of a row tile
 // bounds it: 1024 cycles of products, about 900 of softmax, and four barriers
 // of about 175 from arrival to wake.
@@ -41,7 +41,7 @@ using namespace dev;
 constexpr int kRowTile = 128, kBlockRows = 2 * kRowTile;
 constexpr int kPacked = 3, kHave = 8;
 constexpr uint32_t kTmemCols = 512;
-// not kReady: registers of the softmax warps and of the others, of 128 a thread at launch (kReady: all have 200)
+// not kReady: registers of the softmax warps and of the others, of 128 a thread at launch
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr float kMost = 1048576.f;  // a row's maximum moves only when a tile's sum of p passes this
 
@@ -66,7 +66,11 @@ static_assert(sizeof(TileInfo) <= 256 && sizeof(TileInfo) % 16 == 0, "TileInfo i
 
 template <int D, bool kReady>
 struct Lay {
-  static constexpr int UnpackWarp0 = 8, MmaWarp = kReady ? 8 : 12, LoadWarp = MmaWarp + 1, Threads = kReady ? 320 : 512;
+  // Threads of a row: with two, a sub-core has two warps of a row tile whose
+  // exponentials and other steps overlap (one warp issues in order).
+  static constexpr int Split = kReady ? 2 : 1, Cols = kStageKeys / Split, SoftmaxWarps = 8 * Split;
+  static constexpr int UnpackWarp0 = SoftmaxWarps, MmaWarp = SoftmaxWarps + (kReady ? 0 : 4), LoadWarp = MmaWarp + 2;
+  static constexpr int Threads = kReady ? 608 : 512;
   static constexpr int Tiles = kReady ? 4 : 3;  // ring of operand tiles
   static constexpr uint32_t SmemBytes = 2 * Cfg<D>::QBytes + Tiles * Cfg<D>::TileBytes + (kReady ? 0 : kPacked * Cfg<D>::PackedBytes) + 1024;
 };
@@ -377,6 +381,17 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity)
   }
 }
 
+// Barrier of `threads` threads with the OR of their predicates.
+__device__ __forceinline__ bool bar_red_or(int id, int threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
+
 template <int D, bool kReady>
 __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kernel(PrefillArgs a) {
   using C = Cfg<D>;
@@ -384,11 +399,12 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
   constexpr int kThreads = Y::Threads, kTiles = Y::Tiles;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t packed_full[kPacked], packed_empty[kPacked], tile_full[kTiles], tile_empty[kTiles];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full, q_full;
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], turn[2], q_full;
   __shared__ TileInfo s_info[kHave];
   __shared__ uint32_t s_tmem;
   __shared__ int s_scan[kThreads / 32], s_scan_tiles[kThreads / 32], s_found[6];
   __shared__ float s_qscale[kBlockRows];  // powers of two the query rows were divided by
+  __shared__ float s_pair[2][kBlockRows];  // two threads a row: what they tell each other
   const fw_attn_q4_args& u = a.u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = u.n_q / u.n_kv;
@@ -486,14 +502,15 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
     }
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&tile_full[i], kReady ? 1 : 4);
-      mbar_init(&tile_empty[i], 1);
+      mbar_init(&tile_empty[i], row_tiles);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&turn[i], 1);
+      mbar_init(&p_full[i], 4 * Y::Split);
     }
-    mbar_init(&o_full, 1);
-    mbar_init(&q_full, 8);
+    mbar_init(&q_full, Y::SoftmaxWarps);
     fence_mbar_init();
   }
   if (warp == Y::MmaWarp) {
@@ -517,13 +534,23 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
     return ok;
   };
 
-  if (warp < Y::UnpackWarp0) {
-    // ------------------------------------------------ softmax: a thread a row
+  if (warp < Y::SoftmaxWarps) {
+    // ------------------------------------------------ softmax: one or two threads a row
     if constexpr (!kReady) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int t = warp >> 2, row = t * kRowTile + (warp & 3) * 32 + lane;
+    constexpr int Cols = Y::Cols;
+    const int t = warp / (4 * Y::Split), half = (warp >> 2) & (Y::Split - 1), row = t * kRowTile + (warp & 3) * 32 + lane;
+    // the OR of a predicate over the warps of these 32 rows, which meet it the
+    // same number of times whatever happens (after an abandoned wait the loop
+    // below runs on without meaning)
+    auto any = [&](bool x) {
+      if constexpr (Y::Split == 1)
+        return __any_sync(0xFFFFFFFFu, x) != 0;
+      else
+        return bar_red_or(1 + t * 4 + (warp & 3), 64, x);
+    };
     // this thread's share of Q into shared memory: 16 bytes a lane, rows of a
     // token side by side (all 256 rows: those past the last are zeros)
-    for (int e = tid; e < kBlockRows * (D / 8); e += Y::UnpackWarp0 * 32) {
+    for (int e = tid; e < kBlockRows * (D / 8); e += Y::SoftmaxWarps * 32) {
       const int qr = e / (D / 8), c = e % (D / 8), n = row0 + qr;
       uint4 w = make_uint4(0, 0, 0, 0);
       if (qr < rows)
@@ -570,31 +597,37 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         const int key0 = v.block(i0 + i) * kStageKeys;
         const bool edge = key0 + kStageKeys - 1 > first || (u.window && key0 < last + 1 - u.window);
         wait(&s_full[t], i & 1);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
         // (the first score tells that every row of Q and its scale were written)
         if (i == 0) scale = a.scale_log2 * (1.f / kKeyScale) * s_qscale[row];
-        const uint32_t have = s_info[i % kHave].have;
+        const uint32_t have = s_info[i % kHave].have >> (half * (Cols / 16));
+        const bool masks = edge || (have & ((1u << (Cols / 16)) - 1)) != (1u << (Cols / 16)) - 1;
         // P against the maximum as last set. P and O are exact to their
         // rounding whatever their magnitude, so the maximum only moves (by
         // whole powers of two) when a tile's sum shows that some p is past
         // kMost, or when none was set yet; it is not even taken otherwise.
-        uint32_t pk[4][16];
+        uint32_t pk[Cols / 32][16];
         float sum;
         for (int pass = 0;; ++pass) {
-          uint32_t s[128];
-          tmem_ld128(s_cols, s);
-          if (edge || have != 0xFF) {
-            const int hi = p - key0, lo = u.window ? hi - u.window : -1, sk = u.sinks - key0;  // sees: c <= hi, c > lo or c < sk
+          uint32_t s[Cols];
+          tmem_ld(s_cols + half * Cols, s);
+          if (masks) {
+            const int at = key0 + half * Cols, hi = p - at, lo = u.window ? hi - u.window : -1, sk = u.sinks - at;  // sees: c <= hi, c > lo or c < sk
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
+            for (int c = 0; c < Cols; ++c)
               if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
           }
-          if (__any_sync(0xFFFFFFFFu, pass == 1 || unset)) {
+          if (pass == 1 || i == 0) {
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
-            float up = ceilf(fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale, -mz));
+            for (int c = 0; c < Cols; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
+            float up = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            if constexpr (Y::Split == 2) {
+              s_pair[half][row] = up;
+              any(false);
+              up = fmaxf(up, s_pair[half ^ 1][row]);
+            }
+            up = ceilf(fmaf(up, scale, -mz));
             // a first maximum is taken as it is, a later one only moves up
             if (!unset) up = fmaxf(up, 0.f);
             const bool moves = up != -INFINITY;
@@ -606,9 +639,9 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
             }
             if (i > 0)  // O holds the tiles before: S(i) came after their product
 #pragma unroll 1
-              for (int c = 0; c < D; c += 8) {  // 8 columns at a time: S holds 128 registers
+              for (int c = half * (D / Y::Split); c < (half + 1) * (D / Y::Split); c += 8) {  // 8 columns at a time: S holds the registers
                 uint32_t w[8];
-                tmem_ld8(o_cols + c, w);
+                tmem_ld(o_cols + c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                   if (moves) w[j] = __float_as_uint(__uint_as_float(w[j]) * keep);
@@ -618,7 +651,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
           const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
           f2 sums[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
+          for (int c = 0; c < Cols / 2; ++c) {
             float x, y;
             f2_unpack(f2_fma(f2_pack_bits(s[2 * c], s[2 * c + 1]), sc, mm), x, y);
             x = exp2_fast(x);
@@ -629,11 +662,12 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
           float x, y;
           f2_unpack(f2_add(sums[0], sums[1]), x, y);
           sum = x + y;
-          if (pass == 1 || !__any_sync(0xFFFFFFFFu, sum > kMost)) break;
+          // (P will lie over S: by now all warps of these rows have read it)
+          if (!any(pass == 0 && (unset || sum > kMost))) break;
         }
         l += sum;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_st16(s_cols + 16 * c, pk[c]);
+        for (int c = 0; c < Cols / 32; ++c) tmem_st16(s_cols + half * (Cols / 2) + 16 * c, pk[c]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -643,20 +677,26 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         key_before = key0;
       }
       // ---------------------------------------------- out = O / l
+      if constexpr (Y::Split == 2) {
+        any(false);  // (s_pair may still be read)
+        s_pair[half][row] = l;
+        any(false);
+        l = s_pair[0][row] + s_pair[1][row];
+      }
       if (n_t > 0) {
-        wait(&o_full, 0);
+        wait(&o_full[t], 0);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         if (ok) check_poison(n_t - 1, key_before);
       }
       const int n = row0 + row;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      if (a.splits > 1 && row < rows) a.ml[part * kBlockRows + row] = make_float2(unset ? -INFINITY : mz, l);
+      if (a.splits > 1 && half == 0 && row < rows) a.ml[part * kBlockRows + row] = make_float2(unset ? -INFINITY : mz, l);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = half * (D / Y::Split); c < (half + 1) * (D / Y::Split); c += 32) {
         uint32_t o[32];
         if (n_t > 0 && ok) {
-          tmem_ld32(o_cols + c, o);
+          tmem_ld(o_cols + c, o);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0;
@@ -715,66 +755,59 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
     }
   } else {
     if constexpr (!kReady) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == Y::MmaWarp) {
-      // ---------------------------------------------- MMA issuer
-      // The warp stays together and elects a lane for the MMAs only: their
-      // descriptors are then uniform, and their issue fast enough. One issuer
-      // and a fixed order keep the two row tiles half a period apart: with an
-      // issuer each they fall into step, and softmax and products take turns
-      // instead of overlapping.
+    if (warp < Y::MmaWarp + row_tiles) {
+      // ---------------------------------------------- MMA issuers, one for each row tile
+      // A warp stays together and elects a lane for the MMAs only: their
+      // descriptors are then uniform. What an issuer has to wait for and work
+      // out takes some hundred cycles a tile, which the other's products hide.
+      // The batches PV(i), QK(i + 1) go strictly in turn: left to themselves
+      // the two row tiles fall into step, and softmax and products would take
+      // turns instead of overlapping.
+      const int t = warp - Y::MmaWarp;
       // (a value shuffled from lane 0 is uniform for the compiler, too)
-      const uint32_t q0 = __shfl_sync(0xFFFFFFFFu, sw128_desc_lo(smem_u32(sQ)), 0);
+      const uint32_t q0 = __shfl_sync(0xFFFFFFFFu, sw128_desc_lo(smem_u32(sQ) + t * C::QBytes), 0);
       const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, sw128_desc_lo(smem_u32(sT)), 0);
-      const uint32_t cols = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-      auto qk = [&](int t, uint32_t seq, bool last_use) {
-        const uint32_t k0 = t0 + (seq % kTiles) * (C::TileBytes >> 4), a0 = q0 + t * (C::QBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = ((k / 4) * (kRowTile * 128) + (k % 4) * 32) >> 4;  // (both tiles have 128 rows)
-            mma_ss_lo(cols + t * 128, a0 + at, k0 + at, idesc_f16(kRowTile, kStageKeys), k != 0);
-          }
-          mma_commit(&s_full[t]);
-          if (last_use) mma_commit(&tile_empty[seq % kTiles]);
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int t, uint32_t seq, bool more, bool last_use) {
-        const uint32_t v0 = t0 + (seq % kTiles) * (C::TileBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kStageKeys / 16; ++k)
-            mma_ts_lo(cols + 256 + t * 128, cols + t * 128 + k * 8, v0 + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4),
-                      idesc_bf16(kRowTile, D), more || k != 0);
-          if (last_use) mma_commit(&tile_empty[seq % kTiles]);
-        }
-        __syncwarp();
-      };
+      const uint32_t s_cols = __shfl_sync(0xFFFFFFFFu, tmem + t * 128, 0), o_cols = __shfl_sync(0xFFFFFFFFu, tmem + 256 + t * 128, 0);
       auto ready = [&](uint64_t* bar, uint32_t parity) {
         wait(bar, parity);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        tc_fence_after();
-        return ok;
+        return ok = __all_sync(0xFFFFFFFFu, ok);
       };
       auto tile_ready = [&](uint32_t seq) { return ready(&tile_full[seq % kTiles], (seq / kTiles) & 1); };
-      if (n_t > 0 && ready(&q_full, 0) && tile_ready(0)) {
-        for (int t = 0; t < row_tiles; ++t) qk(t, 0, t == row_tiles - 1);
-        for (int i = 0; i < n_t && ok; ++i) {
-          const bool next = i + 1 < n_t;
-          if (!tile_ready(2 * i + 1)) break;
-          for (int t = 0; t < row_tiles; ++t) {
-            if (!ready(&p_full[t], i & 1)) break;
-            pv(t, 2 * i + 1, i > 0, t == row_tiles - 1);
-            if (next) {
-              if (t == 0 && !tile_ready(2 * i + 2)) break;
-              qk(t, 2 * i + 2, t == row_tiles - 1);
-            }
+      bool go = n_t > 0 && ready(&q_full, 0);
+      for (int i = -1; i < n_t && go; ++i) {  // the batch PV(i), QK(i + 1)
+        const bool first_batch = i < 0, next = i + 1 < n_t;
+        const uint32_t sv = 2 * i + 1, sk = 2 * i + 2;
+        if ((!first_batch && !tile_ready(sv)) || (next && !tile_ready(sk))) break;
+        if (row_tiles == 2 && !(t == 0 && first_batch) && !ready(&turn[t], (i + t) & 1)) break;
+        if (!first_batch && !ready(&p_full[t], i & 1)) break;  // (what comes last is what the chain waits for)
+        tc_fence_after();
+        if (elect_one()) {
+          if (!first_batch) {
+            const uint32_t v0 = t0 + (sv % kTiles) * (C::TileBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < kStageKeys / 16; ++k)
+              mma_ts_lo(o_cols, s_cols + k * 8, v0 + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), idesc_bf16(kRowTile, D), i > 0 || k != 0);
+            mma_commit(&tile_empty[sv % kTiles]);
           }
+          if (next) {
+            const uint32_t k0 = t0 + (sk % kTiles) * (C::TileBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {  // (both tiles have 128 rows)
+              const uint32_t at = ((k / 4) * (kRowTile * 128) + (k % 4) * 32) >> 4;
+              mma_ss_lo(s_cols, q0 + at, k0 + at, idesc_f16(kRowTile, kStageKeys), k != 0);
+            }
+            mma_commit(&s_full[t]);
+            mma_commit(&tile_empty[sk % kTiles]);
+          }
+          if (row_tiles == 2) mbar_arrive(&turn[t ^ 1]);
         }
-        // every MMA issued has finished before tensor memory is read or released
-        if (elect_one()) mma_commit(&o_full);
         __syncwarp();
-        mbar_wait_inline(&o_full, 0);
+      }
+      // every MMA issued has finished before tensor memory is read or released
+      if (go) {
+        if (elect_one()) mma_commit(&o_full[t]);
+        __syncwarp();
+        mbar_wait_inline(&o_full[t], 0);
       }
     } else if (warp == Y::LoadWarp) {
       int issued = 0;  // tiles whose copies were started
@@ -855,8 +888,10 @@ int64_t ready_bytes(const fw_attn_q4_args& a) {
 
 // Whether tiles are unpacked ahead: where a request has kReadyBlocks row blocks
 // or more to read them (on average), and the workspace for all that the block
-// tables can hold stays moderate.
-constexpr int kReadyBlocks = 4;
+// tables can hold stays moderate. Eight requests with 4,000 cached positions
+// and 32 query heads over 4: at 8 blocks 142 us ahead, 157 us in the kernel; at
+// 4 blocks 82 and 79 us; at 2 blocks (16 requests, 8,000 positions) 173 and 141.
+constexpr int kReadyBlocks = 6;
 constexpr int64_t kReadyMost = 1ll << 30;
 bool prefill_ready(const fw_attn_q4_args& a, int sms) {
   return prefill_splits(a, sms) == 1 && (int64_t)a.T * (a.n_q / a.n_kv) >= (int64_t)kReadyBlocks * kBlockRows * a.R &&
