@@ -413,6 +413,35 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
   uint8_t* sQ = base;
   uint8_t* sT = sQ + 2 * C::QBytes;
   uint8_t* sP = sT + kTiles * C::TileBytes;  // packed tiles
+
+  if (tid == 0) {
+    for (int i = 0; i < kPacked; ++i) {
+      mbar_init(&packed_full[i], 1);
+      mbar_init(&packed_empty[i], 4);
+    }
+    for (int i = 0; i < kTiles; ++i) {
+      mbar_init(&tile_full[i], kReady ? 1 : 4);
+      mbar_init(&tile_empty[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&turn[i], 1);
+      mbar_init(&p_full[i], 4 * Y::Split);
+    }
+    mbar_init(&q_full, Y::SoftmaxWarps);
+    fence_mbar_init();
+  }
+  if (warp == Y::MmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  auto tmem_free = [&]() {
+    if (warp == Y::MmaWarp)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(kTmemCols) : "memory");
+  };
   pdl_wait();
   pdl_launch_dependents();
 
@@ -471,6 +500,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
   }
   if (want < 0) {  // fewer blocks than the host had to allow for
     if (a.splits > 1 && z == 0 && tid == 0) a.rec[pair].parts = 0;
+    tmem_free();
     return;
   }
   __syncthreads();
@@ -495,29 +525,6 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
     a.rec[pair] = rec;
   }
 
-  if (tid == 0) {
-    for (int i = 0; i < kPacked; ++i) {
-      mbar_init(&packed_full[i], 1);
-      mbar_init(&packed_empty[i], 4);
-    }
-    for (int i = 0; i < kTiles; ++i) {
-      mbar_init(&tile_full[i], kReady ? 1 : 4);
-      mbar_init(&tile_empty[i], row_tiles);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&turn[i], 1);
-      mbar_init(&p_full[i], 4 * Y::Split);
-    }
-    mbar_init(&q_full, Y::SoftmaxWarps);
-    fence_mbar_init();
-  }
-  if (warp == Y::MmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -549,30 +556,50 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         return bar_red_or(1 + t * 4 + (warp & 3), 64, x);
     };
     // this thread's share of Q into shared memory: 16 bytes a lane, rows of a
-    // token side by side (all 256 rows: those past the last are zeros)
-    for (int e = tid; e < kBlockRows * (D / 8); e += Y::SoftmaxWarps * 32) {
-      const int qr = e / (D / 8), c = e % (D / 8), n = row0 + qr;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (qr < rows)
-        w = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)u.q + (int64_t)(tok0 + n / G) * u.q_stride + (head * G + n % G) * D + 8 * c);
-      float x[8], most = 0.f;
-      bf16x2_to_f32(w.x, x[0], x[1]);
-      bf16x2_to_f32(w.y, x[2], x[3]);
-      bf16x2_to_f32(w.z, x[4], x[5]);
-      bf16x2_to_f32(w.w, x[6], x[7]);
+    // token side by side (all 256 rows: those past the last are zeros); the
+    // loads of a batch all in flight before the first is used
+    constexpr int Step = Y::SoftmaxWarps * 32 / (D / 8), Batch = 8;  // rows between a thread's chunks
+    static_assert(kBlockRows % Step == 0, "a whole number of rows a pass");
+    const int c = tid % (D / 8), step_tok = Step / G, step_head = Step % G;
+    int tok = (row0 + tid / (D / 8)) / G, hd = (row0 + tid / (D / 8)) % G;  // of the next row, kept without dividing again
+    for (int r0 = tid / (D / 8); r0 < kBlockRows; r0 += Step * Batch) {
+      uint4 in[Batch];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
+      for (int k = 0; k < Batch; ++k) {
+        in[k] = make_uint4(0, 0, 0, 0);
+        if (r0 + k * Step < rows)
+          in[k] = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)u.q + (int64_t)(tok0 + tok) * u.q_stride + (head * G + hd) * D + 8 * c);
+        tok += step_tok;
+        hd += step_head;
+        if (hd >= G) {
+          hd -= G;
+          ++tok;
+        }
+      }
 #pragma unroll
-      for (int j = 1; j < D / 8; j <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, j));
-      // 2^e of the largest magnitude; rows of zeros, tiny rows and rows that are not finite as they are
-      const uint32_t ex = __float_as_uint(most) & 0x7F800000u;
-      const bool plain = ex < (64u << 23) || ex == 0x7F800000u;
-      const float down = plain ? 1.f : __uint_as_float((254u << 23) - ex);
-      if (c == 0) s_qscale[qr] = plain ? 1.f : __uint_as_float(ex);
-      w = make_uint4(f16x2_bits(x[0] * down, x[1] * down), f16x2_bits(x[2] * down, x[3] * down), f16x2_bits(x[4] * down, x[5] * down),
-                     f16x2_bits(x[6] * down, x[7] * down));
-      const int rr = qr % kRowTile;
-      *reinterpret_cast<uint4*>(sQ + (qr / kRowTile) * C::QBytes + (c / 8) * (kRowTile * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = w;
+      for (int k = 0; k < Batch; ++k) {
+        const int qr = r0 + k * Step;
+        if (qr >= kBlockRows) break;
+        const uint4 w = in[k];
+        float x[8];
+        bf16x2_to_f32(w.x, x[0], x[1]);
+        bf16x2_to_f32(w.y, x[2], x[3]);
+        bf16x2_to_f32(w.z, x[4], x[5]);
+        bf16x2_to_f32(w.w, x[6], x[7]);
+        // the largest magnitude's exponent: bf16 magnitudes order as their bits
+        uint32_t most = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+#pragma unroll
+        for (int j = 1; j < D / 8; j <<= 1) most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, j));
+        // 2^e of it; rows of zeros, tiny rows and rows that are not finite as they are
+        const uint32_t ex = ::max(most << 16, most & 0xFFFF0000u) & 0x7F800000u;
+        const bool plain = ex < (64u << 23) || ex == 0x7F800000u;
+        const float down = plain ? 1.f : __uint_as_float((254u << 23) - ex);
+        if (c == 0) s_qscale[qr] = plain ? 1.f : __uint_as_float(ex);
+        const int rr = qr % kRowTile;
+        *reinterpret_cast<uint4*>(sQ + (qr / kRowTile) * C::QBytes + (c / 8) * (kRowTile * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+            make_uint4(f16x2_bits(x[0] * down, x[1] * down), f16x2_bits(x[2] * down, x[3] * down),
+                       f16x2_bits(x[4] * down, x[5] * down), f16x2_bits(x[6] * down, x[7] * down));
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -788,6 +815,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
             for (int k = 0; k < kStageKeys / 16; ++k)
               mma_ts_lo(o_cols, s_cols + k * 8, v0 + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), idesc_bf16(kRowTile, D), i > 0 || k != 0);
             mma_commit(&tile_empty[sv % kTiles]);
+            if (row_tiles == 1) mma_commit(&tile_empty[sv % kTiles]);  // (the barrier counts both issuers)
           }
           if (next) {
             const uint32_t k0 = t0 + (sk % kTiles) * (C::TileBytes >> 4);
@@ -798,6 +826,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
             }
             mma_commit(&s_full[t]);
             mma_commit(&tile_empty[sk % kTiles]);
+            if (row_tiles == 1) mma_commit(&tile_empty[sk % kTiles]);
           }
           if (row_tiles == 2) mbar_arrive(&turn[t ^ 1]);
         }
@@ -861,8 +890,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == Y::MmaWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  tmem_free();
 }
 
 int prefill_blocks(const fw_attn_q4_args& a) {
