@@ -9,12 +9,19 @@
 //
 // The block scales are taken out of the products: what enters the tensor
 // cores as their 16-row operand are the bare codes (keys in rows for s, dims in
-// rows for o), which bf16 holds exactly, and the query rows are the 8-column
-// operand, so a group of up to 8 rows wastes nothing. A nibble becomes bf16
-// 128 + c by one AND-OR with 0x4300 (after a shift; two values at once). For the keys the
-// offset is taken back in the accumulator's start (-136 sum q, one block of 32
-// long: exact enough in fp32); the values' sums run over the whole context,
-// where the offset would cancel badly, so 136 is subtracted exactly first.
+// rows for o), and the query rows are the 8-column operand, so a group of up to
+// 8 rows wastes nothing. The codes need no conversion: in a format whose
+// smallest numbers count up linearly from zero (subnormals, then the lowest
+// binade), the bits of a small whole number ARE that number of smallest steps.
+//   keys:   a nibble in its byte is the e4m3 number c 2^-9; one AND, or a shift
+//           and an AND, makes four of them. A query row, scaled by a power of
+//           two, is the exact sum of two e4m3 numbers an element.
+//   values: a nibble in its half word is the bf16 number c 2^-133 or, four bits
+//           up, 16 c 2^-133; the probabilities carry 2^64 to stay in range.
+// What the codes are too large by (8) is taken back by products as well: for
+// the keys one 16-step product of the scales with -8 sum q (in three bf16
+// parts), for the values one with the constant -8 in the codes' place -- in the
+// same accumulators right after, so that nothing grows before it cancels.
 //
 // Work: a unit is 128 keys of one (request, key/value head); the CTAs take
 // equal consecutive shares of all units, so that ragged lengths and few
@@ -37,12 +44,15 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kTeam = 4;          // warps of a stage (32 keys each); two teams take the stages in turn
 constexpr int kChunk = kThreads;  // requests scanned at a time
 constexpr float kLazy = 8.f;      // a row's maximum moves only when a score passes it by 2^8
+constexpr float kShift = 64.f;    // probabilities carry 2^64
+constexpr float kOScale = 590295810358705651712.f, kLScale = 1.f / 18446744073709551616.f;  // 2^69 = 2^(133 - 64), 2^-64
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int NB = D / kKvBlock, Rows = 8 * NT;
   static constexpr uint32_t StageBytes = kStageKeys * D * 9 / 8;
-  static constexpr int Stages = D == 128 ? 4 : 8;
+  static constexpr int Stages = D == 128 ? 4 : 8;  // even: a slot is always the same team's
+  static_assert(Stages % 2 == 0 && Stages <= kWarps, "see the ring's refills");
   static constexpr int Pitch = D + 4;  // floats between rows of the join buffer: its 16-byte accesses meet no bank twice
   static constexpr uint32_t JoinBytes = kWarps / 2 * 8 * Pitch * 4;
   static constexpr uint32_t QBytes = NT == 1 ? 0 : Rows * D * 2;
@@ -65,18 +75,23 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// nibbles j and j + 4 of a word -> bf16 pair 128 + c, in one shift and one
-// three-input logic operation: the mask has to sit in a register the compiler
-// takes for a variable, or it makes the last step two operations with constants
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j, uint32_t mask) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, 0x43004300, 0xEA;" : "=r"(r) : "r"(w >> (4 * j)), "r"(mask));
+__device__ __forceinline__ void mma16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// two floats -> two e4m3 bytes (lo in the low one), and back
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t minus136(uint32_t x) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x43084308u));
-  return r;
+__device__ __forceinline__ float2 e4m3x2_floats(uint32_t x) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   uint32_t r;
@@ -116,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
   __shared__ int s_len[kChunk], s_new[kChunk], s_tok[kChunk];
   __shared__ long long s_scan[kWarps];
   __shared__ float2 s_ml[kWarps][C::Rows];
-  __shared__ float s_qs[C::Rows][NB];        // several row tiles: -136 x a row's sums over the blocks
+  __shared__ float s_qz[C::Rows][NB];        // -8 x a row's sums over the blocks, in units of the products
+  __shared__ float s_qscale[C::Rows];        // what a row's products have to be multiplied by
   float* join = reinterpret_cast<float*>(smem + kStages * C::StageBytes);
   uint8_t* s_q = smem + kStages * C::StageBytes + C::JoinBytes;  // several row tiles: their query rows
   const fw_attn_q4_args& u = a.u;
@@ -189,9 +205,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
   const uint32_t at_v = blk0 + pl.vc + (at0 / 2 + q) * D + g * (NB * 4), at_vs = blk0 + pl.vs + (at0 / 2 + q) * (NB * 4);
   const uint32_t on_k = apart ? hb : 16 * (D / 2), on_ks = apart ? hb : 16 * NB * 2;
   const uint32_t on_v = apart ? hb : 8 * D, on_vs = apart ? hb : 8 * NB * 4;
-  uint32_t mask;
-  asm volatile("mov.u32 %0, 0x000F000F;" : "=r"(mask));
-
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // by a whole warp
     if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity))) {
@@ -260,15 +273,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                  &full[slot]);
       last_fill = j + 1;
     };
-    // the warps take turns at filling, kStages - 1 stages ahead
+    // The first kStages stages by a warp each; then the warps take turns: at the
+    // start of a stage of its team a warp refills the slot of its team's stage
+    // before. It has itself waited for that stage to be full: only so does
+    // the parity it waits for at `empty` name one phase (a warp that had not
+    // seen the slot's last phase could take the one before it for the next).
     const uint32_t it0 = it - from;  // the ring's count at this CTA's first unit
-    if (warp < kStages - 1 && from + warp < to) {
+    if (warp < kStages && from + warp < to) {
       look(from + warp);
       issue(it + warp);
     }
-    // the unit this warp fills next: at the end of the stage kStages - 1 before, one of its team's
     const int turn = 2 * (warp % kTeam) + warp / kTeam;
-    int next = from + kStages - 1 + ((turn - (int)it) & (kWarps - 1));
+    int next = (turn - (int)it) & (kWarps - 1);
+    next += from + kStages - 2 + (next < 2 ? kWarps : 0);  // the unit this warp fills next, kStages - 2 stages ahead of the stage it is at
     look(next);
 
     for (int x = from; x < to; ++k) {
@@ -284,44 +301,86 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
         const int head = (x - p0) / n_st, st0 = x - p0 - head * n_st;
         const int n_here = ::min(n_st - st0, stop - x);
         // Query rows as the 8-column operand: thread (g, q) holds row g's dims
-        // 32 b + 8 q .. + 7. One tile of rows stays in registers, two in shared
-        // memory. qs: -136 x the sums of rows 2 q and 2 q + 1 over block b.
-        auto load_q = [&](int row, int b) {
+        // 32 b + 8 q .. + 7 in two e4m3 parts, bytes in the order of the codes'.
+        // One tile of rows stays in registers, two in shared memory.
+        auto load_q = [&](int row, int b, float (&x)[8]) {
           uint4 w = make_uint4(0, 0, 0, 0);
           if (row < rows)
             w = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)u.q + (int64_t)(tok0 + row / G) * u.q_stride +
                                                 (head * G + row % G) * D + 32 * b + 8 * q);
-          return w;
+          bf16x2_to_f32(w.x, x[0], x[1]);
+          bf16x2_to_f32(w.y, x[2], x[3]);
+          bf16x2_to_f32(w.z, x[4], x[5]);
+          bf16x2_to_f32(w.w, x[6], x[7]);
         };
-        auto sum8 = [&](uint4 w) {
-          float s = 0.f, lo, hi;
-          for (uint32_t x : {w.x, w.y, w.z, w.w}) {
-            bf16x2_to_f32(x, lo, hi);
-            s += lo + hi;
-          }
-          s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-          s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-          return s * -136.f;
-        };
-        uint4 qf[NT == 1 ? NB : 1];
-        float qs[NT == 1 ? NB : 1][2];
-        if constexpr (NT == 1) {
+        auto tile_q = [&](int t, uint4 (&qf)[NB]) {  // by a whole warp
+          float x[NB][8], most = 0.f;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            qf[b] = load_q(g, b);
-            const float s = sum8(qf[b]);
-            qs[b][0] = __shfl_sync(0xFFFFFFFFu, s, 8 * q);
-            qs[b][1] = __shfl_sync(0xFFFFFFFFu, s, 8 * q + 4);
+            load_q(8 * t + g, b, x[b]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) most = max_nan(most, fabsf(x[b][i]));
           }
-        } else {  // (the previous segment's last barrier lies behind)
-          for (int e = warp; e < NT * NB; e += kWarps) {
-            const int t = e / NB, b = e % NB;
-            const uint4 w = load_q(8 * t + g, b);
-            const float s = sum8(w);
-            *reinterpret_cast<uint4*>(s_q + (e * 32 + lane) * 16) = w;
-            if (q == 0) s_qs[8 * t + g][b] = s;
+          most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+          most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+          // to a largest magnitude of 128 .. 256: all of bf16's 8 bits in two
+          // parts of 4, down to 2^-9 of it, and an error of 2^-17 of it below
+          const uint32_t ex = __float_as_uint(most) >> 23 & 0xFF;
+          const float up = ex >= 16 && ex < 240 ? __uint_as_float((261u - ex) << 23) : 1.f;
+          float z[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            uint32_t part[2][4];
+            z[b] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // byte pairs (0, 4), (1, 5), (2, 6), (3, 7)
+              const float lo = x[b][i] * up, hi = x[b][i + 4] * up;
+              part[0][i] = e4m3x2(lo, hi);
+              const float2 a = e4m3x2_floats(part[0][i]);
+              part[1][i] = e4m3x2(lo - a.x, hi - a.y);
+              const float2 c = e4m3x2_floats(part[1][i]);
+              z[b] += (a.x + c.x) + (a.y + c.y);
+            }
+            qf[b] = make_uint4(part[0][0] | part[0][1] << 16, part[0][2] | part[0][3] << 16, part[1][0] | part[1][1] << 16,
+                               part[1][2] | part[1][3] << 16);
+            z[b] += __shfl_xor_sync(0xFFFFFFFFu, z[b], 1);
+            z[b] += __shfl_xor_sync(0xFFFFFFFFu, z[b], 2);
           }
-          __syncthreads();
+          // (saturating, the parts lose what is not finite: such a row's products are all NaN)
+          const float f = ex == 255 ? __uint_as_float(0x7FC00000u) : a.scale_log2 * 512.f / up;
+          if (q == 0) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) s_qz[8 * t + g][b] = z[b] * (-8.f / 512.f);
+            s_qscale[8 * t + g] = f;
+          }
+        };
+        uint4 qf[NT == 1 ? NB : 1];
+        __syncthreads();  // (the previous segment's are no longer read)
+        if constexpr (NT == 1) {
+          tile_q(0, qf);  // every warp for itself; what they write is the same
+        } else if (warp < NT) {
+          uint4 w[NB];
+          tile_q(warp, w);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) *reinterpret_cast<uint4*>(s_q + ((warp * NB + b) * 32 + lane) * 16) = w[b];
+        }
+        __syncthreads();
+        // the three bf16 parts of row g's z as a 16-step operand: step k holds
+        // part k / NB of block k % NB; rows 2 q, 2 q + 1's factors
+        uint32_t qz[NT][2];
+        float qscale[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          auto part = [&](int k) {
+            if (k >= 3 * NB) return 0.f;
+            float x = s_qz[8 * t + g][k % NB];
+            for (int i = 0; i < k / NB; ++i) x -= __bfloat162float(__float2bfloat16_rn(x));
+            return x;
+          };
+          qz[t][0] = bf16x2_bits(part(2 * q), part(2 * q + 1));
+          qz[t][1] = bf16x2_bits(part(2 * q + 8), part(2 * q + 9));
+          qscale[t][0] = s_qscale[8 * t + 2 * q];
+          qscale[t][1] = s_qscale[8 * t + 2 * q + 1];
         }
         int pos[NT][2];  // positions of rows 2 q, 2 q + 1 (rows past the last: none)
 #pragma unroll
@@ -331,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
             const int row2 = 8 * t + 2 * q + i;
             pos[t][i] = row2 < rows ? first + row2 / G : -1;
           }
-        // mz: a row's maximum (0 before there is one); lim: what a score may
-        // pass it by before it moves (-inf: there is none yet)
+        // mz: a row's maximum less 64 (0 before there is one); lim: what a score
+        // may pass it by before it moves (-inf: there is none yet)
         float o[NT][NB][2][4] = {}, mz[NT][2], lim[NT][2], l[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) mz[t][0] = mz[t][1] = l[t][0] = l[t][1] = 0.f, lim[t][0] = lim[t][1] = -INFINITY;
@@ -351,30 +410,28 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
           for (int h = 0; h < U; ++h) {
             const Words<NB> k0 = lds<NB, 0>(in_k + h * on_k), k1 = lds<NB, 8 * (D / 2)>(in_k + h * on_k);
             const Words<NB / 2> d0 = lds<NB / 2, 0>(in_ks + h * on_ks), d1 = lds<NB / 2, 8 * NB * 2>(in_ks + h * on_ks);
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t z0 = NB == 4 && (q & 1) ? d0.w[NB / 2 - 1] : d0.w[0], z1 = NB == 4 && (q & 1) ? d1.w[NB / 2 - 1] : d1.w[0];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(s[h][t], z0, z1, z0, z1, qz[t][0], qz[t][1], zero);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               const float e0 = __uint_as_float(b & 1 ? d0.w[b / 2] & 0xFFFF0000u : d0.w[b / 2] << 16);
               const float e1 = __uint_as_float(b & 1 ? d1.w[b / 2] & 0xFFFF0000u : d1.w[b / 2] << 16);
-              uint32_t x0[4], x1[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) x0[j] = code_pair(k0.w[b], j, mask), x1[j] = code_pair(k1.w[b], j, mask);
+              const uint32_t lo0 = k0.w[b] & 0x0F0F0F0Fu, hi0 = k0.w[b] >> 4 & 0x0F0F0F0Fu;
+              const uint32_t lo1 = k1.w[b] & 0x0F0F0F0Fu, hi1 = k1.w[b] >> 4 & 0x0F0F0F0Fu;
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 uint4 w;
-                float z0, z1;
-                if constexpr (NT == 1) {
-                  w = qf[b], z0 = qs[b][0], z1 = qs[b][1];
-                } else {
+                if constexpr (NT == 1)
+                  w = qf[b];
+                else
                   w = *reinterpret_cast<const uint4*>(s_q + ((t * NB + b) * 32 + lane) * 16);
-                  z0 = s_qs[8 * t + 2 * q][b], z1 = s_qs[8 * t + 2 * q + 1][b];
-                }
-                const float c0[4] = {z0, z1, z0, z1};
                 float c[4];
-                mma16816(c, x0[0], x1[0], x0[1], x1[1], w.x, w.y, c0);
-                mma16816(c, x0[2], x1[2], x0[3], x1[3], w.z, w.w, c);
+                mma16832(c, lo0, lo1, hi0, hi1, w.x, w.y, zero);
+                mma16832(c, lo0, lo1, hi0, hi1, w.z, w.w, c);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  s[h][t][e] = b == 0 ? c[e] * (e < 2 ? e0 : e1) : fmaf(c[e], e < 2 ? e0 : e1, s[h][t][e]);
+                for (int e = 0; e < 4; ++e) s[h][t][e] = fmaf(c[e], e < 2 ? e0 : e1, s[h][t][e]);
               }
             }
           }
@@ -386,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                s[h][t][e] = fmaf(s[h][t][e], a.scale_log2, -mz[t][e & 1]);
+                s[h][t][e] = fmaf(s[h][t][e], qscale[t][e & 1], -mz[t][e & 1]);
                 if (kEdge && !sees(pos[t][e & 1], key0 + 16 * h + g + 8 * (e >> 1), u.window, u.sinks)) s[h][t][e] = -INFINITY;
                 moves |= s[h][t][e] > lim[t][e & 1];
               }
@@ -400,11 +457,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, d));
                 // a first maximum is taken as it is, a later one only moves up
+                up -= kShift;
                 if (lim[t][j] != -INFINITY) up = fmaxf(up, 0.f);
-                if (up == -INFINITY) continue;
-                const float keep = lim[t][j] == -INFINITY ? 0.f : exp2_fast(-up);
+                const bool none = up == -INFINITY;  // (nothing seen yet: all stays as it is)
+                up = none ? 0.f : up;
+                const float keep = none ? 1.f : lim[t][j] == -INFINITY ? 0.f : exp2_fast(-up);
                 mz[t][j] += up;
-                lim[t][j] = kLazy;
+                lim[t][j] = none ? lim[t][j] : kShift + kLazy;
                 l[t][j] *= keep;
 #pragma unroll
                 for (int h = 0; h < U; ++h) {
@@ -464,11 +523,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                 }
               }
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t a0 = minus136(code_pair(v0.w[b], 2 * e, mask)), a1 = minus136(code_pair(v0.w[b], 2 * e + 1, mask));
-                const uint32_t a2 = minus136(code_pair(v1.w[b], 2 * e, mask)), a3 = minus136(code_pair(v1.w[b], 2 * e + 1, mask));
+              for (int e = 0; e < 2; ++e) {  // dims 2 e of the lane's four (x 1) in rows g, 2 e + 1 (x 16) in rows g + 8
+                const uint32_t x0 = e ? v0.w[b] >> 8 : v0.w[b], x1 = e ? v1.w[b] >> 8 : v1.w[b];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma16816(o[t][b][e], a0, a1, a2, a3, w0[t], w1[t], o[t][b][e]);
+                for (int t = 0; t < NT; ++t) {
+                  mma16816(o[t][b][e], x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u, w0[t], w1[t], o[t][b][e]);
+                  mma16816(o[t][b][e], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w0[t], w1[t], o[t][b][e]);  // -8, -8 x 16
+                }
               }
             }
           }
@@ -482,6 +543,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
           const uint32_t j = it + i;
           const int slot = j % kStages;
           wait(&full[slot], (j / kStages) & 1);
+          if (x + i + kStages - 2 == next && next < to) {
+            issue(it0 + next);
+            next += kWarps;
+            look(next);
+          }
           const int key0 = v.block(st0 + i) * kStageKeys + key_w;
           const uint32_t have = ok ? s_have[slot] >> (key_w / 16) & 3 : 0, stage = slot * C::StageBytes;
           if (NT == 1 && have == 3 && key0 + 31 <= first && key0 >= lo_edge) {
@@ -499,12 +565,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[slot]);
-          // this warp's turn: the slot of the stage before, which the other team has left by now
-          if (x + i + kStages - 1 == next && next < to) {
-            issue(it0 + next);
-            next += kWarps;
-            look(next);
-          }
         }
         it += n_here;
 
@@ -516,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[t][j] += __shfl_xor_sync(0xFFFFFFFFu, l[t][j], d);
             const float m = lim[t][j] == -INFINITY ? -INFINITY : mz[t][j];
-            if (g == 0) s_ml[warp][8 * t + 2 * q + j] = make_float2(m, l[t][j]);
+            if (g == 0) s_ml[warp][8 * t + 2 * q + j] = make_float2(m, l[t][j] * kLScale);
           }
         __syncthreads();
         const bool whole = n_here == n_st;
@@ -533,11 +593,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][row].x);
-                const float f = lim[t][j] == -INFINITY ? 0.f : exp2_fast(mz[t][j] - top);
+                const float f = lim[t][j] == -INFINITY ? 0.f : exp2_fast(mz[t][j] - top) * kOScale, f16 = f * 0.0625f;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                   float4* at = reinterpret_cast<float4*>(join + ((warp % (kWarps / 2)) * 8 + 2 * q + j) * C::Pitch + 32 * b + 4 * g);
-                  float4 y = make_float4(o[t][b][0][j] * f, o[t][b][0][j + 2] * f, o[t][b][1][j] * f, o[t][b][1][j + 2] * f);
+                  float4 y = make_float4(o[t][b][0][j] * f, o[t][b][0][j + 2] * f16, o[t][b][1][j] * f, o[t][b][1][j + 2] * f16);
                   if (half == 0) {
                     const float4 z = *at;
                     y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;

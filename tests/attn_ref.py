@@ -34,21 +34,24 @@ def page_bytes(page, D):
     return page * D * 9 // 8
 
 
-def write_block(block, page, D, at, which, codes, scale_bits):
-    """Stores one position's D codes and D / 32 scale words (bf16 bits) into a uint8 (page, head) block."""
-    nb = D // 32
+def places(page, D, which, at):
+    """Where positions `at` (array, places in a page) lie in a (page, head) block: nibble indexes of their D codes, byte indexes of their scales."""
+    nb, at = D // 32, np.asarray(at)[..., None]
     d = np.arange(D)
     b, r = d // 32, d % 32
     if which == "k":
-        byte_nib = 2 * (at * (D // 2) + ((r // 8) * nb + b) * 4) + (r % 8) // 2 + 4 * (r % 2)
-        scale_at = page * D // 2 + 2 * (at * nb + np.arange(nb))
-    else:
-        base = page * D // 2 + page * nb * 2
-        byte_nib = 2 * (base + (at // 2) * D + ((r // 4) * nb + b) * 4) + r % 4 + 4 * (at % 2)
-        scale_at = base + page * D // 2 + 4 * ((at // 2) * nb + np.arange(nb)) + 2 * (at % 2)
-    shift = 4 * (byte_nib % 2)
-    np.bitwise_and.at(block, byte_nib // 2, (0xF0 >> shift).astype(np.uint8))
-    np.bitwise_or.at(block, byte_nib // 2, (codes << shift).astype(np.uint8))
+        return 2 * (at * (D // 2) + ((r // 8) * nb + b) * 4) + (r % 8) // 2 + 4 * (r % 2), page * D // 2 + 2 * (at * nb + np.arange(nb))
+    base = page * D // 2 + page * nb * 2
+    return (2 * (base + (at // 2) * D + ((r // 4) * nb + b) * 4) + r % 4 + 4 * (at % 2),
+            base + page * D // 2 + 4 * ((at // 2) * nb + np.arange(nb)) + 2 * (at % 2))
+
+
+def write_block(block, page, D, at, which, codes, scale_bits):
+    """Stores one position's D codes and D / 32 scale words (bf16 bits) into a uint8 (page, head) block."""
+    nibble, scale_at = places(page, D, which, at)
+    shift = 4 * (nibble % 2)
+    np.bitwise_and.at(block, nibble // 2, (0xF0 >> shift).astype(np.uint8))
+    np.bitwise_or.at(block, nibble // 2, (codes << shift).astype(np.uint8))
     block[scale_at], block[scale_at + 1] = scale_bits & 0xFF, scale_bits >> 8
 
 
@@ -134,7 +137,11 @@ class Case:
         self.max_blocks = max(need + [1]) + 1
         table = np.full((len(lens), self.max_blocks), -1, np.int32)
         # what no request owns is garbage: 0xFF.. scales are NaN
-        cache = np.full((n_pages, n_kv, page_bytes(page, D)), 0xFF if fill is None else fill, np.uint8)
+        byte = 0xFF if fill is None else fill
+        nibbles = np.empty((n_pages, n_kv, page_bytes(page, D), 2), np.uint8)
+        nibbles[..., 0], nibbles[..., 1] = byte & 15, byte >> 4
+        flat = nibbles.reshape(n_pages, n_kv, -1)
+        heads = np.arange(n_kv)[None, :, None]
         self.k, self.v, at = [], [], 0
         for r, (S, _) in enumerate(lens):
             table[r, :need[r]] = order[at:at + need[r]]
@@ -144,16 +151,18 @@ class Case:
                 x = torch.from_numpy(rng.standard_normal((S, n_kv, D))).to(torch.bfloat16).double().numpy()
                 c, d = quantise(x)
                 bits = bf16_bits(d)
-                for j in range(S):
-                    for h in range(n_kv):
-                        write_block(cache[table[r, j // page], h], page, D, j % page, which, c[j, h], bits[j, h])
+                j = np.arange(S)
+                pages, (nibble, scale_at) = table[r, j // page][:, None, None], places(page, D, which, j % page)
+                flat[pages, heads, nibble[:, None]] = c
+                for n in range(4):
+                    flat[pages, heads, 2 * scale_at[:, None] + n] = bits >> (4 * n) & 15
                 kv.append(values(c, d).reshape(x.shape))
             self.k.append(kv[0])
             self.v.append(kv[1])
         starts = np.concatenate([[0], np.cumsum([n for _, n in lens])]).astype(np.int32)
         self.T, self.max_q = int(starts[-1]), max([n for _, n in lens] + [0])
         self.q = torch.from_numpy(q_gain * rng.standard_normal((self.T, n_q, D))).to(torch.bfloat16)
-        self.table, self.starts, self.cache = table, starts, cache
+        self.table, self.starts, self.cache = table, starts, nibbles[..., 0] | nibbles[..., 1] << 4
         self.seq = np.array([s for s, _ in lens], np.int32)
 
     def device(self, dev="cuda"):

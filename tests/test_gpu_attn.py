@@ -357,6 +357,25 @@ def test_attn_same_bits_every_time_and_on_other_streams(new):
     assert all(torch.equal(first, g) for g in got)
 
 
+@pytest.mark.parametrize("n_q, n_kv, D, page, new", [(8, 8, 64, 16, 1), (16, 4, 128, 64, 1), (8, 4, 128, 32, 5), (32, 2, 128, 128, 1)])
+def test_attn_many_segments_many_calls(n_q, n_kv, D, page, new):
+    """Many more 128-key units than CTAs, so that a CTA takes several heads and
+    requests in a row, and many calls without a wait between them."""
+    rng = np.random.default_rng(n_q)
+    c = ref.Case([(int(s), new) for s in rng.integers(new, 2600 if D == 128 else 1200, 60)], n_q, n_kv, D, page, seed=4)
+    first = check_attn(c)
+    d = c.device()
+    args = (d["q"], d["cache"], d["block_table"], d["q_start"], d["seq_lens"], c.max_q)
+    got = [fw.attn_q4(*args) for _ in range(200)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, g) for g in got)
+
+
+def test_attn_long_contexts():
+    """A few long contexts: many units in a row of one head, split over many CTAs."""
+    check_attn(ref.Case([(20000, 1), (9000, 2), (13001, 1)], 8, 2, 128, 128, seed=12))
+
+
 def test_attn_in_a_cuda_graph():
     c = ref.Case([(500, 1), (100, 1), (300, 40)], 8, 2, 128, 16, seed=10)
     d = c.device()
