@@ -10,18 +10,19 @@
 // The block scales are taken out of the products: what enters the tensor
 // cores as their 16-row operand are the bare codes (keys in rows for s, dims in
 // rows for o), and the query rows are the 8-column operand, so a group of up to
-// 8 rows wastes nothing. The codes need no conversion: in a format whose
-// smallest numbers count up linearly from zero (subnormals, then the lowest
-// binade), the bits of a small whole number ARE that number of smallest steps.
-//   keys:   a nibble in its byte is the e4m3 number c 2^-9; one AND, or a shift
-//           and an AND, makes four of them. A query row, scaled by a power of
-//           two, is the exact sum of two e4m3 numbers an element.
-//   values: a nibble in its half word is the bf16 number c 2^-133 or, four bits
-//           up, 16 c 2^-133; the probabilities carry 2^64 to stay in range.
+// 8 rows wastes nothing. The codes need no conversion: bf16's smallest numbers
+// count up linearly from zero (the subnormals, then the lowest binade), so the
+// bits of a whole number c < 256 ARE the bf16 number c 2^-133. A nibble of a
+// word's halves is c 2^-133 or, four bits up, 16 c 2^-133: one AND for two of
+// them, and one shift for the other four. The other operand makes up for it: the queries are
+// multiplied by 2^64 (or 2^60), the probabilities carry 2^64.
 // What the codes are too large by (8) is taken back by products as well: for
 // the keys one 16-step product of the scales with -8 sum q (in three bf16
 // parts), for the values one with the constant -8 in the codes' place -- in the
 // same accumulators right after, so that nothing grows before it cancels.
+// (e4m3, whose smallest numbers do the same for bytes, needs fewer operations
+// on paper; but this GPU turns 8-bit mma.sync operands into f16 by further
+// instructions: 446 instead of 359 of them for 16 keys.)
 //
 // Work: a unit is 128 keys of one (request, key/value head); the CTAs take
 // equal consecutive shares of all units, so that ragged lengths and few
@@ -46,13 +47,14 @@ constexpr int kChunk = kThreads;  // requests scanned at a time
 constexpr float kLazy = 8.f;      // a row's maximum moves only when a score passes it by 2^8
 constexpr float kShift = 64.f;    // probabilities carry 2^64
 constexpr float kOScale = 590295810358705651712.f, kLScale = 1.f / 18446744073709551616.f;  // 2^69 = 2^(133 - 64), 2^-64
+constexpr uint32_t kQUp = 0x5F805F80u, kQUp16 = 0x5D805D80u;  // bf16 pairs of 2^64, 2^60
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int NB = D / kKvBlock, Rows = 8 * NT;
   static constexpr uint32_t StageBytes = kStageKeys * D * 9 / 8;
   static constexpr int Stages = D == 128 ? 4 : 8;  // even: a slot is always the same team's
-  static_assert(Stages % 2 == 0 && Stages <= kWarps, "see the ring's refills");
+  static_assert(Stages % 2 == 0 && Stages <= kWarps, "see the ring");
   static constexpr int Pitch = D + 4;  // floats between rows of the join buffer: its 16-byte accesses meet no bank twice
   static constexpr uint32_t JoinBytes = kWarps / 2 * 8 * Pitch * 4;
   static constexpr uint32_t QBytes = NT == 1 ? 0 : Rows * D * 2;
@@ -75,24 +77,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-__device__ __forceinline__ void mma16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, const float (&c)[4]) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
-// two floats -> two e4m3 bytes (lo in the low one), and back
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 e4m3x2_floats(uint32_t x) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
@@ -103,6 +87,24 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+__device__ __forceinline__ void add_release(uint32_t* p) {
+  asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(p)) : "memory");
+}
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
+  uint32_t r;
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(r) : "r"(smem_u32(p)) : "memory");
+  return r;
+}
+// Bounded wait for a count to reach n. false = gave up.
+__device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t n) {
+  if ((int)(load_acquire(p) - n) >= 0) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if ((int)(load_acquire(p) - n) >= 0) return true;
+    if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
 template <int N>
 struct Words {
   uint32_t w[N];
@@ -125,14 +127,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
   using C = Cfg<D, NT>;
   constexpr int NB = C::NB, kStages = C::Stages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+  __shared__ __align__(8) uint64_t full[kStages];
+  __shared__ uint32_t s_left[kStages];       // how often a warp has left the slot
   __shared__ uint32_t s_have[kStages];       // bit w: the stage's keys 16 w .. 16 w + 15 are there
   __shared__ int s_pref[kChunk + 1];         // units before each request of the chunk, from this CTA's first one on
   __shared__ int s_len[kChunk], s_new[kChunk], s_tok[kChunk];
   __shared__ long long s_scan[kWarps];
   __shared__ float2 s_ml[kWarps][C::Rows];
   __shared__ float s_qz[C::Rows][NB];        // -8 x a row's sums over the blocks, in units of the products
-  __shared__ float s_qscale[C::Rows];        // what a row's products have to be multiplied by
   float* join = reinterpret_cast<float*>(smem + kStages * C::StageBytes);
   uint8_t* s_q = smem + kStages * C::StageBytes + C::JoinBytes;  // several row tiles: their query rows
   const fw_attn_q4_args& u = a.u;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kTeam);
+      s_left[i] = 0;
     }
     fence_mbar_init();
     a.rec[blockIdx.x].parts = 0;
@@ -205,6 +207,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
   const uint32_t at_v = blk0 + pl.vc + (at0 / 2 + q) * D + g * (NB * 4), at_vs = blk0 + pl.vs + (at0 / 2 + q) * (NB * 4);
   const uint32_t on_k = apart ? hb : 16 * (D / 2), on_ks = apart ? hb : 16 * NB * 2;
   const uint32_t on_v = apart ? hb : 8 * D, on_vs = apart ? hb : 8 * NB * 4;
+  // -8 and -8 x 16 as the values' operand, in registers that the compiler does not fill anew for every use
+  uint32_t off[4];
+  asm volatile("mov.u32 %0, 0x80088008;\n\tmov.u32 %1, 0x80808080;\n\tmov.u32 %2, 0x80088008;\n\tmov.u32 %3, 0x80808080;"
+               : "=r"(off[0]), "=r"(off[1]), "=r"(off[2]), "=r"(off[3]));
+
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // by a whole warp
     if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity))) {
@@ -258,7 +265,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
         raise(u.status, FW_KV_BAD_SLOT);
       }
       const uint32_t got = __ballot_sync(0xFFFFFFFFu, copy);
-      wait(&empty[slot], ((j / kStages) & 1) ^ 1);
+      // all readers of the slot's stages before have left it. A count, not a
+      // barrier's parity: this warp need not have seen the phases before, and
+      // two phases apart look alike.
+      if (ok && !__all_sync(0xFFFFFFFFu, wait_count(&s_left[slot], kTeam * (j / kStages)))) {
+        ok = false;
+        raise(u.status, FW_KV_TIMEOUT);
+      }
       if (!ok) return;
       if (lane == 0) {
         uint32_t have = 0;  // a page's bit, for each 16 keys of it
@@ -273,19 +286,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                  &full[slot]);
       last_fill = j + 1;
     };
-    // The first kStages stages by a warp each; then the warps take turns: at the
-    // start of a stage of its team a warp refills the slot of its team's stage
-    // before. It has itself waited for that stage to be full: only so does
-    // the parity it waits for at `empty` name one phase (a warp that had not
-    // seen the slot's last phase could take the one before it for the next).
+    // the warps take turns at filling, kStages - 1 stages ahead
     const uint32_t it0 = it - from;  // the ring's count at this CTA's first unit
-    if (warp < kStages && from + warp < to) {
+    if (warp < kStages - 1 && from + warp < to) {
       look(from + warp);
       issue(it + warp);
     }
+    // the unit this warp fills next: at the end of the stage kStages - 1 before, one of its team's
     const int turn = 2 * (warp % kTeam) + warp / kTeam;
-    int next = (turn - (int)it) & (kWarps - 1);
-    next += from + kStages - 2 + (next < 2 ? kWarps : 0);  // the unit this warp fills next, kStages - 2 stages ahead of the stage it is at
+    int next = from + kStages - 1 + ((turn - (int)it) & (kWarps - 1));
     look(next);
 
     for (int x = from; x < to; ++k) {
@@ -301,57 +310,25 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
         const int head = (x - p0) / n_st, st0 = x - p0 - head * n_st;
         const int n_here = ::min(n_st - st0, stop - x);
         // Query rows as the 8-column operand: thread (g, q) holds row g's dims
-        // 32 b + 8 q .. + 7 in two e4m3 parts, bytes in the order of the codes'.
-        // One tile of rows stays in registers, two in shared memory.
-        auto load_q = [&](int row, int b, float (&x)[8]) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (row < rows)
-            w = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)u.q + (int64_t)(tok0 + row / G) * u.q_stride +
-                                                (head * G + row % G) * D + 32 * b + 8 * q);
-          bf16x2_to_f32(w.x, x[0], x[1]);
-          bf16x2_to_f32(w.y, x[2], x[3]);
-          bf16x2_to_f32(w.z, x[4], x[5]);
-          bf16x2_to_f32(w.w, x[6], x[7]);
-        };
+        // 32 b + 8 q .. + 7, those of the upper nibbles a sixteenth. One tile of
+        // rows stays in registers, two in shared memory.
         auto tile_q = [&](int t, uint4 (&qf)[NB]) {  // by a whole warp
-          float x[NB][8], most = 0.f;
+          const int row = 8 * t + g;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            load_q(8 * t + g, b, x[b]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) most = max_nan(most, fabsf(x[b][i]));
-          }
-          most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-          most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-          // to a largest magnitude of 128 .. 256: all of bf16's 8 bits in two
-          // parts of 4, down to 2^-9 of it, and an error of 2^-17 of it below
-          const uint32_t ex = __float_as_uint(most) >> 23 & 0xFF;
-          const float up = ex >= 16 && ex < 240 ? __uint_as_float((261u - ex) << 23) : 1.f;
-          float z[NB];
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            uint32_t part[2][4];
-            z[b] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // byte pairs (0, 4), (1, 5), (2, 6), (3, 7)
-              const float lo = x[b][i] * up, hi = x[b][i + 4] * up;
-              part[0][i] = e4m3x2(lo, hi);
-              const float2 a = e4m3x2_floats(part[0][i]);
-              part[1][i] = e4m3x2(lo - a.x, hi - a.y);
-              const float2 c = e4m3x2_floats(part[1][i]);
-              z[b] += (a.x + c.x) + (a.y + c.y);
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row < rows)
+              w = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)u.q + (int64_t)(tok0 + row / G) * u.q_stride +
+                                                  (head * G + row % G) * D + 32 * b + 8 * q);
+            float z = 0.f, lo, hi;
+            for (uint32_t x : {w.x, w.y, w.z, w.w}) {
+              bf16x2_to_f32(x, lo, hi);
+              z += lo + hi;
             }
-            qf[b] = make_uint4(part[0][0] | part[0][1] << 16, part[0][2] | part[0][3] << 16, part[1][0] | part[1][1] << 16,
-                               part[1][2] | part[1][3] << 16);
-            z[b] += __shfl_xor_sync(0xFFFFFFFFu, z[b], 1);
-            z[b] += __shfl_xor_sync(0xFFFFFFFFu, z[b], 2);
-          }
-          // (saturating, the parts lose what is not finite: such a row's products are all NaN)
-          const float f = ex == 255 ? __uint_as_float(0x7FC00000u) : a.scale_log2 * 512.f / up;
-          if (q == 0) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) s_qz[8 * t + g][b] = z[b] * (-8.f / 512.f);
-            s_qscale[8 * t + g] = f;
+            z += __shfl_xor_sync(0xFFFFFFFFu, z, 1);
+            z += __shfl_xor_sync(0xFFFFFFFFu, z, 2);
+            if (q == 0) s_qz[row][b] = z * (-8.f / kOScale);
+            qf[b] = make_uint4(mul_bf16x2(w.x, kQUp), mul_bf16x2(w.y, kQUp16), mul_bf16x2(w.z, kQUp), mul_bf16x2(w.w, kQUp16));
           }
         };
         uint4 qf[NT == 1 ? NB : 1];
@@ -366,9 +343,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
         }
         __syncthreads();
         // the three bf16 parts of row g's z as a 16-step operand: step k holds
-        // part k / NB of block k % NB; rows 2 q, 2 q + 1's factors
+        // part k / NB of block k % NB
         uint32_t qz[NT][2];
-        float qscale[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           auto part = [&](int k) {
@@ -379,47 +355,34 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
           };
           qz[t][0] = bf16x2_bits(part(2 * q), part(2 * q + 1));
           qz[t][1] = bf16x2_bits(part(2 * q + 8), part(2 * q + 9));
-          qscale[t][0] = s_qscale[8 * t + 2 * q];
-          qscale[t][1] = s_qscale[8 * t + 2 * q + 1];
         }
-        int pos[NT][2];  // positions of rows 2 q, 2 q + 1 (rows past the last: none)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row2 = 8 * t + 2 * q + i;
-            pos[t][i] = row2 < rows ? first + row2 / G : -1;
-          }
+        auto position = [&](int row) { return row < rows ? first + row / G : -1; };  // (rows past the last see nothing)
         // mz: a row's maximum less 64 (0 before there is one); lim: what a score
         // may pass it by before it moves (-inf: there is none yet)
         float o[NT][NB][2][4] = {}, mz[NT][2], lim[NT][2], l[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) mz[t][0] = mz[t][1] = l[t][0] = l[t][1] = 0.f, lim[t][0] = lim[t][1] = -INFINITY;
 
-        // 16 keys of this warp, or its 32 at once (U = 2: twice the independent
-        // work). kEdge: not every row sees all of them (the last keys, the
-        // window's edge); `stage`: byte offset of their stage, `second`: the
-        // keys are the second 16.
-        auto keys = [&](auto count, auto edge, uint32_t stage, bool second, int key0) {
-          constexpr int U = decltype(count)::value;
+        // 16 keys of this warp. kEdge: not every row sees all of them (the last
+        // keys, the window's edge); `stage`: byte offset of their stage,
+        // `second`: the keys are the second 16 of the warp's 32.
+        auto keys = [&](auto edge, uint32_t stage, bool second, int key0) {
           constexpr bool kEdge = decltype(edge)::value;
           const uint32_t in_k = at_k + stage + (second ? on_k : 0), in_ks = at_ks + stage + (second ? on_ks : 0);
           const uint32_t in_v = at_v + stage + (second ? on_v : 0), in_vs = at_vs + stage + (second ? on_vs : 0);
-          float s[U][NT][4];
-#pragma unroll
-          for (int h = 0; h < U; ++h) {
-            const Words<NB> k0 = lds<NB, 0>(in_k + h * on_k), k1 = lds<NB, 8 * (D / 2)>(in_k + h * on_k);
-            const Words<NB / 2> d0 = lds<NB / 2, 0>(in_ks + h * on_ks), d1 = lds<NB / 2, 8 * NB * 2>(in_ks + h * on_ks);
+          float s[NT][4];
+          {
+            const Words<NB> k0 = lds<NB, 0>(in_k), k1 = lds<NB, 8 * (D / 2)>(in_k);
+            const Words<NB / 2> d0 = lds<NB / 2, 0>(in_ks), d1 = lds<NB / 2, 8 * NB * 2>(in_ks);
             const float zero[4] = {0.f, 0.f, 0.f, 0.f};
             const uint32_t z0 = NB == 4 && (q & 1) ? d0.w[NB / 2 - 1] : d0.w[0], z1 = NB == 4 && (q & 1) ? d1.w[NB / 2 - 1] : d1.w[0];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(s[h][t], z0, z1, z0, z1, qz[t][0], qz[t][1], zero);
+            for (int t = 0; t < NT; ++t) mma16816(s[t], z0, z1, z0, z1, qz[t][0], qz[t][1], zero);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               const float e0 = __uint_as_float(b & 1 ? d0.w[b / 2] & 0xFFFF0000u : d0.w[b / 2] << 16);
               const float e1 = __uint_as_float(b & 1 ? d1.w[b / 2] & 0xFFFF0000u : d1.w[b / 2] << 16);
-              const uint32_t lo0 = k0.w[b] & 0x0F0F0F0Fu, hi0 = k0.w[b] >> 4 & 0x0F0F0F0Fu;
-              const uint32_t lo1 = k1.w[b] & 0x0F0F0F0Fu, hi1 = k1.w[b] >> 4 & 0x0F0F0F0Fu;
+              const uint32_t x0 = k0.w[b], x1 = k1.w[b], y0 = x0 >> 8, y1 = x1 >> 8;
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 uint4 w;
@@ -428,32 +391,29 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                 else
                   w = *reinterpret_cast<const uint4*>(s_q + ((t * NB + b) * 32 + lane) * 16);
                 float c[4];
-                mma16832(c, lo0, lo1, hi0, hi1, w.x, w.y, zero);
-                mma16832(c, lo0, lo1, hi0, hi1, w.z, w.w, c);
+                mma16816(c, x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u, w.x, w.y, zero);
+                mma16816(c, y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u, w.z, w.w, c);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[h][t][e] = fmaf(c[e], e < 2 ? e0 : e1, s[h][t][e]);
+                for (int e = 0; e < 4; ++e) s[t][e] = fmaf(c[e], e < 2 ? e0 : e1, s[t][e]);
               }
             }
           }
           // in units of log2 and less the row's maximum as last taken
           bool moves = false;
 #pragma unroll
-          for (int h = 0; h < U; ++h)
-#pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                s[h][t][e] = fmaf(s[h][t][e], qscale[t][e & 1], -mz[t][e & 1]);
-                if (kEdge && !sees(pos[t][e & 1], key0 + 16 * h + g + 8 * (e >> 1), u.window, u.sinks)) s[h][t][e] = -INFINITY;
-                moves |= s[h][t][e] > lim[t][e & 1];
+                s[t][e] = fmaf(s[t][e], a.scale_log2, -mz[t][e & 1]);
+                if (kEdge && !sees(position(8 * t + 2 * q + (e & 1)), key0 + g + 8 * (e >> 1), u.window, u.sinks)) s[t][e] = -INFINITY;
+                moves |= s[t][e] > lim[t][e & 1];
               }
           if (__any_sync(0xFFFFFFFFu, moves)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                float up = fmaxf(s[0][t][j], s[0][t][j + 2]);
-                if (U == 2) up = fmaxf(up, fmaxf(s[U - 1][t][j], s[U - 1][t][j + 2]));
+                float up = fmaxf(s[t][j], s[t][j + 2]);
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, d));
                 // a first maximum is taken as it is, a later one only moves up
@@ -465,11 +425,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                 mz[t][j] += up;
                 lim[t][j] = none ? lim[t][j] : kShift + kLazy;
                 l[t][j] *= keep;
-#pragma unroll
-                for (int h = 0; h < U; ++h) {
-                  s[h][t][j] -= up;
-                  s[h][t][j + 2] -= up;
-                }
+                s[t][j] -= up;
+                s[t][j + 2] -= up;
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -479,47 +436,42 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                   }
               }
           }
-          uint32_t pf[U][NT][2];  // probabilities: row g, keys 2 q, 2 q + 1 (+ 8)
-#pragma unroll
-          for (int h = 0; h < U; ++h)
+          uint32_t pf[NT][2];  // probabilities: row g, keys 2 q, 2 q + 1 (+ 8)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              float(&x)[4] = s[h][t];
+              float(&x)[4] = s[t];
 #pragma unroll
               for (int e = 0; e < 4; ++e) x[e] = exp2_fast(x[e]);
               l[t][0] += x[0] + x[2];
               l[t][1] += x[1] + x[3];
-              pf[h][t][0] = transpose8x8(bf16x2_bits(x[0], x[1]));
-              pf[h][t][1] = transpose8x8(bf16x2_bits(x[2], x[3]));
+              pf[t][0] = transpose8x8(bf16x2_bits(x[0], x[1]));
+              pf[t][1] = transpose8x8(bf16x2_bits(x[2], x[3]));
             }
           // which of this lane's two key pairs its row g sees, as masks of packed pairs
-          uint32_t keep[U][NT][2];
+          uint32_t keep[NT][2];
           if constexpr (kEdge) {
-#pragma unroll
-            for (int h = 0; h < U; ++h)
 #pragma unroll
               for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const int row = 8 * t + g, p = row < rows ? first + row / G : -1, j = key0 + 16 * h + 8 * e + 2 * q;
-                  keep[h][t][e] = (sees(p, j, u.window, u.sinks) ? 0xFFFFu : 0u) | (sees(p, j + 1, u.window, u.sinks) ? 0xFFFF0000u : 0u);
+                  const int p = position(8 * t + g), j = key0 + 8 * e + 2 * q;
+                  keep[t][e] = (sees(p, j, u.window, u.sinks) ? 0xFFFFu : 0u) | (sees(p, j + 1, u.window, u.sinks) ? 0xFFFF0000u : 0u);
                 }
           }
           // values
-#pragma unroll
-          for (int h = 0; h < U; ++h) {
-            const Words<NB> v0 = lds<NB, 0>(in_v + h * on_v), v1 = lds<NB, 4 * D>(in_v + h * on_v);
-            const Words<NB> f0 = lds<NB, 0>(in_vs + h * on_vs), f1 = lds<NB, 4 * NB * 4>(in_vs + h * on_vs);
+          {
+            const Words<NB> v0 = lds<NB, 0>(in_v), v1 = lds<NB, 4 * D>(in_v);
+            const Words<NB> f0 = lds<NB, 0>(in_vs), f1 = lds<NB, 4 * NB * 4>(in_vs);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               uint32_t w0[NT], w1[NT];
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                w0[t] = mul_bf16x2(pf[h][t][0], f0.w[b]);
-                w1[t] = mul_bf16x2(pf[h][t][1], f1.w[b]);
+                w0[t] = mul_bf16x2(pf[t][0], f0.w[b]);
+                w1[t] = mul_bf16x2(pf[t][1], f1.w[b]);
                 if constexpr (kEdge) {  // a masked key adds nothing, whatever its scale is
-                  w0[t] &= keep[h][t][0];
-                  w1[t] &= keep[h][t][1];
+                  w0[t] &= keep[t][0];
+                  w1[t] &= keep[t][1];
                 }
               }
 #pragma unroll
@@ -528,14 +480,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                   mma16816(o[t][b][e], x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u, w0[t], w1[t], o[t][b][e]);
-                  mma16816(o[t][b][e], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w0[t], w1[t], o[t][b][e]);  // -8, -8 x 16
+                  mma16816(o[t][b][e], off[0], off[1], off[2], off[3], w0[t], w1[t], o[t][b][e]);
                 }
               }
             }
           }
         };
-        using one = std::integral_constant<int, 1>;
-        using two = std::integral_constant<int, 2>;
 
         // the stages of this warp's team
 #pragma unroll 1
@@ -543,28 +493,25 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
           const uint32_t j = it + i;
           const int slot = j % kStages;
           wait(&full[slot], (j / kStages) & 1);
-          if (x + i + kStages - 2 == next && next < to) {
+          const int key0 = v.block(st0 + i) * kStageKeys + key_w;
+          const uint32_t have = ok ? s_have[slot] >> (key_w / 16) & 3 : 0, stage = slot * C::StageBytes;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int key_h = key0 + 16 * h;
+            if (!(have >> h & 1) || key_h >= S_r) continue;
+            if (key_h + 15 <= first && key_h >= lo_edge)
+              keys(std::false_type{}, stage, h, key_h);
+            else
+              keys(std::true_type{}, stage, h, key_h);
+          }
+          __syncwarp();
+          if (lane == 0) add_release(&s_left[slot]);
+          // this warp's turn: the slot of the stage before, which the other team has left by now
+          if (x + i + kStages - 1 == next && next < to) {
             issue(it0 + next);
             next += kWarps;
             look(next);
           }
-          const int key0 = v.block(st0 + i) * kStageKeys + key_w;
-          const uint32_t have = ok ? s_have[slot] >> (key_w / 16) & 3 : 0, stage = slot * C::StageBytes;
-          if (NT == 1 && have == 3 && key0 + 31 <= first && key0 >= lo_edge) {
-            keys(two{}, std::false_type{}, stage, false, key0);
-          } else {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              const int key_h = key0 + 16 * h;
-              if (!(have >> h & 1) || key_h >= S_r) continue;
-              if (NT > 1 && key_h + 15 <= first && key_h >= lo_edge)
-                keys(one{}, std::false_type{}, stage, h, key_h);
-              else
-                keys(one{}, std::true_type{}, stage, h, key_h);
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[slot]);
         }
         it += n_here;
 
@@ -701,7 +648,7 @@ cudaError_t launch_attn_decode(const fw_attn_q4_args& a, void* workspace, int sm
   d.rec = static_cast<SplitRecord*>(workspace);
   d.o = reinterpret_cast<float*>(d.rec + grid);
   d.ml = reinterpret_cast<float2*>(d.o + (int64_t)2 * grid * 8 * nt * a.D);
-  d.scale_log2 = a.scale * kLog2e;
+  d.scale_log2 = a.scale * kLog2e * kOScale;  // the scores' products come in units of 2^-69
   if (a.D == 64) return nt == 1 ? launch<64, 1>(d, grid, s) : launch<64, 2>(d, grid, s);
   return nt == 1 ? launch<128, 1>(d, grid, s) : launch<128, 2>(d, grid, s);
 }
