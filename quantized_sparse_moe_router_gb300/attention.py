@@ -35,51 +35,55 @@ class FwAttnQ4Args(ctypes.Structure):
 
 
 _bf16, _int32, _fp32, _uint8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_byref = ctypes.byref
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # not in builds of torch without CUDA
 
-# Small calls last a few microseconds, most of it here: each check is one
-# expression, and a message is only made for one that failed.
+_empty = torch.empty
 
-
-def _stream(t, stream):
-    return stream if stream is not None else _raw_stream(t.get_device())
-
-
-def _ints(where, name, t):
-    if t is not None and not (t.dtype is _int32 and t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{where}: {name} must be a contiguous int32 CUDA tensor")
-
-
-def _heads(where, name, t):
-    """Elements between tokens of a bf16 [T, heads, D] tensor whose heads lie side by side."""
-    if not (t.dtype is _bf16 and t.is_cuda and t.dim() == 3):
-        raise ValueError(f"{where}: {name} must be a bf16 CUDA tensor [T, heads, D]")
-    T, heads, D = t.shape
-    s = t.stride()
-    if T * heads and not (s[2] == 1 and (s[1] == D or heads == 1)):
-        raise ValueError(f"{where}: {name}'s heads must be contiguous within a token")
-    return s[0] if T > 1 and heads else heads * D
-
-
-def _cache_page(where, cache, D):
-    if not (cache.dtype is _uint8 and cache.is_cuda and cache.dim() == 3 and cache.is_contiguous()):
-        raise ValueError(f"{where}: cache must be a contiguous uint8 CUDA tensor [n_pages, n_kv, page * D * 9 / 8]")
-    page, rest = divmod(cache.shape[2] * 8, D * 9) if D else (0, 1)
-    if rest:
-        raise ValueError(f"{where}: cache blocks of {cache.shape[2]} bytes do not hold whole positions of {D} dims")
-    return page
+# Small calls last a few microseconds on the GPU and more here: what is checked
+# is checked in few expressions, and a message is only made for what failed.
 
 
 def _fail(text):
     raise ValueError(text)
 
 
+def _not_ints(where, **tensors):
+    for name, t in tensors.items():
+        if t is not None and not (t.dtype is _int32 and t.is_cuda and t.is_contiguous()):
+            _fail(f"{where}: {name} must be a contiguous int32 CUDA tensor")
+
+
+def _not_heads(where, name, t):
+    if not (t.dtype is _bf16 and t.is_cuda and t.dim() == 3):
+        _fail(f"{where}: {name} must be a bf16 CUDA tensor [T, heads, D]")
+    _fail(f"{where}: {name}'s heads must be contiguous within a token")
+
+
+def _heads(where, name, t, T, heads, D):
+    """Elements between tokens of a bf16 [T, heads, D] tensor whose heads lie side by side."""
+    a, b, c = t.stride()
+    if t.dtype is not _bf16 or not t.is_cuda or ((c != 1 or (b != D and heads != 1)) and T * heads):
+        _not_heads(where, name, t)
+    return a if T > 1 and heads else heads * D
+
+
+def _cache_shape(where, cache, D):
+    """-> pages, heads, positions a page."""
+    if not (cache.dtype is _uint8 and cache.is_cuda and cache.is_contiguous() and cache.dim() == 3):
+        _fail(f"{where}: cache must be a contiguous uint8 CUDA tensor [n_pages, n_kv, page * D * 9 / 8]")
+    n_pages, n_kv, size = cache.shape
+    page, rest = divmod(size * 8, D * 9) if D else (0, 1)
+    if rest:
+        _fail(f"{where}: cache blocks of {size} bytes do not hold whole positions of {D} dims")
+    return n_pages, n_kv, page
+
+
 def _keep(stream, *tensors):
     """Tensors made here and used on another stream than the current one stay alive until it is done with them."""
     other = torch.cuda.ExternalStream(stream)
     for t in tensors:
-        if t is not None:
-            t.record_stream(other)
+        t.record_stream(other)
 
 
 def kv_cache(n_pages, n_kv, D, page, device="cuda"):
@@ -92,27 +96,30 @@ def kv_plan(cached_lens, new_lens, block_table, free_pages, page, T_cap, free_us
     cached_lens [R], new_lens [R], block_table [R, max_blocks] (fresh entries are
     written), free_pages [n], free_used [1] or None -> KVPlan(q_start [R + 1],
     seq_lens [R], requests, positions, slots [T_cap], counts [3])."""
-    for name, t in (("cached_lens", cached_lens), ("new_lens", new_lens), ("block_table", block_table), ("free_pages", free_pages),
-                    ("free_used", free_used)):
-        _ints("kv_plan", name, t)
-    R = cached_lens.shape[0]
-    if new_lens.shape != cached_lens.shape or block_table.dim() != 2 or block_table.shape[0] != R:
+    R, blocks = block_table.shape
+    if not (cached_lens.dtype is new_lens.dtype is block_table.dtype is free_pages.dtype is _int32 and cached_lens.is_cuda
+            and new_lens.is_cuda and block_table.is_cuda and free_pages.is_cuda and cached_lens.is_contiguous()
+            and new_lens.is_contiguous() and block_table.is_contiguous() and free_pages.is_contiguous()) or free_used is not None:
+        _not_ints("kv_plan", cached_lens=cached_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages,
+                  free_used=free_used)
+    if cached_lens.shape != (R,) or new_lens.shape != (R,):
         _fail("kv_plan: cached_lens [R], new_lens [R] and block_table [R, max_blocks] must agree")
     if T_cap < 1:
         _fail("kv_plan: T_cap must be positive")
-    dev = cached_lens.device
-    # one buffer for all outputs; its rows are cut where the parts start
-    buf = torch.empty(3 * T_cap + 2 * R + 4, dtype=_int32, device=dev)
-    if stream is not None:
+    # one buffer for all outputs
+    buf = _empty(3 * T_cap + 2 * R + 4, dtype=_int32, device=block_table.device)
+    if stream is None:
+        stream = _raw_stream(buf.get_device())
+    else:
         _keep(stream, buf)
     at = buf.data_ptr()
     lens = at + 12 * T_cap
-    rc = _fw.lib().fw_kv_plan(cached_lens.data_ptr(), new_lens.data_ptr(), R, page, block_table.data_ptr(), block_table.shape[1],
-                              free_pages.data_ptr(), free_pages.shape[0], _fw._ptr(free_used), T_cap, lens, lens + 4 * (R + 1),
-                              at, at + 4 * T_cap, at + 8 * T_cap, lens + 4 * (2 * R + 1), _stream(buf, stream))
+    rc = _fw.lib().fw_kv_plan(cached_lens.data_ptr(), new_lens.data_ptr(), R, page, block_table.data_ptr(), blocks,
+                              free_pages.data_ptr(), free_pages.shape[0], None if free_used is None else free_used.data_ptr(), T_cap,
+                              lens, lens + 4 * (R + 1), at, at + 4 * T_cap, at + 8 * T_cap, lens + 4 * (2 * R + 1), stream)
     if rc:
         _fw._check(rc, "fw_kv_plan")
-    req, pos, slots, q_start, seq, counts = buf.split((T_cap, T_cap, T_cap, R + 1, R, 3))
+    req, pos, slots, q_start, seq, counts = buf.split_with_sizes((T_cap, T_cap, T_cap, R + 1, R, 3))
     return KVPlan(q_start, seq, req, pos, slots, counts)
 
 
@@ -124,52 +131,68 @@ def qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, i
     v are stored into slots in 4 bits and k_out is made only when it is given.
     -> (q_out, k_out or None)."""
     w = "qk_norm_rope"
-    qs, ks = _heads(w, "q", q), _heads(w, "k", k)
+    if q.dim() != 3 or k.dim() != 3:
+        _not_heads(w, "q" if q.dim() != 3 else "k", q if q.dim() != 3 else k)
     T, n_q, D = q.shape
-    n_kv = k.shape[1]
-    if k.shape[0] != T or k.shape[2] != D:
+    shape_k = k.shape
+    n_kv = shape_k[1]
+    if shape_k[0] != T or shape_k[2] != D:
         _fail(f"{w}: q [T, n_q, D] and k [T, n_kv, D] must agree")
-    for name, t in (("positions", positions), ("slots", slots), ("status", status)):
-        _ints(w, name, t)
-    if not (cos_sin.dtype is _fp32 and cos_sin.is_cuda and cos_sin.dim() == 2 and cos_sin.is_contiguous()):
+    qs, ks = _heads(w, "q", q, T, n_q, D), _heads(w, "k", k, T, n_kv, D)
+    if not (positions.dtype is _int32 and positions.is_cuda and positions.is_contiguous()) or status is not None:
+        _not_ints(w, positions=positions, status=status)
+    if not (cos_sin.dtype is _fp32 and cos_sin.is_cuda and cos_sin.is_contiguous() and cos_sin.dim() == 2):
         _fail(f"{w}: cos_sin must be a contiguous fp32 CUDA tensor [n_pos, rot]")
-    if positions.shape[0] != T or positions.dim() != 1:
+    if positions.shape != (T,):
         _fail(f"{w}: positions must be [T]")
+    n_pos, rot = cos_sin.shape
+    q_norm_at = k_norm_at = None
     for t in (q_norm, k_norm):
-        if t is not None and not (t.dtype is _fp32 and t.is_cuda and t.dim() == 1 and t.shape[0] == D and t.is_contiguous()):
+        if t is not None and not (t.dtype is _fp32 and t.is_cuda and t.is_contiguous() and t.shape == (D,)):
             _fail(f"{w}: norms must be contiguous fp32 CUDA tensors [D]")
+    if q_norm is not None:
+        q_norm_at = q_norm.data_ptr()
+    if k_norm is not None:
+        k_norm_at = k_norm.data_ptr()
     page = n_pages = vs = 0
+    v_at = cache_at = slots_at = None
     if cache is not None:
-        page, n_pages = _cache_page(w, cache, D), cache.shape[0]
-        if cache.shape[1] != n_kv:
-            _fail(f"{w}: cache holds {cache.shape[1]} heads, k has {n_kv}")
-        if v is None or v.shape != k.shape:
+        n_pages, heads, page = _cache_shape(w, cache, D)
+        if heads != n_kv:
+            _fail(f"{w}: cache holds {heads} heads, k has {n_kv}")
+        if v is None or v.shape != shape_k:
             _fail(f"{w}: a cache needs v [T, n_kv, D]")
-        if slots is None or slots.dim() != 1 or slots.shape[0] != T:
+        if slots is None or slots.shape != (T,):
             _fail(f"{w}: a cache needs slots [T]")
-        vs = _heads(w, "v", v)
+        _not_ints(w, slots=slots)
+        vs = _heads(w, "v", v, T, n_kv, D)
+        v_at, cache_at, slots_at = v.data_ptr(), cache.data_ptr(), slots.data_ptr()
+    made = []
     if q_out is None:
-        q_out = torch.empty((T, n_q, D), dtype=_bf16, device=q.device)
-        qos = n_q * D
-        if stream is not None:
-            _keep(stream, q_out)
+        q_out, qos = _empty((T, n_q, D), dtype=_bf16, device=q.device), n_q * D
+        made.append(q_out)
     else:
-        qos = _heads(w, "q_out", q_out)
-    kos = 0
-    if k_out is not None:
-        kos = _heads(w, "k_out", k_out)
-    elif cache is None:
-        k_out = torch.empty((T, n_kv, D), dtype=_bf16, device=q.device)
-        kos = n_kv * D
-        if stream is not None:
-            _keep(stream, k_out)
-    if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
-        _fail(f"{w}: outputs must have their inputs' shapes")
-    ptr = _fw._ptr
-    args = FwQkNormRopeArgs(T, n_q, n_kv, D, cos_sin.shape[1], 1 if interleaved else 0, eps, cos_sin.shape[0], q.data_ptr(),
-                            k.data_ptr(), ptr(v), qs, ks, vs, ptr(q_norm), ptr(k_norm), cos_sin.data_ptr(), positions.data_ptr(),
-                            q_out.data_ptr(), ptr(k_out), qos, kos, ptr(cache), ptr(slots), page, n_pages, ptr(status))
-    rc = _fw.lib().fw_qk_norm_rope(ctypes.byref(args), _stream(q, stream))
+        if q_out.shape != q.shape:
+            _fail(f"{w}: outputs must have their inputs' shapes")
+        qos = _heads(w, "q_out", q_out, T, n_q, D)
+    kos, k_out_at = n_kv * D, None
+    if k_out is None:
+        if cache is None:
+            k_out = _empty((T, n_kv, D), dtype=_bf16, device=q.device)
+            made.append(k_out)
+            k_out_at = k_out.data_ptr()
+    else:
+        if k_out.shape != shape_k:
+            _fail(f"{w}: outputs must have their inputs' shapes")
+        kos, k_out_at = _heads(w, "k_out", k_out, T, n_kv, D), k_out.data_ptr()
+    if stream is None:
+        stream = _raw_stream(q.get_device())
+    else:
+        _keep(stream, *made)
+    args = FwQkNormRopeArgs(T, n_q, n_kv, D, rot, 1 if interleaved else 0, eps, n_pos, q.data_ptr(), k.data_ptr(), v_at, qs, ks, vs,
+                            q_norm_at, k_norm_at, cos_sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), k_out_at, qos, kos,
+                            cache_at, slots_at, page, n_pages, None if status is None else status.data_ptr())
+    rc = _fw.lib().fw_qk_norm_rope(_byref(args), stream)
     if rc:
         _fw._check(rc, "fw_qk_norm_rope")
     return q_out, k_out
@@ -177,19 +200,20 @@ def qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, i
 
 def kv_export(cache, slots, D, status=None, stream=None):
     """What slots (int32 [T]) of a cache hold (fw_kv_export) -> k, v bf16 [T, n_kv, D]."""
-    page = _cache_page("kv_export", cache, D)
-    _ints("kv_export", "slots", slots)
-    _ints("kv_export", "status", status)
-    T, n_kv = slots.shape[0], cache.shape[1]
-    k = torch.empty((T, n_kv, D), dtype=_bf16, device=cache.device)
-    v = torch.empty((T, n_kv, D), dtype=_bf16, device=cache.device)
-    if stream is not None:
-        _keep(stream, k, v)
-    rc = _fw.lib().fw_kv_export(cache.data_ptr(), cache.shape[0], n_kv, D, page, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
-                                _fw._ptr(status), _stream(cache, stream))
+    n_pages, n_kv, page = _cache_shape("kv_export", cache, D)
+    _not_ints("kv_export", slots=slots, status=status)
+    T = slots.shape[0]
+    kv = _empty((2, T, n_kv, D), dtype=_bf16, device=cache.device)
+    if stream is None:
+        stream = _raw_stream(kv.get_device())
+    else:
+        _keep(stream, kv)
+    at = kv.data_ptr()
+    rc = _fw.lib().fw_kv_export(cache.data_ptr(), n_pages, n_kv, D, page, slots.data_ptr(), T, at, at + 2 * T * n_kv * D,
+                                None if status is None else status.data_ptr(), stream)
     if rc:
         _fw._check(rc, "fw_kv_export")
-    return k, v
+    return kv.unbind(0)
 
 
 def attn_q4(q, cache, block_table, q_start, seq_lens, max_q, scale=None, window=0, sinks=0, out=None, status=None, stream=None):
@@ -198,35 +222,45 @@ def attn_q4(q, cache, block_table, q_start, seq_lens, max_q, scale=None, window=
     int32 [R + 1], seq_lens int32 [R] (new tokens included), max_q the most new
     tokens of a request; scale None: 1 / sqrt(D) -> out bf16 [T, n_q, D]."""
     w = "attn_q4"
-    qs = _heads(w, "q", q)
+    if q.dim() != 3:
+        _not_heads(w, "q", q)
     T, n_q, D = q.shape
-    page = _cache_page(w, cache, D)
-    for name, t in (("block_table", block_table), ("q_start", q_start), ("seq_lens", seq_lens), ("status", status)):
-        _ints(w, name, t)
-    R = seq_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != R or q_start.dim() != 1 or q_start.shape[0] != R + 1:
+    qs = _heads(w, "q", q, T, n_q, D)
+    n_pages, n_kv, page = _cache_shape(w, cache, D)
+    if not (block_table.dtype is q_start.dtype is seq_lens.dtype is _int32 and block_table.is_cuda and q_start.is_cuda
+            and seq_lens.is_cuda and block_table.is_contiguous() and q_start.is_contiguous()
+            and seq_lens.is_contiguous()) or status is not None:
+        _not_ints(w, block_table=block_table, q_start=q_start, seq_lens=seq_lens, status=status)
+    R, blocks = block_table.shape
+    if seq_lens.shape != (R,) or q_start.shape != (R + 1,):
         _fail(f"{w}: block_table [R, max_blocks], q_start [R + 1] and seq_lens [R] must agree")
+    dev = q.device
     if out is None:
-        out = torch.empty((T, n_q, D), dtype=_bf16, device=q.device)
-        os = n_q * D
-        if stream is not None:
-            _keep(stream, out)
+        out, os, made = _empty((T, n_q, D), dtype=_bf16, device=dev), n_q * D, True
     else:
-        os = _heads(w, "out", out)
         if out.shape != q.shape:
             _fail(f"{w}: out must have q's shape")
-    args = FwAttnQ4Args(R, T, max_q, n_q, cache.shape[1], D, page, cache.shape[0], block_table.shape[1], window, sinks,
-                        1.0 / math.sqrt(D) if scale is None else scale, q.data_ptr(), out.data_ptr(), qs, os, cache.data_ptr(),
-                        block_table.data_ptr(), q_start.data_ptr(), seq_lens.data_ptr(), _fw._ptr(status))
-    L, ref, need, ws = _fw.lib(), ctypes.byref(args), _i64(), None
-    rc = L.fw_attn_q4_workspace(ref, ctypes.byref(need))
+        os, made = _heads(w, "out", out, T, n_q, D), False
+    args = _byref(FwAttnQ4Args(R, T, max_q, n_q, n_kv, D, page, n_pages, blocks, window, sinks,
+                               1.0 / math.sqrt(D) if scale is None else scale, q.data_ptr(), out.data_ptr(), qs, os,
+                               cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(), seq_lens.data_ptr(),
+                               None if status is None else status.data_ptr()))
+    L, need = _fw.lib(), _i64()
+    rc = L.fw_attn_q4_workspace(args, _byref(need))
     if rc:
         _fw._check(rc, "fw_attn_q4_workspace")
-    if need.value:
-        ws = torch.empty(need.value, dtype=_uint8, device=q.device)
-        if stream is not None:
+    size, at = need.value, None
+    if size:
+        ws = _empty(size, dtype=_uint8, device=dev)
+        at = ws.data_ptr()
+    if stream is None:
+        stream = _raw_stream(q.get_device())
+    else:
+        if made:
+            _keep(stream, out)
+        if size:
             _keep(stream, ws)
-    rc = L.fw_attn_q4(ref, _fw._ptr(ws), need.value, _stream(q, stream))
+    rc = L.fw_attn_q4(args, at, size, stream)
     if rc:
         _fw._check(rc, "fw_attn_q4")
     return out
