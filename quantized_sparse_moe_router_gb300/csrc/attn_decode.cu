@@ -25,10 +25,14 @@
 // instructions: 446 instead of 359 of them for 16 keys.)
 //
 // Work: a unit is 128 keys of one (request, key/value head); the CTAs take
-// equal consecutive shares of all units, so that ragged lengths and few
-// requests both fill the GPU. A unit's pages come into a shared-memory ring by
-// one bulk copy each, which the CTA's eight warps issue in turn; each warp
-// takes 16 of the unit's keys, with a softmax state of its own that is joined
+// consecutive shares of all units, so that ragged lengths and few requests both
+// fill the GPU. The shares are equal in cost: a pair costs its units and
+// kPairCost more for its query rows, its empty pipeline and its join (64
+// requests of 100 to 8191 keys: 66 us at 0, 52 at 3, 50 at 6, 52 at 8; 48 drafts
+// over a window 32, 30, 28.4, 28.9; 4 long contexts 72, 70, 68, 68).
+// A unit's pages come into a shared-memory ring by one bulk copy each, which
+// the CTA's eight warps issue in turn. Four of them take a unit, 32 keys each,
+// the other four the next; each has a softmax state of its own that is joined
 // at the end of a segment. A pair whose units fall into several CTAs leaves
 // partial results that a second small kernel joins. (Eight warps and no ninth
 // as producer: two CTAs of eight leave each warp 128 registers, of nine 96.)
@@ -44,6 +48,7 @@ using namespace dev;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kTeam = 4;          // warps of a stage (32 keys each); two teams take the stages in turn
 constexpr int kChunk = kThreads;  // requests scanned at a time
+constexpr int kPairCost = 6;      // units that a pair costs beside its own: see the work's shares above
 constexpr float kLazy = 8.f;      // a row's maximum moves only when a score passes it by 2^8
 constexpr float kShift = 64.f;    // probabilities carry 2^64
 constexpr float kOScale = 590295810358705651712.f, kLScale = 1.f / 18446744073709551616.f;  // 2^69 = 2^(133 - 64), 2^-64
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
   __shared__ uint32_t s_have[kStages];       // bit w: the stage's keys 16 w .. 16 w + 15 are there
   __shared__ int s_pref[kChunk + 1];         // units before each request of the chunk, from this CTA's first one on
   __shared__ int s_len[kChunk], s_new[kChunk], s_tok[kChunk];
-  __shared__ long long s_scan[kWarps];
+  __shared__ long long s_scan[kWarps][2], s_bound[2];
   __shared__ float2 s_ml[kWarps][C::Rows];
   __shared__ float s_qz[C::Rows][NB];        // -8 x a row's sums over the blocks, in units of the products
   float* join = reinterpret_cast<float*>(smem + kStages * C::StageBytes);
@@ -165,36 +170,62 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
     // an empty context is one unit without keys: its rows are zeros
     return (long long)::max(1, visible_stages(::max(S, 0), S - n, u.window, u.sinks).count()) * u.n_kv;
   };
-  // sum over the CTA; also the running sum before each thread
-  auto scan = [&](long long v, long long& before) -> long long {
-    long long inc = v;
+  // sums over the CTA of units and of their cost; also what lies before each thread
+  struct Sum {
+    long long units, cost;
+  };
+  auto scan = [&](long long units, long long cost, Sum& before) -> Sum {
+    long long v0 = units, v1 = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += x;
+      const long long x0 = __shfl_up_sync(0xFFFFFFFFu, v0, o), x1 = __shfl_up_sync(0xFFFFFFFFu, v1, o);
+      if (lane >= o) v0 += x0, v1 += x1;
     }
     __syncthreads();
-    if (lane == 31) s_scan[warp] = inc;
+    if (lane == 31) s_scan[warp][0] = v0, s_scan[warp][1] = v1;
     __syncthreads();
-    long long sum = 0;
-    before = inc - v;
+    Sum sum = {0, 0};
+    before = {v0 - units, v1 - cost};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_scan[w];
-      sum += s_scan[w];
+      if (w < warp) before.units += s_scan[w][0], before.cost += s_scan[w][1];
+      sum.units += s_scan[w][0];
+      sum.cost += s_scan[w][1];
     }
     return sum;
   };
-  long long total = 0, before, mine = 0;
+  auto cost = [&](long long units) { return units ? units + (long long)kPairCost * u.n_kv : 0; };
+  Sum total = {0, 0}, before;
+  long long mine = 0;
   int S = 0, n = 0, q0 = 0;
   for (int r0 = 0; r0 < u.R; r0 += kChunk) {
     mine = request(r0 + tid, S, n, q0);
-    total += scan(mine, before);
+    const Sum sum = scan(mine, cost(mine), before);
+    total.units += sum.units;
+    total.cost += sum.cost;
   }
-  // no more CTAs than units: the parts of a split pair are then consecutive CTAs
-  const int grid = (int)::min((long long)gridDim.x, ::max(total, 1ll)), cta = ::min((int)blockIdx.x, grid);
-  const long long u_begin = total * cta / grid;
-  const int u_end = (int)(total * (cta + 1) / grid - u_begin);
+  // no more CTAs than the cost can be shared among: the parts of a split pair are then consecutive CTAs
+  const int grid = (int)::min((long long)gridDim.x, ::max(total.cost, 1ll)), cta = ::min((int)blockIdx.x, grid);
+  const long long cost_end = total.cost * (cta + 1) / grid;
+  if (tid < 2) s_bound[tid] = total.units;  // (what no request holds is the end)
+  Sum base = {0, 0};
+  for (int r0 = 0; r0 < u.R; r0 += kChunk) {
+    if (u.R > kChunk) mine = request(r0 + tid, S, n, q0);  // else they are still in registers
+    const Sum sum = scan(mine, cost(mine), before);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // the units before this CTA's share and before its end
+      const long long rel = (e ? cost_end : total.cost * cta / grid) - base.cost - before.cost;
+      if (mine && rel >= 0 && rel < cost(mine)) {
+        const long long n_st = mine / u.n_kv, head = rel / (n_st + kPairCost);
+        s_bound[e] = base.units + before.units + head * n_st + ::max(0ll, rel - head * (n_st + kPairCost) - kPairCost);
+      }
+    }
+    base.units += sum.units;
+    base.cost += sum.cost;
+  }
+  __syncthreads();
+  const long long u_begin = s_bound[0];
+  const int u_end = (int)(s_bound[1] - u_begin);
   const KvPlanes pl = kv_planes(u.page, D);
   const uint32_t hb = (uint32_t)kv_head_bytes(u.page, D);
   const int page_shift = __ffs(u.page) - 1;
@@ -220,17 +251,20 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
     }
   };
   uint32_t it = 0, last_fill = 0;  // stages consumed; one past the last stage this warp filled
-  long long base = -u_begin;
-  for (int r0 = 0; r0 < u.R && base < u_end; r0 += kChunk) {
-    if (u.R > kChunk) mine = request(r0 + tid, S, n, q0);  // else they are still in registers
-    const long long sum = scan(mine, before);
+  long long chunk = total.units;  // a chunk's units
+  base.units = -u_begin;
+  for (int r0 = 0; r0 < u.R && base.units < u_end; r0 += kChunk) {
+    if (u.R > kChunk) {
+      mine = request(r0 + tid, S, n, q0);
+      chunk = scan(mine, 0, before).units;
+    }
     // (a request's units and a CTA's share fit 32 bits: checked on the host; what lies before the CTA's share does not matter)
-    s_pref[tid] = (int)::max(base + before, -(1ll << 30));
+    s_pref[tid] = (int)::max(::min(base.units + before.units, 1ll << 30), -(1ll << 30));
     s_len[tid] = S;
     s_new[tid] = n;
     s_tok[tid] = q0;
-    base += sum;
-    if (tid == 0) s_pref[kChunk] = (int)::max(::min(base, 1ll << 30), -(1ll << 30));
+    base.units += chunk;
+    if (tid == 0) s_pref[kChunk] = (int)::max(::min(base.units, 1ll << 30), -(1ll << 30));
     __syncthreads();
     const int from = ::max(0, s_pref[0]), to = ::min(u_end, s_pref[kChunk]);
     if (from >= to) continue;
@@ -332,7 +366,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
           }
         };
         uint4 qf[NT == 1 ? NB : 1];
-        __syncthreads();  // (the previous segment's are no longer read)
         if constexpr (NT == 1) {
           tile_q(0, qf);  // every warp for itself; what they write is the same
         } else if (warp < NT) {
@@ -341,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
 #pragma unroll
           for (int b = 0; b < NB; ++b) *reinterpret_cast<uint4*>(s_q + ((warp * NB + b) * 32 + lane) * 16) = w[b];
         }
-        __syncthreads();
+        __syncthreads();  // (the previous segment's buffers are no longer read either)
         // the three bf16 parts of row g's z as a 16-step operand: step k holds
         // part k / NB of block k % NB
         uint32_t qz[NT][2];
@@ -581,12 +614,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
               if (d4 == 0) a.ml[(int64_t)part * C::Rows + row] = make_float2(top, sum);
             }
           }
-          __syncthreads();
+          if (t + 1 < NT) __syncthreads();
         }
         if (!whole && st0 == 0 && tid == 0) {
-          const long long last = u_begin + x + n_st - 1;  // this head's last unit, and the CTA that has it
+          // the share ends n_here units into this head; the CTA that has its last one
           SplitRecord rec;
-          rec.parts = (int)(((last + 1) * grid - 1) / total) - cta + 1;
+          rec.parts = (int)(((cost_end + n_st - n_here) * grid - 1) / total.cost) - cta + 1;
           rec.slot0 = part;
           rec.slot1 = 2 * cta;
           rec.step = 2;
