@@ -57,6 +57,7 @@ constexpr uint32_t kQUp = 0x5F805F80u, kQUp16 = 0x5D805D80u;  // bf16 pairs of 2
 template <int D, int NT>
 struct Cfg {
   static constexpr int NB = D / kKvBlock, Rows = 8 * NT;
+  static constexpr int Halves = NT == 1 ? 2 : 1;  // of a warp's 32 keys that are in registers together
   static constexpr uint32_t StageBytes = kStageKeys * D * 9 / 8;
   static constexpr int Stages = D == 128 ? 4 : 8;  // even: a slot is always the same team's
   static_assert(Stages % 2 == 0 && Stages <= kWarps, "see the ring");
@@ -130,7 +131,7 @@ __device__ __forceinline__ Words<N> lds(uint32_t p) {
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) {
   using C = Cfg<D, NT>;
-  constexpr int NB = C::NB, kStages = C::Stages;
+  constexpr int NB = C::NB, kStages = C::Stages, H = C::Halves;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kStages];
   __shared__ uint32_t s_left[kStages];       // how often a warp has left the slot
@@ -396,21 +397,22 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
 #pragma unroll
         for (int t = 0; t < NT; ++t) mz[t][0] = mz[t][1] = l[t][0] = l[t][1] = 0.f, lim[t][0] = lim[t][1] = -INFINITY;
 
-        // 16 keys of this warp. kEdge: not every row sees all of them (the last
-        // keys, the window's edge); `stage`: byte offset of their stage,
-        // `second`: the keys are the second 16 of the warp's 32.
-        auto keys = [&](auto edge, uint32_t stage, bool second, int key0) {
+        // 16 H keys of this warp, from its `half`-th 16 on. kEdge: not every row
+        // sees all of them (the last keys, the window's edge) or not all are
+        // there (bits of `have`); `stage`: byte offset of their stage.
+        auto keys = [&](auto edge, uint32_t stage, int half, uint32_t have, int key0) {
           constexpr bool kEdge = decltype(edge)::value;
-          const uint32_t in_k = at_k + stage + (second ? on_k : 0), in_ks = at_ks + stage + (second ? on_ks : 0);
-          const uint32_t in_v = at_v + stage + (second ? on_v : 0), in_vs = at_vs + stage + (second ? on_vs : 0);
-          float s[NT][4];
-          {
+          float s[H][NT][4];
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const bool second = H == 2 ? h : half;
+            const uint32_t in_k = at_k + stage + (second ? on_k : 0), in_ks = at_ks + stage + (second ? on_ks : 0);
             const Words<NB> k0 = lds<NB, 0>(in_k), k1 = lds<NB, 8 * (D / 2)>(in_k);
             const Words<NB / 2> d0 = lds<NB / 2, 0>(in_ks), d1 = lds<NB / 2, 8 * NB * 2>(in_ks);
             const float zero[4] = {0.f, 0.f, 0.f, 0.f};
             const uint32_t z0 = NB == 4 && (q & 1) ? d0.w[NB / 2 - 1] : d0.w[0], z1 = NB == 4 && (q & 1) ? d1.w[NB / 2 - 1] : d1.w[0];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(s[t], z0, z1, z0, z1, qz[t][0], qz[t][1], zero);
+            for (int t = 0; t < NT; ++t) mma16816(s[h][t], z0, z1, z0, z1, qz[t][0], qz[t][1], zero);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               const float e0 = __uint_as_float(b & 1 ? d0.w[b / 2] & 0xFFFF0000u : d0.w[b / 2] << 16);
@@ -427,26 +429,32 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                 mma16816(c, x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u, w.x, w.y, zero);
                 mma16816(c, y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u, w.z, w.w, c);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][e] = fmaf(c[e], e < 2 ? e0 : e1, s[t][e]);
+                for (int e = 0; e < 4; ++e) s[h][t][e] = fmaf(c[e], e < 2 ? e0 : e1, s[h][t][e]);
               }
             }
           }
           // in units of log2 and less the row's maximum as last taken
           bool moves = false;
 #pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                s[t][e] = fmaf(s[t][e], a.scale_log2, -mz[t][e & 1]);
-                if (kEdge && !sees(position(8 * t + 2 * q + (e & 1)), key0 + g + 8 * (e >> 1), u.window, u.sinks)) s[t][e] = -INFINITY;
-                moves |= s[t][e] > lim[t][e & 1];
+                float& x = s[h][t][e];
+                x = fmaf(x, a.scale_log2, -mz[t][e & 1]);
+                if (kEdge && !((have >> h & 1) &&
+                               sees(position(8 * t + 2 * q + (e & 1)), key0 + 16 * h + g + 8 * (e >> 1), u.window, u.sinks)))
+                  x = -INFINITY;
+                moves |= x > lim[t][e & 1];
               }
           if (__any_sync(0xFFFFFFFFu, moves)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                float up = fmaxf(s[t][j], s[t][j + 2]);
+                float up = fmaxf(s[0][t][j], s[0][t][j + 2]);
+                if constexpr (H == 2) up = fmaxf(up, fmaxf(s[H - 1][t][j], s[H - 1][t][j + 2]));
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, d));
                 // a first maximum is taken as it is, a later one only moves up
@@ -458,8 +466,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                 mz[t][j] += up;
                 lim[t][j] = none ? lim[t][j] : kShift + kLazy;
                 l[t][j] *= keep;
-                s[t][j] -= up;
-                s[t][j + 2] -= up;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                  s[h][t][j] -= up;
+                  s[h][t][j + 2] -= up;
+                }
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -469,30 +480,36 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
                   }
               }
           }
-          uint32_t pf[NT][2];  // probabilities: row g, keys 2 q, 2 q + 1 (+ 8)
+          uint32_t pf[H][NT][2];  // probabilities: row g, keys 2 q, 2 q + 1 (+ 8)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              float(&x)[4] = s[t];
+              float(&x)[4] = s[h][t];
 #pragma unroll
               for (int e = 0; e < 4; ++e) x[e] = exp2_fast(x[e]);
               l[t][0] += x[0] + x[2];
               l[t][1] += x[1] + x[3];
-              pf[t][0] = transpose8x8(bf16x2_bits(x[0], x[1]));
-              pf[t][1] = transpose8x8(bf16x2_bits(x[2], x[3]));
+              pf[h][t][0] = transpose8x8(bf16x2_bits(x[0], x[1]));
+              pf[h][t][1] = transpose8x8(bf16x2_bits(x[2], x[3]));
             }
-          // which of this lane's two key pairs its row g sees, as masks of packed pairs
-          uint32_t keep[NT][2];
-          if constexpr (kEdge) {
+          // values
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const bool second = H == 2 ? h : half;
+            const uint32_t in_v = at_v + stage + (second ? on_v : 0), in_vs = at_vs + stage + (second ? on_vs : 0);
+            // which of this lane's two key pairs its row g sees, as masks of packed pairs
+            uint32_t keep[NT][2];
+            if constexpr (kEdge) {
 #pragma unroll
               for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const int p = position(8 * t + g), j = key0 + 8 * e + 2 * q;
+                  const int p = position(8 * t + g), j = key0 + 16 * h + 8 * e + 2 * q;
                   keep[t][e] = (sees(p, j, u.window, u.sinks) ? 0xFFFFu : 0u) | (sees(p, j + 1, u.window, u.sinks) ? 0xFFFF0000u : 0u);
+                  if (!(have >> h & 1)) keep[t][e] = 0;
                 }
-          }
-          // values
-          {
+            }
             const Words<NB> v0 = lds<NB, 0>(in_v), v1 = lds<NB, 4 * D>(in_v);
             const Words<NB> f0 = lds<NB, 0>(in_vs), f1 = lds<NB, 4 * NB * 4>(in_vs);
 #pragma unroll
@@ -500,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
               uint32_t w0[NT], w1[NT];
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                w0[t] = mul_bf16x2(pf[t][0], f0.w[b]);
-                w1[t] = mul_bf16x2(pf[t][1], f1.w[b]);
+                w0[t] = mul_bf16x2(pf[h][t][0], f0.w[b]);
+                w1[t] = mul_bf16x2(pf[h][t][1], f1.w[b]);
                 if constexpr (kEdge) {  // a masked key adds nothing, whatever its scale is
                   w0[t] &= keep[t][0];
                   w1[t] &= keep[t][1];
@@ -529,13 +546,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
           const int key0 = v.block(st0 + i) * kStageKeys + key_w;
           const uint32_t have = ok ? s_have[slot] >> (key_w / 16) & 3 : 0, stage = slot * C::StageBytes;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; h += H) {
             const int key_h = key0 + 16 * h;
-            if (!(have >> h & 1) || key_h >= S_r) continue;
-            if (key_h + 15 <= first && key_h >= lo_edge)
-              keys(std::false_type{}, stage, h, key_h);
+            const uint32_t there = have >> h & ((1u << H) - 1);
+            if (!there || key_h >= S_r) continue;
+            if (there == (1u << H) - 1 && key_h + 16 * H - 1 <= first && key_h >= lo_edge)
+              keys(std::false_type{}, stage, h, there, key_h);
             else
-              keys(std::true_type{}, stage, h, key_h);
+              keys(std::true_type{}, stage, h, there, key_h);
           }
           __syncwarp();
           if (lane == 0) add_release(&s_left[slot]);
