@@ -170,8 +170,14 @@ struct RopeArgs {
 // One row's 4-bit block halves: the scale of the 4 lanes' 32 values (already
 // bf16) and this lane's 8 codes, x / d rounded half to even. The scale is the
 // element of largest magnitude (the positive one of a tie) over -8: exact in
-// bf16 for bf16 values.
-__device__ __forceinline__ float quantise8(const float (&x)[8], int (&code)[8]) {
+// bf16 for bf16 values. No quotient is needed to know how x / d rounds: with
+// X, Y of 8 bits, x / d and a half-integer h / 2 from 1/2 on differ by
+// |2 X 2^a - h Y| / 2 Y with a >= -2, so by nothing or by 2^-10 or more. x times
+// 1 / d, rounded to a multiple of 2^-11, is on the right side of it or on it.
+constexpr float kSnap = 6144.f;      // 1.5 x 2^12: sums with it are multiples of 2^-11
+constexpr float kWhole = 12582912.f;  // 1.5 x 2^23: of 1, and the low bits of the sum are the whole number
+
+__device__ __forceinline__ float quantise8(const float (&x)[8], uint32_t (&code)[8]) {
   float hi = x[0], lo = x[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
@@ -184,9 +190,19 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], int (&code)[8]) 
     lo = min_nan(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
   }
   const float d = (hi >= -lo ? hi : lo) * -0.125f;
+  if (fabsf(d) > 1e-30f && fabsf(d) < 1e30f) {
+    const float r = __fdiv_rn(1.f, d);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    code[i] = d != 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(x[i], d)) + 8.f, 0.f), 15.f) : 8;
+    for (int i = 0; i < 8; ++i) {
+      // |x| <= 8 |d|: only an extreme of the other sign passes what a code holds
+      const float t = fminf(__fadd_rn(__fadd_rn(__fmul_rn(x[i], r), kSnap), -kSnap), 7.f);
+      code[i] = __float_as_uint(__fadd_rn(t, kWhole + 8.f)) & 15;
+    }
+  } else {  // zeros, what is not finite, and where 1 / d would not do
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      code[i] = d != 0.f ? (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(x[i], d)) + 8.f, 0.f), 15.f) : 8;
+  }
   return d;
 }
 
@@ -215,6 +231,18 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs 
       raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
     }
   }
+  // the norms' weights of this lane's dims, for queries or keys: with the rows, not after their sums
+  float ww[8];
+  const float* ww_of = nullptr;
+  auto weights = [&](const float* w) {
+    if (!w || w == ww_of) return;
+    ww_of = w;
+    const float4 w0 = *reinterpret_cast<const float4*>(w + 8 * l), w1 = *reinterpret_cast<const float4*>(w + 8 * l + 4);
+    ww[0] = w0.x; ww[1] = w0.y; ww[2] = w0.z; ww[3] = w0.w;
+    ww[4] = w1.x; ww[5] = w1.y; ww[6] = w1.z; ww[7] = w1.w;
+  };
+  auto norm_of = [&](int r) { return r < u.n_q ? u.q_norm : r < u.n_q + u.n_kv ? u.k_norm : nullptr; };
+  weights(norm_of(row0));
   // the rotation of this lane's 8 dims: y' = y * cs + partner * sn (sn signed)
   float cs[8], sn[8];
   const bool turns = 8 * l < u.rot;
@@ -263,7 +291,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs 
     bf16x2_to_f32(raw[i].z, x[4], x[5]);
     bf16x2_to_f32(raw[i].w, x[6], x[7]);
     const bool is_q = r < u.n_q, is_v = r >= u.n_q + u.n_kv;
-    const float* w = is_v ? nullptr : is_q ? u.q_norm : u.k_norm;
+    const float* w = norm_of(r);
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += x[j] * x[j];
@@ -271,8 +299,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs 
     for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (w) {
       const float inv = __fdiv_rn(1.f, __fsqrt_rn(sum * (1.f / D) + u.eps));
-      const float4 w0 = *reinterpret_cast<const float4*>(w + 8 * l), w1 = *reinterpret_cast<const float4*>(w + 8 * l + 4);
-      const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      weights(w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], inv), ww[j]);
     }
@@ -300,12 +327,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs 
                                 : (__nv_bfloat16*)u.k_out + t * u.k_out_stride + (r - u.n_q) * D;
       if (is_q || u.k_out) *reinterpret_cast<uint4*>(dst + 8 * l) = o4;
     }
-    if (u.cache) {
+    if (u.cache && __any_sync(0xFFFFFFFFu, !is_q && r < a.rows)) {
       bf16x2_to_f32(o4.x, x[0], x[1]);
       bf16x2_to_f32(o4.y, x[2], x[3]);
       bf16x2_to_f32(o4.z, x[4], x[5]);
       bf16x2_to_f32(o4.w, x[6], x[7]);
-      int c[8];
+      uint32_t c[8];
       const float d = quantise8(x, c);
       if (!is_q && r < a.rows && block >= 0) {
         const int head = is_v ? r - u.n_q - u.n_kv : r - u.n_q;
@@ -316,7 +343,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs 
         if (!is_v) {
           uint32_t word = 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) word |= (uint32_t)c[j] << (4 * (j / 2) + 16 * (j % 2));
+          for (int j = 0; j < 8; ++j) word |= c[j] << (4 * (j / 2) + 16 * (j % 2));
           reinterpret_cast<uint32_t*>(base + at * (D / 2))[q * NB + b] = word;
           if (q == 0) reinterpret_cast<__nv_bfloat16*>(base + p.ks)[at * NB + b] = db;
         } else {

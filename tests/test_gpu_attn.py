@@ -182,6 +182,30 @@ def test_store_ties_extremes_and_non_finite_blocks():
         assert not torch.isfinite(e[2, 5]) and e[2, 40] == -2.0 and e[2, 32:].abs().sum() == 2.0
 
 
+@pytest.mark.parametrize("power", [0, -97, -120, 102, 110])
+def test_store_every_quotient(power):
+    """Codes are x / d rounded half to even for every pair of bf16 significands,
+    at magnitudes around and past those where 1 / d is taken."""
+    D, page = 128, 128
+    x = np.zeros((128, 6, 5, 32))
+    for y in range(128):
+        for e in range(6):
+            body = np.resize((128 + np.arange(128)) * 2.0 ** -e, (5, 31)) * np.where(np.arange(31) % 2, -1, 1)
+            x[y, e, :, 1:] = np.where(np.abs(body) <= 128 + y, body, body / 2)
+            x[y, e, :, 0] = (128 + y) * (1 if (y + e) % 2 else -1)
+    v = torch.from_numpy(x.reshape(-1, 1, D) * 2.0 ** (power - 7)).to(torch.bfloat16)
+    T = v.shape[0]
+    cache, slots = fw.kv_cache(-(-T // page), 1, D, page), torch.arange(T, dtype=torch.int32, device=DEV)
+    k = v.flip(0).contiguous().to(DEV)
+    fw.qk_norm_rope(torch.zeros_like(k), k, torch.zeros_like(slots), torch.zeros((1, 0), device=DEV), v=v.to(DEV), cache=cache, slots=slots)
+    want = np.zeros(tuple(cache.shape), np.uint8)
+    for t in range(T):
+        for which, w in (("k", k.cpu()), ("v", v)):
+            c, d = ref.quantise(w[t].double().numpy())
+            ref.write_block(want[t // page, 0], page, D, t % page, which, c[0], ref.bf16_bits(d)[0])
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
 def test_bad_slots_and_positions_are_reported_and_skipped():
     q, k, v, cos_sin, pos, _ = rope_case(4, 2, 1, 64, 64, 8)
     cache = fw.kv_cache(2, 1, 64, 16)
