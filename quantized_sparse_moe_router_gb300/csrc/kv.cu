@@ -3,6 +3,7 @@
 // the store into the 4-bit cache, and the read-back.
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 
 #include "kvcache.cuh"
 
@@ -159,12 +160,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 // and sines are loaded once for all of them and every row's 16-byte load is
 // in flight before the first sum. Bound by HBM at many tokens; at few, by the
 // chain of loads (position -> table row) of one warp.
-constexpr int kRopeWarps = 4, kRopeRows = 4;
+constexpr int kRopeWarps = 8, kRopeRows = 4;  // warps of a CTA at most
 
 struct RopeArgs {
   fw_qk_norm_rope_args u;
-  int rows;    // n_q + n_kv, + n_kv when storing
-  int tasks;   // warps a token takes
+  int rows;        // n_q + n_kv, + n_kv when storing
+  int page_shift;
+  uint32_t head_bytes;
 };
 
 // One row's 4-bit block halves: the scale of the 4 lanes' 32 values (already
@@ -207,31 +209,36 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], uint32_t (&code)
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 3) qk_norm_rope_kernel(RopeArgs a) {
   constexpr int L = D / 8, Groups = 32 / L, NB = D / kKvBlock;  // lanes of a row, rows side by side in a warp
   const fw_qk_norm_rope_args& u = a.u;
-  const int lane = threadIdx.x & 31, grp = lane / L, l = lane % L;
+  const int lane = threadIdx.x & 31, grp = lane / L, l = lane % L, half = u.rot / 2;
+  const int64_t t = blockIdx.x;
+  const int base = (int)(blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32) * (Groups * kRopeRows), row0 = base + grp;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t task = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int64_t t = task / a.tasks;
-  if (t >= u.T) return;  // a whole warp
-  const int row0 = (int)(task % a.tasks) * (Groups * kRopeRows) + grp;
-  const int half = u.rot / 2;
+  if (base >= a.rows) return;  // a whole warp
+  const bool first = l == 0 && row0 == 0;
 
   uint4 raw[kRopeRows];
+  auto load = [&](auto queries) {  // (true: all of the warp's rows are)
 #pragma unroll
-  for (int i = 0; i < kRopeRows; ++i) {
-    const int r = row0 + i * Groups;
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (r < a.rows) {
-      const __nv_bfloat16* src = r < u.n_q ? (const __nv_bfloat16*)u.q + t * u.q_stride + r * D
-                                 : r < u.n_q + u.n_kv ? (const __nv_bfloat16*)u.k + t * u.k_stride + (r - u.n_q) * D
-                                                      : (const __nv_bfloat16*)u.v + t * u.v_stride + (r - u.n_q - u.n_kv) * D;
-      raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
+    for (int i = 0; i < kRopeRows; ++i) {
+      const int r = row0 + i * Groups;
+      const __nv_bfloat16* src = (const __nv_bfloat16*)u.q + t * u.q_stride + r * D;
+      if (!decltype(queries)::value && r >= u.n_q)
+        src = r < u.n_q + u.n_kv ? (const __nv_bfloat16*)u.k + t * u.k_stride + (r - u.n_q) * D
+                                 : (const __nv_bfloat16*)u.v + t * u.v_stride + (r - u.n_q - u.n_kv) * D;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (decltype(queries)::value || r < a.rows) raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
     }
-  }
-  // the norms' weights of this lane's dims, for queries or keys: with the rows, not after their sums
+  };
+  const bool queries = base + Groups * kRopeRows <= u.n_q;
+  if (queries)
+    load(std::true_type{});
+  else
+    load(std::false_type{});
+  // the norms' weights of this lane's dims: with the rows, not after their sums
   float ww[8];
   const float* ww_of = nullptr;
   auto weights = [&](const float* w) {
@@ -243,6 +250,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs 
   };
   auto norm_of = [&](int r) { return r < u.n_q ? u.q_norm : r < u.n_q + u.n_kv ? u.k_norm : nullptr; };
   weights(norm_of(row0));
+  int slot = -1;
+  if (u.cache && !queries) slot = u.slots[t];
   // the rotation of this lane's 8 dims: y' = y * cs + partner * sn (sn signed)
   float cs[8], sn[8];
   const bool turns = 8 * l < u.rot;
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs 
     int pos = u.positions[t];
     if (pos < 0 || pos >= u.n_pos) {
       // a padding row (-1) keeps position 0's rotation: nothing reads it
-      if (pos != -1 && l == 0 && row0 == 0) raise(u.status, FW_KV_BAD_POSITION);
+      if (pos != -1 && first) raise(u.status, FW_KV_BAD_POSITION);
       pos = 0;
     }
     const float* row = u.cos_sin + (int64_t)pos * u.rot;
@@ -270,91 +279,92 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(RopeArgs 
       }
     }
   }
-  int64_t block = -1;  // byte offset of the token's page block of head 0, and its place in the page
-  int at = 0;
-  if (u.cache) {
-    const int slot = u.slots[t];
-    if (slot >= 0 && slot / u.page < u.n_pages) {
-      block = (int64_t)(slot / u.page) * u.n_kv * kv_head_bytes(u.page, D);
-      at = slot % u.page;
-    } else if (slot != -1 && l == 0 && row0 == 0) {
-      raise(u.status, FW_KV_BAD_SLOT);
-    }
-  }
+  const int other = (lane & ~(L - 1)) + (8 * l < half ? l + half / 8 : l - half / 8);  // the partners' lane; shfl reads it mod 32
 
-#pragma unroll
-  for (int i = 0; i < kRopeRows; ++i) {
-    const int r = row0 + i * Groups;
-    float x[8];
-    bf16x2_to_f32(raw[i].x, x[0], x[1]);
-    bf16x2_to_f32(raw[i].y, x[2], x[3]);
-    bf16x2_to_f32(raw[i].z, x[4], x[5]);
-    bf16x2_to_f32(raw[i].w, x[6], x[7]);
-    const bool is_q = r < u.n_q, is_v = r >= u.n_q + u.n_kv;
-    const float* w = norm_of(r);
+  // one row: normed and rotated, in bf16
+  auto turn = [&](uint4 in, const float* w, bool rotate) {
+    float x[8], y[8];
+    bf16x2_to_f32(in.x, x[0], x[1]);
+    bf16x2_to_f32(in.y, x[2], x[3]);
+    bf16x2_to_f32(in.z, x[4], x[5]);
+    bf16x2_to_f32(in.w, x[6], x[7]);
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += x[j] * x[j];
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (w) {
-      const float inv = __fdiv_rn(1.f, __fsqrt_rn(sum * (1.f / D) + u.eps));
+      const float inv = rsqrtf(sum * (1.f / D) + u.eps);
       weights(w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], inv), ww[j]);
     }
-    // products rounded one by one, as the definition writes them
-    float y[8];
     if (u.interleaved) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
     } else {
-      const int other = (lane & ~(L - 1)) + (8 * l < half ? l + half / 8 : l - half / 8);  // shfl reads it mod 32
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xFFFFFFFFu, x[j], other);
     }
-    if (turns && !is_v) {
+    // products rounded one by one, as the definition writes them
+    if (rotate) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(y[j], sn[j]));
     }
-    uint4 o4;
-    o4.x = bf16x2_bits(x[0], x[1]);
-    o4.y = bf16x2_bits(x[2], x[3]);
-    o4.z = bf16x2_bits(x[4], x[5]);
-    o4.w = bf16x2_bits(x[6], x[7]);
-    if (r < a.rows && !is_v) {
-      __nv_bfloat16* dst = is_q ? (__nv_bfloat16*)u.q_out + t * u.q_out_stride + r * D
-                                : (__nv_bfloat16*)u.k_out + t * u.k_out_stride + (r - u.n_q) * D;
-      if (is_q || u.k_out) *reinterpret_cast<uint4*>(dst + 8 * l) = o4;
-    }
-    if (u.cache && __any_sync(0xFFFFFFFFu, !is_q && r < a.rows)) {
-      bf16x2_to_f32(o4.x, x[0], x[1]);
-      bf16x2_to_f32(o4.y, x[2], x[3]);
-      bf16x2_to_f32(o4.z, x[4], x[5]);
-      bf16x2_to_f32(o4.w, x[6], x[7]);
-      uint32_t c[8];
-      const float d = quantise8(x, c);
-      if (!is_q && r < a.rows && block >= 0) {
-        const int head = is_v ? r - u.n_q - u.n_kv : r - u.n_q;
-        uint8_t* base = (uint8_t*)u.cache + block + head * kv_head_bytes(u.page, D);
-        const KvPlanes p = kv_planes(u.page, D);
-        const int b = l / 4, q = l % 4;
-        const __nv_bfloat16 db = __float2bfloat16_rn(d);
-        if (!is_v) {
-          uint32_t word = 0;
+    return make_uint4(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]), bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7]));
+  };
+  __nv_bfloat16* const q_out = (__nv_bfloat16*)u.q_out + t * u.q_out_stride + 8 * l;
+  if (queries) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) word |= c[j] << (4 * (j / 2) + 16 * (j % 2));
-          reinterpret_cast<uint32_t*>(base + at * (D / 2))[q * NB + b] = word;
-          if (q == 0) reinterpret_cast<__nv_bfloat16*>(base + p.ks)[at * NB + b] = db;
-        } else {
-          uint16_t* codes = reinterpret_cast<uint16_t*>(base + p.vc + (at / 2) * D);
+    for (int i = 0; i < kRopeRows; ++i)
+      *reinterpret_cast<uint4*>(q_out + (row0 + i * Groups) * D) = turn(raw[i], u.q_norm, turns);
+    if (!first) return;
+  }
+  // the slot is this token's place in a page; the warp of the first row says if there is none
+  uint8_t* block = nullptr;  // the token's page block of head 0
+  if (u.cache) {
+    if (queries) slot = u.slots[t];
+    if (slot >= 0 && slot >> a.page_shift < u.n_pages)
+      block = (uint8_t*)u.cache + (int64_t)(slot >> a.page_shift) * u.n_kv * a.head_bytes;
+    else if (slot != -1 && first)
+      raise(u.status, FW_KV_BAD_SLOT);
+  }
+  if (queries) return;
+  const int at = slot & (u.page - 1);
+  const KvPlanes p = kv_planes(u.page, D);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            codes[2 * ((2 * q + k) * NB + b) + (at & 1)] =
-                (uint16_t)(c[4 * k] | c[4 * k + 1] << 4 | c[4 * k + 2] << 8 | c[4 * k + 3] << 12);
-          if (q == 0) reinterpret_cast<__nv_bfloat16*>(base + p.vs)[2 * ((at / 2) * NB + b) + (at & 1)] = db;
-        }
-      }
+  for (int i = 0; i < kRopeRows; ++i) {
+    const int r = row0 + i * Groups;
+    const bool is_q = r < u.n_q, is_v = r >= u.n_q + u.n_kv;
+    const uint4 o4 = turn(raw[i], norm_of(r), turns && !is_v);
+    if (is_q)
+      *reinterpret_cast<uint4*>(q_out + r * D) = o4;
+    else if (!is_v && u.k_out)
+      *reinterpret_cast<uint4*>((__nv_bfloat16*)u.k_out + t * u.k_out_stride + (r - u.n_q) * D + 8 * l) = o4;
+    if (!u.cache) continue;
+    float x[8];
+    bf16x2_to_f32(o4.x, x[0], x[1]);
+    bf16x2_to_f32(o4.y, x[2], x[3]);
+    bf16x2_to_f32(o4.z, x[4], x[5]);
+    bf16x2_to_f32(o4.w, x[6], x[7]);
+    uint32_t c[8];
+    const float d = quantise8(x, c);
+    if (is_q || r >= a.rows || !block) continue;
+    uint8_t* to = block + (is_v ? r - u.n_q - u.n_kv : r - u.n_q) * a.head_bytes;
+    const int b = l / 4, q = l % 4;
+    const __nv_bfloat16 db = __float2bfloat16_rn(d);
+    if (!is_v) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) word |= c[j] << (4 * (j / 2) + 16 * (j % 2));
+      reinterpret_cast<uint32_t*>(to + at * (D / 2))[q * NB + b] = word;
+      if (q == 0) reinterpret_cast<__nv_bfloat16*>(to + p.ks)[at * NB + b] = db;
+    } else {
+      uint16_t* codes = reinterpret_cast<uint16_t*>(to + p.vc + (at / 2) * D);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        codes[2 * ((2 * q + k) * NB + b) + (at & 1)] = (uint16_t)(c[4 * k] | c[4 * k + 1] << 4 | c[4 * k + 2] << 8 | c[4 * k + 3] << 12);
+      if (q == 0) reinterpret_cast<__nv_bfloat16*>(to + p.vs)[2 * ((at / 2) * NB + b) + (at & 1)] = db;
     }
   }
 }
@@ -482,13 +492,15 @@ extern "C" fw_status fw_qk_norm_rope(const fw_qk_norm_rope_args* u, void* stream
   RopeArgs a;
   a.u = *u;
   a.rows = u->n_q + u->n_kv + (u->cache ? u->n_kv : 0);
-  const int per_warp = 32 / (u->D / 8) * kRopeRows;
-  a.tasks = (a.rows + per_warp - 1) / per_warp;
-  const int64_t ctas = ((int64_t)u->T * a.tasks + kRopeWarps - 1) / kRopeWarps;
-  if (ctas > 0x7FFFFFFF) return set_error(FW_EINVAL, "fw_qk_norm_rope: too many rows for one launch");
+  a.head_bytes = u->cache ? (uint32_t)kv_head_bytes(u->page, u->D) : 0;
+  a.page_shift = 0;
+  while (u->cache && (1 << a.page_shift) < u->page) ++a.page_shift;
+  // a token's rows on the warps of one CTA, or of as few as hold them, evenly
+  const int per_warp = 32 / (u->D / 8) * kRopeRows, tasks = (a.rows + per_warp - 1) / per_warp;
+  const int ctas = (tasks + kRopeWarps - 1) / kRopeWarps, warps = (tasks + ctas - 1) / ctas;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dev::launch_dependent(u->D == 64 ? qk_norm_rope_kernel<64> : qk_norm_rope_kernel<128>,
-                                              dim3((unsigned)ctas), dim3(kRopeWarps * 32), 0, s, a);
+                                              dim3(u->T, ctas), dim3(warps * 32), 0, s, a);
   if (e != cudaSuccess) return set_error(FW_ECUDA, "fw_qk_norm_rope: launch failed");
   return FW_OK;
 }
