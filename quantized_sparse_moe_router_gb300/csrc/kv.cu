@@ -156,11 +156,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 // A head's row of D values lies in D / 8 lanes, 16 bytes each, so its sum of
 // squares, its rotation partners and a 4-bit block's extreme are a few
 // shuffles away. A warp takes kRows rows per lane group of ONE token (its
-// queries, then keys, then values, as one row index), so the token's cosines
-// and sines are loaded once for all of them and every row's 16-byte load is
-// in flight before the first sum. Bound by HBM at many tokens; at few, by the
-// chain of loads (position -> table row) of one warp.
-constexpr int kRopeWarps = 8, kRopeRows = 4;  // warps of a CTA at most
+// queries, then keys, then values, as one row index), so every row's load is
+// in flight before the first sum, and the cosines and sines are loaded once
+// for all of them and already multiplied by the norm's weights:
+//   y = (x (w cos) + x' (w' sin)) / rms(x)
+// At few tokens the chain of loads (position -> table row) is what it takes:
+// 4.4 us for one token with the store and its read-back (1 row a group 3.8, 4
+// rows 6.1). At many, instructions: 4096 tokens of 32 + 4 + 4 rows of 128
+// take 28 us, of which moving them alone is 11, the table's rows and weights 7,
+// the rows' arithmetic 10 (1 row a group 40, 4 rows 30; a persistent grid with
+// the next token's rows loaded ahead 41: too few warps to hide the arithmetic).
+constexpr int kRopeWarps = 8, kRopeRows = 2;  // warps of a CTA at most
 
 struct RopeArgs {
   fw_qk_norm_rope_args u;
@@ -209,7 +215,7 @@ __device__ __forceinline__ float quantise8(const float (&x)[8], uint32_t (&code)
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRopeWarps * 32, 3) qk_norm_rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 5) qk_norm_rope_kernel(RopeArgs a) {
   constexpr int L = D / 8, Groups = 32 / L, NB = D / kKvBlock;  // lanes of a row, rows side by side in a warp
   const fw_qk_norm_rope_args& u = a.u;
   const int lane = threadIdx.x & 31, grp = lane / L, l = lane % L, half = u.rot / 2;
@@ -218,135 +224,144 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 3) qk_norm_rope_kernel(RopeAr
   pdl_wait();
   pdl_launch_dependents();
   if (base >= a.rows) return;  // a whole warp
-  const bool first = l == 0 && row0 == 0;
+  const bool first = l == 0 && row0 == 0, turns = 8 * l < u.rot, low = 8 * l < half;
+  const bool queries = base + Groups * kRopeRows <= u.n_q;  // all of the warp's rows are
 
   uint4 raw[kRopeRows];
-  auto load = [&](auto queries) {  // (true: all of the warp's rows are)
 #pragma unroll
-    for (int i = 0; i < kRopeRows; ++i) {
-      const int r = row0 + i * Groups;
-      const __nv_bfloat16* src = (const __nv_bfloat16*)u.q + t * u.q_stride + r * D;
-      if (!decltype(queries)::value && r >= u.n_q)
-        src = r < u.n_q + u.n_kv ? (const __nv_bfloat16*)u.k + t * u.k_stride + (r - u.n_q) * D
-                                 : (const __nv_bfloat16*)u.v + t * u.v_stride + (r - u.n_q - u.n_kv) * D;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (decltype(queries)::value || r < a.rows) raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
-    }
-  };
-  const bool queries = base + Groups * kRopeRows <= u.n_q;
-  if (queries)
-    load(std::true_type{});
-  else
-    load(std::false_type{});
-  // the norms' weights of this lane's dims: with the rows, not after their sums
-  float ww[8];
-  const float* ww_of = nullptr;
-  auto weights = [&](const float* w) {
-    if (!w || w == ww_of) return;
-    ww_of = w;
-    const float4 w0 = *reinterpret_cast<const float4*>(w + 8 * l), w1 = *reinterpret_cast<const float4*>(w + 8 * l + 4);
-    ww[0] = w0.x; ww[1] = w0.y; ww[2] = w0.z; ww[3] = w0.w;
-    ww[4] = w1.x; ww[5] = w1.y; ww[6] = w1.z; ww[7] = w1.w;
-  };
-  auto norm_of = [&](int r) { return r < u.n_q ? u.q_norm : r < u.n_q + u.n_kv ? u.k_norm : nullptr; };
-  weights(norm_of(row0));
-  int slot = -1;
-  if (u.cache && !queries) slot = u.slots[t];
-  // the rotation of this lane's 8 dims: y' = y * cs + partner * sn (sn signed)
-  float cs[8], sn[8];
-  const bool turns = 8 * l < u.rot;
+  for (int i = 0; i < kRopeRows; ++i) {
+    const int r = row0 + i * Groups;
+    const __nv_bfloat16* src = (const __nv_bfloat16*)u.q + t * u.q_stride + r * D;
+    if (!queries && r >= u.n_q)
+      src = r < u.n_q + u.n_kv ? (const __nv_bfloat16*)u.k + t * u.k_stride + (r - u.n_q) * D
+                               : (const __nv_bfloat16*)u.v + t * u.v_stride + (r - u.n_q - u.n_kv) * D;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (r < a.rows) raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
+  }
+  int slot = -1, pos = 0;
+  if (u.cache && (!queries || first)) slot = u.slots[t];
   if (turns) {
-    int pos = u.positions[t];
+    pos = u.positions[t];
     if (pos < 0 || pos >= u.n_pos) {
       // a padding row (-1) keeps position 0's rotation: nothing reads it
       if (pos != -1 && first) raise(u.status, FW_KV_BAD_POSITION);
       pos = 0;
     }
-    const float* row = u.cos_sin + (int64_t)pos * u.rot;
-    if (u.interleaved) {
-      const float4 c = *reinterpret_cast<const float4*>(row + 4 * l), s = *reinterpret_cast<const float4*>(row + half + 4 * l);
-      cs[0] = cs[1] = c.x; cs[2] = cs[3] = c.y; cs[4] = cs[5] = c.z; cs[6] = cs[7] = c.w;
-      sn[1] = s.x; sn[3] = s.y; sn[5] = s.z; sn[7] = s.w;
-      sn[0] = -s.x; sn[2] = -s.y; sn[4] = -s.z; sn[6] = -s.w;
-    } else {
-      const bool low = 8 * l < half;
-      const int at = low ? 8 * l : 8 * l - half;
+  }
+  // The lane whose dims are this one's partners (shfl reads it mod 32), and
+  // those dims: with interleaved pairs the lane has them itself.
+  const int other = u.interleaved || !turns ? l : low ? l + half / 8 : l - half / 8;
+  // What a row's values are multiplied by: the norm's weight and the cosine,
+  // and for its partners' the weight there and the signed sine. The same for
+  // all of the token's queries, and for all of its keys.
+  float cw[8], sw[8];
+  const float* made_for = nullptr;
+  bool made = false;
+  auto factors = [&](const float* w) {
+    if (made && made_for == w) return;
+    made = true;
+    made_for = w;
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const float4 c = *reinterpret_cast<const float4*>(row + at + j), s = *reinterpret_cast<const float4*>(row + half + at + j);
-        cs[j] = c.x; cs[j + 1] = c.y; cs[j + 2] = c.z; cs[j + 3] = c.w;
-        sn[j] = low ? -s.x : s.x; sn[j + 1] = low ? -s.y : s.y; sn[j + 2] = low ? -s.z : s.z; sn[j + 3] = low ? -s.w : s.w;
+    for (int j = 0; j < 8; ++j) cw[j] = 1.f, sw[j] = 0.f;
+    if (turns) {
+      const float* row = u.cos_sin + (int64_t)pos * u.rot;
+      if (u.interleaved) {
+        const float4 c = *reinterpret_cast<const float4*>(row + 4 * l), s = *reinterpret_cast<const float4*>(row + half + 4 * l);
+        cw[0] = cw[1] = c.x; cw[2] = cw[3] = c.y; cw[4] = cw[5] = c.z; cw[6] = cw[7] = c.w;
+        sw[1] = s.x; sw[3] = s.y; sw[5] = s.z; sw[7] = s.w;
+        sw[0] = -s.x; sw[2] = -s.y; sw[4] = -s.z; sw[6] = -s.w;
+      } else {
+        const float* at = row + (low ? 8 * l : 8 * l - half);
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const float4 c = *reinterpret_cast<const float4*>(at + j), s = *reinterpret_cast<const float4*>(at + half + j);
+          cw[j] = c.x; cw[j + 1] = c.y; cw[j + 2] = c.z; cw[j + 3] = c.w;
+          sw[j] = low ? -s.x : s.x; sw[j + 1] = low ? -s.y : s.y; sw[j + 2] = low ? -s.z : s.z; sw[j + 3] = low ? -s.w : s.w;
+        }
       }
     }
-  }
-  const int other = (lane & ~(L - 1)) + (8 * l < half ? l + half / 8 : l - half / 8);  // the partners' lane; shfl reads it mod 32
-
-  // one row: normed and rotated, in bf16
-  auto turn = [&](uint4 in, const float* w, bool rotate) {
-    float x[8], y[8];
-    bf16x2_to_f32(in.x, x[0], x[1]);
-    bf16x2_to_f32(in.y, x[2], x[3]);
-    bf16x2_to_f32(in.z, x[4], x[5]);
-    bf16x2_to_f32(in.w, x[6], x[7]);
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += x[j] * x[j];
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (w) {
-      const float inv = rsqrtf(sum * (1.f / D) + u.eps);
-      weights(w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], inv), ww[j]);
+      const float4 w0 = *reinterpret_cast<const float4*>(w + 8 * l), w1 = *reinterpret_cast<const float4*>(w + 8 * l + 4);
+      const float4 p0 = *reinterpret_cast<const float4*>(w + 8 * other), p1 = *reinterpret_cast<const float4*>(w + 8 * other + 4);
+      cw[0] *= w0.x; cw[1] *= w0.y; cw[2] *= w0.z; cw[3] *= w0.w;
+      cw[4] *= w1.x; cw[5] *= w1.y; cw[6] *= w1.z; cw[7] *= w1.w;
+      if (u.interleaved) {
+        sw[0] *= p0.y; sw[1] *= p0.x; sw[2] *= p0.w; sw[3] *= p0.z;
+        sw[4] *= p1.y; sw[5] *= p1.x; sw[6] *= p1.w; sw[7] *= p1.z;
+      } else {
+        sw[0] *= p0.x; sw[1] *= p0.y; sw[2] *= p0.z; sw[3] *= p0.w;
+        sw[4] *= p1.x; sw[5] *= p1.y; sw[6] *= p1.z; sw[7] *= p1.w;
+      }
     }
+  };
+  auto unpack = [](uint4 v, float (&x)[8]) {
+    bf16x2_to_f32(v.x, x[0], x[1]);
+    bf16x2_to_f32(v.y, x[2], x[3]);
+    bf16x2_to_f32(v.z, x[4], x[5]);
+    bf16x2_to_f32(v.w, x[6], x[7]);
+  };
+  auto swap_halves = [](uint32_t v) { return __funnelshift_l(v, v, 16); };
+  // one row of queries or keys, normed and rotated, in bf16
+  auto turn = [&](uint4 in, bool norm) {
+    uint4 far;
     if (u.interleaved) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+      far = make_uint4(swap_halves(in.x), swap_halves(in.y), swap_halves(in.z), swap_halves(in.w));
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xFFFFFFFFu, x[j], other);
+      const int from = (lane & ~(L - 1)) + other;
+      far.x = __shfl_sync(0xFFFFFFFFu, in.x, from);
+      far.y = __shfl_sync(0xFFFFFFFFu, in.y, from);
+      far.z = __shfl_sync(0xFFFFFFFFu, in.z, from);
+      far.w = __shfl_sync(0xFFFFFFFFu, in.w, from);
     }
-    // products rounded one by one, as the definition writes them
-    if (rotate) {
+    float x[8], y[8], sum = 0.f, inv = 1.f;
+    unpack(in, x);
+    unpack(far, y);
+    if (u.q_norm || u.k_norm) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(y[j], sn[j]));
+      for (int j = 0; j < 8; ++j) sum += x[j] * x[j];
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      if (norm) inv = rsqrtf(sum * (1.f / D) + u.eps);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] *= cw[j];
+      if (turns) x[j] = fmaf(y[j], sw[j], x[j]);
+      x[j] *= inv;
     }
     return make_uint4(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]), bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7]));
   };
   __nv_bfloat16* const q_out = (__nv_bfloat16*)u.q_out + t * u.q_out_stride + 8 * l;
-  if (queries) {
-#pragma unroll
-    for (int i = 0; i < kRopeRows; ++i)
-      *reinterpret_cast<uint4*>(q_out + (row0 + i * Groups) * D) = turn(raw[i], u.q_norm, turns);
-    if (!first) return;
-  }
   // the slot is this token's place in a page; the warp of the first row says if there is none
   uint8_t* block = nullptr;  // the token's page block of head 0
-  if (u.cache) {
-    if (queries) slot = u.slots[t];
-    if (slot >= 0 && slot >> a.page_shift < u.n_pages)
-      block = (uint8_t*)u.cache + (int64_t)(slot >> a.page_shift) * u.n_kv * a.head_bytes;
-    else if (slot != -1 && first)
-      raise(u.status, FW_KV_BAD_SLOT);
+  if (slot >= 0 && slot >> a.page_shift < u.n_pages)
+    block = (uint8_t*)u.cache + (int64_t)(slot >> a.page_shift) * u.n_kv * a.head_bytes;
+  else if (slot != -1 && first)
+    raise(u.status, FW_KV_BAD_SLOT);
+  if (queries) {
+    factors(u.q_norm);
+#pragma unroll
+    for (int i = 0; i < kRopeRows; ++i)
+      *reinterpret_cast<uint4*>(q_out + (row0 + i * Groups) * D) = turn(raw[i], u.q_norm != nullptr);
+    return;
   }
-  if (queries) return;
   const int at = slot & (u.page - 1);
   const KvPlanes p = kv_planes(u.page, D);
 #pragma unroll
   for (int i = 0; i < kRopeRows; ++i) {
     const int r = row0 + i * Groups;
     const bool is_q = r < u.n_q, is_v = r >= u.n_q + u.n_kv;
-    const uint4 o4 = turn(raw[i], norm_of(r), turns && !is_v);
+    const float* w = is_q ? u.q_norm : u.k_norm;
+    if (!is_v) factors(w);
+    uint4 o4 = turn(raw[i], w != nullptr);
+    if (is_v) o4 = raw[i];
     if (is_q)
       *reinterpret_cast<uint4*>(q_out + r * D) = o4;
     else if (!is_v && u.k_out)
       *reinterpret_cast<uint4*>((__nv_bfloat16*)u.k_out + t * u.k_out_stride + (r - u.n_q) * D + 8 * l) = o4;
     if (!u.cache) continue;
     float x[8];
-    bf16x2_to_f32(o4.x, x[0], x[1]);
-    bf16x2_to_f32(o4.y, x[2], x[3]);
-    bf16x2_to_f32(o4.z, x[4], x[5]);
-    bf16x2_to_f32(o4.w, x[6], x[7]);
+    unpack(o4, x);
     uint32_t c[8];
     const float d = quantise8(x, c);
     if (is_q || r >= a.rows || !block) continue;
