@@ -400,6 +400,38 @@ def test_attn_long_contexts():
     check_attn(ref.Case([(20000, 1), (9000, 2), (13001, 1)], 8, 2, 128, 128, seed=12))
 
 
+def many_blocks(D, page, n_q=16, n_kv=2, seed=21):
+    """Prompts and chunks of several 256-row blocks, the last ones of 128 rows and
+    fewer among them, with single tokens and short drafts in between."""
+    new = [290, 261, 33, 16, 300, 1, 272, 250, 10, 288, 299, 230, 303, 2, 281]
+    past = [0, 130, 500, 3, 0, 700, 17, 128, 260, 1, 0, 511, 64, 9, 390]
+    return ref.Case([(n + s, n) for n, s in zip(new, past)], n_q, n_kv, D, page, seed=seed)
+
+
+@pytest.mark.parametrize("D, page, window, sinks", [(64, 16, 0, 0), (128, 64, 0, 0), (64, 128, 70, 3), (128, 32, 200, 0)])
+def test_attn_many_blocks(D, page, window, sinks):
+    c = many_blocks(D, page)
+    first = check_attn(c, window, sinks)
+    d = c.device()
+    for _ in range(20):
+        got = fw.attn_q4(d["q"], d["cache"], d["block_table"], d["q_start"], d["seq_lens"], c.max_q, window=window, sinks=sinks)
+    assert torch.equal(got, first)
+
+
+def test_attn_many_blocks_infinite_value():
+    """The only rows that a value block that is not finite reaches are those of its request and head at its position or after."""
+    c = many_blocks(64, 32, seed=22)
+    r, at, head = 4, 150, 1
+    want, tol = c.reference()
+    ref.write_block(c.cache[c.table[r, at // 32], head], 32, 64, at % 32, "v", np.full(64, 9), np.array([0x7F80, 0x3F80]))
+    d = c.device()
+    out = fw.attn_q4(d["q"], d["cache"], d["block_table"], d["q_start"], d["seq_lens"], c.max_q).double().cpu().numpy()
+    hit = np.zeros(out.shape, bool)
+    hit[c.starts[r] + at:c.starts[r + 1], 8 * head:8 * head + 8] = True
+    assert (np.abs(out - want) <= tol)[~hit].all()
+    assert not np.isfinite(out[hit].reshape(-1, 64)[:, :32]).any() and np.isfinite(out[hit].reshape(-1, 64)[:, 32:]).all()
+
+
 def test_attn_in_a_cuda_graph():
     c = ref.Case([(500, 1), (100, 1), (300, 40)], 8, 2, 128, 16, seed=10)
     d = c.device()
