@@ -338,9 +338,11 @@ fw_status fw_kv_export(const void *cache, int32_t n_pages, int32_t n_kv, int32_t
  *   j <= p and (window == 0 or j > p - window or j < sinks)
  * Query head h reads key/value head h / (n_q / n_kv). A row that sees nothing
  * gives zeros; what is masked is never part of a result, whatever it holds.
- * Softmax statistics and sums are fp32; probabilities and 4-bit values enter
- * the tensor cores in bf16. max_q is the largest number of new tokens of a
- * request, or more. Rows of q past q_start[R] are neither read nor written.
+ * Softmax statistics and sums are fp32. What is rounded: probabilities to bf16,
+ * and once more with their block's scale or with the value; keys stay exact
+ * (but for a part of 2^-19 of the smallest, in steps with more than 16 query
+ * rows a request). max_q is the largest number of new tokens of a request, or
+ * more. Rows of q past q_start[R] are neither read nor written.
  * workspace: DEVICE, 16-byte aligned, at least fw_attn_q4_workspace bytes; its
  * contents mean nothing between calls, and calls that may overlap need one each. */
 typedef struct {
@@ -354,7 +356,7 @@ typedef struct {
   int64_t q_stride, out_stride; /* elements between tokens; multiples of 8 */
   const void *cache;         /* DEVICE */
   const int32_t *block_table, *q_start, *seq_lens; /* DEVICE [R][max_blocks], [R + 1], [R] */
-  int32_t *status;           /* DEVICE, FW_KV_BAD_SLOT is OR-ed in; or NULL */
+  int32_t *status;           /* DEVICE, FW_KV_BAD_SLOT and FW_KV_TIMEOUT are OR-ed in; or NULL */
 } fw_attn_q4_args;
 fw_status fw_attn_q4_workspace(const fw_attn_q4_args *args, int64_t *bytes);
 fw_status fw_attn_q4(const fw_attn_q4_args *args, void *workspace, int64_t bytes, void *stream);
