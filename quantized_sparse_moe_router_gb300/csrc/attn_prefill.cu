@@ -29,6 +29,7 @@
 // 64 columns of its S. Shared memory: Q, a ring of operand tiles taken in the
 // order K0 V0 K1 V1 ..., and (not kReady) a ring of packed tiles.
 #include <initializer_list>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "tcgen05.cuh"
@@ -392,7 +393,10 @@ __device__ __forceinline__ bool bar_red_or(int id, int threads, bool pred) {
   return r != 0;
 }
 
-template <int D, bool kReady>
+// kWindow: with a sliding window nearly all tiles are edges, and what masks
+// them has to be cheap; without one only a block's last tiles are, and the
+// registers of the other tiles decide.
+template <int D, bool kReady, bool kWindow>
 __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kernel(PrefillArgs a) {
   using C = Cfg<D>;
   using Y = Lay<D, kReady>;
@@ -622,7 +626,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
       };
       for (int i = 0; i < n_t; ++i) {
         const int key0 = v.block(i0 + i) * kStageKeys;
-        const bool edge = key0 + kStageKeys - 1 > first || (u.window && key0 < last + 1 - u.window);
+        const bool edge = key0 + kStageKeys - 1 > first || (kWindow && key0 < last + 1 - u.window);
         wait(&s_full[t], i & 1);
         tc_fence_after();
         // (the first score tells that every row of Q and its scale were written)
@@ -633,62 +637,112 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         // rounding whatever their magnitude, so the maximum only moves (by
         // whole powers of two) when a tile's sum shows that some p is past
         // kMost, or when none was set yet; it is not even taken otherwise.
-        uint32_t pk[Cols / 32][16];
-        float sum;
-        for (int pass = 0;; ++pass) {
-          uint32_t s[Cols];
-          tmem_ld(s_cols + half * Cols, s);
-          if (masks) {
-            const int at = key0 + half * Cols, hi = p - at, lo = u.window ? hi - u.window : -1, sk = u.sinks - at;  // sees: c <= hi, c > lo or c < sk
-#pragma unroll
-            for (int c = 0; c < Cols; ++c)
-              if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
+        // a new maximum from this thread's largest score
+        auto move = [&](float up) {
+          if constexpr (Y::Split == 2) {
+            s_pair[half][row] = up;
+            any(false);
+            up = fmaxf(up, s_pair[half ^ 1][row]);
           }
-          if (pass == 1 || i == 0) {
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < Cols; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
-            float up = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            if constexpr (Y::Split == 2) {
-              s_pair[half][row] = up;
-              any(false);
-              up = fmaxf(up, s_pair[half ^ 1][row]);
-            }
-            up = ceilf(fmaf(up, scale, -mz));
-            // a first maximum is taken as it is, a later one only moves up
-            if (!unset) up = fmaxf(up, 0.f);
-            const bool moves = up != -INFINITY;
-            const float keep = unset ? 0.f : exp2_fast(-up);
-            if (moves) {
-              mz += up;
-              l *= keep;
-              unset = false;
-            }
-            if (i > 0)  // O holds the tiles before: S(i) came after their product
+          up = ceilf(fmaf(up, scale, -mz));
+          // a first maximum is taken as it is, a later one only moves up
+          if (!unset) up = fmaxf(up, 0.f);
+          const bool moves = up != -INFINITY;
+          const float keep = unset ? 0.f : exp2_fast(-up);
+          if (moves) {
+            mz += up;
+            l *= keep;
+            unset = false;
+          }
+          if (i > 0)  // O holds the tiles before: S(i) came after their product
 #pragma unroll 1
-              for (int c = half * (D / Y::Split); c < (half + 1) * (D / Y::Split); c += 8) {  // 8 columns at a time: S holds the registers
-                uint32_t w[8];
-                tmem_ld(o_cols + c, w);
+            for (int c = half * (D / Y::Split); c < (half + 1) * (D / Y::Split); c += 8) {  // 8 columns at a time: S holds the registers
+              uint32_t w[8];
+              tmem_ld(o_cols + c, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if (moves) w[j] = __float_as_uint(__uint_as_float(w[j]) * keep);
-                tmem_st8(o_cols + c, w);
-              }
-          }
+              for (int j = 0; j < 8; ++j)
+                if (moves) w[j] = __float_as_uint(__uint_as_float(w[j]) * keep);
+              tmem_st8(o_cols + c, w);
+            }
+        };
+        uint32_t pk[Cols / 32][16];
+        // p of scores, into pk from column c0 on, and their sum
+        auto exps = [&](auto& s, int c0) {
+          constexpr int N = sizeof(s) / 8;
           const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
           f2 sums[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < Cols / 2; ++c) {
+          for (int c = 0; c < N; ++c) {
             float x, y;
             f2_unpack(f2_fma(f2_pack_bits(s[2 * c], s[2 * c + 1]), sc, mm), x, y);
             x = exp2_fast(x);
             y = exp2_fast(y);
             sums[c & 1] = f2_add(sums[c & 1], f2_pack(x, y));
-            pk[c / 16][c % 16] = bf16x2_bits(x, y);
+            pk[(c0 / 2 + c) / 16][c % 16] = bf16x2_bits(x, y);
           }
           float x, y;
           f2_unpack(f2_add(sums[0], sums[1]), x, y);
-          sum = x + y;
+          return x + y;
+        };
+        auto largest = [](auto& s) {
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < (int)(sizeof(s) / 4); ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
+          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        };
+        float sum;
+        for (int pass = 0;; ++pass) {
+          if constexpr (!kWindow) {
+            uint32_t s[Cols];
+            tmem_ld(s_cols + half * Cols, s);
+            if (masks) {
+              // (the full condition, although there is no window: the compiler
+              // makes worse code of the shorter one: 458 us for three chunks instead of 325)
+              const int at = key0 + half * Cols, hi = p - at, lo = u.window ? hi - u.window : -1, sk = u.sinks - at;
+#pragma unroll
+              for (int c = 0; c < Cols; ++c)
+                if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
+            }
+            if (pass == 1 || i == 0) move(largest(s));
+            sum = exps(s, 0);
+          } else {
+            // 32 columns at a time; what a row sees of them (c <= hi, and c > lo
+            // or c < sk) as a word of bits: a test and a select each (three
+            // comparisons each: windowed prompts 67 us instead of 55)
+            auto scores = [&](auto masked, uint32_t(&s)[32], int w) {
+              tmem_ld(s_cols + half * Cols + 32 * w, s);
+              if constexpr (decltype(masked)::value) {
+                const int at = key0 + half * Cols + 32 * w, hi = p - at, lo = hi - u.window, sk = u.sinks - at;
+                auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+                const uint32_t there = (have >> (2 * w) & 1 ? 0xFFFFu : 0u) | (have >> (2 * w + 1) & 1 ? 0xFFFF0000u : 0u);
+                const uint32_t m = below(hi + 1) & (~below(lo + 1) | below(sk)) & there;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(m >> c & 1)) s[c] = 0xFF800000u;
+              }
+            };
+            if (pass == 1 || i == 0) {
+              float up = -INFINITY;
+#pragma unroll 1
+              for (int w = 0; w < Cols / 32; ++w) {
+                uint32_t s[32];
+                scores(std::true_type{}, s, w);
+                up = fmaxf(up, largest(s));
+              }
+              move(up);
+            }
+            auto all = [&](auto masked) {
+              float sum = 0.f;
+#pragma unroll
+              for (int w = 0; w < Cols / 32; ++w) {
+                uint32_t s[32];
+                scores(masked, s, w);
+                sum += exps(s, 32 * w);
+              }
+              return sum;
+            };
+            sum = masks ? all(std::true_type{}) : all(std::false_type{});
+          }
           // (P will lie over S: by now all warps of these rows have read it)
           if (!any(pass == 0 && (unset || sum > kMost))) break;
         }
@@ -926,32 +980,39 @@ bool prefill_ready(const fw_attn_q4_args& a, int sms) {
          ready_bytes(a) <= kReadyMost;
 }
 
+template <int D, bool kReady, bool kWindow>
+cudaError_t configure() {
+  using Y = Lay<D, kReady>;
+  const auto kernel = attn_prefill_kernel<D, kReady, kWindow>;
+  if (!kReady) {
+    // the warps' register shares (setmaxnreg) must fit what the launch gives
+    // the CTA, or the growing ones would wait for ever
+    cudaFuncAttributes f;
+    const cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs * Y::Threads < kSoftmaxRegs * 256 + kOtherRegs * (Y::Threads - 256)) return cudaErrorInvalidDeviceFunction;
+  }
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Y::SmemBytes);
+}
 template <int D>
 cudaError_t configure() {
-  // the warps' register shares (setmaxnreg) must fit what the launch gives
-  // the CTA, or the growing ones would wait for ever
-  using Y = Lay<D, false>;
-  cudaFuncAttributes f;
-  cudaError_t e = cudaFuncGetAttributes(&f, attn_prefill_kernel<D, false>);
-  if (e != cudaSuccess) return e;
-  if (f.numRegs * Y::Threads < kSoftmaxRegs * 256 + kOtherRegs * (Y::Threads - 256)) return cudaErrorInvalidDeviceFunction;
-  e = cudaFuncSetAttribute(attn_prefill_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Y::SmemBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_prefill_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, true>::SmemBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(unpack_ahead_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AheadSmem<D>::Bytes);
-  return e;
+  for (const cudaError_t e : {configure<D, false, false>(), configure<D, false, true>(), configure<D, true, false>(), configure<D, true, true>()})
+    if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(unpack_ahead_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AheadSmem<D>::Bytes);
 }
 
+template <int D, bool kReady>
+cudaError_t launch_attention(const PrefillArgs& d, int64_t ctas, cudaStream_t s) {
+  using Y = Lay<D, kReady>;
+  return launch_dependent(d.u.window ? attn_prefill_kernel<D, kReady, true> : attn_prefill_kernel<D, kReady, false>, dim3((unsigned)ctas),
+                          dim3(Y::Threads), Y::SmemBytes, s, d);
+}
 template <int D>
 cudaError_t launch(const PrefillArgs& d, int64_t ctas, cudaStream_t s) {
-  if (!d.ready)
-    return launch_dependent(attn_prefill_kernel<D, false>, dim3((unsigned)ctas), dim3(Lay<D, false>::Threads), Lay<D, false>::SmemBytes, s, d);
+  if (!d.ready) return launch_attention<D, false>(d, ctas, s);
   const int64_t tiles = most_tiles(d.u) * d.u.n_kv;
-  cudaError_t e = launch_dependent(unpack_ahead_kernel<D>, dim3((unsigned)tiles), dim3(kAheadThreads), AheadSmem<D>::Bytes, s, d);
-  if (e == cudaSuccess)
-    e = launch_dependent(attn_prefill_kernel<D, true>, dim3((unsigned)ctas), dim3(Lay<D, true>::Threads), Lay<D, true>::SmemBytes, s, d);
-  return e;
+  const cudaError_t e = launch_dependent(unpack_ahead_kernel<D>, dim3((unsigned)tiles), dim3(kAheadThreads), AheadSmem<D>::Bytes, s, d);
+  return e == cudaSuccess ? launch_attention<D, true>(d, ctas, s) : e;
 }
 
 }  // namespace
