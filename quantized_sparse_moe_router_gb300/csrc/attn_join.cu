@@ -1,8 +1,9 @@
 // Joins the partial results of rows whose keys several CTAs shared:
 //   o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i
-// A row's D / 4 lanes read 16 bytes each; with few rows (decode) the parts of a
-// row are shared out among the lane groups of a CTA, with many (prefill) every
-// group has a row of its own. Bound by the latency of reading the parts.
+// A row's D / 4 lanes read 16 bytes each. With few rows (decode) the lane groups
+// of a CTA share a row's parts; with many (prefill) every group has a row of
+// its own. Bound by launch and latency: 2-4 us of a call (48 drafts of 16 rows
+// 24.5 us; with a CTA a row, four waves of them, 28.5).
 #include "attn.cuh"
 
 namespace fw {
@@ -11,6 +12,11 @@ namespace {
 using namespace dev;
 
 constexpr int kThreads = 256;
+// Where groups share rows: rows of a CTA. Of 16 rows (several tokens a request,
+// so many requests or heads) four, so that the records' CTAs are one wave; of 8
+// one, so that the many parts of a long context are read at once (4 long
+// contexts 63.8 us a call, two rows a CTA 65.2; 64 ragged requests 49.4, 48.9).
+__host__ __device__ constexpr int share_rows(int rows_max) { return rows_max > 8 ? 4 : 1; }
 
 struct JoinArgs {
   const SplitRecord* rec;
@@ -29,12 +35,14 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const SplitRecord rec = a.rec[blockIdx.x];
-  const int l = threadIdx.x % L, grp = threadIdx.x / L, row = kShare ? blockIdx.y : blockIdx.y * Groups + grp;
-  if (rec.parts == 0 || row >= rec.rows) return;
+  const int l = threadIdx.x % L, grp = threadIdx.x / L;
+  const int here = kShare ? share_rows(a.rows_max) : Groups, share = Groups / here;  // rows of this CTA, groups of a row
+  const int row = blockIdx.y * here + grp / share, first = grp % share;
+  if (rec.parts == 0 || (!kShare && row >= rec.rows)) return;
   float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = kShare ? grp : 0; i < rec.parts; i += kShare ? Groups : 1) {
+  for (int i = row < rec.rows ? first : rec.parts; i < rec.parts; i += kShare ? share : 1) {
     const int64_t at = (int64_t)(i == 0 ? rec.slot0 : rec.slot1 + i * rec.step) * a.rows_max + row;
     const float2 ml = __ldcg(a.ml + at);
     // a part in which the row saw nothing has no output; NaN has to go on
@@ -53,15 +61,16 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinArgs a) {
     s_o[threadIdx.x] = acc;
     if (l == 0) s_ml[grp] = make_float2(m, sum);
     __syncthreads();
-    if (grp) return;
+    if (first || row >= rec.rows) return;
     float top = -INFINITY;
-    for (int i = 0; i < Groups; ++i) top = fmaxf(top, s_ml[i].x);
+    for (int i = 0; i < share; ++i) top = fmaxf(top, s_ml[grp + i].x);
     acc = make_float4(0.f, 0.f, 0.f, 0.f);
     sum = 0.f;
-    for (int i = 0; i < Groups; ++i) {
-      const float f = s_ml[i].x == -INFINITY ? 0.f : exp2_fast(s_ml[i].x - top);
-      const float4 o = s_o[i * L + l];
-      sum += s_ml[i].y * f;
+    for (int i = 0; i < share; ++i) {
+      const float2 ml = s_ml[grp + i];
+      const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+      const float4 o = s_o[(grp + i) * L + l];
+      sum += ml.y * f;
       acc.x += o.x * f;
       acc.y += o.y * f;
       acc.z += o.z * f;
@@ -81,7 +90,7 @@ cudaError_t launch_attn_join(const fw_attn_q4_args& a, const SplitRecord* rec, c
   const JoinArgs j = {rec, o, ml, (__nv_bfloat16*)a.out, a.out_stride, rows_max, a.n_q / a.n_kv};
   const bool share = rows_max <= kDecodeRows;
   const int groups = kThreads / (a.D / 4);
-  const dim3 grid(records, share ? rows_max : rows_max / groups);
+  const dim3 grid(records, rows_max / (share ? share_rows(rows_max) : groups));
   if (a.D == 64) return launch_dependent(share ? attn_join_kernel<64, true> : attn_join_kernel<64, false>, grid, dim3(kThreads), 0, s, j);
   return launch_dependent(share ? attn_join_kernel<128, true> : attn_join_kernel<128, false>, grid, dim3(kThreads), 0, s, j);
 }
