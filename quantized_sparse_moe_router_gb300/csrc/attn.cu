@@ -29,9 +29,11 @@ static fw_status check_args(const fw_attn_q4_args* a, bool pointers) {
   if (a->window < 0 || a->sinks < 0) return set_error(FW_EINVAL, "fw_attn_q4: window and sinks must not be negative");
   if ((int64_t)a->max_blocks * a->page > 0x7FFFFFFFll)
     return set_error(FW_EINVAL, "fw_attn_q4: need max_blocks * page < 2^31");
-  // a request's 128-key units over all heads are counted in 32 bits, and so is a CTA's share of all (at least 152 CTAs)
+  // a request's 128-key units over all heads are counted in 32 bits, and so is
+  // what a CTA takes of all of them: shares are equal in cost, and a pair's
+  // fixed cost is six units, so no share is more than seven times the mean
   const int64_t units = ((int64_t)a->max_blocks * a->page / 128 + 2) * a->n_kv;
-  if (units >= 1 << 30 || units / 128 * a->R >= 1 << 30)
+  if (units >= 1 << 30 || units / 32 * a->R >= 1 << 30)
     return set_error(FW_EUNSUPPORTED, "fw_attn_q4: R block-table rows of max_blocks pages are beyond any cache");
   if (!(a->scale > 0.f) || a->scale > 3e38f) return set_error(FW_EINVAL, "fw_attn_q4: scale must be positive and finite");
   if (!pointers || a->R == 0 || a->T == 0 || a->max_q == 0) return FW_OK;
