@@ -566,6 +566,73 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
         }
         it += n_here;
 
+        // Whether some value of the segment's keys is not zero, by the lanes of a row.
+        auto has_values = [&](int d4) {
+          const uint32_t group = D == 128 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
+#pragma unroll 1
+          for (int i = 0; i < n_here; ++i) {
+            const int key0 = v.block(st0 + i) * kStageKeys;
+            uint32_t bits = 0;
+#pragma unroll
+            for (int kp = d4; kp < kStageKeys / 2; kp += D / 4) {
+              const int j = key0 + 2 * kp;
+              const int id = j < S_r ? u.block_table[(int64_t)(r0 + k) * u.max_blocks + (j >> page_shift)] : -1;
+              if (id < 0 || id >= u.n_pages) continue;
+              const uint8_t* blk = (const uint8_t*)u.cache + ((int64_t)id * u.n_kv + head) * hb;
+#pragma unroll
+              for (int b = 0; b < NB; ++b) bits |= reinterpret_cast<const uint32_t*>(blk + pl.vs)[(j & (u.page - 1)) / 2 * NB + b];
+            }
+            if (__any_sync(group, (bits & 0x7FFF7FFFu) != 0)) return true;
+          }
+          return false;
+        };
+        // The same from the definition, a key at a time, by the D / 4 lanes of a
+        // row: for what the products' range does not hold (see below). acc
+        // becomes the mean of the values, sum 1.
+        auto plainly = [&](int row, int d4, float4& acc, float& top, float& sum) {
+          const uint32_t group = D == 128 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
+          const int b = d4 / 8, in = d4 % 8, p = first + row / G;
+          const uint2 qw = *reinterpret_cast<const uint2*>((const __nv_bfloat16*)u.q + (int64_t)(tok0 + row / G) * u.q_stride +
+                                                           (head * G + row % G) * D + 4 * d4);
+          float q4[4], o4[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+          bf16x2_to_f32(qw.x, q4[0], q4[1]);
+          bf16x2_to_f32(qw.y, q4[2], q4[3]);
+#pragma unroll 1
+          for (int i = 0; i < n_here; ++i) {
+            const int key0 = v.block(st0 + i) * kStageKeys, end = ::min(key0 + kStageKeys, S_r);
+#pragma unroll 1
+            for (int j = key0; j < end; ++j) {
+              if (!sees(p, j, u.window, u.sinks)) continue;
+              const int id = u.block_table[(int64_t)(r0 + k) * u.max_blocks + (j >> page_shift)], at = j & (u.page - 1);
+              if (id < 0 || id >= u.n_pages) continue;
+              const uint8_t* blk = (const uint8_t*)u.cache + ((int64_t)id * u.n_kv + head) * hb;
+              const uint32_t kw = reinterpret_cast<const uint32_t*>(blk + at * (D / 2))[in / 2 * NB + b];
+              const uint32_t vw = reinterpret_cast<const uint32_t*>(blk + pl.vc + at / 2 * D)[in * NB + b] >> (16 * (at & 1));
+              const float dk = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + pl.ks)[at * NB + b]);
+              const float dv = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + pl.vs)[2 * (at / 2 * NB + b) + (at & 1)]);
+              float sc = 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int dim = 4 * (in & 1) + e, nibble = dim / 2 + 4 * (dim % 2);
+                sc = fmaf(q4[e], (float)((int)(kw >> (4 * nibble) & 15) - 8), sc);
+              }
+              sc *= dk;
+#pragma unroll
+              for (int d = 1; d < D / 4; d <<= 1) sc += __shfl_xor_sync(group, sc, d);
+              sc *= u.scale * kLog2e;
+              const float up = fmaxf(m, sc), x = exp2_fast(sc - up);
+              l = (m == -INFINITY ? 0.f : l * exp2_fast(m - up)) + x;
+              m = up;
+              const float w = x / l;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o4[e] += w * ((float)((int)(vw >> (4 * e) & 15) - 8) * dv - o4[e]);
+            }
+          }
+          acc = make_float4(o4[0], o4[1], o4[2], o4[3]);
+          top = m == -INFINITY ? m : m + log2f(l) - kShift;
+          sum = m == -INFINITY ? 0.f : 1.f;
+        };
+
         // -------------------------------- join the eight warps, a tile of rows at a time
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -622,6 +689,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
             for (int w = 0; w < kWarps / 2; ++w) {
               const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 + r8) * C::Pitch + 4 * d4);
               acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
+            }
+            // Codes at 2^-133 and probabilities at 2^64 leave a range: products p d
+            // above 2^63 are infinite and below 2^-57 are lost. A row that has
+            // something infinite, or nothing above 2^-24 although not all values
+            // are zero, is taken plainly: about a microsecond a key, for what no
+            // model's values are. (The checks: 1 % of a call.)
+            const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
+            const uint32_t mine = D == 128 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
+            const bool finite = big < INFINITY && acc.x == acc.x && acc.y == acc.y && acc.z == acc.z && acc.w == acc.w;
+            if (ok && sum != 0.f) {
+              const bool some = __any_sync(mine, big != 0.f);
+              if (__any_sync(mine, !finite) || (!__any_sync(mine, big > 5.9e-8f * sum) && (some || has_values(d4))))
+                plainly(row, d4, acc, top, sum);
             }
             if (whole) {
               const float inv = sum == 0.f ? 0.f : 1.f / sum;

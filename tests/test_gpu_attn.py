@@ -325,6 +325,25 @@ def test_attn_extreme_scores():
     check_attn(ref.Case([(300, 1), (140, 130)], 8, 2, 128, 16, seed=5, q_gain=1.5), scale=1e-6)
 
 
+@pytest.mark.parametrize("new, n_q", [(1, 8), (20, 4), (470, 8)])
+@pytest.mark.parametrize("gains", [(1e-25, 0.0, 1.0, 1e30), (1e30, 1.0, 0.0, 1e-25), (0.0, 2.0 ** -30, 2.0 ** 30, 1e-3), (1e36, 1e36, 1e36, 1e36),
+                                   (2.0 ** -110,) * 4])
+def test_attn_values_of_any_magnitude(new, n_q, gains):
+    """Values whose magnitude changes along the context, and by block of dims
+    (whole tiles of zeros among them): each row is as exact as what it sees."""
+    S, D, page = 480, 64, 32
+    c = ref.Case([(S, new)], n_q, 1, D, page, seed=new)
+    rng = np.random.default_rng(new)
+    x = rng.standard_normal((S, 1, D)).clip(-3, 3) * np.repeat(gains, S // 4)[:, None, None] * np.repeat([1.0, 0.25], 32)
+    x = torch.from_numpy(x).to(torch.bfloat16).double().numpy()
+    codes, d = ref.quantise(x)
+    bits = ref.bf16_bits(d)
+    for j in range(S):
+        ref.write_block(c.cache[c.table[0, j // page], 0], page, D, j % page, "v", codes[j, 0], bits[j, 0])
+    c.v[0] = ref.values(codes, d).reshape(S, 1, D)
+    check_attn(c)
+
+
 def test_attn_strided_and_into_out():
     c = ref.Case([(60, 1), (90, 30)], 8, 2, 64, 16, seed=6)
     d = c.device()
