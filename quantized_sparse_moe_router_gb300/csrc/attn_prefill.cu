@@ -25,7 +25,7 @@
 // bounds it: 1024 cycles of products, about 900 of softmax, and four barriers
 // of about 175 from arrival to wake.
 //
-// Tensor memory: S0 | S1 | O0 | O1, 128 columns each; P (bf16) over the first
+// Tensor memory: S0 | S1 | O0 | O1, 128 columns each; P (f16) over the first
 // 64 columns of its S. Shared memory: Q, a ring of operand tiles taken in the
 // order K0 V0 K1 V1 ..., and (not kReady) a ring of packed tiles.
 #include <initializer_list>
@@ -44,13 +44,16 @@ constexpr int kPacked = 3, kHave = 8;
 constexpr uint32_t kTmemCols = 512;
 // not kReady: registers of the softmax warps and of the others, of 128 a thread at launch
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
-constexpr float kMost = 1048576.f;  // a row's maximum moves only when a tile's sum of p passes this
+constexpr float kMost = 32768.f;  // a row's maximum moves only when a tile's sum of p passes this (f16 holds 65504)
+
+constexpr int kWide = 1000;
 
 // What goes with an unpacked tile of a head.
 struct __align__(16) TileInfo {
   uint32_t have;                // bit g: the keys 16 g .. 16 g + 15 are there
   uint8_t flag[4];              // per 32 keys: some scale of V is not finite
-  uint32_t pad[2];
+  int32_t exp;                  // its values are 2^exp times the operand tile's, in f16; kWide: as they are, in bf16
+  uint32_t pad;
   uint8_t poison[kStageKeys];   // then: the key's blocks (bits) that are not
 };
 
@@ -88,12 +91,19 @@ struct PrefillArgs {
   float scale_log2;
 };
 
-// Keys go to f16, values to bf16. A key d (c - 8) has at most 8 + 3 significant
-// bits, so f16 holds it exactly (scores are then exact up to the fp32 sums,
-// however large); what f16 lacks in range is made up by powers of two: a
-// query row is scaled to a magnitude of 1..2, and all keys by 2^-6, which
-// leaves them 4 10^6 at the top and an absolute error of 2^-19 at the bottom.
-// Values keep bf16's range; they and the probabilities are rounded once.
+// Keys and values go to f16: d (c - 8) has at most 8 + 3 significant bits, so
+// f16 holds it exactly, and what it lacks in range is made up by powers of two.
+// Keys: a query row is scaled to a magnitude of 1..2, and all keys by 2^-6,
+// which leaves them 4 10^6 at the top and an absolute error of 2^-19 at the
+// bottom. Values: a tile's are divided by a power 2^e that brings its largest
+// scale to 2^11..2^12, and its probabilities are multiplied by it before they
+// are rounded -- as f16, so to 2^-12: the output's own rounding is then all the
+// error there is (0.0017 against 64 bits; with bf16 for both 0.0026, and 2 to 3 %
+// of the time less). A tile
+// whose scales differ by more than 2^13 (some may be keys that a row does not
+// see) or are below 2^-87 goes in bf16, values and probabilities rounded (of
+// these what f16 keeps: 2^-25 of a row's largest): each tile's product has its
+// own type.
 constexpr float kKeyScale = 1.f / 64.f;
 
 // nibbles 2 k + {0, 1} (and + 4) of a word, shifted to the low byte of each
@@ -113,21 +123,25 @@ __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ uint32_t bf16x2_op_sub136(uint32_t x) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x43084308u));
-  return r;
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t v) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return bf16x2_bits(f.x, f.y);
 }
-__device__ __forceinline__ uint32_t bf16x2_op_mul(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
-// nibbles at bit `shift` of a word's halves -> (c - 8) * d, rounded once to bf16
+// nibbles at bit `shift` of a word's halves -> (c - 8) * d, exact in f16 or
+// rounded once to bf16
+template <bool kHalf>
 __device__ __forceinline__ uint32_t unpack(uint32_t w, int shift, uint32_t mask, uint32_t d) {
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, 0x43004300, 0xEA;" : "=r"(r) : "r"(w >> shift), "r"(mask));
-  return bf16x2_op_mul(bf16x2_op_sub136(r), d);
+  if constexpr (kHalf) {
+    asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(r) : "r"(w >> shift), "r"(mask));  // 1024 + c
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x64086408u));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(d));
+  } else {
+    asm("lop3.b32 %0, %1, %2, 0x43004300, 0xEA;" : "=r"(r) : "r"(w >> shift), "r"(mask));  // 128 + c
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x43084308u));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(d));
+  }
+  return r;
 }
 __device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7F80u) != 0x7F80u; }
 
@@ -181,6 +195,30 @@ __device__ __forceinline__ void unpack_keys(uint8_t* tile, const uint8_t* pk, in
   }
 }
 
+// The exponent of a packed tile's values (see kKeyScale) from the finite scales,
+// other than zero, of the keys that are there; by a whole warp.
+template <int D>
+__device__ __forceinline__ int value_exponent(const uint8_t* pk, int lane, int page, int page_shift, uint32_t hb, const KvPlanes& pl,
+                                              int key0, int S, uint32_t have) {
+  constexpr int NB = Cfg<D>::NB;
+  uint32_t top = 0, low = 0x7F80u;
+#pragma unroll
+  for (int kp = lane; kp < kStageKeys / 2; kp += 32) {
+    const uint8_t* at = pk + ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (page / 2 - 1)) * (NB * 4);
+    const bool there = have >> (kp / 8) & 1;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t sc = *reinterpret_cast<const uint32_t*>(at + b * 4), even = sc & 0x7FFFu, odd = sc >> 16 & 0x7FFFu;
+      if (there && key0 + 2 * kp < S && even < 0x7F80u && even) top = ::max(top, even), low = ::min(low, even);
+      if (there && key0 + 2 * kp + 1 < S && odd < 0x7F80u && odd) top = ::max(top, odd), low = ::min(low, odd);
+    }
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  low = __reduce_min_sync(0xFFFFFFFFu, low);
+  if (top == 0) return 0;
+  return (top >> 7) - (low >> 7) > 12 || (low >> 7) < 40 ? kWide : (int)(top >> 7) - 127 - 11;
+}
+
 // 32 keys of a packed tile -> V operand tile, as four 8-key chunks, a lane four
 // dims of one block. key0: the tile's first key; have: its keys that are there.
 // Scales that must not enter the product -- of keys past the last or of a
@@ -190,6 +228,8 @@ template <int D>
 __device__ __forceinline__ void unpack_values(uint8_t* tile, const uint8_t* pk, int w, int lane, int page, int page_shift, uint32_t hb,
                                               const KvPlanes& pl, uint32_t mask, int key0, int S, uint32_t have, TileInfo* info) {
   constexpr int NB = Cfg<D>::NB;
+  const bool wide = info->exp == kWide;
+  const float down = __uint_as_float((uint32_t)(127 - (wide ? 0 : info->exp)) << 23);  // 2^-exp
   // byte offset of a key pair's codes and scales within the packed tile
   auto codes_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vc + (kp & (page / 2 - 1)) * D; };
   auto scales_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (page / 2 - 1)) * (NB * 4); };
@@ -244,15 +284,26 @@ __device__ __forceinline__ void unpack_values(uint8_t* tile, const uint8_t* pk, 
         if (!there || j + 1 >= S || !finite_bf16(d[k] >> 16)) d[k] &= 0xFFFFu;
       }
     }
+    if (!wide)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        d[k] = f16x2_bits(__uint_as_float(d[k] << 16) * down, __uint_as_float(d[k] & 0xFFFF0000u) * down);
     uint8_t* col = tile + (c / 8) * (D * 128) + (32 * b + 4 * g) * 128;
     const int c4 = (c & 7) ^ ((g & 1) << 2);  // ((dim & 7) = 4 (g & 1) + j)
+    auto write = [&](auto half) {
+      constexpr bool kHalf = decltype(half)::value;
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      const int j = (jj + (NB == 4 ? b : 2 * b + (g >> 1))) & 3;  // (the writes of 8 lanes fall into different banks)
-      *reinterpret_cast<uint4*>(col + j * 128 + ((c4 ^ j) << 4)) =
-          make_uint4(unpack(x[0], 4 * j, mask, d[0]), unpack(x[1], 4 * j, mask, d[1]), unpack(x[2], 4 * j, mask, d[2]),
-                     unpack(x[3], 4 * j, mask, d[3]));
-    }
+      for (int jj = 0; jj < 4; ++jj) {
+        const int j = (jj + (NB == 4 ? b : 2 * b + (g >> 1))) & 3;  // (the writes of 8 lanes fall into different banks)
+        *reinterpret_cast<uint4*>(col + j * 128 + ((c4 ^ j) << 4)) =
+            make_uint4(unpack<kHalf>(x[0], 4 * j, mask, d[0]), unpack<kHalf>(x[1], 4 * j, mask, d[1]),
+                       unpack<kHalf>(x[2], 4 * j, mask, d[2]), unpack<kHalf>(x[3], 4 * j, mask, d[3]));
+      }
+    };
+    if (wide)
+      write(std::false_type{});
+    else
+      write(std::true_type{});
   }
 }
 
@@ -356,9 +407,15 @@ __global__ void __launch_bounds__(kAheadThreads) unpack_ahead_kernel(PrefillArgs
   __syncthreads();
   if (!mbar_wait(&full, 0)) raise(u.status, FW_KV_TIMEOUT);
   const uint32_t mask = code_mask();
+  if (warp == 4) {
+    const int e = value_exponent<D>(pk, lane, u.page, page_shift, hb, pl, key0, S, info->have);
+    if (lane == 0) info->exp = e;
+  }
   if (warp < 4)
     unpack_keys<D>(smem, pk, warp, lane, u.page, page_shift, hb, pl, mask);
   else
+    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+  if (warp >= 4)
     unpack_values<D>(smem + C::TileBytes, pk, warp - 4, lane, u.page, page_shift, hb, pl, mask, key0, S, info->have, info);
   fence_proxy_async_smem();
   __syncthreads();
@@ -632,6 +689,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         // (the first score tells that every row of Q and its scale were written)
         if (i == 0) scale = a.scale_log2 * (1.f / kKeyScale) * s_qscale[row];
         const uint32_t have = s_info[i % kHave].have >> (half * (Cols / 16));
+        const int kind = s_info[i % kHave].exp, e = kind == kWide ? 0 : kind;
         const bool masks = edge || (have & ((1u << (Cols / 16)) - 1)) != (1u << (Cols / 16)) - 1;
         // P against the maximum as last set. P and O are exact to their
         // rounding whatever their magnitude, so the maximum only moves (by
@@ -644,7 +702,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
             any(false);
             up = fmaxf(up, s_pair[half ^ 1][row]);
           }
-          up = ceilf(fmaf(up, scale, -mz));
+          up = ceilf(fmaf(up, scale, (float)e - mz));
           // a first maximum is taken as it is, a later one only moves up
           if (!unset) up = fmaxf(up, 0.f);
           const bool moves = up != -INFINITY;
@@ -669,7 +727,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         // p of scores, into pk from column c0 on, and their sum
         auto exps = [&](auto& s, int c0) {
           constexpr int N = sizeof(s) / 8;
-          const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
+          const f2 sc = f2_pack(scale, scale), mm = f2_pack((float)e - mz, (float)e - mz);
           f2 sums[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < N; ++c) {
@@ -678,7 +736,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
             x = exp2_fast(x);
             y = exp2_fast(y);
             sums[c & 1] = f2_add(sums[c & 1], f2_pack(x, y));
-            pk[(c0 / 2 + c) / 16][c % 16] = bf16x2_bits(x, y);
+            pk[(c0 / 2 + c) / 16][c % 16] = f16x2_bits(x, y);
           }
           float x, y;
           f2_unpack(f2_add(sums[0], sums[1]), x, y);
@@ -746,7 +804,11 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
           // (P will lie over S: by now all warps of these rows have read it)
           if (!any(pass == 0 && (unset || sum > kMost))) break;
         }
-        l += sum;
+        if (kind == kWide) {
+#pragma unroll
+          for (int c = 0; c < Cols / 2; ++c) pk[c / 16][c % 16] = f16x2_to_bf16x2(pk[c / 16][c % 16]);
+        }
+        l = fmaf(sum, __uint_as_float((uint32_t)(127 - e) << 23), l);
 #pragma unroll
         for (int c = 0; c < Cols / 32; ++c) tmem_st16(s_cols + half * (Cols / 2) + 16 * c, pk[c]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -817,6 +879,9 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         uint32_t seq = 2 * i;
         wait(&tile_empty[seq % kTiles], ((seq / kTiles) & 1) ^ 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        // (each of the four warps finds the tile's exponent, and writes the same before it says that K is there)
+        const int e = value_exponent<D>(pk, lane, u.page, page_shift, hb, pl, v.block(i0 + i) * kStageKeys, S, s_info[i % kHave].have);
+        if (lane == 0) s_info[i % kHave].exp = e;
         unpack_keys<D>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask);
         fence_proxy_async_smem();
         __syncwarp();
@@ -860,6 +925,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         const uint32_t sv = 2 * i + 1, sk = 2 * i + 2;
         if ((!first_batch && !tile_ready(sv)) || (next && !tile_ready(sk))) break;
         if (row_tiles == 2 && !(t == 0 && first_batch) && !ready(&turn[t], (i + t) & 1)) break;
+        const uint32_t idesc_v = !first_batch && s_info[i % kHave].exp == kWide ? idesc_bf16(kRowTile, D) : idesc_f16(kRowTile, D);
         if (!first_batch && !ready(&p_full[t], i & 1)) break;  // (what comes last is what the chain waits for)
         tc_fence_after();
         if (elect_one()) {
@@ -867,7 +933,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
             const uint32_t v0 = t0 + (sv % kTiles) * (C::TileBytes >> 4);
 #pragma unroll
             for (int k = 0; k < kStageKeys / 16; ++k)
-              mma_ts_lo(o_cols, s_cols + k * 8, v0 + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), idesc_bf16(kRowTile, D), i > 0 || k != 0);
+              mma_ts_lo(o_cols, s_cols + k * 8, v0 + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), idesc_v, i > 0 || k != 0);
             mma_commit(&tile_empty[sv % kTiles]);
             if (row_tiles == 1) mma_commit(&tile_empty[sv % kTiles]);  // (the barrier counts both issuers)
           }
