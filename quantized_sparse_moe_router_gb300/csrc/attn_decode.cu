@@ -128,6 +128,87 @@ __device__ __forceinline__ Words<N> lds(uint32_t p) {
   return r;
 }
 
+// A segment of a head's keys, for what follows.
+struct Segment {
+  const uint8_t* cache;   // page 0's block of the head
+  const int32_t* pages;   // the request's
+  const __nv_bfloat16* q; // the row
+  Stages v;
+  int st0, n_here, S, p;  // its stages; positions of the request and of the row
+};
+
+// Whether some value of a segment's keys is not zero, by the D / 4 lanes of a row.
+template <int D>
+__device__ __noinline__ bool has_values(const fw_attn_q4_args& u, const Segment& g, int lane4, uint32_t group) {
+  constexpr int NB = D / kKvBlock;
+  const KvPlanes pl = kv_planes(u.page, D);
+  const int page_shift = __ffs(u.page) - 1;
+  const int64_t stride = u.n_kv * kv_head_bytes(u.page, D);
+#pragma unroll 1
+  for (int i = 0; i < g.n_here; ++i) {
+    const int key0 = g.v.block(g.st0 + i) * kStageKeys;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int kp = lane4; kp < kStageKeys / 2; kp += D / 4) {
+      const int j = key0 + 2 * kp, id = j < g.S ? g.pages[j >> page_shift] : -1;
+      if (id < 0 || id >= u.n_pages) continue;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        bits |= reinterpret_cast<const uint32_t*>(g.cache + id * stride + pl.vs)[(j & (u.page - 1)) / 2 * NB + b];
+    }
+    if (__any_sync(group, (bits & 0x7FFF7FFFu) != 0)) return true;
+  }
+  return false;
+}
+
+// A segment's result for a row from the definition, a key at a time, by its D / 4
+// lanes: the mean of the values (this lane's four dims) -> log2 of the sum of
+// 2^score (-inf: no key).
+template <int D>
+__device__ __noinline__ float plainly(const fw_attn_q4_args& u, const Segment& g, int lane4, uint32_t group, float4& mean) {
+  constexpr int NB = D / kKvBlock;
+  const KvPlanes pl = kv_planes(u.page, D);
+  const int page_shift = __ffs(u.page) - 1, b = lane4 / 8, in = lane4 % 8;
+  const int64_t stride = u.n_kv * kv_head_bytes(u.page, D);
+  const uint2 qw = *reinterpret_cast<const uint2*>(g.q + 4 * lane4);
+  float q4[4], o4[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+  bf16x2_to_f32(qw.x, q4[0], q4[1]);
+  bf16x2_to_f32(qw.y, q4[2], q4[3]);
+#pragma unroll 1
+  for (int i = 0; i < g.n_here; ++i) {
+    const int key0 = g.v.block(g.st0 + i) * kStageKeys, end = ::min(key0 + kStageKeys, g.S);
+#pragma unroll 1
+    for (int j = key0; j < end; ++j) {
+      if (!sees(g.p, j, u.window, u.sinks)) continue;
+      const int id = g.pages[j >> page_shift], at = j & (u.page - 1);
+      if (id < 0 || id >= u.n_pages) continue;
+      const uint8_t* blk = g.cache + id * stride;
+      const uint32_t kw = reinterpret_cast<const uint32_t*>(blk + at * (D / 2))[in / 2 * NB + b];
+      const uint32_t vw = reinterpret_cast<const uint32_t*>(blk + pl.vc + at / 2 * D)[in * NB + b] >> (16 * (at & 1));
+      const float dk = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + pl.ks)[at * NB + b]);
+      const float dv = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + pl.vs)[2 * (at / 2 * NB + b) + (at & 1)]);
+      float sc = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int dim = 4 * (in & 1) + e, nibble = dim / 2 + 4 * (dim % 2);
+        sc = fmaf(q4[e], (float)((int)(kw >> (4 * nibble) & 15) - 8), sc);
+      }
+      sc *= dk;
+#pragma unroll
+      for (int d = 1; d < D / 4; d <<= 1) sc += __shfl_xor_sync(group, sc, d);
+      sc *= u.scale * kLog2e;
+      const float up = fmaxf(m, sc), x = exp2_fast(sc - up);
+      l = (m == -INFINITY ? 0.f : l * exp2_fast(m - up)) + x;
+      m = up;
+      const float w = x / l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o4[e] += w * ((float)((int)(vw >> (4 * e) & 15) - 8) * dv - o4[e]);
+    }
+  }
+  mean = make_float4(o4[0], o4[1], o4[2], o4[3]);
+  return m == -INFINITY ? m : m + log2f(l);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) {
   using C = Cfg<D, NT>;
@@ -566,73 +647,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
         }
         it += n_here;
 
-        // Whether some value of the segment's keys is not zero, by the lanes of a row.
-        auto has_values = [&](int d4) {
-          const uint32_t group = D == 128 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
-#pragma unroll 1
-          for (int i = 0; i < n_here; ++i) {
-            const int key0 = v.block(st0 + i) * kStageKeys;
-            uint32_t bits = 0;
-#pragma unroll
-            for (int kp = d4; kp < kStageKeys / 2; kp += D / 4) {
-              const int j = key0 + 2 * kp;
-              const int id = j < S_r ? u.block_table[(int64_t)(r0 + k) * u.max_blocks + (j >> page_shift)] : -1;
-              if (id < 0 || id >= u.n_pages) continue;
-              const uint8_t* blk = (const uint8_t*)u.cache + ((int64_t)id * u.n_kv + head) * hb;
-#pragma unroll
-              for (int b = 0; b < NB; ++b) bits |= reinterpret_cast<const uint32_t*>(blk + pl.vs)[(j & (u.page - 1)) / 2 * NB + b];
-            }
-            if (__any_sync(group, (bits & 0x7FFF7FFFu) != 0)) return true;
-          }
-          return false;
-        };
-        // The same from the definition, a key at a time, by the D / 4 lanes of a
-        // row: for what the products' range does not hold (see below). acc
-        // becomes the mean of the values, sum 1.
-        auto plainly = [&](int row, int d4, float4& acc, float& top, float& sum) {
-          const uint32_t group = D == 128 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
-          const int b = d4 / 8, in = d4 % 8, p = first + row / G;
-          const uint2 qw = *reinterpret_cast<const uint2*>((const __nv_bfloat16*)u.q + (int64_t)(tok0 + row / G) * u.q_stride +
-                                                           (head * G + row % G) * D + 4 * d4);
-          float q4[4], o4[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-          bf16x2_to_f32(qw.x, q4[0], q4[1]);
-          bf16x2_to_f32(qw.y, q4[2], q4[3]);
-#pragma unroll 1
-          for (int i = 0; i < n_here; ++i) {
-            const int key0 = v.block(st0 + i) * kStageKeys, end = ::min(key0 + kStageKeys, S_r);
-#pragma unroll 1
-            for (int j = key0; j < end; ++j) {
-              if (!sees(p, j, u.window, u.sinks)) continue;
-              const int id = u.block_table[(int64_t)(r0 + k) * u.max_blocks + (j >> page_shift)], at = j & (u.page - 1);
-              if (id < 0 || id >= u.n_pages) continue;
-              const uint8_t* blk = (const uint8_t*)u.cache + ((int64_t)id * u.n_kv + head) * hb;
-              const uint32_t kw = reinterpret_cast<const uint32_t*>(blk + at * (D / 2))[in / 2 * NB + b];
-              const uint32_t vw = reinterpret_cast<const uint32_t*>(blk + pl.vc + at / 2 * D)[in * NB + b] >> (16 * (at & 1));
-              const float dk = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + pl.ks)[at * NB + b]);
-              const float dv = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + pl.vs)[2 * (at / 2 * NB + b) + (at & 1)]);
-              float sc = 0.f;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int dim = 4 * (in & 1) + e, nibble = dim / 2 + 4 * (dim % 2);
-                sc = fmaf(q4[e], (float)((int)(kw >> (4 * nibble) & 15) - 8), sc);
-              }
-              sc *= dk;
-#pragma unroll
-              for (int d = 1; d < D / 4; d <<= 1) sc += __shfl_xor_sync(group, sc, d);
-              sc *= u.scale * kLog2e;
-              const float up = fmaxf(m, sc), x = exp2_fast(sc - up);
-              l = (m == -INFINITY ? 0.f : l * exp2_fast(m - up)) + x;
-              m = up;
-              const float w = x / l;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o4[e] += w * ((float)((int)(vw >> (4 * e) & 15) - 8) * dv - o4[e]);
-            }
-          }
-          acc = make_float4(o4[0], o4[1], o4[2], o4[3]);
-          top = m == -INFINITY ? m : m + log2f(l) - kShift;
-          sum = m == -INFINITY ? 0.f : 1.f;
-        };
-
         // -------------------------------- join the eight warps, a tile of rows at a time
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -699,9 +713,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
             const uint32_t mine = D == 128 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
             const bool finite = big < INFINITY && acc.x == acc.x && acc.y == acc.y && acc.z == acc.z && acc.w == acc.w;
             if (ok && sum != 0.f) {
-              const bool some = __any_sync(mine, big != 0.f);
-              if (__any_sync(mine, !finite) || (!__any_sync(mine, big > 5.9e-8f * sum) && (some || has_values(d4))))
-                plainly(row, d4, acc, top, sum);
+              const bool lost = !__any_sync(mine, big > 5.9e-8f * sum), some = __any_sync(mine, big != 0.f);
+              if (__any_sync(mine, !finite) || lost) {
+                const Segment g = {(const uint8_t*)u.cache + (int64_t)head * hb, u.block_table + (int64_t)(r0 + k) * u.max_blocks,
+                                   (const __nv_bfloat16*)u.q + (int64_t)(tok0 + row / G) * u.q_stride + (head * G + row % G) * D,
+                                   v, st0, n_here, S_r, first + row / G};
+                if (!lost || some || has_values<D>(u, g, d4, mine)) {
+                  top = plainly<D>(u, g, d4, mine, acc);
+                  sum = top == -INFINITY ? 0.f : 1.f;
+                  top -= kShift;
+                }
+              }
             }
             if (whole) {
               const float inv = sum == 0.f ? 0.f : 1.f / sum;
