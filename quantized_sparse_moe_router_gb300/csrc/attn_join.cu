@@ -12,11 +12,12 @@ namespace {
 using namespace dev;
 
 constexpr int kThreads = 256;
-// Where groups share rows: rows of a CTA. Of 16 rows (several tokens a request,
-// so many requests or heads) four, so that the records' CTAs are one wave; of 8
-// one, so that the many parts of a long context are read at once (4 long
-// contexts 63.8 us a call, two rows a CTA 65.2; 64 ragged requests 49.4, 48.9).
-__host__ __device__ constexpr int share_rows(int rows_max) { return rows_max > 8 ? 4 : 1; }
+// Where groups share rows: rows of a CTA. Four of 16 rows if there are pairs
+// enough that a record has few parts, or prompts in the call (few records then
+// have any): the records' CTAs are one wave (48 drafts 24.5 us a call, a row a CTA
+// 28.5; windowed prompts 51.6, 55.7). Else one, so that many parts are read at
+// once (one token of 16 rows over 68,000 keys: 304 parts, 39 us instead of 93).
+constexpr int kFewParts = 4;  // on average
 
 struct JoinArgs {
   const SplitRecord* rec;
@@ -25,6 +26,7 @@ struct JoinArgs {
   __nv_bfloat16* out;
   int64_t out_stride;
   int rows_max, G;
+  int here;  // kShare: rows of a CTA
 };
 
 template <int D, bool kShare>
@@ -36,12 +38,12 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinArgs a) {
   pdl_launch_dependents();
   const SplitRecord rec = a.rec[blockIdx.x];
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
-  const int here = kShare ? share_rows(a.rows_max) : Groups, share = Groups / here;  // rows of this CTA, groups of a row
+  const int here = kShare ? a.here : Groups, share = Groups / here;  // rows of this CTA, groups of a row
   const int row = blockIdx.y * here + grp / share, first = grp % share;
   if (rec.parts == 0 || (!kShare && row >= rec.rows)) return;
   float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = row < rec.rows ? first : rec.parts; i < rec.parts; i += kShare ? share : 1) {
     const int64_t at = (int64_t)(i == 0 ? rec.slot0 : rec.slot1 + i * rec.step) * a.rows_max + row;
     const float2 ml = __ldcg(a.ml + at);
@@ -87,10 +89,12 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinArgs a) {
 
 cudaError_t launch_attn_join(const fw_attn_q4_args& a, const SplitRecord* rec, const float* o, const float2* ml, int records,
                              int rows_max, cudaStream_t s) {
-  const JoinArgs j = {rec, o, ml, (__nv_bfloat16*)a.out, a.out_stride, rows_max, a.n_q / a.n_kv};
   const bool share = rows_max <= kDecodeRows;
+  const bool prompts = (int64_t)a.max_q * (a.n_q / a.n_kv) > kDecodeRows;
+  const int here = rows_max > 8 && (prompts || (int64_t)a.R * a.n_kv * kFewParts >= records) ? 4 : 1;
+  const JoinArgs j = {rec, o, ml, (__nv_bfloat16*)a.out, a.out_stride, rows_max, a.n_q / a.n_kv, here};
   const int groups = kThreads / (a.D / 4);
-  const dim3 grid(records, rows_max / (share ? share_rows(rows_max) : groups));
+  const dim3 grid(records, rows_max / (share ? here : groups));
   if (a.D == 64) return launch_dependent(share ? attn_join_kernel<64, true> : attn_join_kernel<64, false>, grid, dim3(kThreads), 0, s, j);
   return launch_dependent(share ? attn_join_kernel<128, true> : attn_join_kernel<128, false>, grid, dim3(kThreads), 0, s, j);
 }
