@@ -338,14 +338,14 @@ fw_status fw_kv_export(const void *cache, int32_t n_pages, int32_t n_kv, int32_t
  *   j <= p and (window == 0 or j > p - window or j < sinks)
  * Query head h reads key/value head h / (n_q / n_kv). A row that sees nothing
  * gives zeros; what is masked is never part of a result, whatever it holds.
- * Softmax statistics and sums are fp32. Besides the output, what is rounded:
- * for requests of up to 16 query rows (new tokens x n_q / n_kv) a probability
- * to bf16, and once more with its value block's scale; for others a probability
- * to f16, 2^-12, and only where the scales of 128 neighbouring positions differ by
- * more than 2^13 it and the values to bf16. Keys are exact (for the latter
- * requests but for a part of 2^-19 of the smallest). max_q is the largest number
- * of new tokens of a request, or
- * more. Rows of q past q_start[R] are neither read nor written.
+ * Softmax statistics and sums are fp32. Besides the output, what is rounded: a
+ * probability to bf16, and once more with its value block's scale (requests of up
+ * to 16 query rows, new tokens x n_q / n_kv) or the value with its scale (others).
+ * Where requests bring 1,536 query rows and more on average it is a probability
+ * alone, to f16, 2^-12, unless the scales of 128 neighbouring positions differ by
+ * more than 2^13. Keys are exact (for requests of more than 16 rows but for a part
+ * of 2^-19 of the smallest). max_q is the largest number of new tokens of a
+ * request, or more. Rows of q past q_start[R] are neither read nor written.
  * workspace: DEVICE, 16-byte aligned, at least fw_attn_q4_workspace bytes; its
  * contents mean nothing between calls, and calls that may overlap need one each. */
 typedef struct {
