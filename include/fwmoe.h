@@ -342,8 +342,9 @@ fw_status fw_kv_export(const void *cache, int32_t n_pages, int32_t n_kv, int32_t
  * probability to bf16, and once more with its value block's scale (requests of up
  * to 16 query rows, new tokens x n_q / n_kv) or the value with its scale (others).
  * Where requests bring 1,536 query rows and more on average it is a probability
- * alone, to f16, 2^-12, unless the scales of 128 neighbouring positions differ by
- * more than 2^13. Keys are exact (for requests of more than 16 rows but for a part
+ * alone, to f16 (2^-12, and 2^-28 of the row's largest), in all 128 neighbouring
+ * positions whose blocks of values are zero or have largest magnitudes from 2^-7
+ * to 2^7. Sums of values past 2^100 may be infinite. Keys are exact (for requests of more than 16 rows but for a part
  * of 2^-19 of the smallest). max_q is the largest number of new tokens of a
  * request, or more. Rows of q past q_start[R] are neither read nor written.
  * workspace: DEVICE, 16-byte aligned, at least fw_attn_q4_workspace bytes; its

@@ -45,14 +45,16 @@ constexpr uint32_t kTmemCols = 512;
 // not kReady: registers of the softmax warps and of the others, of 128 a thread at launch
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr float kMost = 32768.f;  // a row's maximum moves only when a tile's sum of p passes this (f16 holds 65504)
-
-constexpr int kWide = 1000;
+// kReady: log2 of a row's largest p when its maximum is set. p as f16, good to
+// 2^-25 at least, is then good to 2^-28 of the row's largest. (At 8 rows of windowed
+// prompts pass kMost more often: 60.8 us instead of 53.8; at 0 52.9.)
+constexpr int kTop = 4;
 
 // What goes with an unpacked tile of a head.
 struct __align__(16) TileInfo {
   uint32_t have;                // bit g: the keys 16 g .. 16 g + 15 are there
   uint8_t flag[4];              // per 32 keys: some scale of V is not finite
-  int32_t exp;                  // its values are 2^exp times the operand tile's, in f16; kWide: as they are, in bf16
+  int32_t wide;                 // values and probabilities in bf16, else in f16
   uint32_t pad;
   uint8_t poison[kStageKeys];   // then: the key's blocks (bits) that are not
 };
@@ -95,19 +97,21 @@ struct PrefillArgs {
 // f16 holds it exactly, and what it lacks in range is made up by powers of two.
 // Keys: a query row is scaled to a magnitude of 1..2, and all keys by 2^-6,
 // which leaves them 4 10^6 at the top and an absolute error of 2^-19 at the
-// bottom. Values: a tile's are divided by a power 2^e that brings its largest
-// scale to 2^11..2^12, and its probabilities are multiplied by it before they
-// are rounded -- as f16, so to 2^-12: the output's own rounding is then all the
-// error there is (0.0017 against 64 bits; with bf16 for both 0.0026, and 2 to 3 %
-// of the time less). A tile
-// whose scales differ by more than 2^13 (some may be keys that a row does not
-// see) or are below 2^-87 goes in bf16, values and probabilities rounded (of
-// these what f16 keeps: 2^-25 of a row's largest): each tile's product has its
-// own type.
-// Where the CTA unpacks its own tiles (not kReady) all of them go in bf16: the
-// exponents would be found on the way of every tile (8 prompts of 60 to 128 tokens
+// bottom. Values: a tile whose scales all lie in [2^-10, 2^4) -- blocks with a
+// largest magnitude of 2^-7 to 2^7 -- or are zero goes in f16, exactly, and so do
+// its probabilities, to 2^-12: the output's own rounding is then all the error
+// there is (0.0017 against 64 bits; with bf16 for both 0.0026, and 2 to 3 % of the
+// time less). Any other tile goes in bf16, values and probabilities rounded: each
+// tile's product has its own type. What size a tile's values have never enters its
+// probabilities: f16 has no room for it (kTop) beside the weights themselves, and
+// what it drops at the bottom, 2^-28 of a row's largest, is nothing only as long as
+// the values it belongs to are not that much larger than the others: at most 2^14
+// times, by the window.
+// Where the CTA unpacks its own tiles (not kReady) all of them go in bf16: their
+// type would be found on the way of every tile (8 prompts of 60 to 128 tokens
 // over 4,000 to 8,000: 160 us instead of 143).
 constexpr float kKeyScale = 1.f / 64.f;
+constexpr uint32_t kNarrowLow = 127 - 10, kNarrow = 14;  // f16 tiles: lowest exponent of a scale (biased), and how many
 
 // nibbles 2 k + {0, 1} (and + 4) of a word, shifted to the low byte of each
 // half -> two f16 pairs (c - 8) d: the upper nibble stands for 16 c as it is,
@@ -126,10 +130,6 @@ __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t v) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-  return bf16x2_bits(f.x, f.y);
-}
 // nibbles at bit `shift` of a word's halves -> (c - 8) * d, exact in f16 or
 // rounded once to bf16
 template <bool kHalf>
@@ -198,28 +198,27 @@ __device__ __forceinline__ void unpack_keys(uint8_t* tile, const uint8_t* pk, in
   }
 }
 
-// The exponent of a packed tile's values (see kKeyScale) from the finite scales,
-// other than zero, of the keys that are there; by a whole warp.
+// Whether a packed tile's values need bf16 (see kKeyScale): some finite scale,
+// other than zero, of the keys that are there is outside of f16's window; by a
+// whole warp.
 template <int D>
-__device__ __forceinline__ int value_exponent(const uint8_t* pk, int lane, int page, int page_shift, uint32_t hb, const KvPlanes& pl,
-                                              int key0, int S, uint32_t have) {
+__device__ __forceinline__ bool wide_values(const uint8_t* pk, int lane, int page, int page_shift, uint32_t hb, const KvPlanes& pl,
+                                            int key0, int S, uint32_t have) {
   constexpr int NB = Cfg<D>::NB;
-  uint32_t top = 0, low = 0x7F80u;
+  bool wide = false;
 #pragma unroll
   for (int kp = lane; kp < kStageKeys / 2; kp += 32) {
     const uint8_t* at = pk + ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (page / 2 - 1)) * (NB * 4);
     const bool there = have >> (kp / 8) & 1;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const uint32_t sc = *reinterpret_cast<const uint32_t*>(at + b * 4), even = sc & 0x7FFFu, odd = sc >> 16 & 0x7FFFu;
-      if (there && key0 + 2 * kp < S && even < 0x7F80u && even) top = ::max(top, even), low = ::min(low, even);
-      if (there && key0 + 2 * kp + 1 < S && odd < 0x7F80u && odd) top = ::max(top, odd), low = ::min(low, odd);
+      const uint32_t sc = *reinterpret_cast<const uint32_t*>(at + b * 4);
+      auto outside = [](uint32_t d) { return d && d < 0x7F80u && (d >> 7) - kNarrowLow >= kNarrow; };
+      wide |= there && key0 + 2 * kp < S && outside(sc & 0x7FFFu);
+      wide |= there && key0 + 2 * kp + 1 < S && outside(sc >> 16 & 0x7FFFu);
     }
   }
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  low = __reduce_min_sync(0xFFFFFFFFu, low);
-  if (top == 0) return 0;
-  return (top >> 7) - (low >> 7) > 12 || (low >> 7) < 40 ? kWide : (int)(top >> 7) - 127 - 11;
+  return __any_sync(0xFFFFFFFFu, wide);
 }
 
 // 32 keys of a packed tile -> V operand tile, as four 8-key chunks, a lane four
@@ -227,12 +226,11 @@ __device__ __forceinline__ int value_exponent(const uint8_t* pk, int lane, int p
 // Scales that must not enter the product -- of keys past the last or of a
 // missing page (whatever is there), and what is not finite (noted for the rows
 // that see it) -- count as zero.
-template <int D, bool kScaled>
+template <int D, bool kReady>
 __device__ __forceinline__ void unpack_values(uint8_t* tile, const uint8_t* pk, int w, int lane, int page, int page_shift, uint32_t hb,
                                               const KvPlanes& pl, uint32_t mask, int key0, int S, uint32_t have, TileInfo* info) {
   constexpr int NB = Cfg<D>::NB;
-  const bool wide = !kScaled || info->exp == kWide;
-  const float down = __uint_as_float((uint32_t)(127 - (wide ? 0 : info->exp)) << 23);  // 2^-exp
+  const bool wide = !kReady || info->wide;
   // byte offset of a key pair's codes and scales within the packed tile
   auto codes_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vc + (kp & (page / 2 - 1)) * D; };
   auto scales_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (page / 2 - 1)) * (NB * 4); };
@@ -290,7 +288,7 @@ __device__ __forceinline__ void unpack_values(uint8_t* tile, const uint8_t* pk, 
     if (!wide)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        d[k] = f16x2_bits(__uint_as_float(d[k] << 16) * down, __uint_as_float(d[k] & 0xFFFF0000u) * down);
+        d[k] = f16x2_bits(__uint_as_float(d[k] << 16), __uint_as_float(d[k] & 0xFFFF0000u));
     uint8_t* col = tile + (c / 8) * (D * 128) + (32 * b + 4 * g) * 128;
     const int c4 = (c & 7) ^ ((g & 1) << 2);  // ((dim & 7) = 4 (g & 1) + j)
     auto write = [&](auto half) {
@@ -411,8 +409,8 @@ __global__ void __launch_bounds__(kAheadThreads) unpack_ahead_kernel(PrefillArgs
   if (!mbar_wait(&full, 0)) raise(u.status, FW_KV_TIMEOUT);
   const uint32_t mask = code_mask();
   if (warp == 4) {
-    const int e = value_exponent<D>(pk, lane, u.page, page_shift, hb, pl, key0, S, info->have);
-    if (lane == 0) info->exp = e;
+    const bool wide = wide_values<D>(pk, lane, u.page, page_shift, hb, pl, key0, S, info->have);
+    if (lane == 0) info->wide = wide;
   }
   if (warp < 4)
     unpack_keys<D>(smem, pk, warp, lane, u.page, page_shift, hb, pl, mask);
@@ -692,128 +690,136 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         // (the first score tells that every row of Q and its scale were written)
         if (i == 0) scale = a.scale_log2 * (1.f / kKeyScale) * s_qscale[row];
         const uint32_t have = s_info[i % kHave].have >> (half * (Cols / 16));
-        const int kind = kReady ? s_info[i % kHave].exp : kWide, e = kind == kWide ? 0 : kind;
         const bool masks = edge || (have & ((1u << (Cols / 16)) - 1)) != (1u << (Cols / 16)) - 1;
-        // P against the maximum as last set. P and O are exact to their
-        // rounding whatever their magnitude, so the maximum only moves (by
-        // whole powers of two) when a tile's sum shows that some p is past
-        // kMost, or when none was set yet; it is not even taken otherwise.
-        // a new maximum from this thread's largest score
-        auto move = [&](float up) {
-          if constexpr (Y::Split == 2) {
-            s_pair[half][row] = up;
-            any(false);
-            up = fmaxf(up, s_pair[half ^ 1][row]);
-          }
-          up = ceilf(fmaf(up, scale, (float)e - mz));
-          // a first maximum is taken as it is, a later one only moves up
-          if (!unset) up = fmaxf(up, 0.f);
-          const bool moves = up != -INFINITY;
-          const float keep = unset ? 0.f : exp2_fast(-up);
-          if (moves) {
-            mz += up;
-            l *= keep;
-            unset = false;
-          }
-          if (i > 0)  // O holds the tiles before: S(i) came after their product
-#pragma unroll 1
-            for (int c = half * (D / Y::Split); c < (half + 1) * (D / Y::Split); c += 8) {  // 8 columns at a time: S holds the registers
-              uint32_t w[8];
-              tmem_ld(o_cols + c, w);
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (moves) w[j] = __float_as_uint(__uint_as_float(w[j]) * keep);
-              tmem_st8(o_cols + c, w);
+        // A tile's scores to its P, in f16 or in bf16. The whole of it is there
+        // twice: with the two conversions beside each other in the inner loop
+        // three chunks take 413 us instead of 327.
+        auto tile = [&](auto narrow) {
+          // P against the maximum as last set. P and O are exact to their
+          // rounding whatever their magnitude, so the maximum only moves (by
+          // whole powers of two) when a tile's sum shows that some p is past
+          // kMost, or when none was set yet; it is not even taken otherwise.
+          // a new maximum from this thread's largest score
+          auto move = [&](float up) {
+            if constexpr (Y::Split == 2) {
+              s_pair[half][row] = up;
+              any(false);
+              up = fmaxf(up, s_pair[half ^ 1][row]);
             }
-        };
-        uint32_t pk[Cols / 32][16];
-        // p of scores, into pk from column c0 on, and their sum
-        auto exps = [&](auto& s, int c0) {
-          constexpr int N = sizeof(s) / 8;
-          const f2 sc = f2_pack(scale, scale), mm = f2_pack((float)e - mz, (float)e - mz);
-          f2 sums[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+            up = ceilf(fmaf(up, scale, -mz)) - (kReady ? kTop : 0);
+            // a first maximum is taken as it is, a later one only moves up
+            if (!unset) up = fmaxf(up, 0.f);
+            const bool moves = up != -INFINITY;
+            const float keep = unset ? 0.f : exp2_fast(-up);
+            if (moves) {
+              mz += up;
+              l *= keep;
+              unset = false;
+            }
+            if (i > 0)  // O holds the tiles before: S(i) came after their product
+#pragma unroll 1
+              for (int c = half * (D / Y::Split); c < (half + 1) * (D / Y::Split); c += 8) {  // 8 columns at a time: S holds the registers
+                uint32_t w[8];
+                tmem_ld(o_cols + c, w);
 #pragma unroll
-          for (int c = 0; c < N; ++c) {
+                for (int j = 0; j < 8; ++j)
+                  if (moves) w[j] = __float_as_uint(__uint_as_float(w[j]) * keep);
+                tmem_st8(o_cols + c, w);
+              }
+          };
+          uint32_t pk[Cols / 32][16];
+          // p of scores, into pk from column c0 on, and their sum
+          auto exps = [&](auto& s, int c0) {
+            constexpr int N = sizeof(s) / 8;
+            const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
+            f2 sums[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+              float x, y;
+              f2_unpack(f2_fma(f2_pack_bits(s[2 * c], s[2 * c + 1]), sc, mm), x, y);
+              x = exp2_fast(x);
+              y = exp2_fast(y);
+              sums[c & 1] = f2_add(sums[c & 1], f2_pack(x, y));
+              pk[(c0 / 2 + c) / 16][c % 16] = decltype(narrow)::value ? f16x2_bits(x, y) : bf16x2_bits(x, y);
+            }
             float x, y;
-            f2_unpack(f2_fma(f2_pack_bits(s[2 * c], s[2 * c + 1]), sc, mm), x, y);
-            x = exp2_fast(x);
-            y = exp2_fast(y);
-            sums[c & 1] = f2_add(sums[c & 1], f2_pack(x, y));
-            pk[(c0 / 2 + c) / 16][c % 16] = kReady ? f16x2_bits(x, y) : bf16x2_bits(x, y);
-          }
-          float x, y;
-          f2_unpack(f2_add(sums[0], sums[1]), x, y);
-          return x + y;
-        };
-        auto largest = [](auto& s) {
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            f2_unpack(f2_add(sums[0], sums[1]), x, y);
+            return x + y;
+          };
+          auto largest = [](auto& s) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < (int)(sizeof(s) / 4); ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
-          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        };
-        float sum;
-        for (int pass = 0;; ++pass) {
-          if constexpr (!kWindow) {
-            uint32_t s[Cols];
-            tmem_ld(s_cols + half * Cols, s);
-            if (masks) {
-              // (the full condition, although there is no window: the compiler
-              // makes worse code of the shorter one: 458 us for three chunks instead of 325)
-              const int at = key0 + half * Cols, hi = p - at, lo = u.window ? hi - u.window : -1, sk = u.sinks - at;
+            for (int c = 0; c < (int)(sizeof(s) / 4); ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
+            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          };
+          float sum;
+          for (int pass = 0;; ++pass) {
+            if constexpr (!kWindow) {
+              uint32_t s[Cols];
+              tmem_ld(s_cols + half * Cols, s);
+              if (masks) {
+                // (the full condition, although there is no window: the compiler
+                // makes worse code of the shorter one: 458 us for three chunks instead of 325)
+                const int at = key0 + half * Cols, hi = p - at, lo = u.window ? hi - u.window : -1, sk = u.sinks - at;
 #pragma unroll
-              for (int c = 0; c < Cols; ++c)
-                if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
-            }
-            if (pass == 1 || i == 0) move(largest(s));
-            sum = exps(s, 0);
-          } else {
-            // 32 columns at a time; what a row sees of them (c <= hi, and c > lo
-            // or c < sk) as a word of bits: a test and a select each (three
-            // comparisons each: windowed prompts 67 us instead of 55)
-            auto scores = [&](auto masked, uint32_t(&s)[32], int w) {
-              tmem_ld(s_cols + half * Cols + 32 * w, s);
-              if constexpr (decltype(masked)::value) {
-                const int at = key0 + half * Cols + 32 * w, hi = p - at, lo = hi - u.window, sk = u.sinks - at;
-                auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
-                const uint32_t there = (have >> (2 * w) & 1 ? 0xFFFFu : 0u) | (have >> (2 * w + 1) & 1 ? 0xFFFF0000u : 0u);
-                const uint32_t m = below(hi + 1) & (~below(lo + 1) | below(sk)) & there;
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!(m >> c & 1)) s[c] = 0xFF800000u;
+                for (int c = 0; c < Cols; ++c)
+                  if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
               }
-            };
-            if (pass == 1 || i == 0) {
-              float up = -INFINITY;
+              if (pass == 1 || i == 0) move(largest(s));
+              sum = exps(s, 0);
+            } else {
+              // 32 columns at a time; what a row sees of them (c <= hi, and c > lo
+              // or c < sk) as a word of bits: a test and a select each (three
+              // comparisons each: windowed prompts 67 us instead of 55)
+              auto scores = [&](auto masked, uint32_t(&s)[32], int w) {
+                tmem_ld(s_cols + half * Cols + 32 * w, s);
+                if constexpr (decltype(masked)::value) {
+                  const int at = key0 + half * Cols + 32 * w, hi = p - at, lo = hi - u.window, sk = u.sinks - at;
+                  auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+                  const uint32_t there = (have >> (2 * w) & 1 ? 0xFFFFu : 0u) | (have >> (2 * w + 1) & 1 ? 0xFFFF0000u : 0u);
+                  const uint32_t m = below(hi + 1) & (~below(lo + 1) | below(sk)) & there;
+#pragma unroll
+                  for (int c = 0; c < 32; ++c)
+                    if (!(m >> c & 1)) s[c] = 0xFF800000u;
+                }
+              };
+              if (pass == 1 || i == 0) {
+                float up = -INFINITY;
 #pragma unroll 1
-              for (int w = 0; w < Cols / 32; ++w) {
-                uint32_t s[32];
-                scores(std::true_type{}, s, w);
-                up = fmaxf(up, largest(s));
+                for (int w = 0; w < Cols / 32; ++w) {
+                  uint32_t s[32];
+                  scores(std::true_type{}, s, w);
+                  up = fmaxf(up, largest(s));
+                }
+                move(up);
               }
-              move(up);
+              auto all = [&](auto masked) {
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < Cols / 32; ++w) {
+                  uint32_t s[32];
+                  scores(masked, s, w);
+                  sum += exps(s, 32 * w);
+                }
+                return sum;
+              };
+              sum = masks ? all(std::true_type{}) : all(std::false_type{});
             }
-            auto all = [&](auto masked) {
-              float sum = 0.f;
-#pragma unroll
-              for (int w = 0; w < Cols / 32; ++w) {
-                uint32_t s[32];
-                scores(masked, s, w);
-                sum += exps(s, 32 * w);
-              }
-              return sum;
-            };
-            sum = masks ? all(std::true_type{}) : all(std::false_type{});
+            // (P will lie over S: by now all warps of these rows have read it)
+            if (!any(pass == 0 && (unset || sum > kMost))) break;
           }
-          // (P will lie over S: by now all warps of these rows have read it)
-          if (!any(pass == 0 && (unset || sum > kMost))) break;
-        }
-        if (kReady && kind == kWide) {
+          l += sum;
 #pragma unroll
-          for (int c = 0; c < Cols / 2; ++c) pk[c / 16][c % 16] = f16x2_to_bf16x2(pk[c / 16][c % 16]);
+          for (int c = 0; c < Cols / 32; ++c) tmem_st16(s_cols + half * (Cols / 2) + 16 * c, pk[c]);
+        };
+        if constexpr (kReady) {
+          if (__builtin_expect(s_info[i % kHave].wide, 0))
+            tile(std::false_type{});
+          else
+            tile(std::true_type{});
+        } else {
+          tile(std::false_type{});
         }
-        l = fmaf(sum, __uint_as_float((uint32_t)(127 - e) << 23), l);
-#pragma unroll
-        for (int c = 0; c < Cols / 32; ++c) tmem_st16(s_cols + half * (Cols / 2) + 16 * c, pk[c]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -925,7 +931,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         const uint32_t sv = 2 * i + 1, sk = 2 * i + 2;
         if ((!first_batch && !tile_ready(sv)) || (next && !tile_ready(sk))) break;
         if (row_tiles == 2 && !(t == 0 && first_batch) && !ready(&turn[t], (i + t) & 1)) break;
-        const uint32_t idesc_v = !kReady || (!first_batch && s_info[i % kHave].exp == kWide) ? idesc_bf16(kRowTile, D) : idesc_f16(kRowTile, D);
+        const uint32_t idesc_v = !kReady || (!first_batch && s_info[i % kHave].wide) ? idesc_bf16(kRowTile, D) : idesc_f16(kRowTile, D);
         if (!first_batch && !ready(&p_full[t], i & 1)) break;  // (what comes last is what the chain waits for)
         tc_fence_after();
         if (elect_one()) {
