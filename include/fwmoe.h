@@ -344,9 +344,12 @@ fw_status fw_kv_export(const void *cache, int32_t n_pages, int32_t n_kv, int32_t
  * Where requests bring 1,536 query rows and more on average it is a probability
  * alone, to f16 (2^-12, and 2^-28 of the row's largest), in all 128 neighbouring
  * positions whose blocks of values are zero or have largest magnitudes from 2^-7
- * to 2^7. Sums of values past 2^100 may be infinite. Keys are exact (for requests of more than 16 rows but for a part
- * of 2^-19 of the smallest). max_q is the largest number of new tokens of a
- * request, or more. Rows of q past q_start[R] are neither read nor written.
+ * to 2^7. Sums of values past 2^100 may be infinite. Keys and queries are exact
+ * (for requests of more than 16 rows but for what is below 2^-37 of the largest key
+ * of 128 neighbours, or 2^-25 of the largest element of a query row; a row with
+ * none above 2^-100 is taken to have that). max_q is the largest number of new
+ * tokens of a request, or more. Rows of q past q_start[R] are neither read nor
+ * written.
  * workspace: DEVICE, 16-byte aligned, at least fw_attn_q4_workspace bytes; its
  * contents mean nothing between calls, and calls that may overlap need one each. */
 typedef struct {

@@ -56,6 +56,7 @@ struct __align__(16) TileInfo {
   uint8_t flag[4];              // per 32 keys: some scale of V is not finite
   int32_t wide;                 // values and probabilities in bf16, else in f16
   uint32_t pad;
+  float key[4];                 // per 32 keys: the power of two their scales were divided by (kReady: all the same)
   uint8_t poison[kStageKeys];   // then: the key's blocks (bits) that are not
 };
 
@@ -94,10 +95,14 @@ struct PrefillArgs {
 };
 
 // Keys and values go to f16: d (c - 8) has at most 8 + 3 significant bits, so
-// f16 holds it exactly, and what it lacks in range is made up by powers of two.
-// Keys: a query row is scaled to a magnitude of 1..2, and all keys by 2^-6,
-// which leaves them 4 10^6 at the top and an absolute error of 2^-19 at the
-// bottom. Values: a tile whose scales all lie in [2^-10, 2^4) -- blocks with a
+// f16 holds it exactly from 2^-17 of scale to 2^13, and what it lacks in range is
+// made up by powers of two. Keys: a query row is divided by its largest
+// magnitude's power, and the keys of a tile (kReady, else of 32 positions: one
+// warp's, which need not wait for the others') by one that brings their largest
+// scale to 2^11..2^12; both go back into the factor of the scores. So keys are
+// exact unless scales of one tile differ by 2^28 and more, and then good to 2^-37 of
+// the largest key, as a row's elements below 2^-14 of its largest are to 2^-25 of that:
+// what the fp32 sums of the products leave. Values: a tile whose scales all lie in
 // largest magnitude of 2^-7 to 2^7 -- or are zero goes in f16, exactly, and so do
 // its probabilities, to 2^-12: the output's own rounding is then all the error
 // there is (0.0017 against 64 bits; with bf16 for both 0.0026, and 2 to 3 % of the
@@ -110,20 +115,18 @@ struct PrefillArgs {
 // Where the CTA unpacks its own tiles (not kReady) all of them go in bf16: their
 // type would be found on the way of every tile (8 prompts of 60 to 128 tokens
 // over 4,000 to 8,000: 160 us instead of 143).
-constexpr float kKeyScale = 1.f / 64.f;
 constexpr uint32_t kNarrowLow = 127 - 10, kNarrow = 14;  // f16 tiles: lowest exponent of a scale (biased), and how many
 
 // nibbles 2 k + {0, 1} (and + 4) of a word, shifted to the low byte of each
-// half -> two f16 pairs (c - 8) d: the upper nibble stands for 16 c as it is,
-// and takes d / 16
-__device__ __forceinline__ void unpack_f16(uint32_t w, uint32_t mask, uint32_t mask4, uint32_t d, uint32_t d16, uint32_t& lo, uint32_t& hi) {
+// half -> two f16 pairs (c - 8) d, exact; the upper nibble stands for 16 c as it is
+__device__ __forceinline__ void unpack_f16(uint32_t w, uint32_t mask, uint32_t mask4, uint32_t d, uint32_t& lo, uint32_t& hi) {
   uint32_t x, y;
   asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(x) : "r"(w), "r"(mask));        // 1024 + c
   asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(w), "r"(mask4));   // 1024 + 16 c
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0x64086408u));               // - 1032
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(y), "r"(0x64806480u));               // - 1152
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(y), "r"(0x2C002C00u), "r"(0xD480D480u));  // / 16 - 72
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(d));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(d16));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(d));
 }
 __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -158,20 +161,41 @@ __device__ __forceinline__ bool prefill_request(const PrefillArgs& a, int r, int
 }
 __device__ __forceinline__ int key_tiles(int S) { return S > 0 ? (S + kStageKeys - 1) / kStageKeys : 0; }
 
-// 32 keys of a packed tile (a lane a key) -> K operand tile.
-template <int D>
+// 32 keys of a packed tile (a lane a key) -> K operand tile. key0: the tile's
+// first key; have: its keys that are there. Only those, up to the request's last,
+// decide what the scales are divided by: anything may lie in the others' places.
+template <int D, bool kReady>
 __device__ __forceinline__ void unpack_keys(uint8_t* tile, const uint8_t* pk, int w, int lane, int page, int page_shift, uint32_t hb,
-                                            const KvPlanes& pl, uint32_t mask) {
+                                            const KvPlanes& pl, uint32_t mask, int key0, int S, uint32_t have, TileInfo* info) {
   constexpr int NB = Cfg<D>::NB;
   const int key = 32 * w + lane, at = key & (page - 1);
   const uint8_t* blk = pk + (key >> page_shift) * hb;
   const uint8_t* codes = blk + at * (D / 2);
-  uint32_t d[NB], d16[NB];
+  uint32_t sc[NB / 2], top = 0;
+#pragma unroll
+  for (int k = 0; k < NB / 2; ++k) {
+    sc[k] = reinterpret_cast<const uint32_t*>(blk + pl.ks)[at * (NB / 2) + k];
+    const uint32_t even = sc[k] & 0x7FFFu, odd = sc[k] >> 16 & 0x7FFFu;
+    top = ::max(top, ::max(even < 0x7F80u ? even : 0u, odd < 0x7F80u ? odd : 0u));
+  }
+  if (!(have >> (key / 16) & 1) || key0 + key >= S) top = 0;
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if constexpr (kReady) {  // of the tile's four warps
+    if (lane == 0) info->key[w] = __uint_as_float(top);
+    asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = ::max(top, __float_as_uint(info->key[k]));
+    asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+  }
+  // 2^e (any for zeros): between 2^-126 and 2^116
+  const int e = top ? ::max((int)(top >> 7) - 127 - 11, -126) : 0;
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+  if (lane == 0) info->key[w] = __uint_as_float((uint32_t)(127 + e) << 23);
+  uint32_t d[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const float x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(blk + pl.ks)[at * NB + b] << 16) * kKeyScale;
+    const float x = __uint_as_float(b & 1 ? sc[b / 2] & 0xFFFF0000u : sc[b / 2] << 16) * down;
     d[b] = f16x2_bits(x, x);
-    d16[b] = f16x2_bits(x * 0.0625f, x * 0.0625f);
   }
   // the 16-byte chunk 4 b + q of this key lies at ((4 (b & 1) + q) ^ (key & 7)) in panel b / 2
   uint8_t* row = tile + key * 128;
@@ -191,8 +215,8 @@ __device__ __forceinline__ void unpack_keys(uint8_t* tile, const uint8_t* pk, in
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       uint4 o;
-      unpack_f16(x[b], mask, mask << 4, d[b], d16[b], o.x, o.y);
-      unpack_f16(x[b] >> 8, mask, mask << 4, d[b], d16[b], o.z, o.w);
+      unpack_f16(x[b], mask, mask << 4, d[b], o.x, o.y);
+      unpack_f16(x[b] >> 8, mask, mask << 4, d[b], o.z, o.w);
       *reinterpret_cast<uint4*>(at_q + (b / 2) * (kStageKeys * 128) + (x4 ^ ((b & 1) << 6))) = o;
     }
   }
@@ -413,7 +437,7 @@ __global__ void __launch_bounds__(kAheadThreads) unpack_ahead_kernel(PrefillArgs
     if (lane == 0) info->wide = wide;
   }
   if (warp < 4)
-    unpack_keys<D>(smem, pk, warp, lane, u.page, page_shift, hb, pl, mask);
+    unpack_keys<D, true>(smem, pk, warp, lane, u.page, page_shift, hb, pl, mask, key0, S, info->have, info);
   else
     asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
   if (warp >= 4)
@@ -652,11 +676,11 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         uint32_t most = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
 #pragma unroll
         for (int j = 1; j < D / 8; j <<= 1) most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, j));
-        // 2^e of it; rows of zeros, tiny rows and rows that are not finite as they are
-        const uint32_t ex = ::max(most << 16, most & 0xFFFF0000u) & 0x7F800000u;
-        const bool plain = ex < (64u << 23) || ex == 0x7F800000u;
-        const float down = plain ? 1.f : __uint_as_float((254u << 23) - ex);
-        if (c == 0) s_qscale[qr] = plain ? 1.f : __uint_as_float(ex);
+        // 2^e of it, from 2^-100 to 2^126; rows that are not finite as they are
+        uint32_t ex = ::max(most << 16, most & 0xFFFF0000u) & 0x7F800000u;
+        ex = ex == 0x7F800000u ? 127u << 23 : ::min(::max(ex, 27u << 23), 253u << 23);
+        const float down = __uint_as_float((254u << 23) - ex);
+        if (c == 0) s_qscale[qr] = __uint_as_float(ex);
         const int rr = qr % kRowTile;
         *reinterpret_cast<uint4*>(sQ + (qr / kRowTile) * C::QBytes + (c / 8) * (kRowTile * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
             make_uint4(f16x2_bits(x[0] * down, x[1] * down), f16x2_bits(x[2] * down, x[3] * down),
@@ -670,7 +694,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_cols = tmem + lanes + t * 128, o_cols = tmem + lanes + 256 + t * 128;
       const int p = row < rows ? S - n_new + (row0 + row) / G : -1;
-      float mz = 0.f, l = 0.f, scale = 0.f;
+      float mz = 0.f, l = 0.f, q_scale = 0.f;
       bool unset = true;  // no maximum yet
       uint32_t poison = 0;
       int key_before = 0;
@@ -688,7 +712,14 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         wait(&s_full[t], i & 1);
         tc_fence_after();
         // (the first score tells that every row of Q and its scale were written)
-        if (i == 0) scale = a.scale_log2 * (1.f / kKeyScale) * s_qscale[row];
+        if (i == 0) q_scale = s_qscale[row];
+        // what the scores' products stand for, for each 32 keys (kReady: for all);
+        // never zero or infinite, so that -inf and 0 stay what they are
+        auto factor = [&](int g) { return fminf(fmaxf(a.scale_log2 * s_info[i % kHave].key[g] * q_scale, 1e-37f), 1e38f); };
+        constexpr int Groups = kReady ? 1 : Cols / 32;
+        float scale[Groups];
+#pragma unroll
+        for (int g = 0; g < Groups; ++g) scale[g] = factor(g);
         const uint32_t have = s_info[i % kHave].have >> (half * (Cols / 16));
         const bool masks = edge || (have & ((1u << (Cols / 16)) - 1)) != (1u << (Cols / 16)) - 1;
         // A tile's scores to its P, in f16 or in bf16. The whole of it is there
@@ -699,14 +730,14 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
           // rounding whatever their magnitude, so the maximum only moves (by
           // whole powers of two) when a tile's sum shows that some p is past
           // kMost, or when none was set yet; it is not even taken otherwise.
-          // a new maximum from this thread's largest score
+          // a new maximum from this thread's largest score, in log2
           auto move = [&](float up) {
             if constexpr (Y::Split == 2) {
               s_pair[half][row] = up;
               any(false);
               up = fmaxf(up, s_pair[half ^ 1][row]);
             }
-            up = ceilf(fmaf(up, scale, -mz)) - (kReady ? kTop : 0);
+            up = ceilf(up - mz) - (kReady ? kTop : 0);
             // a first maximum is taken as it is, a later one only moves up
             if (!unset) up = fmaxf(up, 0.f);
             const bool moves = up != -INFINITY;
@@ -731,12 +762,13 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
           // p of scores, into pk from column c0 on, and their sum
           auto exps = [&](auto& s, int c0) {
             constexpr int N = sizeof(s) / 8;
-            const f2 sc = f2_pack(scale, scale), mm = f2_pack(-mz, -mz);
+            const f2 mm = f2_pack(-mz, -mz);
             f2 sums[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < N; ++c) {
               float x, y;
-              f2_unpack(f2_fma(f2_pack_bits(s[2 * c], s[2 * c + 1]), sc, mm), x, y);
+              const float k = scale[(c0 / 32 + c / 16) % Groups];
+              f2_unpack(f2_fma(f2_pack_bits(s[2 * c], s[2 * c + 1]), f2_pack(k, k), mm), x, y);
               x = exp2_fast(x);
               y = exp2_fast(y);
               sums[c & 1] = f2_add(sums[c & 1], f2_pack(x, y));
@@ -746,10 +778,10 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
             f2_unpack(f2_add(sums[0], sums[1]), x, y);
             return x + y;
           };
-          auto largest = [](auto& s) {
+          auto largest = [](auto& s, int c0) {  // of 32 columns
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < (int)(sizeof(s) / 4); ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
+            for (int c = 0; c < 32; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c0 + c]));
             return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           };
           float sum;
@@ -765,7 +797,12 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
                 for (int c = 0; c < Cols; ++c)
                   if (!(c <= hi && (c > lo || c < sk) && (have >> (c / 16) & 1))) s[c] = 0xFF800000u;  // -inf
               }
-              if (pass == 1 || i == 0) move(largest(s));
+              if (pass == 1 || i == 0) {
+                float up = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < Cols / 32; ++w) up = fmaxf(up, largest(s, 32 * w) * scale[w % Groups]);
+                move(up);
+              }
               sum = exps(s, 0);
             } else {
               // 32 columns at a time; what a row sees of them (c <= hi, and c > lo
@@ -789,7 +826,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
                 for (int w = 0; w < Cols / 32; ++w) {
                   uint32_t s[32];
                   scores(std::true_type{}, s, w);
-                  up = fmaxf(up, largest(s));
+                  up = fmaxf(up, largest(s, 0) * factor(kReady ? 0 : w));
                 }
                 move(up);
               }
@@ -888,7 +925,8 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         uint32_t seq = 2 * i;
         wait(&tile_empty[seq % kTiles], ((seq / kTiles) & 1) ^ 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        unpack_keys<D>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask);
+        unpack_keys<D, false>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask,
+                              v.block(i0 + i) * kStageKeys, S, s_info[i % kHave].have, &s_info[i % kHave]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tile_full[seq % kTiles]);
