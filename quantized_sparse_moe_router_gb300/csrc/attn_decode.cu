@@ -52,6 +52,7 @@ constexpr int kPairCost = 6;      // units that a pair costs beside its own: see
 constexpr float kLazy = 8.f;      // a row's maximum moves only when a score passes it by 2^8
 constexpr float kShift = 64.f;    // probabilities carry 2^64
 constexpr float kOScale = 590295810358705651712.f, kLScale = 1.f / 18446744073709551616.f;  // 2^69 = 2^(133 - 64), 2^-64
+constexpr uint32_t kLeast = (127 - 48) << 7;  // 2^-48 in bf16
 constexpr uint32_t kQUp = 0x5F805F80u, kQUp16 = 0x5D805D80u;  // bf16 pairs of 2^64, 2^60
 
 template <int D, int NT>
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
         // rows stays in registers, two in shared memory.
         auto tile_q = [&](int t, uint4 (&qf)[NB]) {  // by a whole warp
           const int row = 8 * t + g;
+          uint32_t most = 0;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             uint4 w = make_uint4(0, 0, 0, 0);
@@ -444,8 +446,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
             z += __shfl_xor_sync(0xFFFFFFFFu, z, 1);
             z += __shfl_xor_sync(0xFFFFFFFFu, z, 2);
             if (q == 0) s_qz[row][b] = z * (-8.f / kOScale);
+            most = __vmaxu2(most, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
             qf[b] = make_uint4(mul_bf16x2(w.x, kQUp), mul_bf16x2(w.y, kQUp16), mul_bf16x2(w.z, kQUp), mul_bf16x2(w.w, kQUp16));
           }
+          // Products in units of 2^-69 of a row without an element of kLeast fall
+          // out of fp32: made NaN, it is taken plainly at the join.
+          most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+          most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+          most = ::max(most & 0xFFFFu, most >> 16);
+          if (q == 0 && most && most < kLeast) s_qz[row][0] = __uint_as_float(0x7FC00000u);
         };
         uint4 qf[NT == 1 ? NB : 1];
         if constexpr (NT == 1) {
@@ -705,8 +714,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
               acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
             }
             // Codes at 2^-133 and probabilities at 2^64 leave a range: products p d
-            // above 2^63 are infinite and below 2^-57 are lost. A row that has
-            // something infinite, or nothing above 2^-24 although not all values
+            // above 2^63 are infinite and below 2^-57 are lost, and so are scores of
+            // queries above 2^63 and below kLeast. A row that has
+            // something infinite or NaN, or nothing above 2^-24 although not all values
             // are zero, is taken plainly: about a microsecond a key, for what no
             // model's values are. (The checks: 1 % of a call.)
             const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));

@@ -46,6 +46,17 @@ def test_attn_tiny_queries_over_large_keys(kind, n):
     check(c)
 
 
+@pytest.mark.parametrize("n", [-100, -70, 40, 60, 90, 110])
+@pytest.mark.parametrize("heads", [8, 4])
+def test_attn_few_rows_of_queries_of_any_magnitude(n, heads):
+    """Rows that the products' units cannot hold are taken from the definition (one and two tiles of rows)."""
+    c = ref.Case([(300, 2), (200, 4), (1, 1)], heads, 2, 64, 16, seed=6)
+    scale_keys(c, n)
+    c.q = scaled(c.q, -n)
+    c.q[1] = 0
+    check(c)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_attn_keys_of_unequal_magnitude(kind):
     """A few positions with keys 2^12 times larger or smaller than their neighbours':
