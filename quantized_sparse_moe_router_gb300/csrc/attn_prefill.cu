@@ -425,7 +425,8 @@ __global__ void __launch_bounds__(kAheadThreads) unpack_ahead_kernel(PrefillArgs
   TileInfo* info = reinterpret_cast<TileInfo*>(smem + 2 * C::TileBytes);
   if (warp == 0) {
     const int key = key0 + (lane << page_shift);
-    const bool need = lane < (kStageKeys >> page_shift) && key < S;
+    // (pages in sight only: behind a window they may be others' by now)
+    const bool need = lane < (kStageKeys >> page_shift) && key < S && (key + u.page > lo_key || key < u.sinks);
     const int id = need ? u.block_table[(int64_t)r * u.max_blocks + (key >> page_shift)] : 0;
     copy_pages(pk, &full, u, need, id, head, hb, page_shift, lane, &info->have);
   }
