@@ -276,7 +276,8 @@ enum {
   FW_KV_BAD_LENGTH = 8,   /* a negative length, or one above 2^30 (taken as 0) */
   FW_KV_BAD_SLOT = 16,    /* a slot or page id outside the cache */
   FW_KV_BAD_POSITION = 32, /* a position outside the cos_sin table */
-  FW_KV_TIMEOUT = 64      /* a kernel gave up a bounded wait; its outputs mean nothing */
+  FW_KV_TIMEOUT = 64,     /* a kernel gave up a bounded wait; its outputs mean nothing */
+  FW_KV_BAD_QUERIES = 128 /* a request's q_start entries decrease, leave 0..T or bring more than max_q */
 };
 
 /* The plan of a step, made on the GPU from the requests' lengths: all DEVICE
@@ -348,8 +349,9 @@ fw_status fw_kv_export(const void *cache, int32_t n_pages, int32_t n_kv, int32_t
  * (for requests of more than 16 rows but for what is below 2^-37 of the largest key
  * of 128 neighbours, or 2^-25 of the largest element of a query row; a row with
  * none above 2^-100 is taken to have that). max_q is the largest number of new
- * tokens of a request, or more. Rows of q past q_start[R] are neither read nor
- * written.
+ * tokens of a request, or more. A request that brings more than max_q, or whose
+ * q_start entries decrease or leave 0..T, is reported and its rows are not written.
+ * Rows of q past q_start[R] are neither read nor written.
  * workspace: DEVICE, 16-byte aligned, at least fw_attn_q4_workspace bytes; its
  * contents mean nothing between calls, and calls that may overlap need one each. */
 typedef struct {
@@ -363,7 +365,7 @@ typedef struct {
   int64_t q_stride, out_stride; /* elements between tokens; multiples of 8 */
   const void *cache;         /* DEVICE */
   const int32_t *block_table, *q_start, *seq_lens; /* DEVICE [R][max_blocks], [R + 1], [R] */
-  int32_t *status;           /* DEVICE, FW_KV_BAD_SLOT and FW_KV_TIMEOUT are OR-ed in; or NULL */
+  int32_t *status;           /* DEVICE, FW_KV_BAD_SLOT, _BAD_QUERIES and _TIMEOUT are OR-ed in; or NULL */
 } fw_attn_q4_args;
 fw_status fw_attn_q4_workspace(const fw_attn_q4_args *args, int64_t *bytes);
 fw_status fw_attn_q4(const fw_attn_q4_args *args, void *workspace, int64_t bytes, void *stream);

@@ -328,7 +328,7 @@ class MoELayer:
 # are looked up on first use so that this module itself does not.
 _ATTENTION = ("KVPlan", "kv_cache", "kv_plan", "qk_norm_rope", "kv_export", "attn_q4", "FwQkNormRopeArgs", "FwAttnQ4Args",
               "KV_POOL_EMPTY", "KV_TABLE_FULL", "KV_TOKENS_FULL", "KV_BAD_LENGTH", "KV_BAD_SLOT", "KV_BAD_POSITION",
-              "KV_TIMEOUT")
+              "KV_TIMEOUT", "KV_BAD_QUERIES")
 
 
 def __getattr__(name):

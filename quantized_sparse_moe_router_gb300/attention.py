@@ -12,7 +12,7 @@ import torch
 
 import quantized_sparse_moe_router_gb300 as _fw
 
-KV_POOL_EMPTY, KV_TABLE_FULL, KV_TOKENS_FULL, KV_BAD_LENGTH, KV_BAD_SLOT, KV_BAD_POSITION, KV_TIMEOUT = 1, 2, 4, 8, 16, 32, 64
+KV_POOL_EMPTY, KV_TABLE_FULL, KV_TOKENS_FULL, KV_BAD_LENGTH, KV_BAD_SLOT, KV_BAD_POSITION, KV_TIMEOUT, KV_BAD_QUERIES = 1, 2, 4, 8, 16, 32, 64, 128
 
 KVPlan = collections.namedtuple("KVPlan", "q_start seq_lens requests positions slots counts")
 

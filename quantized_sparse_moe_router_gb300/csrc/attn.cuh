@@ -35,6 +35,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+// Whether a request's n new tokens from row q0 on are rows that the call has, no
+// more than it allows for; reported if not.
+__device__ __forceinline__ bool sound_queries(const fw_attn_q4_args& u, int q0, int n) {
+  if (n >= 0 && n <= u.max_q && q0 >= 0 && q0 <= u.T - n) return true;
+  raise(u.status, FW_KV_BAD_QUERIES);
+  return false;
+}
+
 // Whether the query at position p sees key j (j >= 0).
 __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
   return j <= p && (window == 0 || j > p - window || j < sinks);

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a) 
     q0 = u.q_start[r];
     n = u.q_start[r + 1] - q0;
     S = u.seq_lens[r];
-    if (n < 1 || n * (long long)G > kDecodeRows || q0 < 0 || q0 > u.T - n) return 0;
+    if (!sound_queries(u, q0, n) || n < 1 || n * (long long)G > kDecodeRows) return 0;
     if (S > u.max_blocks * u.page) {
       S = u.max_blocks * u.page;
       raise(u.status, FW_KV_BAD_SLOT);

@@ -157,7 +157,7 @@ __device__ __forceinline__ bool prefill_request(const PrefillArgs& a, int r, int
   q0 = u.q_start[r];
   n = u.q_start[r + 1] - q0;
   S = ::min(u.seq_lens[r], u.max_blocks * u.page);
-  return n * (long long)(u.n_q / u.n_kv) > a.min_rows && q0 >= 0 && q0 <= u.T - n;
+  return sound_queries(u, q0, n) && n * (long long)(u.n_q / u.n_kv) > a.min_rows;
 }
 __device__ __forceinline__ int key_tiles(int S) { return S > 0 ? (S + kStageKeys - 1) / kStageKeys : 0; }
 
