@@ -289,7 +289,8 @@ enum {
  * exclusive sum of new_lens; seq_lens [R] = cached + new; for each of T_cap
  * token places requests, positions and slots (-1 past the last token); counts
  * [3] = {tokens, free-list entries used, *free_used included, FW_KV_* bits}.
- * Without a page for it a token's slot, and its table entry, is -1; tokens past
+ * Without a page for it a token's slot, and its table entry, is -1; of a page id
+ * that no cache can have the slot is 2^31 - 1; tokens past
  * T_cap are not placed and the entries of pages they open not written. The next
  * step may pass this call's counts + 1 as free_used, with other counts. */
 fw_status fw_kv_plan(const int32_t *cached_lens, const int32_t *new_lens, int32_t R, int32_t page,

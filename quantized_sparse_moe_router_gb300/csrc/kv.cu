@@ -24,6 +24,7 @@ using namespace dev;
 constexpr int kPlanThreads = 512, kPlanItems = 4, kPlanChunk = kPlanThreads * kPlanItems;
 constexpr int kPlanTokens = 1024;  // tokens per CTA
 constexpr int kMaxLen = 1 << 30;
+constexpr int kMaxSlot = 0x7FFFFFFF;  // past every cache: these have fewer positions
 
 struct PlanArgs {
   const int32_t *ctx, *fresh, *free_pages, *free_used;
@@ -131,7 +132,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
       }
       a.req[t] = r;
       a.pos[t] = pos;
-      a.slot[t] = page < 0 ? -1 : (page << a.page_shift) + (pos & (P - 1));
+      // (an id that no cache has must not come out as a slot that one has)
+      a.slot[t] = page < 0 ? -1 : page > kMaxSlot >> a.page_shift ? kMaxSlot : (page << a.page_shift) + (pos & (P - 1));
     }
     __syncthreads();
   }
