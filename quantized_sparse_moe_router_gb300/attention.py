@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import math
 
 import torch
@@ -79,11 +80,16 @@ def _cache_shape(where, cache, D):
     return n_pages, n_kv, page
 
 
-def _keep(stream, *tensors):
-    """Tensors made here and used on another stream than the current one stay alive until it is done with them."""
-    other = torch.cuda.ExternalStream(stream)
-    for t in tensors:
-        t.record_stream(other)
+def _empty_on(stream, shape, dtype, device, result=True):
+    """Memory for a call on another stream than the current one, out of that
+    stream's own pool: what the current stream's pool has may still be in use by
+    its queued work, which the other does not wait for. A result is also the
+    current stream's from here on."""
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        t = _empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def kv_cache(n_pages, n_kv, D, page, device="cuda"):
@@ -107,11 +113,12 @@ def kv_plan(cached_lens, new_lens, block_table, free_pages, page, T_cap, free_us
     if T_cap < 1:
         _fail("kv_plan: T_cap must be positive")
     # one buffer for all outputs
-    buf = _empty(3 * T_cap + 2 * R + 4, dtype=_int32, device=block_table.device)
+    size, dev = 3 * T_cap + 2 * R + 4, block_table.device
     if stream is None:
+        buf = _empty(size, dtype=_int32, device=dev)
         stream = _raw_stream(buf.get_device())
     else:
-        _keep(stream, buf)
+        buf = _empty_on(stream, (size,), _int32, dev)
     at = buf.data_ptr()
     lens = at + 12 * T_cap
     rc = _fw.lib().fw_kv_plan(cached_lens.data_ptr(), new_lens.data_ptr(), R, page, block_table.data_ptr(), blocks,
@@ -167,10 +174,9 @@ def qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, i
         _not_ints(w, slots=slots)
         vs = _heads(w, "v", v, T, n_kv, D)
         v_at, cache_at, slots_at = v.data_ptr(), cache.data_ptr(), slots.data_ptr()
-    made = []
+    new = _empty if stream is None else functools.partial(_empty_on, stream)
     if q_out is None:
-        q_out, qos = _empty((T, n_q, D), dtype=_bf16, device=q.device), n_q * D
-        made.append(q_out)
+        q_out, qos = new((T, n_q, D), dtype=_bf16, device=q.device), n_q * D
     else:
         if q_out.shape != q.shape:
             _fail(f"{w}: outputs must have their inputs' shapes")
@@ -178,8 +184,7 @@ def qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, i
     kos, k_out_at = n_kv * D, None
     if k_out is None:
         if cache is None:
-            k_out = _empty((T, n_kv, D), dtype=_bf16, device=q.device)
-            made.append(k_out)
+            k_out = new((T, n_kv, D), dtype=_bf16, device=q.device)
             k_out_at = k_out.data_ptr()
     else:
         if k_out.shape != shape_k:
@@ -187,8 +192,6 @@ def qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, i
         kos, k_out_at = _heads(w, "k_out", k_out, T, n_kv, D), k_out.data_ptr()
     if stream is None:
         stream = _raw_stream(q.get_device())
-    else:
-        _keep(stream, *made)
     args = FwQkNormRopeArgs(T, n_q, n_kv, D, rot, 1 if interleaved else 0, eps, n_pos, q.data_ptr(), k.data_ptr(), v_at, qs, ks, vs,
                             q_norm_at, k_norm_at, cos_sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), k_out_at, qos, kos,
                             cache_at, slots_at, page, n_pages, None if status is None else status.data_ptr())
@@ -203,11 +206,11 @@ def kv_export(cache, slots, D, status=None, stream=None):
     n_pages, n_kv, page = _cache_shape("kv_export", cache, D)
     _not_ints("kv_export", slots=slots, status=status)
     T = slots.shape[0]
-    kv = _empty((2, T, n_kv, D), dtype=_bf16, device=cache.device)
     if stream is None:
+        kv = _empty((2, T, n_kv, D), dtype=_bf16, device=cache.device)
         stream = _raw_stream(kv.get_device())
     else:
-        _keep(stream, kv)
+        kv = _empty_on(stream, (2, T, n_kv, D), _bf16, cache.device)
     at = kv.data_ptr()
     rc = _fw.lib().fw_kv_export(cache.data_ptr(), n_pages, n_kv, D, page, slots.data_ptr(), T, at, at + 2 * T * n_kv * D,
                                 None if status is None else status.data_ptr(), stream)
@@ -236,11 +239,12 @@ def attn_q4(q, cache, block_table, q_start, seq_lens, max_q, scale=None, window=
         _fail(f"{w}: block_table [R, max_blocks], q_start [R + 1] and seq_lens [R] must agree")
     dev = q.device
     if out is None:
-        out, os, made = _empty((T, n_q, D), dtype=_bf16, device=dev), n_q * D, True
+        out = _empty((T, n_q, D), dtype=_bf16, device=dev) if stream is None else _empty_on(stream, (T, n_q, D), _bf16, dev)
+        os = n_q * D
     else:
         if out.shape != q.shape:
             _fail(f"{w}: out must have q's shape")
-        os, made = _heads(w, "out", out, T, n_q, D), False
+        os = _heads(w, "out", out, T, n_q, D)
     args = _byref(FwAttnQ4Args(R, T, max_q, n_q, n_kv, D, page, n_pages, blocks, window, sinks,
                                1.0 / math.sqrt(D) if scale is None else scale, q.data_ptr(), out.data_ptr(), qs, os,
                                cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(), seq_lens.data_ptr(),
@@ -251,15 +255,10 @@ def attn_q4(q, cache, block_table, q_start, seq_lens, max_q, scale=None, window=
         _fw._check(rc, "fw_attn_q4_workspace")
     size, at = need.value, None
     if size:
-        ws = _empty(size, dtype=_uint8, device=dev)
+        ws = _empty(size, dtype=_uint8, device=dev) if stream is None else _empty_on(stream, (size,), _uint8, dev, False)
         at = ws.data_ptr()
     if stream is None:
         stream = _raw_stream(q.get_device())
-    else:
-        if made:
-            _keep(stream, out)
-        if size:
-            _keep(stream, ws)
     rc = L.fw_attn_q4(args, at, size, stream)
     if rc:
         _fw._check(rc, "fw_attn_q4")
