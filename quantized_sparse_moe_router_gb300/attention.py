@@ -39,6 +39,9 @@ _bf16, _int32, _fp32, _uint8 = torch.bfloat16, torch.int32, torch.float32, torch
 _byref = ctypes.byref
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # not in builds of torch without CUDA
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_several = None  # more than one device, once it is known
+
 _empty = torch.empty
 
 # Small calls last a few microseconds on the GPU and more here: what is checked
@@ -67,6 +70,18 @@ def _heads(where, name, t, T, heads, D):
     if t.dtype is not _bf16 or not t.is_cuda or ((c != 1 or (b != D and heads != 1)) and T * heads):
         _not_heads(where, name, t)
     return a if T > 1 and heads else heads * D
+
+
+def _one_device(where, *tensors):
+    """The library launches on the current device: all tensors (or None) have to be there."""
+    global _several
+    if _several is None:
+        _several = torch.cuda.device_count() > 1
+    if _several:
+        now = _current_device()
+        for t in tensors:
+            if t is not None and t.get_device() != now:
+                _fail(f"{where}: a tensor is on cuda:{t.get_device()}, the current device is cuda:{now}")
 
 
 def _cache_shape(where, cache, D):
@@ -112,6 +127,7 @@ def kv_plan(cached_lens, new_lens, block_table, free_pages, page, T_cap, free_us
         _fail("kv_plan: cached_lens [R], new_lens [R] and block_table [R, max_blocks] must agree")
     if T_cap < 1:
         _fail("kv_plan: T_cap must be positive")
+    _one_device("kv_plan", cached_lens, new_lens, block_table, free_pages, free_used)
     # one buffer for all outputs
     size, dev = 3 * T_cap + 2 * R + 4, block_table.device
     if stream is None:
@@ -161,6 +177,7 @@ def qk_norm_rope(q, k, positions, cos_sin, q_norm=None, k_norm=None, eps=1e-6, i
         q_norm_at = q_norm.data_ptr()
     if k_norm is not None:
         k_norm_at = k_norm.data_ptr()
+    _one_device(w, q, k, positions, cos_sin, q_norm, k_norm, v, cache, slots, q_out, k_out, status)
     page = n_pages = vs = 0
     v_at = cache_at = slots_at = None
     if cache is not None:
@@ -205,6 +222,7 @@ def kv_export(cache, slots, D, status=None, stream=None):
     """What slots (int32 [T]) of a cache hold (fw_kv_export) -> k, v bf16 [T, n_kv, D]."""
     n_pages, n_kv, page = _cache_shape("kv_export", cache, D)
     _not_ints("kv_export", slots=slots, status=status)
+    _one_device("kv_export", cache, slots, status)
     T = slots.shape[0]
     if stream is None:
         kv = _empty((2, T, n_kv, D), dtype=_bf16, device=cache.device)
@@ -237,6 +255,7 @@ def attn_q4(q, cache, block_table, q_start, seq_lens, max_q, scale=None, window=
     R, blocks = block_table.shape
     if seq_lens.shape != (R,) or q_start.shape != (R + 1,):
         _fail(f"{w}: block_table [R, max_blocks], q_start [R + 1] and seq_lens [R] must agree")
+    _one_device(w, q, cache, block_table, q_start, seq_lens, out, status)
     dev = q.device
     if out is None:
         out = _empty((T, n_q, D), dtype=_bf16, device=dev) if stream is None else _empty_on(stream, (T, n_q, D), _bf16, dev)
