@@ -105,6 +105,10 @@ bool needs_prefill(const Handle* h) {
 
 // Record the text of a failed call for fw_moe_last_error (other source files).
 fw_status set_error(fw_status st, const char* text) { return fail(st, "%s", text); }
+fw_status set_cuda_error(cudaError_t e, const char* what) {
+  cudaGetLastError();  // said here, and not once more by the caller's next check
+  return cuda_fail(e, what);
+}
 
 }  // namespace fw
 

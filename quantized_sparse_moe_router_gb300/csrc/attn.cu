@@ -48,20 +48,23 @@ static fw_status check_args(const fw_attn_q4_args* a, bool pointers) {
   return FW_OK;
 }
 
-// The current device's SM count, its kernels configured once; 0: no such device.
-static int device_sms() {
+// The current device's SM count; its kernels are configured once.
+static cudaError_t device_sms(int* sms) {
   static std::mutex mu;
-  static int sms[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  static int known[64] = {};
+  int dev = 0, n = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> g(mu);
-  if (!sms[dev]) {
-    int n = 0;
-    if (configure_decode_attn() != cudaSuccess || configure_prefill_attn() != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return 0;
-    sms[dev] = n;
+  if (!known[dev]) {
+    cudaError_t e = configure_decode_attn();
+    if (e == cudaSuccess) e = configure_prefill_attn();
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    known[dev] = n;
   }
-  return sms[dev];
+  *sms = known[dev];
+  return cudaSuccess;
 }
 
 // Whether the decode kernel runs. Not where no request can bring few enough
@@ -80,8 +83,8 @@ extern "C" fw_status fw_attn_q4_workspace(const fw_attn_q4_args* a, int64_t* byt
   if (fw_status st = check_args(a, false); st != FW_OK) return st;
   if (a->R == 0 || a->T == 0 || a->max_q == 0) return FW_OK;
   if (fw_status st = check_device("fw_attn_q4: needs an sm_103 device"); st != FW_OK) return st;
-  const int sms = device_sms();
-  if (!sms) return set_error(FW_ECUDA, "fw_attn_q4: the device could not be set up");
+  int sms = 0;
+  if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return set_cuda_error(e, "fw_attn_q4: setting the device up");
   // (the kernels of a call run one after the other: they share the workspace)
   if (may_decode(a)) *bytes = decode_workspace(*a, sms);
   if (may_prefill(a)) *bytes = std::max(*bytes, prefill_workspace(*a, sms));
@@ -95,11 +98,12 @@ extern "C" fw_status fw_attn_q4(const fw_attn_q4_args* a, void* workspace, int64
   if (fw_status st = fw_attn_q4_workspace(a, &need); st != FW_OK) return st;
   if (need && (!workspace || bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16))
     return set_error(FW_EINVAL, "fw_attn_q4: the workspace is too small (see fw_attn_q4_workspace) or not 16-byte aligned");
-  const int sms = device_sms();
+  int sms = 0;
+  if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return set_cuda_error(e, "fw_attn_q4: setting the device up");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (may_decode(a)) e = launch_attn_decode(*a, workspace, sms, s);
   if (e == cudaSuccess && may_prefill(a)) e = launch_attn_prefill(*a, may_decode(a) ? kDecodeRows : 0, workspace, sms, s);
-  if (e != cudaSuccess) return set_error(FW_ECUDA, "fw_attn_q4: launch failed");
+  if (e != cudaSuccess) return set_cuda_error(e, "fw_attn_q4: launch");
   return FW_OK;
 }

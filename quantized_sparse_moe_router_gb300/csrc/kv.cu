@@ -2,6 +2,7 @@
 // tables, slots, positions), the norms and rotation of queries and keys with
 // the store into the 4-bit cache, and the read-back.
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -435,13 +436,14 @@ const char* kv_format_error(int n_kv, int page, int64_t n_pages) {
 
 // Refuses devices other than sm_103 (the only code in this library), once per device.
 fw_status check_device(const char* text) {
-  static bool ok[64] = {};
+  static std::atomic<bool> ok[64] = {};
   int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_error(FW_ECUDA, text);
-  if (ok[dev]) return FW_OK;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return set_error(FW_ECUDA, text);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess && ok[dev]) return FW_OK;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (e != cudaSuccess) return set_cuda_error(e, text);
   if (major != 10 || minor != 3) return set_error(FW_EUNSUPPORTED, text);
   ok[dev] = true;
   return FW_OK;
@@ -473,9 +475,9 @@ extern "C" fw_status fw_kv_plan(const int32_t* cached_lens, const int32_t* new_l
   PlanArgs a = {cached_lens, new_lens, free_pages, free_used, block_table, R, max_blocks, n_free, 0, T_cap,
                 q_start, seq_lens, requests, positions, slots, counts};
   while ((1 << a.page_shift) < page) ++a.page_shift;
-  if (dev::launch_dependent(plan_kernel, dim3((T_cap + kPlanTokens - 1) / kPlanTokens), dim3(kPlanThreads), 0,
-                            static_cast<cudaStream_t>(stream), a) != cudaSuccess)
-    return set_error(FW_ECUDA, "fw_kv_plan: launch failed");
+  const cudaError_t e = dev::launch_dependent(plan_kernel, dim3((T_cap + kPlanTokens - 1) / kPlanTokens), dim3(kPlanThreads), 0,
+                                              static_cast<cudaStream_t>(stream), a);
+  if (e != cudaSuccess) return set_cuda_error(e, "fw_kv_plan: launch");
   return FW_OK;
 }
 
@@ -518,7 +520,7 @@ extern "C" fw_status fw_qk_norm_rope(const fw_qk_norm_rope_args* u, void* stream
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dev::launch_dependent(u->D == 64 ? qk_norm_rope_kernel<64> : qk_norm_rope_kernel<128>,
                                               dim3(u->T, ctas), dim3(warps * 32), 0, s, a);
-  if (e != cudaSuccess) return set_error(FW_ECUDA, "fw_qk_norm_rope: launch failed");
+  if (e != cudaSuccess) return set_cuda_error(e, "fw_qk_norm_rope: launch");
   return FW_OK;
 }
 
@@ -537,6 +539,6 @@ extern "C" fw_status fw_kv_export(const void* cache, int32_t n_pages, int32_t n_
   const cudaError_t e = dev::launch_dependent(D == 64 ? kv_export_kernel<64> : kv_export_kernel<128>, dim3((unsigned)ctas),
                                               dim3(256), 0, static_cast<cudaStream_t>(stream), (const uint8_t*)cache,
                                               n_pages, n_kv, page, slots, rows, (__nv_bfloat16*)k, (__nv_bfloat16*)v, status);
-  if (e != cudaSuccess) return set_error(FW_ECUDA, "fw_kv_export: launch failed");
+  if (e != cudaSuccess) return set_cuda_error(e, "fw_kv_export: launch");
   return FW_OK;
 }
