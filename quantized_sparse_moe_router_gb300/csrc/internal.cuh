@@ -178,8 +178,6 @@ inline cudaError_t allow_max_dynamic_smem(K kernel) {
 
 // Record the text of a failed call for fw_moe_last_error; returns st.
 fw_status set_error(fw_status st, const char* text);
-// The same for a CUDA call that failed, with its error's name and text.
-fw_status set_cuda_error(cudaError_t e, const char* what);
 
 // ---------------------------------------------------------------- launchers
 cudaError_t configure_route_kernels();

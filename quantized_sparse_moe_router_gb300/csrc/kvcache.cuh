@@ -36,6 +36,8 @@ __host__ __device__ inline KvPlanes kv_planes(int page, int D) {
 // Text of what is wrong with a cache's shape, or null; refusal of devices other than sm_103.
 const char* kv_format_error(int n_kv, int page, int64_t n_pages);
 fw_status check_device(const char* text);
+// Records the error of a CUDA call that failed, with its name and text, for fw_moe_last_error; returns the status.
+fw_status set_cuda_error(cudaError_t e, const char* what);
 
 namespace dev {
 
