@@ -27,8 +27,9 @@ static fw_status check_args(const fw_attn_q4_args* a, bool pointers) {
   if (a->R < 0 || a->R > (1 << 20) || a->T < 0 || a->max_q < 0 || a->max_q > a->T || a->max_blocks < 1)
     return set_error(FW_EINVAL, "fw_attn_q4: need 0 <= R <= 2^20, 0 <= max_q <= T and max_blocks >= 1");
   if (a->window < 0 || a->sinks < 0) return set_error(FW_EINVAL, "fw_attn_q4: window and sinks must not be negative");
-  if ((int64_t)a->max_blocks * a->page > 0x7FFFFFFFll)
-    return set_error(FW_EINVAL, "fw_attn_q4: need max_blocks * page < 2^31");
+  // (positions are rounded up to whole stages in 32 bits)
+  if ((int64_t)a->max_blocks * a->page > 0x7FFFFFFFll - kStageKeys)
+    return set_error(FW_EINVAL, "fw_attn_q4: need max_blocks * page < 2^31 - 128");
   // a request's 128-key units over all heads are counted in 32 bits, and so is
   // what a CTA takes of all of them: shares are equal in cost, and a pair's
   // fixed cost is six units, so no share is more than seven times the mean

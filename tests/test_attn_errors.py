@@ -1,4 +1,4 @@
-"""What the attention side's entry points say of a CUDA call that failed."""
+"""What the attention side's entry points say of a CUDA call that failed, and of sizes past their numbers."""
 import ctypes
 
 import pytest
@@ -25,6 +25,13 @@ def test_no_device_is_named():
     need = ctypes.c_int64()
     assert fw.lib().fw_attn_q4_workspace(args(), ctypes.byref(need)) == fw.FW_ECUDA
     assert "cudaError" in fw.fw_moe_last_error()
+
+
+def test_positions_that_pass_32_bits_when_rounded_up_are_refused():
+    need = ctypes.c_int64()
+    for page in (16, 128):
+        few = dict(n_q=8, n_kv=1, page=page, max_blocks=(1 << 31) // page - 1)
+        assert fw.lib().fw_attn_q4_workspace(args(**few), ctypes.byref(need)) == fw.FW_EINVAL and "max_blocks" in fw.fw_moe_last_error()
 
 
 @pytest.mark.gpu
