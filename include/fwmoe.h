@@ -341,8 +341,8 @@ fw_status fw_kv_export(const void *cache, int32_t n_pages, int32_t n_kv, int32_t
  * Query head h reads key/value head h / (n_q / n_kv). A row that sees nothing
  * gives zeros; what is masked is never part of a result, whatever it holds.
  * Softmax statistics and sums are fp32. Besides the output, what is rounded: a
- * probability to bf16, and once more with its value block's scale (requests of up
- * to 16 query rows, new tokens x n_q / n_kv) or the value with its scale (others).
+ * probability times its value block's scale, to bf16 (requests of up to 16 query
+ * rows, new tokens x n_q / n_kv), or a probability and a value, to bf16 (others).
  * Where requests bring 1,536 query rows and more on average it is a probability
  * alone, to f16 (2^-12, and 2^-28 of the row's largest), in all 128 neighbouring
  * positions whose blocks of values are zero or have largest magnitudes from 2^-7

@@ -67,6 +67,16 @@ def test_attn_rounds_what_it_says(sizes, roundings, keys):
     compare(c, roundings)
 
 
+@pytest.mark.parametrize("keys", [1.0, 2.0 ** -9])
+@pytest.mark.parametrize("sizes", [FEW[0], DRAFTS[0], ([(6000, 1), (9000, 1)], 32, 4, 128, 128, False)], ids=["few", "drafts", "long"])
+def test_attn_few_rows_round_once(sizes, keys):
+    """A probability times its value's scale, and nothing before."""
+    c = ref.Case(*sizes[:-1], seed=13, q_gain=1.5)
+    scale_keys(c, int(np.log2(keys)))
+    c.q = (c.q.double() / keys).to(torch.bfloat16)
+    compare(c, [BF16])
+
+
 @pytest.mark.parametrize("gain, roundings", [(1.0, [F16]), (2.0 ** -5, [F16]), (2.0 ** -9, [BF16, BF16]), (2.0 ** 9, [BF16, BF16])])
 def test_attn_values_unpacked_ahead_by_size(gain, roundings):
     """f16 while a tile's largest magnitudes lie in the window that the header gives, else bf16."""
