@@ -340,17 +340,16 @@ fw_status fw_kv_export(const void *cache, int32_t n_pages, int32_t n_kv, int32_t
  *   j <= p and (window == 0 or j > p - window or j < sinks)
  * Query head h reads key/value head h / (n_q / n_kv). A row that sees nothing
  * gives zeros; what is masked is never part of a result, whatever it holds.
- * Softmax statistics and sums are fp32. Besides the output, what is rounded: a
- * probability times its value block's scale, to bf16 (requests of up to 16 query
- * rows, new tokens x n_q / n_kv), or a probability and a value, to bf16 (others).
- * Where requests bring 1,536 query rows and more on average it is a probability
- * alone, to f16 (2^-12, and 2^-28 of the row's largest), in all 128 neighbouring
- * positions whose blocks of values are zero or have largest magnitudes from 2^-7
- * to 2^7. Sums of values past 2^100 may be infinite. Keys and queries are exact
+ * Softmax statistics and sums are fp32. Besides the output, what is rounded:
+ * for requests of up to 16 query rows (new tokens x n_q / n_kv) a probability times
+ * its value block's scale, to bf16; for others a probability alone, to f16 (2^-11,
+ * and 2^-28 of the row's largest), but a probability and a value, to bf16, in 128
+ * neighbouring positions with a block of values whose largest magnitude is neither
+ * zero nor within 2^-7 .. 2^7. Sums of values past 2^100 may be infinite. Keys and queries are exact
  * (for requests of more than 16 rows but for what is below 2^-37 of the largest key
  * of 128 neighbours, or 2^-25 of the largest element of a query row; a row with
  * none above 2^-100 is taken to have that). max_q is the largest number of new
- * tokens of a request, or more. A request that brings more than max_q, or whose
+ * tokens of a request, or more, up to T. A request that brings more than max_q, or whose
  * q_start entries decrease or leave 0..T, is reported and its rows are not written.
  * Rows of q past q_start[R] are neither read nor written.
  * workspace: DEVICE, 16-byte aligned, at least fw_attn_q4_workspace bytes; its

@@ -45,7 +45,7 @@ constexpr uint32_t kTmemCols = 512;
 // not kReady: registers of the softmax warps and of the others, of 128 a thread at launch
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr float kMost = 32768.f;  // a row's maximum moves only when a tile's sum of p passes this (f16 holds 65504)
-// kReady: log2 of a row's largest p when its maximum is set. p as f16, good to
+// log2 of a row's largest p when its maximum is set. p as f16, good to
 // 2^-25 at least, is then good to 2^-28 of the row's largest. (At 8 rows of windowed
 // prompts pass kMost more often: 60.8 us instead of 53.8; at 0 52.9.)
 constexpr int kTop = 4;
@@ -95,26 +95,24 @@ struct PrefillArgs {
 };
 
 // Keys and values go to f16: d (c - 8) has at most 8 + 3 significant bits, so
-// f16 holds it exactly from 2^-17 of scale to 2^13, and what it lacks in range is
-// made up by powers of two. Keys: a query row is divided by its largest
-// magnitude's power, and the keys of a tile (kReady, else of 32 positions: one
-// warp's, which need not wait for the others') by one that brings their largest
-// scale to 2^11..2^12; both go back into the factor of the scores. So keys are
-// exact unless scales of one tile differ by 2^28 and more, and then good to 2^-37 of
-// the largest key, as a row's elements below 2^-14 of its largest are to 2^-25 of that:
-// what the fp32 sums of the products leave. Values: a tile whose scales all lie in
-// largest magnitude of 2^-7 to 2^7 -- or are zero goes in f16, exactly, and so do
-// its probabilities, to 2^-12: the output's own rounding is then all the error
-// there is (0.0017 against 64 bits; with bf16 for both 0.0026, and 2 to 3 % of the
-// time less). Any other tile goes in bf16, values and probabilities rounded: each
-// tile's product has its own type. What size a tile's values have never enters its
+// f16 holds it exactly from 2^-17 of scale to 2^13.
+// Keys: what f16 lacks in range is made up by powers of two. A query row is
+// divided by its largest magnitude's, and the keys of a tile (kReady, else of 32
+// positions: one warp's, which need not wait for the others') by one that brings
+// their largest scale to 2^11..2^12; both go back into the factor of the scores. So
+// keys are exact unless scales of one tile differ by 2^28 and more, and then good
+// to 2^-37 of the largest key, as a row's elements below 2^-14 of its largest are to
+// 2^-25 of that.
+// Values: a tile whose scales all lie in [2^-10, 2^4) -- blocks with a largest
+// magnitude of 2^-7 to 2^7 -- or are zero goes in f16, exactly, and so do its
+// probabilities, to 2^-11: the output's own rounding is then all the error there
+// is (0.0017 against 64 bits; with bf16 for both 0.0026, and 1 to 4 % of the time
+// less). Any other tile goes in bf16, values and probabilities rounded: each tile's
+// product has its own type. What size a tile's values have never enters its
 // probabilities: f16 has no room for it (kTop) beside the weights themselves, and
 // what it drops at the bottom, 2^-28 of a row's largest, is nothing only as long as
 // the values it belongs to are not that much larger than the others: at most 2^14
 // times, by the window.
-// Where the CTA unpacks its own tiles (not kReady) all of them go in bf16: their
-// type would be found on the way of every tile (8 prompts of 60 to 128 tokens
-// over 4,000 to 8,000: 160 us instead of 143).
 constexpr uint32_t kNarrowLow = 127 - 10, kNarrow = 14;  // f16 tiles: lowest exponent of a scale (biased), and how many
 
 // nibbles 2 k + {0, 1} (and + 4) of a word, shifted to the low byte of each
@@ -222,27 +220,35 @@ __device__ __forceinline__ void unpack_keys(uint8_t* tile, const uint8_t* pk, in
   }
 }
 
-// Whether a packed tile's values need bf16 (see kKeyScale): some finite scale,
-// other than zero, of the keys that are there is outside of f16's window; by a
-// whole warp.
+// Barrier of `threads` threads with the OR of their predicates.
+__device__ __forceinline__ bool bar_red_or(int id, int threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
+
+// Whether a packed tile's values need bf16 (see kNarrow): some finite scale, other
+// than zero, of the keys that are there is outside of f16's window. This warp's 32
+// keys, half a pair's blocks to a lane.
 template <int D>
-__device__ __forceinline__ bool wide_values(const uint8_t* pk, int lane, int page, int page_shift, uint32_t hb, const KvPlanes& pl,
+__device__ __forceinline__ bool wide_values(const uint8_t* pk, int w, int lane, int page, int page_shift, uint32_t hb, const KvPlanes& pl,
                                             int key0, int S, uint32_t have) {
   constexpr int NB = Cfg<D>::NB;
-  bool wide = false;
+  const int kp = 16 * w + lane / 2;
+  const uint8_t* at = pk + ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (page / 2 - 1)) * (NB * 4) + (lane & 1) * (NB * 2);
+  auto outside = [](uint32_t d) { return d && d < 0x7F80u && (d >> 7) - kNarrowLow >= kNarrow; };
+  bool even = false, odd = false;
 #pragma unroll
-  for (int kp = lane; kp < kStageKeys / 2; kp += 32) {
-    const uint8_t* at = pk + ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (page / 2 - 1)) * (NB * 4);
-    const bool there = have >> (kp / 8) & 1;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t sc = *reinterpret_cast<const uint32_t*>(at + b * 4);
-      auto outside = [](uint32_t d) { return d && d < 0x7F80u && (d >> 7) - kNarrowLow >= kNarrow; };
-      wide |= there && key0 + 2 * kp < S && outside(sc & 0x7FFFu);
-      wide |= there && key0 + 2 * kp + 1 < S && outside(sc >> 16 & 0x7FFFu);
-    }
+  for (int k = 0; k < NB / 2; ++k) {
+    const uint32_t sc = reinterpret_cast<const uint32_t*>(at)[k];
+    even |= outside(sc & 0x7FFFu);
+    odd |= outside(sc >> 16 & 0x7FFFu);
   }
-  return __any_sync(0xFFFFFFFFu, wide);
+  return (have >> (kp / 8) & 1) && ((even && key0 + 2 * kp < S) || (odd && key0 + 2 * kp + 1 < S));
 }
 
 // 32 keys of a packed tile -> V operand tile, as four 8-key chunks, a lane four
@@ -250,11 +256,11 @@ __device__ __forceinline__ bool wide_values(const uint8_t* pk, int lane, int pag
 // Scales that must not enter the product -- of keys past the last or of a
 // missing page (whatever is there), and what is not finite (noted for the rows
 // that see it) -- count as zero.
-template <int D, bool kReady>
+template <int D>
 __device__ __forceinline__ void unpack_values(uint8_t* tile, const uint8_t* pk, int w, int lane, int page, int page_shift, uint32_t hb,
                                               const KvPlanes& pl, uint32_t mask, int key0, int S, uint32_t have, TileInfo* info) {
   constexpr int NB = Cfg<D>::NB;
-  const bool wide = !kReady || info->wide;
+  const bool wide = info->wide;
   // byte offset of a key pair's codes and scales within the packed tile
   auto codes_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vc + (kp & (page / 2 - 1)) * D; };
   auto scales_at = [&](int kp) { return ((2 * kp) >> page_shift) * hb + pl.vs + (kp & (page / 2 - 1)) * (NB * 4); };
@@ -433,16 +439,13 @@ __global__ void __launch_bounds__(kAheadThreads) unpack_ahead_kernel(PrefillArgs
   __syncthreads();
   if (!mbar_wait(&full, 0)) raise(u.status, FW_KV_TIMEOUT);
   const uint32_t mask = code_mask();
-  if (warp == 4) {
-    const bool wide = wide_values<D>(pk, lane, u.page, page_shift, hb, pl, key0, S, info->have);
-    if (lane == 0) info->wide = wide;
-  }
-  if (warp < 4)
+  if (warp < 4) {
     unpack_keys<D, true>(smem, pk, warp, lane, u.page, page_shift, hb, pl, mask, key0, S, info->have, info);
-  else
-    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-  if (warp >= 4)
-    unpack_values<D, true>(smem + C::TileBytes, pk, warp - 4, lane, u.page, page_shift, hb, pl, mask, key0, S, info->have, info);
+  } else {
+    info->wide = bar_red_or(1, 128, wide_values<D>(pk, warp - 4, lane, u.page, page_shift, hb, pl, key0, S, info->have));
+    __syncwarp();
+    unpack_values<D>(smem + C::TileBytes, pk, warp - 4, lane, u.page, page_shift, hb, pl, mask, key0, S, info->have, info);
+  }
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
@@ -463,17 +466,6 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity)
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) return false;
   }
-}
-
-// Barrier of `threads` threads with the OR of their predicates.
-__device__ __forceinline__ bool bar_red_or(int id, int threads, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"((uint32_t)pred)
-      : "memory");
-  return r != 0;
 }
 
 // kWindow: with a sliding window nearly all tiles are edges, and what masks
@@ -738,7 +730,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
               any(false);
               up = fmaxf(up, s_pair[half ^ 1][row]);
             }
-            up = ceilf(up - mz) - (kReady ? kTop : 0);
+            up = ceilf(up - mz) - kTop;
             // a first maximum is taken as it is, a later one only moves up
             if (!unset) up = fmaxf(up, 0.f);
             const bool moves = up != -INFINITY;
@@ -850,14 +842,10 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
 #pragma unroll
           for (int c = 0; c < Cols / 32; ++c) tmem_st16(s_cols + half * (Cols / 2) + 16 * c, pk[c]);
         };
-        if constexpr (kReady) {
-          if (__builtin_expect(s_info[i % kHave].wide, 0))
-            tile(std::false_type{});
-          else
-            tile(std::true_type{});
-        } else {
+        if (__builtin_expect(s_info[i % kHave].wide, 0))
           tile(std::false_type{});
-        }
+        else
+          tile(std::true_type{});
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -922,20 +910,26 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
       const uint32_t mask = code_mask();
       for (int i = 0; i < n_t; ++i) {
         const uint8_t* pk = sP + (i % kPacked) * C::PackedBytes;
+        TileInfo* info = &s_info[i % kHave];
+        const int key0 = v.block(i0 + i) * kStageKeys;
         wait(&packed_full[i % kPacked], (i / kPacked) & 1);
+        // the tile's type, of all four warps; these meet as often as there are
+        // tiles, whatever happens (after an abandoned wait without meaning)
+        const bool wide = bar_red_or(1, 128, ok && wide_values<D>(pk, w, lane, u.page, page_shift, hb, pl, key0, S, info->have));
         uint32_t seq = 2 * i;
         wait(&tile_empty[seq % kTiles], ((seq / kTiles) & 1) ^ 1);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        unpack_keys<D, false>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask,
-                              v.block(i0 + i) * kStageKeys, S, s_info[i % kHave].have, &s_info[i % kHave]);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) continue;
+        info->wide = wide;
+        unpack_keys<D, false>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask, key0, S, info->have, info);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tile_full[seq % kTiles]);
         seq = 2 * i + 1;
         wait(&tile_empty[seq % kTiles], ((seq / kTiles) & 1) ^ 1);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        unpack_values<D, false>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask,
-                         v.block(i0 + i) * kStageKeys, S, s_info[i % kHave].have, &s_info[i % kHave]);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) continue;
+        unpack_values<D>(sT + (seq % kTiles) * C::TileBytes, pk, w, lane, u.page, page_shift, hb, pl, mask, key0, S, info->have, info);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -970,7 +964,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         const uint32_t sv = 2 * i + 1, sk = 2 * i + 2;
         if ((!first_batch && !tile_ready(sv)) || (next && !tile_ready(sk))) break;
         if (row_tiles == 2 && !(t == 0 && first_batch) && !ready(&turn[t], (i + t) & 1)) break;
-        const uint32_t idesc_v = !kReady || (!first_batch && s_info[i % kHave].wide) ? idesc_bf16(kRowTile, D) : idesc_f16(kRowTile, D);
+        const uint32_t idesc_v = !first_batch && s_info[i % kHave].wide ? idesc_bf16(kRowTile, D) : idesc_f16(kRowTile, D);
         if (!first_batch && !ready(&p_full[t], i & 1)) break;  // (what comes last is what the chain waits for)
         tc_fence_after();
         if (elect_one()) {

@@ -77,6 +77,20 @@ def test_attn_few_rows_round_once(sizes, keys):
     compare(c, [BF16])
 
 
+@pytest.mark.parametrize("sizes", [SPLIT[0], HERE[0]], ids=["split", "here"])
+def test_attn_more_rows_round_in_f16(sizes):
+    """Where the CTA unpacks its own tiles as well."""
+    compare(ref.Case(*sizes[:-1], seed=14, q_gain=1.5), [F16])
+
+
+@pytest.mark.parametrize("gain, roundings", [(1.0, [F16]), (2.0 ** -5, [F16]), (2.0 ** -9, [BF16, BF16]), (2.0 ** 9, [BF16, BF16])])
+def test_attn_values_by_size_where_the_cta_unpacks(gain, roundings):
+    c = ref.Case(*HERE[0][:-1], seed=15, q_gain=1.5)
+    for r, (S, _) in enumerate(c.lens):
+        set_values(c, r, gain * np.random.default_rng(r).standard_normal((S, c.n_kv, c.D)))
+    compare(c, roundings)
+
+
 @pytest.mark.parametrize("gain, roundings", [(1.0, [F16]), (2.0 ** -5, [F16]), (2.0 ** -9, [BF16, BF16]), (2.0 ** 9, [BF16, BF16])])
 def test_attn_values_unpacked_ahead_by_size(gain, roundings):
     """f16 while a tile's largest magnitudes lie in the window that the header gives, else bf16."""

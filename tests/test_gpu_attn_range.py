@@ -8,7 +8,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import attn_ref as ref
-from attn_cases import call, check, scale_keys, unpacked_ahead
+from attn_cases import call, check, scale_keys, set_values, unpacked_ahead
 
 pytestmark = pytest.mark.gpu
 
@@ -54,6 +54,20 @@ def test_attn_few_rows_of_queries_of_any_magnitude(n, heads):
     scale_keys(c, n)
     c.q = scaled(c.q, -n)
     c.q[1] = 0
+    check(c)
+
+
+@pytest.mark.parametrize("gains", [(0.0, 0.05, 0.05), (0.0, 2.0 ** -30, 2.0 ** -30), (1e-3, 1e30, 1.0), (2.0 ** 41, 1.0, 2.0 ** 20)])
+@pytest.mark.parametrize("small", [None, 1e-6, 1e6])
+@pytest.mark.parametrize("kind", KINDS)
+def test_attn_values_of_unequal_tiles(kind, small, gains):
+    """Values whose size changes along the context, one position of each tile unlike its neighbours."""
+    c = case(kind, 8)
+    for r, (S, _) in enumerate(c.lens):
+        gain = np.repeat(gains, -(-S // 3))[:S]
+        if small:
+            gain[7::128] = small
+        set_values(c, r, np.random.default_rng(r).standard_normal((S, c.n_kv, c.D)).clip(-3, 3) * gain[:, None, None])
     check(c)
 
 
