@@ -267,7 +267,8 @@ fw_status fw_q8_0_quantize(const float *w, int64_t rows, int64_t K, uint8_t *blo
  * The value of a code c in 0..15 is d * (c - 8). A block of 32 values x takes
  * d = its element of largest magnitude (of a tie the positive one) / -8 and
  * c = round-half-even(x / d) + 8 clamped to 0..15 (d = 0: c = 8); d is exact in
- * bf16 for the bf16 keys and values stored here. A block holding an infinity
+ * bf16 for the bf16 keys and values stored here (of blocks with a largest
+ * magnitude below 2^-123 rounded to a multiple of 2^-133). A block holding an infinity
  * or NaN stands for non-finite values. A slot is page * P + place in the page. */
 enum {
   FW_KV_POOL_EMPTY = 1,   /* the plan ran out of free pages */

@@ -1,8 +1,10 @@
 // Attention for requests that bring few query rows (new tokens x heads that
 // share a key/value head, at most 16): single tokens and short drafts over
-// long contexts. Every key and value is used by few rows, so the kernel is
-// bound by streaming the 4-bit cache from HBM, and by the instructions that
-// unpack it.
+// long contexts. Every key and value is used by few rows: what the kernel cannot
+// do without is streaming the 4-bit cache from HBM. What bounds it is latency, with
+// 16 warps an SM (128 registers a thread) and some 330 instructions for 16 keys:
+// half of the issue slots, 42 to 54 % of HBM and a third of the tensor pipe are busy,
+// and warps wait for the results of their own instructions most.
 //
 //   s[t, n] = sum_b d_k[t, b] sum_{i in b} q[n, i] (c[t, i] - 8)
 //   o[n, i] = sum_t (p[t, n] d_v[t, b(i)]) (c'[t, i] - 8)
@@ -27,14 +29,15 @@
 // instead of 68).
 // (e4m3, whose smallest numbers do the same for bytes, needs fewer operations
 // on paper; but this GPU turns 8-bit mma.sync operands into f16 by further
-// instructions: 446 instead of 359 of them for 16 keys.)
+// instructions: 446 instead of 343 of them for 16 keys when both were there.)
 //
 // Work: a unit is 128 keys of one (request, key/value head); the CTAs take
 // consecutive shares of all units, so that ragged lengths and few requests both
 // fill the GPU. The shares are equal in cost: a pair costs its units and
 // kPairCost more for its query rows, its empty pipeline and its join (64
-// requests of 100 to 8191 keys: 66 us at 0, 52 at 3, 50 at 6, 52 at 8; 48 drafts
-// over a window 32, 30, 28.4, 28.9; 4 long contexts 72, 70, 68, 68).
+// requests of 100 to 8191 keys: 77 us at 0, 60 at 3, 52.7 at 6, 52.1 at 8, 53.3 at
+// 10; 48 drafts over a window 30.1, 27.9, 26.6, 26.7, 26.9; 4 long contexts 71.6,
+// 69.6, 67.8, 67.3, 68.0).
 // A unit's pages come into a shared-memory ring by one bulk copy each, which
 // the CTA's eight warps issue in turn. Four of them take a unit, 32 keys each,
 // the other four the next; each has a softmax state of its own that is joined

@@ -3,7 +3,7 @@
 // A row's D / 4 lanes read 16 bytes each. With few rows (decode) the lane groups
 // of a CTA share a row's parts; with many (prefill) every group has a row of
 // its own. Bound by launch and latency: 2-4 us of a call (48 drafts of 16 rows
-// 24.5 us; with a CTA a row, four waves of them, 28.5).
+// 26.2 us; with a CTA a row, four waves of them, 29.7).
 #include "attn.cuh"
 
 namespace fw {
@@ -14,9 +14,9 @@ using namespace dev;
 constexpr int kThreads = 256;
 // Where groups share rows: rows of a CTA. Four of 16 rows if there are pairs
 // enough that a record has few parts, or prompts in the call (few records then
-// have any): the records' CTAs are one wave (48 drafts 24.5 us a call, a row a CTA
-// 28.5; windowed prompts 51.6, 55.7). Else one, so that many parts are read at
-// once (one token of 16 rows over 68,000 keys: 304 parts, 39 us instead of 93).
+// have any): the records' CTAs are one wave (48 drafts 26.2 us a call, a row a CTA
+// 29.7; windowed prompts 53.5, 57.4). Else one, so that many parts are read at
+// once (one token of 16 rows over 68,000 keys: 304 parts, 38 us instead of 93).
 constexpr int kFewParts = 4;  // on average
 
 struct JoinArgs {

@@ -47,7 +47,7 @@ constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr float kMost = 32768.f;  // a row's maximum moves only when a tile's sum of p passes this (f16 holds 65504)
 // log2 of a row's largest p when its maximum is set. p as f16, good to
 // 2^-25 at least, is then good to 2^-28 of the row's largest. (At 8 rows of windowed
-// prompts pass kMost more often: 60.8 us instead of 53.8; at 0 52.9.)
+// prompts pass kMost more often: 59.9 us instead of 53.0; at 0 51.5.)
 constexpr int kTop = 4;
 
 // What goes with an unpacked tile of a head.
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
         const bool masks = edge || (have & ((1u << (Cols / 16)) - 1)) != (1u << (Cols / 16)) - 1;
         // A tile's scores to its P, in f16 or in bf16. The whole of it is there
         // twice: with the two conversions beside each other in the inner loop
-        // three chunks take 413 us instead of 327.
+        // three chunks took 413 us instead of 327.
         auto tile = [&](auto narrow) {
           // P against the maximum as last set. P and O are exact to their
           // rounding whatever their magnitude, so the maximum only moves (by
@@ -784,7 +784,8 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
               tmem_ld(s_cols + half * Cols, s);
               if (masks) {
                 // (the full condition, although there is no window: the compiler
-                // makes worse code of the shorter one: 458 us for three chunks instead of 325)
+                // makes worse code of the shorter one, three chunks 461 us instead of
+                // 331, and of words of bits as below 338)
                 const int at = key0 + half * Cols, hi = p - at, lo = u.window ? hi - u.window : -1, sk = u.sinks - at;
 #pragma unroll
                 for (int c = 0; c < Cols; ++c)
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(Lay<D, kReady>::Threads, 1) attn_prefill_kerne
             } else {
               // 32 columns at a time; what a row sees of them (c <= hi, and c > lo
               // or c < sk) as a word of bits: a test and a select each (three
-              // comparisons each: windowed prompts 67 us instead of 55)
+              // comparisons each: windowed prompts took 67 us instead of 55)
               auto scores = [&](auto masked, uint32_t(&s)[32], int w) {
                 tmem_ld(s_cols + half * Cols + 32 * w, s);
                 if constexpr (decltype(masked)::value) {
@@ -1076,8 +1077,8 @@ int64_t ready_bytes(const fw_attn_q4_args& a) {
 // Whether tiles are unpacked ahead: where a request has kReadyBlocks row blocks
 // or more to read them (on average), and the workspace for all that the block
 // tables can hold stays moderate. Eight requests with 4,000 cached positions
-// and 32 query heads over 4: at 8 blocks 142 us ahead, 157 us in the kernel; at
-// 4 blocks 82 and 79 us; at 2 blocks (16 requests, 8,000 positions) 173 and 141.
+// and 32 query heads over 4: at 8 blocks 140 us ahead, 162 us in the kernel; at 6
+// 137 and 158, at 4 80 and 82; at 2 blocks (16 requests, 8,000 positions) 177 and 143.
 constexpr int kReadyBlocks = 6;
 constexpr int64_t kReadyMost = 1ll << 30;
 bool prefill_ready(const fw_attn_q4_args& a, int sms) {

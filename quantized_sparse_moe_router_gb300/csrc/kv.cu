@@ -181,7 +181,7 @@ struct RopeArgs {
 // One row's 4-bit block halves: the scale of the 4 lanes' 32 values (already
 // bf16) and this lane's 8 codes, x / d rounded half to even. The scale is the
 // element of largest magnitude (the positive one of a tie) over -8: exact in
-// bf16 for bf16 values. No quotient is needed to know how x / d rounds: with
+// bf16 for bf16 values (from 2^-123 on). No quotient is needed to know how x / d rounds: with
 // X, Y of 8 bits, x / d and a half-integer h / 2 from 1/2 on differ by
 // |2 X 2^a - h Y| / 2 Y with a >= -2, so by nothing or by 2^-10 or more. x times
 // 1 / d, rounded to a multiple of 2^-11, is on the right side of it or on it.
