@@ -371,6 +371,82 @@ typedef struct {
 fw_status fw_attn_q4_workspace(const fw_attn_q4_args *args, int64_t *bytes);
 fw_status fw_attn_q4(const fw_attn_q4_args *args, void *workspace, int64_t bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * What a layer needs between its attention and its experts: linear layers in 8
+ * bits and the norms at the residual stream. (The Flyweight README, §Quantization,
+ * names kernels with quantised activations for dense projections and the LM head;
+ * the pages name neither this format nor a formula, and the readings below are this
+ * library's own.) Like the attention side these calls need no handle, never
+ * synchronise and allocate nothing.
+ *
+ * 8-bit blocks. A block of values x has m = max(its largest magnitude, 2^-96),
+ * scale = m / 448 and codes e4m3(x * (448 / m)); quotients and product are
+ * fp32, rounded to nearest, the codes to nearest even. A block with an
+ * infinity or NaN stands for non-finite values. Activations: a block is 128
+ * neighbours of one token (the last one of a token may be shorter); codes
+ * [T][K], scales fp32 [ceil(K / 128)][T]. Weights: a block is 128 x 128 of
+ * [N][K] (smaller at the edges); codes [N][K], scales fp32
+ * [ceil(N / 128)][ceil(K / 128)], as checkpoints of 8-bit block-scaled models
+ * hold them. */
+
+/* x DEVICE bf16 [T][K], x_stride elements between tokens (a multiple of 8), K a
+ * multiple of 16; codes DEVICE e4m3 [T][K], 16-byte aligned; scales DEVICE fp32. */
+fw_status fw_fp8_quantize(const void *x, int64_t x_stride, int32_t T, int32_t K, void *codes, float *scales, void *stream);
+
+/* w DEVICE [N][K] bf16 (w_fp32 == 0) or fp32 (1), K a multiple of 16. */
+fw_status fw_fp8_quantize_weight(const void *w, int32_t w_fp32, int32_t N, int32_t K, void *codes, float *scales, void *stream);
+
+/* A linear layer: out[t][n] = sum over k of x[t][k] w[n][k], both as their codes and
+ * scales stand for. Products of codes are exact, the sum over the at most 128 of a
+ * block is the tensor core's (fp32), and blocks are scaled and added in fp32; out is
+ * rounded once. x may be bf16: it is then quantised by the rule above, with the same
+ * result as fw_fp8_quantize before the call. out may not overlap x or w.
+ * workspace: DEVICE, 16-byte aligned, at least fw_linear_fp8_workspace bytes (0 for
+ * some calls); its contents mean nothing between calls, and calls that may overlap
+ * need one each. */
+typedef struct {
+  int32_t T, K, N;           /* T >= 0; K a multiple of 16; N >= 1 */
+  int32_t out_fp32;          /* 0: out is bf16, 1: fp32 */
+  const void *x;             /* DEVICE, 16-byte aligned: bf16 [T][K], or with x_scale e4m3 codes */
+  const float *x_scale;      /* DEVICE fp32 [ceil(K / 128)][T], or NULL */
+  int64_t x_stride;          /* elements between tokens: a multiple of 8 (bf16) or 16 (codes) */
+  const void *w;             /* DEVICE e4m3 [N][K], 16-byte aligned */
+  const float *w_scale;      /* DEVICE fp32 [ceil(N / 128)][ceil(K / 128)] */
+  void *out;                 /* DEVICE [T][N] */
+  int64_t out_stride;        /* elements between tokens, at least N */
+  int32_t *status;           /* DEVICE, FW_KV_TIMEOUT is OR-ed in; or NULL */
+} fw_linear_fp8_args;
+fw_status fw_linear_fp8_workspace(const fw_linear_fp8_args *args, int64_t *bytes);
+fw_status fw_linear_fp8(const fw_linear_fp8_args *args, void *workspace, int64_t bytes, void *stream);
+
+/* The norms after a block and before the next one, with the block's gate, the
+ * residual scale and the sum between them:
+ *   r = residual + scale * gate * y / sqrt(mean(y^2) + eps) * post_norm
+ *       (post_norm NULL: y as it is; gate NULL: 1; residual NULL: 0)
+ *   h = r / sqrt(mean(r^2) + eps) * norm           (norm NULL: h = r)
+ * in fp32, r and h each rounded once (h is made of r before it is rounded). h is
+ * written as bf16, as 8-bit codes (of the bf16 values, by the rule above) or both.
+ * residual_out may be residual, and h may be y, with the same strides. */
+typedef struct {
+  int32_t T, H;              /* H a multiple of 8 (of 16 with h_codes), at most 32768 */
+  int32_t residual_fp32;     /* residual and residual_out: 0 bf16, 1 fp32 */
+  int32_t gate_fp32;         /* gate: 0 bf16, 1 fp32 */
+  int32_t gate_per_token;    /* 1: gate is one value a token, gate_stride elements apart; 0: H values,
+                              * gate_stride elements between tokens (0: the same for every token) */
+  float eps, scale;
+  const void *y;             /* DEVICE bf16 [T][H] */
+  const void *residual;      /* DEVICE [T][H], or NULL */
+  const void *gate;          /* DEVICE, or NULL */
+  int64_t y_stride, residual_stride, gate_stride; /* elements between tokens; multiples of 8 (gate_stride: unless per token) */
+  const float *post_norm, *norm; /* DEVICE fp32 [H] or NULL */
+  void *residual_out;        /* DEVICE [T][H], or NULL */
+  void *h;                   /* DEVICE bf16 [T][H], or NULL */
+  int64_t residual_out_stride, h_stride;
+  void *h_codes;             /* DEVICE e4m3 [T][H], or NULL */
+  float *h_scale;            /* DEVICE fp32 [ceil(H / 128)][T], with h_codes */
+} fw_norm_residual_args;
+fw_status fw_norm_residual(const fw_norm_residual_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

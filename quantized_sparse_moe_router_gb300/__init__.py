@@ -11,7 +11,9 @@ fw_q8_0_quantize), taking raw pointers and ints.
 
 High level: `MoELayer` (one handle = one layer) and `quantize_q8_0`, taking
 torch tensors, and the attention side of a layer: `kv_cache`, `kv_plan`,
-`qk_norm_rope`, `kv_export`, `attn_q4` (attention.py).
+`qk_norm_rope`, `kv_export`, `attn_q4` (attention.py), and what stands between
+the two: `quantize_fp8`, `quantize_fp8_weight`, `linear_fp8`, `norm_residual`
+(linear.py).
 """
 from __future__ import annotations
 
@@ -54,7 +56,8 @@ EXPORTED = ("fw_moe_init", "fw_moe_route", "fw_moe_ffn", "fw_moe_forward", "fw_m
             "fw_moe_get_permutation", "fw_moe_export_q8_0", "fw_moe_status", "fw_moe_free", "fw_moe_last_error",
             "fw_q8_0_quantize", "fw_moe_profile_begin", "fw_moe_profile_end", "fw_moe_route_noalloc",
             "fw_moe_graph_create", "fw_moe_graph_launch", "fw_moe_graph_destroy", "fw_kv_plan", "fw_qk_norm_rope",
-            "fw_kv_export", "fw_attn_q4_workspace", "fw_attn_q4")
+            "fw_kv_export", "fw_attn_q4_workspace", "fw_attn_q4", "fw_fp8_quantize", "fw_fp8_quantize_weight",
+            "fw_linear_fp8_workspace", "fw_linear_fp8", "fw_norm_residual")
 
 KERNEL_KINDS = ("route_decode", "route_tiles", "route_scan", "route_scatter", "decode_experts", "reserved",
                 "prefill_gateup", "prefill_down", "prefill_combine", "prefill_gather", "prefill_gateup_small",
@@ -92,6 +95,11 @@ def lib():
             "fw_kv_export": [vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp],
             "fw_attn_q4_workspace": [vp, vp],
             "fw_attn_q4": [vp, vp, i64, vp],
+            "fw_fp8_quantize": [vp, i64, i32, i32, vp, vp, vp],
+            "fw_fp8_quantize_weight": [vp, i32, i32, i32, vp, vp, vp],
+            "fw_linear_fp8_workspace": [vp, vp],
+            "fw_linear_fp8": [vp, vp, i64, vp],
+            "fw_norm_residual": [vp, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -324,17 +332,20 @@ class MoELayer:
             pass
 
 
-# The attention side's torch-level calls import torch at their top; the names
-# are looked up on first use so that this module itself does not.
+# These torch-level calls import torch at their modules' tops; the names are
+# looked up on first use so that this module itself does not.
 _ATTENTION = ("KVPlan", "kv_cache", "kv_plan", "qk_norm_rope", "kv_export", "attn_q4", "FwQkNormRopeArgs", "FwAttnQ4Args",
               "KV_POOL_EMPTY", "KV_TABLE_FULL", "KV_TOKENS_FULL", "KV_BAD_LENGTH", "KV_BAD_SLOT", "KV_BAD_POSITION",
               "KV_TIMEOUT", "KV_BAD_QUERIES")
+_LINEAR = ("quantize_fp8", "quantize_fp8_weight", "linear_fp8", "norm_residual", "FwLinearFp8Args", "FwNormResidualArgs")
 
 
 def __getattr__(name):
-    if name in _ATTENTION:
-        from . import attention
-        for n in _ATTENTION:
-            globals()[n] = getattr(attention, n)
-        return globals()[name]
+    for names, module in ((_ATTENTION, "attention"), (_LINEAR, "linear")):
+        if name in names:
+            import importlib
+            m = importlib.import_module(f".{module}", __name__)
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,89 @@
+// Blocks of 8-bit floating point values (e4m3) with a scale, and the linear
+// layers over them.
+//
+//   m = max(largest magnitude, 2^-96),  scale = m / 448,  code = e4m3(x (448 / m))
+//
+// 448 is e4m3's largest value, so the largest element of a block takes the
+// largest code. The least m keeps 448 / m finite (a block of zeros, or of
+// subnormals, needs no case of its own: its codes round to zero). The largest
+// magnitude of bf16 values is taken on their bits, as whole numbers: an
+// infinity is above every number and a NaN above it, so both reach m, and the
+// scale takes them into every output of the block.
+#pragma once
+
+#include "kvcache.cuh"
+
+namespace fw {
+
+constexpr int kFp8Block = 128;  // values along K that share a scale
+
+__host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+namespace dev {
+
+constexpr uint32_t kFp8LeastBits = 0x0F800000u;  // 2^-96
+constexpr float kFp8Max = 448.f;
+
+// The largest magnitude of eight bf16 values, as the bits of a float.
+__device__ __forceinline__ uint32_t bf16x8_amax_bits(const uint4 v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  return ::max(m << 16, m & 0xFFFF0000u);
+}
+
+// Two fp32 values -> two e4m3 codes (the first in the low byte), nearest even.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight bf16 values times r -> eight codes.
+__device__ __forceinline__ uint2 bf16x8_to_e4m3(const uint4 v, float r) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    bf16x2_to_f32(w[i], lo, hi);
+    c[i] = e4m3x2(lo * r, hi * r);
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// A block of 128 bf16 values over 16 neighbouring lanes, eight a lane (all 32
+// lanes of the warp take part): this lane's codes, and the block's scale.
+__device__ __forceinline__ uint2 fp8_block_of_lanes(const uint4 v, float* scale) {
+  uint32_t m = bf16x8_amax_bits(v);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) m = ::max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float top = __uint_as_float(::max(m, kFp8LeastBits));
+  *scale = __fdiv_rn(top, kFp8Max);
+  return bf16x8_to_e4m3(v, __fdiv_rn(kFp8Max, top));
+}
+
+}  // namespace dev
+
+// What the linear kernels take: codes of the tokens with their scales, or (few
+// tokens) bf16 values that the kernel quantises itself.
+struct LinearArgs {
+  int T, K, N, KB;          // KB = blocks along K
+  const __nv_bfloat16* x;   // bf16 [T][x_stride], where the kernel quantises
+  int64_t x_stride;
+  const float* x_scale;     // [KB][T]
+  const float* w_scale;     // [ceil(N / 128)][KB]
+  void* out;
+  int64_t out_stride;
+  int out_fp32;
+  int32_t* status;
+};
+
+cudaError_t launch_fp8_quantize(const void* x, int64_t x_stride, int T, int K, void* codes, float* scales, cudaStream_t s);
+
+// A tensor map of codes: rows of K bytes, `stride` apart, in boxes of 128 bytes by `box` rows, 128-byte swizzle.
+cudaError_t encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, int64_t stride, int box);
+
+cudaError_t configure_linear_few();
+bool linear_few_quantises(int T);  // whether the kernel for few tokens takes bf16 itself
+cudaError_t launch_linear_few(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s);
+
+}  // namespace fw

@@ -1,0 +1,83 @@
+// Linear layers in 8 bits: argument checks and the choice of kernel.
+#include <mutex>
+
+#include "fp8.cuh"
+
+using namespace fw;
+
+static int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+static fw_status check_args(const fw_linear_fp8_args* a, bool pointers) {
+  auto al = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  if (!a) return set_error(FW_EINVAL, "fw_linear_fp8: null argument struct");
+  if (a->T < 0 || a->N < 1 || a->K < 16 || a->K % 16) return set_error(FW_EINVAL, "fw_linear_fp8: need T >= 0, N >= 1 and K a positive multiple of 16");
+  if (a->out_fp32 != 0 && a->out_fp32 != 1) return set_error(FW_EINVAL, "fw_linear_fp8: out_fp32 must be 0 or 1");
+  if (a->T > (1 << 22) || a->N > (1 << 26)) return set_error(FW_EUNSUPPORTED, "fw_linear_fp8: at most 2^22 tokens and 2^26 outputs a call");
+  if (!pointers || a->T == 0) return FW_OK;
+  if (!a->x || !a->w || !a->w_scale || !a->out) return set_error(FW_EINVAL, "fw_linear_fp8: null pointer");
+  if (!al(a->x, 16) || !al(a->w, 16) || !al(a->x_scale, 4) || !al(a->w_scale, 4) || !al(a->out, a->out_fp32 ? 4 : 2) || !al(a->status, 4))
+    return set_error(FW_EINVAL, "fw_linear_fp8: x and w need 16-byte alignment, the rest that of its elements");
+  if (a->x_stride < a->K || a->x_stride % (a->x_scale ? 16 : 8) || a->out_stride < a->N)
+    return set_error(FW_EINVAL, "fw_linear_fp8: token strides must cover the rows; x_stride a multiple of 8 (bf16) or 16 (codes) elements");
+  return FW_OK;
+}
+
+// The current device's SM count; its kernels are configured once.
+static cudaError_t device_sms(int* sms) {
+  static std::mutex mu;
+  static int known[64] = {};
+  int dev = 0, n = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> g(mu);
+  if (!known[dev]) {
+    cudaError_t e = configure_linear_few();
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    known[dev] = n;
+  }
+  *sms = known[dev];
+  return cudaSuccess;
+}
+
+// The workspace: codes and scales of bf16 tokens that no kernel quantises itself.
+static bool quantises_first(const fw_linear_fp8_args* a) { return !a->x_scale && !linear_few_quantises(a->T); }
+static int64_t codes_bytes(const fw_linear_fp8_args* a) { return round_up((int64_t)a->T * a->K, 256); }
+
+extern "C" fw_status fw_linear_fp8_workspace(const fw_linear_fp8_args* a, int64_t* bytes) {
+  if (!bytes) return set_error(FW_EINVAL, "fw_linear_fp8_workspace: null pointer");
+  *bytes = 0;
+  if (fw_status st = check_args(a, false); st != FW_OK) return st;
+  if (a->T > 0 && quantises_first(a)) *bytes = codes_bytes(a) + round_up((int64_t)a->T * fp8_blocks(a->K) * 4, 256);
+  return FW_OK;
+}
+
+extern "C" fw_status fw_linear_fp8(const fw_linear_fp8_args* a, void* workspace, int64_t bytes, void* stream) {
+  if (fw_status st = check_args(a, true); st != FW_OK) return st;
+  if (a->T == 0) return FW_OK;
+  int64_t need = 0;
+  if (fw_status st = fw_linear_fp8_workspace(a, &need); st != FW_OK) return st;
+  if (need && (!workspace || bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16))
+    return set_error(FW_EINVAL, "fw_linear_fp8: the workspace is too small (see fw_linear_fp8_workspace) or not 16-byte aligned");
+  if (fw_status st = check_device("fw_linear_fp8: needs an sm_103 device"); st != FW_OK) return st;
+  int sms = 0;
+  if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return set_cuda_error(e, "fw_linear_fp8: setting the device up");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LinearArgs l = {a->T, a->K, a->N, fp8_blocks(a->K), nullptr, 0, a->x_scale, a->w_scale, a->out, a->out_stride, a->out_fp32, a->status};
+  const void* codes = a->x;
+  int64_t codes_stride = a->x_stride;
+  cudaError_t e = cudaSuccess;
+  if (quantises_first(a)) {
+    float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + codes_bytes(a));
+    e = launch_fp8_quantize(a->x, a->x_stride, a->T, a->K, workspace, scales, s);
+    codes = workspace;
+    codes_stride = a->K;
+    l.x_scale = scales;
+  } else if (!a->x_scale) {
+    l.x = static_cast<const __nv_bfloat16*>(a->x);
+    l.x_stride = a->x_stride;
+  }
+  if (e == cudaSuccess) e = launch_linear_few(l, a->w, codes, codes_stride, sms, s);
+  if (e != cudaSuccess) return set_cuda_error(e, "fw_linear_fp8: launch");
+  return FW_OK;
+}

@@ -1,0 +1,219 @@
+// The norms after a block and before the next one, fused with the block's gate,
+// the residual scale and the sum between them:
+//
+//   r = residual + scale * gate * y / sqrt(mean(y^2) + eps) * post_norm
+//   h = r / sqrt(mean(r^2) + eps) * norm
+//
+// One pass: a row's values stay in registers between the two sums over it, so
+// y and the residual are read once and r and h written once, which bounds many
+// rows by HBM. A single row is bound by latency: its loads are all issued
+// before anything waits for them.
+//
+// h may leave as 8-bit codes with a scale per 128 values (the linear layers'
+// input): a thread holds eight neighbours, so a block is 16 neighbouring lanes.
+#include <algorithm>
+
+#include "fp8.cuh"
+
+namespace fw {
+namespace {
+
+using namespace dev;
+
+constexpr int kMaxThreads = 1024, kMaxNormH = 32768;
+
+// Sum over the row: a warp's own, or the CTA's (buf: one float a warp, used once).
+template <bool kWarp>
+__device__ __forceinline__ float row_sum(float v, float* buf) {
+  v = warp_sum(v);
+  if constexpr (!kWarp) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
+    if (lane == 0) buf[warp] = v;
+    __syncthreads();
+    v = warp_sum(lane < n ? buf[lane] : 0.f);
+  }
+  return v;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
+  bf16x2_to_f32(v.x, f[0], f[1]);
+  bf16x2_to_f32(v.y, f[2], f[3]);
+  bf16x2_to_f32(v.z, f[4], f[5]);
+  bf16x2_to_f32(v.w, f[6], f[7]);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]), bf16x2_bits(f[6], f[7]));
+}
+// (weights: read by every row, kept in L1)
+__device__ __forceinline__ void weight8(const float* w, int at, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w + at)), b = __ldg(reinterpret_cast<const float4*>(w + at) + 1);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+__device__ __forceinline__ void floats8(const uint4 a, const uint4 b, float (&f)[8]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+}
+
+// kVec: vectors of eight values a thread holds. kWarp: a warp a row, otherwise a
+// CTA a row. kWide: residuals are fp32.
+template <int kVec, bool kWarp, bool kWide>
+__global__ void __launch_bounds__(kWarp ? 256 : kMaxThreads) norm_residual_kernel(const __grid_constant__ fw_norm_residual_args u) {
+  __shared__ float s_sum[2][32];
+  const int width = kWarp ? 32 : blockDim.x, l = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = kWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  const bool in = row < u.T;  // (kWarp: a warp past the last row goes along without loads or stores)
+  pdl_wait();
+  pdl_launch_dependents();
+  const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(u.y) + row * u.y_stride;
+  uint4 yv[kVec], rv[kVec], rw[kWide ? kVec : 1];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = 8 * (i * width + l);
+    const bool has = in && at < u.H;
+    yv[i] = has ? *reinterpret_cast<const uint4*>(y + at) : make_uint4(0u, 0u, 0u, 0u);
+    rv[i] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (kWide) {
+      rw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (has && u.residual) {
+        const uint4* r = reinterpret_cast<const uint4*>(static_cast<const float*>(u.residual) + row * u.residual_stride + at);
+        rv[i] = r[0];
+        rw[i] = r[1];
+      }
+    } else if (has && u.residual) {
+      rv[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.residual) + row * u.residual_stride + at);
+    }
+  }
+  float by = u.scale;
+  if (u.gate && u.gate_per_token && in)
+    by *= u.gate_fp32 ? __ldg(static_cast<const float*>(u.gate) + row * u.gate_stride)
+                      : __bfloat162float(static_cast<const __nv_bfloat16*>(u.gate)[row * u.gate_stride]);
+  if (u.post_norm) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      float f[8];
+      unpack8(yv[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+    }
+    by *= rsqrtf(row_sum<kWarp>(sum, s_sum[0]) / (float)u.H + u.eps);
+  }
+  float r[kVec][8], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = 8 * (i * width + l);
+    if (!in || at >= u.H) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
+      continue;
+    }
+    float f[8], w[8];
+    unpack8(yv[i], f);
+    if constexpr (kWide)
+      floats8(rv[i], rw[i], r[i]);
+    else
+      unpack8(rv[i], r[i]);
+    if (u.post_norm) {
+      weight8(u.post_norm, at, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= w[j];
+    }
+    if (u.gate && !u.gate_per_token) {
+      if (u.gate_fp32)
+        weight8(static_cast<const float*>(u.gate) + row * u.gate_stride, at, w);
+      else
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.gate) + row * u.gate_stride + at), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= w[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      r[i][j] = fmaf(f[j], by, r[i][j]);
+      sum = fmaf(r[i][j], r[i][j], sum);
+    }
+    if (u.residual_out) {
+      if constexpr (kWide) {
+        float4* to = reinterpret_cast<float4*>(static_cast<float*>(u.residual_out) + row * u.residual_out_stride + at);
+        to[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
+        to[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(u.residual_out) + row * u.residual_out_stride + at) = pack8(r[i]);
+      }
+    }
+  }
+  if (!u.h && !u.h_codes) return;
+  const float inv = u.norm ? rsqrtf(row_sum<kWarp>(sum, s_sum[1]) / (float)u.H + u.eps) : 1.f;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = 8 * (i * width + l);
+    const bool has = in && at < u.H;
+    if (u.norm && has) {
+      float w[8];
+      weight8(u.norm, at, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[i][j] *= inv * w[j];
+    }
+    const uint4 out = pack8(r[i]);
+    if (u.h && has) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(u.h) + row * u.h_stride + at) = out;
+    if (u.h_codes) {  // (every lane takes part: past the row's end with zeros)
+      float scale;
+      const uint2 c = fp8_block_of_lanes(out, &scale);
+      if (has) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(u.h_codes) + row * u.H + at) = c;
+        if ((l & 15) == 0) u.h_scale[(int64_t)(at / kFp8Block) * u.T + row] = scale;
+      }
+    }
+  }
+}
+
+template <int kVec, bool kWarp>
+cudaError_t launch(const fw_norm_residual_args& u, unsigned grid, int threads, cudaStream_t s) {
+  return u.residual_fp32 ? launch_dependent(norm_residual_kernel<kVec, kWarp, true>, dim3(grid), dim3(threads), 0, s, u)
+                         : launch_dependent(norm_residual_kernel<kVec, kWarp, false>, dim3(grid), dim3(threads), 0, s, u);
+}
+
+}  // namespace
+}  // namespace fw
+
+using namespace fw;
+
+extern "C" fw_status fw_norm_residual(const fw_norm_residual_args* u, void* stream) {
+  auto al = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  if (!u) return set_error(FW_EINVAL, "fw_norm_residual: null argument struct");
+  if (u->T < 0 || u->H < 8 || u->H % 8) return set_error(FW_EINVAL, "fw_norm_residual: need T >= 0 and H a positive multiple of 8");
+  if (u->H > kMaxNormH) return set_error(FW_EUNSUPPORTED, "fw_norm_residual: H is at most 32768");
+  if (u->h_codes && u->H % 16) return set_error(FW_EINVAL, "fw_norm_residual: 8-bit codes need H a multiple of 16");
+  if ((u->residual_fp32 | u->gate_fp32 | u->gate_per_token) & ~1) return set_error(FW_EINVAL, "fw_norm_residual: flags must be 0 or 1");
+  if (!(u->eps >= 0.f)) return set_error(FW_EINVAL, "fw_norm_residual: eps must not be negative");
+  if (u->T == 0) return FW_OK;
+  if (!u->y || (!u->residual_out && !u->h && !u->h_codes) || (u->h_codes && !u->h_scale))
+    return set_error(FW_EINVAL, "fw_norm_residual: null pointer (y, some output, and h_scale with h_codes are needed)");
+  const int64_t H = u->H;
+  if (u->y_stride < H || u->y_stride % 8 || (u->residual && (u->residual_stride < H || u->residual_stride % 8)) ||
+      (u->residual_out && (u->residual_out_stride < H || u->residual_out_stride % 8)) || (u->h && (u->h_stride < H || u->h_stride % 8)))
+    return set_error(FW_EINVAL, "fw_norm_residual: token strides must cover H and be multiples of 8 elements");
+  if (u->gate && (u->gate_per_token ? u->gate_stride < 0 : (u->gate_stride % 8 || (u->gate_stride != 0 && u->gate_stride < H))))
+    return set_error(FW_EINVAL, "fw_norm_residual: gate_stride must be 0, or cover H and be a multiple of 8 (per token: not negative)");
+  for (const void* p : {u->y, u->residual, u->gate_per_token ? nullptr : u->gate, (const void*)u->post_norm, (const void*)u->norm, (const void*)u->residual_out,
+                        (const void*)u->h, (const void*)u->h_codes})
+    if (!al(p, 16)) return set_error(FW_EINVAL, "fw_norm_residual: tensors need 16-byte alignment");
+  if (!al(u->gate, u->gate_fp32 ? 4 : 2) || !al(u->h_scale, 4)) return set_error(FW_EINVAL, "fw_norm_residual: gate and h_scale need the alignment of their elements");
+  if (fw_status st = check_device("fw_norm_residual: needs an sm_103 device"); st != FW_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int vecs = u->H / 8;
+  cudaError_t e;
+  if (vecs <= 128 && u->T > 1) {
+    const int warps = 8;
+    const unsigned grid = (unsigned)(((int64_t)u->T + warps - 1) / warps);
+    const int per = (vecs + 31) / 32;
+    e = per == 1 ? launch<1, true>(*u, grid, 32 * warps, s) : per == 2 ? launch<2, true>(*u, grid, 32 * warps, s) : launch<4, true>(*u, grid, 32 * warps, s);
+  } else {
+    const int per = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+    const int threads = ((vecs + per - 1) / per + 31) / 32 * 32;
+    const unsigned grid = (unsigned)u->T;
+    e = per == 1 ? launch<1, false>(*u, grid, threads, s) : per == 2 ? launch<2, false>(*u, grid, threads, s) : launch<4, false>(*u, grid, threads, s);
+  }
+  if (e != cudaSuccess) return set_cuda_error(e, "fw_norm_residual: launch");
+  return FW_OK;
+}
