@@ -90,6 +90,26 @@ typedef struct { /* all DEVICE pointers, read only during fw_moe_init */
   const uint8_t *shared_down;  /* [H x I/32] Q8_0, or NULL when n_shared == 0 */
 } fw_moe_weights;
 
+/* How a layer's router chooses and weights its experts. The default (until
+ * fw_moe_set_routing) is the step above. Under a rule:
+ *   s[t,e]   = softmax of z[t,.] over all E, or 1 / (1 + e^-z[t,e])
+ *   c[t,e]   = s[t,e] + select_bias[e]
+ *   groups   : n_group runs of E / n_group neighbouring experts; a group's score is
+ *              the sum of its two largest c (its only one); the top_group groups of
+ *              largest score stay, ties to the lower group
+ *   ids[t,:] = the k largest c of the groups that stay, descending, ties to the lower id
+ *   gates    = scale * s[t,ids], divided by (their sum of s + 1e-20) when renorm
+ * (The vOOM README speaks of DeepSeek-shaped experts and routers, the Flyweight
+ * README's served families name that MoE too; the pages print no formula, and this
+ * is the reading used.) A NaN among the logits ranks below every number. */
+typedef struct {
+  int32_t score;               /* 0 softmax over all experts, 1 sigmoid */
+  int32_t n_group, top_group;  /* 1..32, dividing E; 1..n_group, with k experts at least in that many groups. 1, 1: no groups */
+  int32_t renorm;              /* 0 or 1 */
+  float scale;                 /* positive, finite */
+  const float *select_bias;    /* DEVICE [E] or NULL (zeros); only moves the choice */
+} fw_moe_routing;
+
 /* Create a layer (the pages' runtime loads routed experts of GGUF Q8_0 models
  * onto the GPU for its grouped kernels: Flyweight README, §Quantization and
  * §Features): validates the shapes, copies the router and repacks every
@@ -98,6 +118,13 @@ typedef struct { /* all DEVICE pointers, read only during fw_moe_init */
  * workspace for T_max tokens and synchronises `stream` once. The caller may
  * free its weight buffers afterwards. *out receives the handle. */
 fw_status fw_moe_init(const fw_moe_config *cfg, const fw_moe_weights *w, void *stream, fw_moe_handle **out);
+
+/* Set the layer's routing rule (NULL: back to the default step) for the routes and
+ * forwards from here on; a route made before is no longer valid for fw_moe_ffn.
+ * select_bias is copied into the handle in stream order (the first rule of a handle
+ * also allocates for it: not inside a stream capture). A captured graph keeps the
+ * rule that it was captured with, and reads the bias set last. */
+fw_status fw_moe_set_routing(fw_moe_handle *h, const fw_moe_routing *routing, void *stream);
 
 /* The router step (Flyweight README, §Current limitations: dynamic MoE routing;
  * vOOM README, router/top-k substeps; the reading: fp32 logits, top-k with ties

@@ -39,6 +39,10 @@ class FwMoeWeights(ctypes.Structure):
                                                "shared_gate", "shared_up", "shared_down")]
 
 
+class FwMoeRouting(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_group", "top_group", "renorm")] + [("scale", ctypes.c_float), ("select_bias", ctypes.c_void_p)]
+
+
 class FwError(RuntimeError):
     def __init__(self, status: int, where: str, text: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {text}")
@@ -57,7 +61,7 @@ EXPORTED = ("fw_moe_init", "fw_moe_route", "fw_moe_ffn", "fw_moe_forward", "fw_m
             "fw_q8_0_quantize", "fw_moe_profile_begin", "fw_moe_profile_end", "fw_moe_route_noalloc",
             "fw_moe_graph_create", "fw_moe_graph_launch", "fw_moe_graph_destroy", "fw_kv_plan", "fw_qk_norm_rope",
             "fw_kv_export", "fw_attn_q4_workspace", "fw_attn_q4", "fw_fp8_quantize", "fw_fp8_quantize_weight",
-            "fw_linear_fp8_workspace", "fw_linear_fp8", "fw_norm_residual")
+            "fw_linear_fp8_workspace", "fw_linear_fp8", "fw_norm_residual", "fw_moe_set_routing")
 
 KERNEL_KINDS = ("route_decode", "route_tiles", "route_scan", "route_scatter", "decode_experts", "reserved",
                 "prefill_gateup", "prefill_down", "prefill_combine", "prefill_gather", "prefill_gateup_small",
@@ -100,6 +104,7 @@ def lib():
             "fw_linear_fp8_workspace": [vp, vp],
             "fw_linear_fp8": [vp, vp, i64, vp],
             "fw_norm_residual": [vp, vp],
+            "fw_moe_set_routing": [vp, ctypes.POINTER(FwMoeRouting), vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -125,6 +130,11 @@ def fw_moe_init(cfg: FwMoeConfig, weights: FwMoeWeights, stream: int) -> int:
     h = ctypes.c_void_p()
     _check(lib().fw_moe_init(ctypes.byref(cfg), ctypes.byref(weights), stream, ctypes.byref(h)), "fw_moe_init")
     return h.value
+
+
+def fw_moe_set_routing(h, routing, stream):
+    """routing: an FwMoeRouting, or None for the default step."""
+    _check(lib().fw_moe_set_routing(h, None if routing is None else ctypes.byref(routing), stream), "fw_moe_set_routing")
 
 
 def fw_moe_route(h, x, T, expert_ids, gates, stream):
@@ -259,9 +269,12 @@ class MoELayer:
     (GGUF Q8_0 blocks), and shared_gate / shared_up / shared_down for
     n_shared == 1. The library copies what it needs: the tensors may be freed
     after construction.
+
+    routing: None for the softmax over the chosen experts, or the arguments of
+    set_routing as a dict.
     """
 
-    def __init__(self, H, I, E, k, n_shared=0, T_max=16, decode_T_max=0, weights=None, stream=None, act_q8=False):
+    def __init__(self, H, I, E, k, n_shared=0, T_max=16, decode_T_max=0, weights=None, stream=None, act_q8=False, routing=None):
         self.H, self.I, self.E, self.k, self.S, self.T_max = H, I, E, k, n_shared, T_max
         cfg = FwMoeConfig(H, I, E, k, n_shared, T_max, decode_T_max, 1 if act_q8 else 0)
         w = FwMoeWeights()
@@ -269,6 +282,23 @@ class MoELayer:
             t = weights.get(name) if weights else None
             setattr(w, name, _ptr(t))
         self.handle = fw_moe_init(cfg, w, _stream(stream))
+        if routing is not None:
+            self.set_routing(stream=stream, **routing)
+
+    def set_routing(self, score="softmax", n_group=1, top_group=1, renorm=True, scale=1.0, bias=None, stream=None):
+        """How the experts are chosen and weighted from here on (fw_moe_set_routing): score "softmax" (over
+        all experts) or "sigmoid", the k best of the top_group best of n_group groups by score + bias (fp32
+        CUDA tensor [E] or None), gates scale * score, renormalised or not. score None: back to the softmax
+        over the chosen experts."""
+        if score is None:
+            return fw_moe_set_routing(self.handle, None, _stream(stream))
+        if score not in ("softmax", "sigmoid"):
+            raise ValueError('set_routing: score must be "softmax", "sigmoid" or None')
+        if bias is not None:
+            import torch
+            if not (bias.dtype is torch.float32 and bias.is_cuda and bias.is_contiguous() and bias.shape == (self.E,)):
+                raise ValueError("set_routing: bias must be a contiguous fp32 CUDA tensor [E]")
+        fw_moe_set_routing(self.handle, FwMoeRouting(1 if score == "sigmoid" else 0, n_group, top_group, 1 if renorm else 0, scale, _ptr(bias)), _stream(stream))
 
     def route(self, x, expert_ids=None, gates=None, stream=None):
         import torch

@@ -71,7 +71,7 @@ void free_handle_memory(Handle* h) {
   void* ptrs[] = {h->q_gu, h->q_dc, h->st_d, h->t_gu, h->t_d, h->wr3, h->wr, h->bias, h->ids, h->gates,
                   h->logits, h->counts, h->offsets, h->perm, h->inv, h->row_token, h->row_gate, h->uinfo,
                   h->hist, h->minfo, h->minfo_m, h->minfo_s, h->xperm, h->hbuf, h->yp, h->partial, h->zpart, h->meta,
-                  h->x_dev, h->out_dev, h->ids_dev};
+                  h->x_dev, h->out_dev, h->ids_dev, h->select_bias};
   for (void* p : ptrs)
     if (p) cudaFree(p);
 }
@@ -261,6 +261,41 @@ fw_status fw_moe_init(const fw_moe_config* cfg, const fw_moe_weights* w, void* s
     g_live.insert(h);
   }
   *out = reinterpret_cast<fw_moe_handle*>(h);
+  return FW_OK;
+}
+
+fw_status fw_moe_set_routing(fw_moe_handle* hh, const fw_moe_routing* r, void* stream) {
+  Handle* h = reinterpret_cast<Handle*>(hh);
+  if (!live(h)) return fail(FW_EINVAL, "fw_moe_set_routing: not a live handle");
+  int dev = -1;
+  cudaGetDevice(&dev);
+  if (dev != h->device) return fail(FW_EINVAL, "fw_moe_set_routing: current device %d is not the handle's device %d", dev, h->device);
+  const int E = h->cfg.E;
+  if (!r) {
+    h->rule = RouteRule{};
+    h->last_T = -1;
+    return FW_OK;
+  }
+  if (r->score != 0 && r->score != 1) return fail(FW_EINVAL, "fw_moe_set_routing: score=%d must be 0 (softmax) or 1 (sigmoid)", r->score);
+  if (r->renorm != 0 && r->renorm != 1) return fail(FW_EINVAL, "fw_moe_set_routing: renorm=%d must be 0 or 1", r->renorm);
+  if (r->n_group < 1 || r->n_group > 32 || E % r->n_group)
+    return fail(FW_EINVAL, "fw_moe_set_routing: n_group=%d must be in [1, 32] and divide E=%d", r->n_group, E);
+  if (r->top_group < 1 || r->top_group > r->n_group || r->top_group * (E / r->n_group) < h->cfg.k)
+    return fail(FW_EINVAL, "fw_moe_set_routing: top_group=%d must be in [1, n_group=%d] and its groups hold k=%d experts", r->top_group, r->n_group, h->cfg.k);
+  if (!(r->scale > 0.f) || r->scale > 3e38f) return fail(FW_EINVAL, "fw_moe_set_routing: scale must be positive and finite");
+  if (!aligned(r->select_bias, 4)) return fail(FW_EINVAL, "fw_moe_set_routing: select_bias must be 4-byte aligned");
+  if (!h->select_bias) {
+    float* p = nullptr;
+    cudaError_t e = cudaMalloc(&p, E * 4 < 256 ? 256 : E * 4);
+    if (e != cudaSuccess) return cuda_fail(e, "fw_moe_set_routing: select_bias");
+    h->select_bias = p;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = r->select_bias ? cudaMemcpyAsync(h->select_bias, r->select_bias, E * 4, cudaMemcpyDeviceToDevice, s)
+                                 : cudaMemsetAsync(h->select_bias, 0, E * 4, s);
+  if (e != cudaSuccess) return cuda_fail(e, "fw_moe_set_routing: select_bias");
+  h->rule = RouteRule{r->score == 0 ? kScoreSoftmax : kScoreSigmoid, r->n_group, r->top_group, r->renorm, r->scale, h->select_bias};
+  h->last_T = -1;
   return FW_OK;
 }
 

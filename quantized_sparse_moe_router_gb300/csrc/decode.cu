@@ -46,7 +46,7 @@
 #include <algorithm>
 #include <cstdio>
 
-#include "routing.cuh"
+#include "route_rule.cuh"
 
 namespace fw {
 namespace {
@@ -100,6 +100,7 @@ struct DecodeArgs {
   uint32_t off_info, off_acc, off_h, off_hp, off_ring;  // dynamic shared memory layout (bytes)
   uint32_t grid_extra;   // arrivals the grid wait expects beyond the grid (0; > 0 only to test the bound)
   uint64_t grid_wait_ns; // bound of the grid-wide wait
+  RouteRule rule;        // kRule: how the experts are chosen
 };
 
 // ------------------------------------------------------------- helpers
@@ -365,7 +366,9 @@ constexpr uint32_t kTmemCols = 512;  // several tokens: 16 warps x (16 tokens x 
 // ------------------------------------------------------------- the kernel
 // kMulti: several tokens (T <= 16, H <= 2048; partial output in registers);
 // otherwise one token (partial output in shared memory).
-template <bool kMulti, bool kQ8>
+// kRule: the experts are chosen by a.rule (kernels of their own: the default
+// step's code stays as it is).
+template <bool kMulti, bool kQ8, bool kRule>
 __global__ void __launch_bounds__(kThreads, 1) decode_experts_kernel(DecodeArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
@@ -482,7 +485,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_experts_kernel(DecodeArgs 
   }
   pdl_wait();  // the router's logits (and its reset of the grid counter)
   float* zbuf = reinterpret_cast<float*>(ring);  // the ring is not yet in use
-  if (kMulti) {
+  if constexpr (kRule) {
+    if (kMulti)
+      route_in_smem_by_rule<kThreads>(a.logits, T, a.E, a.k, a.S, a.rule, r);
+    else
+      route_one_in_smem_by_rule<kThreads>(a.logits, a.E, a.k, a.S, a.rule, r);
+  } else if (kMulti) {
     route_in_smem<kThreads>(a.logits, T, a.E, a.k, a.S, r, zbuf);
   } else {
     route_one_in_smem<kThreads>(a.logits, a.E, a.k, a.S, r);
@@ -874,6 +882,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_experts_kernel(DecodeArgs 
   }
 }
 
+constexpr int kNumKernels = 8;
+void (*const kKernels[kNumKernels])(DecodeArgs) = {
+    decode_experts_kernel<false, false, false>, decode_experts_kernel<true, false, false>, decode_experts_kernel<false, true, false>,
+    decode_experts_kernel<true, true, false>,   decode_experts_kernel<false, false, true>, decode_experts_kernel<true, false, true>,
+    decode_experts_kernel<false, true, true>,   decode_experts_kernel<true, true, true>};
+
 // The grid-wide wait needs every CTA resident: the grid is one CTA per SM
 // and each CTA takes more than half of an SM's shared memory (checked at
 // init), so once earlier work has drained all of them are; if something else
@@ -890,11 +904,7 @@ cudaError_t launch(const DecodeArgs& a, bool multi, bool q8, unsigned grid, size
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (q8)
-    return multi ? cudaLaunchKernelEx(&cfg, decode_experts_kernel<true, true>, a)
-                 : cudaLaunchKernelEx(&cfg, decode_experts_kernel<false, true>, a);
-  return multi ? cudaLaunchKernelEx(&cfg, decode_experts_kernel<true, false>, a)
-               : cudaLaunchKernelEx(&cfg, decode_experts_kernel<false, false>, a);
+  return cudaLaunchKernelEx(&cfg, kKernels[multi + 2 * q8 + 4 * (a.rule.score != kScoreChosen)], a);
 }
 
 int g_smem_optin = 0;  // dynamic shared memory per CTA the kernels may use
@@ -907,17 +917,16 @@ cudaError_t configure_decode_kernels() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&g_smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-  const void* kern[4] = {(const void*)decode_experts_kernel<false, false>,
-                         (const void*)decode_experts_kernel<true, false>,
-                         (const void*)decode_experts_kernel<false, true>, (const void*)decode_experts_kernel<true, true>};
-  cudaFuncAttributes fk[4];
+  const void* kern[kNumKernels];
+  for (int m = 0; m < kNumKernels; ++m) kern[m] = (const void*)kKernels[m];
+  cudaFuncAttributes fk[kNumKernels];
   size_t static_max = 0;
-  for (int m = 0; m < 4 && e == cudaSuccess; ++m) {
+  for (int m = 0; m < kNumKernels && e == cudaSuccess; ++m) {
     e = cudaFuncGetAttributes(&fk[m], kern[m]);
     static_max = std::max(static_max, fk[m].sharedSizeBytes);
   }
   if (e == cudaSuccess) g_smem_optin -= (int)static_max;
-  for (int m = 0; m < 4 && e == cudaSuccess; ++m) {
+  for (int m = 0; m < kNumKernels && e == cudaSuccess; ++m) {
     e = cudaFuncSetAttribute(kern[m], cudaFuncAttributeMaxDynamicSharedMemorySize, g_smem_optin);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kern[m], cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -925,7 +934,7 @@ cudaError_t configure_decode_kernels() {
   }
   // one CTA per SM must fit with the least shared memory a launch asks for:
   // the grid-wide wait relies on every CTA of the grid being resident
-  for (int m = 0; m < 4 && e == cudaSuccess; ++m) {
+  for (int m = 0; m < kNumKernels && e == cudaSuccess; ++m) {
     int n = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern[m], kThreads, (size_t)g_smem_optin / 2 + 1024);
     if (e == cudaSuccess && n < 1) {
@@ -957,6 +966,7 @@ cudaError_t launch_ffn_decode(Handle* h, const __nv_bfloat16* x, int T, __nv_bfl
   a.ro = RoutingOut{ids_out, gates_out, h->ids,      h->gates,    h->counts, h->offsets,
                     h->perm, h->inv,    h->row_token, h->row_gate, h->uinfo,  h->meta};
   a.meta = h->meta;
+  a.rule = h->rule;
   a.H = H;
   a.I = I;
   a.E = h->cfg.E;

@@ -77,6 +77,17 @@ struct Meta {
   int32_t diag[4];      // first failed wait: (site, block, stage, detail); site 0 = none
 };
 
+// How experts are chosen and weighted (fw_moe_set_routing); kScoreChosen is the
+// default step, a softmax over the chosen experts' logits.
+enum { kScoreChosen = 0, kScoreSoftmax = 1, kScoreSigmoid = 2 };
+struct RouteRule {
+  int score;
+  int n_group, top_group;
+  int renorm;
+  float scale;
+  const float* bias;  // [E], added to the scores for the choice alone (device; the handle's)
+};
+
 // Host-side event pool of the optional per-kernel timing.
 struct Timing {
   cudaEvent_t* ev = nullptr;  // 2 * cap events
@@ -117,6 +128,8 @@ struct Handle {
   float* bias;        // [E] (zeros when none)
   __nv_bfloat16* wr3; // [3][E][H] bf16 planes summing exactly to wr (prefill router), or null
   // ---- workspace (device), sized for T_max
+  RouteRule rule;     // kScoreChosen: the default step
+  float* select_bias; // [E], made by the first fw_moe_set_routing, or null
   int64_t rows_max;   // T_max * (k + S)
   int32_t* ids;       // [T_max][k]
   float* gates;       // [T_max][k]
@@ -209,6 +222,8 @@ bool route_prefill_mma_available(const Handle* h);
 cudaError_t launch_route_prefill_mma(Handle* h, const __nv_bfloat16* x, int T, int32_t* ids_out, float* gates_out,
                                      cudaStream_t s);
 cudaError_t launch_split_router(Handle* h, cudaStream_t s);
+// Under a rule: the choice from `parts` partial logits in h->zpart (their sum plus zbias, if not null).
+cudaError_t launch_route_rule_select(Handle* h, int T, int parts, const float* zbias, int32_t* ids_out, float* gates_out, cudaStream_t s);
 cudaError_t launch_get_permutation(const Handle* h, int T, int32_t* offsets, int32_t* perm, int32_t* inv,
                                    cudaStream_t s);
 

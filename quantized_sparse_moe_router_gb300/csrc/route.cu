@@ -8,7 +8,7 @@
 // lower id, ordered by descending z, gates = softmax restricted to the k and
 // renormalised; then the (token, slot) pairs grouped by expert, stable in
 // token order, with every count and offset kept on the device.
-#include "routing.cuh"
+#include "route_rule.cuh"
 
 namespace fw {
 namespace {
@@ -34,6 +34,8 @@ struct RouteArgs {
   float* row_gate;
   int4* uinfo;
   Meta* meta;
+  RouteRule rule;
+  float* zpart;        // tiled router under a rule: logits [T][E] for the choice after it; else null
 };
 
 constexpr int kRouteThreads = 256;
@@ -178,7 +180,10 @@ __global__ void __launch_bounds__(kNT, kNT == 128 ? 16 : 1) route_decode_kernel(
     __threadfence();
     __shared__ SmemRouting r;
     __shared__ __align__(16) float zbuf[kMaxDecodeT * kMaxE];
-    route_in_smem<kNT>(a.logits, T, a.E, a.k, a.S, r, zbuf);
+    if (a.rule.score == kScoreChosen)
+      route_in_smem<kNT>(a.logits, T, a.E, a.k, a.S, r, zbuf);
+    else
+      route_in_smem_by_rule<kNT>(a.logits, T, a.E, a.k, a.S, a.rule, r);
     RoutingOut o{a.ids_out, a.gates_out, a.ids,      a.gates,    a.counts, a.offsets,
                  a.perm,    a.inv,       a.row_token, a.row_gate, a.uinfo,  a.meta};
     publish_routing<kNT>(r, T, a.E, a.k, a.S, o);
@@ -282,6 +287,13 @@ __global__ void __launch_bounds__(256) route_tiles_kernel(RouteArgs a, int32_t* 
     }
   for (int i = tid; i < kMaxE; i += 256) s_cnt[i] = 0;
   __syncthreads();
+  if (a.zpart) {  // under a rule the choice is a kernel of its own
+    for (int i = tid; i < kRouteTileM * E; i += 256) {
+      const int tl = i / E, e = i - tl * E;
+      if (t0 + tl < T) a.zpart[(int64_t)(t0 + tl) * E + e] = zs[tl * zp + e];
+    }
+    return;
+  }
   for (int i = 0; i < 4; ++i) {
     int tl = warp * 4 + i, t = t0 + tl;
     if (t >= T) break;
@@ -526,6 +538,8 @@ RouteArgs route_args(Handle* h, const __nv_bfloat16* x, int T, int32_t* ids_out,
   a.row_gate = h->row_gate;
   a.uinfo = h->uinfo;
   a.meta = h->meta;
+  a.rule = h->rule;
+  a.zpart = h->rule.score == kScoreChosen ? nullptr : h->zpart;
   return a;
 }
 
@@ -606,6 +620,7 @@ cudaError_t launch_route_prefill(Handle* h, const __nv_bfloat16* x, int T, int32
     case 7: err = launch_tiles<7>(a, h->hist, n_tiles, s); break;
     default: err = launch_tiles<8>(a, h->hist, n_tiles, s); break;
   }
+  if (err == cudaSuccess && a.zpart) err = launch_route_rule_select(h, T, 1, nullptr, ids_out, gates_out, s);
   }
   if (err != cudaSuccess) return err;
   {

@@ -111,6 +111,65 @@ struct SmemRouting {
   int rows;
 };
 
+// One warp, once the selection's ids and masks are there: counts, offsets, the
+// table of touched experts and the grouped positions (and the shared expert's gates).
+__device__ __forceinline__ void group_in_smem(int T, int E, int k, int S, SmemRouting& r, int lane) {
+  const int EU = E + S;
+  // lane l owns the consecutive experts [l per, l per + per), in registers;
+  // both scans (rows and touched experts) in one pass of shuffles
+  constexpr int kPer = (kMaxE + 1 + 31) / 32;
+  const int per = (EU + 31) / 32, b0 = lane * per;
+  int cn[kPer];
+  int sc = 0, sn = 0;
+#pragma unroll
+  for (int m = 0; m < kPer; ++m) {
+    const int i = b0 + m;
+    cn[m] = (m < per && i < EU) ? (i < E ? __popc(r.mask[i]) : T) : 0;
+    sc += cn[m];
+    sn += cn[m] > 0;
+  }
+  int ic = sc, in = sn;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int uc = __shfl_up_sync(0xFFFFFFFFu, ic, o), un = __shfl_up_sync(0xFFFFFFFFu, in, o);
+    if (lane >= o) {
+      ic += uc;
+      in += un;
+    }
+  }
+  int rc = ic - sc, rn = in - sn;
+#pragma unroll
+  for (int m = 0; m < kPer; ++m) {
+    const int i = b0 + m;
+    if (m < per && i < EU) {
+      r.cnt[i] = cn[m];
+      r.off[i] = rc;
+      if (cn[m] > 0) r.u[rn++] = make_int4(i, rc, cn[m], 0);
+      rc += cn[m];
+    }
+  }
+  if (lane == 31) {
+    r.off[EU] = ic;
+    r.rows = ic;
+    r.n_unique = in;
+  }
+  __syncwarp();
+  // grouped positions: within an expert, ascending token
+  for (int p = lane; p < T * k; p += 32) {
+    const int t = p / k, ee = r.ids[p];
+    const int pos = r.off[ee] + __popc(r.mask[ee] & ((1u << t) - 1u));
+    r.tok[pos] = t;
+    r.slot[pos] = p;
+  }
+  if (S)
+    for (int t = lane; t < T; t += 32) {
+      const int pos = r.off[E] + t;
+      r.tok[pos] = t;
+      r.slot[pos] = T * k + t;
+      r.gates[T * k + t] = 1.0f;
+    }
+}
+
 // Whole block (NT threads): selection for T <= 16 tokens from logits [T][E]
 // (global, written by an earlier kernel), gates, and the grouping. Three
 // block barriers; after the last one every field is valid.
@@ -184,59 +243,7 @@ __device__ void route_in_smem(const float* logits, int T, int E, int k, int S, S
   __syncthreads();
 
   if (warp == 0) {
-    // lane l owns the consecutive experts [l per, l per + per), in registers;
-    // both scans (rows and touched experts) in one pass of shuffles
-    constexpr int kPer = (kMaxE + 1 + 31) / 32;
-    const int per = (EU + 31) / 32, b0 = lane * per;
-    int cn[kPer];
-    int sc = 0, sn = 0;
-#pragma unroll
-    for (int m = 0; m < kPer; ++m) {
-      const int i = b0 + m;
-      cn[m] = (m < per && i < EU) ? (i < E ? __popc(r.mask[i]) : T) : 0;
-      sc += cn[m];
-      sn += cn[m] > 0;
-    }
-    int ic = sc, in = sn;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int uc = __shfl_up_sync(0xFFFFFFFFu, ic, o), un = __shfl_up_sync(0xFFFFFFFFu, in, o);
-      if (lane >= o) {
-        ic += uc;
-        in += un;
-      }
-    }
-    int rc = ic - sc, rn = in - sn;
-#pragma unroll
-    for (int m = 0; m < kPer; ++m) {
-      const int i = b0 + m;
-      if (m < per && i < EU) {
-        r.cnt[i] = cn[m];
-        r.off[i] = rc;
-        if (cn[m] > 0) r.u[rn++] = make_int4(i, rc, cn[m], 0);
-        rc += cn[m];
-      }
-    }
-    if (lane == 31) {
-      r.off[EU] = ic;
-      r.rows = ic;
-      r.n_unique = in;
-    }
-    __syncwarp();
-    // grouped positions: within an expert, ascending token
-    for (int p = lane; p < T * k; p += 32) {
-      const int t = p / k, ee = r.ids[p];
-      const int pos = r.off[ee] + __popc(r.mask[ee] & ((1u << t) - 1u));
-      r.tok[pos] = t;
-      r.slot[pos] = p;
-    }
-    if (S)
-      for (int t = lane; t < T; t += 32) {
-        const int pos = r.off[E] + t;
-        r.tok[pos] = t;
-        r.slot[pos] = T * k + t;
-        r.gates[T * k + t] = 1.0f;
-      }
+    group_in_smem(T, E, k, S, r, lane);
   } else {
     for (int t = warp - 1; t < T; t += NW - 1) {
       const float zj = lane < k ? r.zsel[t * k + lane] : 0.f;
@@ -245,6 +252,30 @@ __device__ void route_in_smem(const float* logits, int T, int E, int k, int S, S
     }
   }
   __syncthreads();
+}
+
+// One warp, one token: lane j < k brings the expert of rank j; each gets one grouped
+// row, in the ascending order of the ids.
+__device__ __forceinline__ void group_one_in_smem(int id, int E, int k, int S, SmemRouting& r, int lane) {
+  // lane j < k: the expert of rank j, its row among the k ids in ascending order
+  const int e = lane < k ? id : 0x7FFFFFFF;
+  int pos = 0;
+  for (int m = 0; m < k; ++m) pos += __shfl_sync(0xFFFFFFFFu, e, m) < e;
+  if (lane < k) {
+    r.ids[lane] = id;
+    r.u[pos] = make_int4(e, pos, 1, 0);
+    r.tok[pos] = 0;
+    r.slot[pos] = lane;
+  }
+  if (lane == 0) {
+    if (S) {
+      r.u[k] = make_int4(E, k, 1, 0);
+      r.tok[k] = 0;
+      r.slot[k] = k;
+    }
+    r.n_unique = k + S;
+    r.rows = k + S;
+  }
 }
 
 // The same for one token (T = 1), with less work and code: warp 0 selects
@@ -266,26 +297,8 @@ __device__ void route_one_in_smem(const float* logits, int E, int k, int S, Smem
     int id;
     float zv;
     warp_topk(zl, E, k, lane, &id, &zv);
-    // lane j < k: the expert of rank j, its row among the k ids in ascending order
-    const int e = lane < k ? id : 0x7FFFFFFF;
-    int pos = 0;
-    for (int m = 0; m < k; ++m) pos += __shfl_sync(0xFFFFFFFFu, e, m) < e;
-    if (lane < k) {
-      r.ids[lane] = id;
-      r.zsel[lane] = zv;
-      r.u[pos] = make_int4(e, pos, 1, 0);
-      r.tok[pos] = 0;
-      r.slot[pos] = lane;
-    }
-    if (lane == 0) {
-      if (S) {
-        r.u[k] = make_int4(E, k, 1, 0);
-        r.tok[k] = 0;
-        r.slot[k] = k;
-      }
-      r.n_unique = k + S;
-      r.rows = k + S;
-    }
+    if (lane < k) r.zsel[lane] = zv;
+    group_one_in_smem(id, E, k, S, r, lane);
   }
   __syncthreads();
 }
