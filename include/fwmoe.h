@@ -411,14 +411,16 @@ fw_status fw_attn_q4(const fw_attn_q4_args *args, void *workspace, int64_t bytes
  * fp32, rounded to nearest, the codes to nearest even. A block with an
  * infinity or NaN stands for non-finite values. Activations: a block is 128
  * neighbours of one token (the last one of a token may be shorter); codes
- * [T][K], scales fp32 [ceil(K / 128)][T]. Weights: a block is 128 x 128 of
+ * [T][K], scales fp32 [ceil(K / 128)] rows of T, scale_stride elements apart (a
+ * multiple of 4, 16-byte aligned: rows are copied in bulk). Weights: a block is 128 x 128 of
  * [N][K] (smaller at the edges); codes [N][K], scales fp32
  * [ceil(N / 128)][ceil(K / 128)], as checkpoints of 8-bit block-scaled models
  * hold them. */
 
 /* x DEVICE bf16 [T][K], x_stride elements between tokens (a multiple of 8), K a
- * multiple of 16; codes DEVICE e4m3 [T][K], 16-byte aligned; scales DEVICE fp32. */
-fw_status fw_fp8_quantize(const void *x, int64_t x_stride, int32_t T, int32_t K, void *codes, float *scales, void *stream);
+ * multiple of 16; codes DEVICE e4m3 [T][K] and scales DEVICE fp32, 16-byte aligned. */
+fw_status fw_fp8_quantize(const void *x, int64_t x_stride, int32_t T, int32_t K, void *codes, float *scales, int64_t scale_stride,
+                          void *stream);
 
 /* w DEVICE [N][K] bf16 (w_fp32 == 0) or fp32 (1), K a multiple of 16. */
 fw_status fw_fp8_quantize_weight(const void *w, int32_t w_fp32, int32_t N, int32_t K, void *codes, float *scales, void *stream);
@@ -435,8 +437,9 @@ typedef struct {
   int32_t T, K, N;           /* T >= 0; K a multiple of 16; N >= 1 */
   int32_t out_fp32;          /* 0: out is bf16, 1: fp32 */
   const void *x;             /* DEVICE, 16-byte aligned: bf16 [T][K], or with x_scale e4m3 codes */
-  const float *x_scale;      /* DEVICE fp32 [ceil(K / 128)][T], or NULL */
+  const float *x_scale;      /* DEVICE fp32 [ceil(K / 128)] rows of T, 16-byte aligned, or NULL */
   int64_t x_stride;          /* elements between tokens: a multiple of 8 (bf16) or 16 (codes) */
+  int64_t x_scale_stride;    /* elements between rows of x_scale: at least T, a multiple of 4 */
   const void *w;             /* DEVICE e4m3 [N][K], 16-byte aligned */
   const float *w_scale;      /* DEVICE fp32 [ceil(N / 128)][ceil(K / 128)] */
   void *out;                 /* DEVICE [T][N] */
@@ -470,7 +473,8 @@ typedef struct {
   void *h;                   /* DEVICE bf16 [T][H], or NULL */
   int64_t residual_out_stride, h_stride;
   void *h_codes;             /* DEVICE e4m3 [T][H], or NULL */
-  float *h_scale;            /* DEVICE fp32 [ceil(H / 128)][T], with h_codes */
+  float *h_scale;            /* DEVICE fp32 [ceil(H / 128)] rows of T, 16-byte aligned, with h_codes */
+  int64_t h_scale_stride;    /* elements between its rows: at least T, a multiple of 4 */
 } fw_norm_residual_args;
 fw_status fw_norm_residual(const fw_norm_residual_args *args, void *stream);
 

@@ -99,7 +99,7 @@ def lib():
             "fw_kv_export": [vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp],
             "fw_attn_q4_workspace": [vp, vp],
             "fw_attn_q4": [vp, vp, i64, vp],
-            "fw_fp8_quantize": [vp, i64, i32, i32, vp, vp, vp],
+            "fw_fp8_quantize": [vp, i64, i32, i32, vp, vp, i64, vp],
             "fw_fp8_quantize_weight": [vp, i32, i32, i32, vp, vp, vp],
             "fw_linear_fp8_workspace": [vp, vp],
             "fw_linear_fp8": [vp, vp, i64, vp],

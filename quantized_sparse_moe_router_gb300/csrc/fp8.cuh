@@ -61,6 +61,30 @@ __device__ __forceinline__ uint2 fp8_block_of_lanes(const uint4 v, float* scale)
   return bf16x8_to_e4m3(v, __fdiv_rn(kFp8Max, top));
 }
 
+// Whether the barrier's phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait without a call (around which the caller's registers would have to be
+// saved) and without sleep: what waits here is on the way of every block.
+__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    if ((i & 1023u) == 0) {  // (the clock takes long to read)
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) return false;
+    }
+  return true;
+}
+
 }  // namespace dev
 
 // What the linear kernels take: codes of the tokens with their scales, or (few
@@ -69,21 +93,41 @@ struct LinearArgs {
   int T, K, N, KB;          // KB = blocks along K
   const __nv_bfloat16* x;   // bf16 [T][x_stride], where the kernel quantises
   int64_t x_stride;
-  const float* x_scale;     // [KB][T]
+  const float* x_scale;     // [KB] rows of T, x_scale_stride apart
+  int64_t x_scale_stride;
   const float* w_scale;     // [ceil(N / 128)][KB]
   void* out;
   int64_t out_stride;
   int out_fp32;
   int32_t* status;
+  // The predecessor in the stream is the quantisation of x, which began when all before
+  // it was complete: nothing but the tokens' codes and scales has to be waited for.
+  int x_alone;
 };
 
-cudaError_t launch_fp8_quantize(const void* x, int64_t x_stride, int T, int K, void* codes, float* scales, cudaStream_t s);
+cudaError_t configure_fp8_quantize();
+cudaError_t launch_fp8_quantize(const void* x, int64_t x_stride, int T, int K, void* codes, float* scales, int64_t scale_stride, cudaStream_t s);
 
 // A tensor map of codes: rows of K bytes, `stride` apart, in boxes of 128 bytes by `box` rows, 128-byte swizzle.
 cudaError_t encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, int64_t stride, int box);
 
+// The same of results: rows of `cols` bf16 or fp32 values, in boxes of 128 bytes by `box` rows, 128-byte swizzle.
+cudaError_t encode_rows(CUtensorMap* map, const void* out, bool fp32, int64_t rows, int64_t cols, int64_t row_bytes, int box);
+
+// The same of bf16 values: rows of K, `stride` elements apart, in boxes of 128 by `box` rows, no swizzle.
+cudaError_t encode_values(CUtensorMap* map, const __nv_bfloat16* x, int64_t T, int64_t K, int64_t stride, int box);
+
+// The same of tokens' scales: KB rows of T, in boxes of `box` by one row, no swizzle.
+cudaError_t encode_scales(CUtensorMap* map, const float* scales, int64_t T, int KB, int64_t stride, int box);
+
 cudaError_t configure_linear_few();
 bool linear_few_quantises(int T);  // whether the kernel for few tokens takes bf16 itself
+// Blocks of K that an SM takes one after the other at most, at more than 64 tokens.
+int64_t linear_few_blocks(int T, int N, int KB, int sms);
 cudaError_t launch_linear_few(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s);
+
+cudaError_t configure_linear_many();
+int64_t linear_many_cycles(int T, int N, int KB, int sms);  // about how many its products take
+cudaError_t launch_linear_many(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s);
 
 }  // namespace fw

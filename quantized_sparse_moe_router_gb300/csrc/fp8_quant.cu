@@ -14,7 +14,7 @@ using namespace dev;
 constexpr int kQuantThreads = 256, kPairs = 4;
 
 __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T, int K, int KB,
-                                                                     uint8_t* __restrict__ codes, float* __restrict__ scales) {
+                                                                     uint8_t* __restrict__ codes, float* __restrict__ scales, int64_t scale_stride) {
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
   pdl_wait();
   pdl_launch_dependents();
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
     const int k = b[i] * kFp8Block + 8 * l;
     if (first + 2 * i < blocks) {
       if (k < K) *reinterpret_cast<uint2*>(codes + (int64_t)t[i] * K + k) = c;
-      if (l == 0) scales[(int64_t)b[i] * T + t[i]] = scale;
+      if (l == 0) scales[b[i] * scale_stride + t[i]] = scale;
     }
   }
 }
@@ -98,27 +98,34 @@ bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 
 }  // namespace
 
-cudaError_t launch_fp8_quantize(const void* x, int64_t x_stride, int T, int K, void* codes, float* scales, cudaStream_t s) {
+cudaError_t configure_fp8_quantize() {
+  // with the linear kernels' carve-out of shared memory they can start beside it
+  return cudaFuncSetAttribute(fp8_quantize_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
+}
+
+cudaError_t launch_fp8_quantize(const void* x, int64_t x_stride, int T, int K, void* codes, float* scales, int64_t scale_stride, cudaStream_t s) {
   const int KB = fp8_blocks(K);
   const int64_t per = kQuantThreads / 32 * 2 * kPairs, ctas = ((int64_t)T * KB + per - 1) / per;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_dependent(fp8_quantize_kernel, dim3((unsigned)ctas), dim3(kQuantThreads), 0, s, static_cast<const __nv_bfloat16*>(x), x_stride, T, K, KB,
-                          static_cast<uint8_t*>(codes), scales);
+                          static_cast<uint8_t*>(codes), scales, scale_stride);
 }
 
 }  // namespace fw
 
 using namespace fw;
 
-extern "C" fw_status fw_fp8_quantize(const void* x, int64_t x_stride, int32_t T, int32_t K, void* codes, float* scales, void* stream) {
+extern "C" fw_status fw_fp8_quantize(const void* x, int64_t x_stride, int32_t T, int32_t K, void* codes, float* scales, int64_t scale_stride,
+                                     void* stream) {
   if (T < 0 || K < 16 || K % 16) return set_error(FW_EINVAL, "fw_fp8_quantize: need T >= 0 and K a positive multiple of 16");
   if (T == 0) return FW_OK;
   if (!x || !codes || !scales) return set_error(FW_EINVAL, "fw_fp8_quantize: null pointer");
   if (x_stride < K || x_stride % 8) return set_error(FW_EINVAL, "fw_fp8_quantize: x_stride must cover K and be a multiple of 8 elements");
-  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4))
-    return set_error(FW_EINVAL, "fw_fp8_quantize: x and codes need 16-byte, scales 4-byte alignment");
+  if (scale_stride < T || scale_stride % 4) return set_error(FW_EINVAL, "fw_fp8_quantize: scale_stride must cover T and be a multiple of 4 elements");
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16))
+    return set_error(FW_EINVAL, "fw_fp8_quantize: x, codes and scales need 16-byte alignment");
   if (fw_status st = check_device("fw_fp8_quantize: needs an sm_103 device"); st != FW_OK) return st;
-  const cudaError_t e = launch_fp8_quantize(x, x_stride, T, K, codes, scales, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_fp8_quantize(x, x_stride, T, K, codes, scales, scale_stride, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_cuda_error(e, "fw_fp8_quantize: launch");
   return FW_OK;
 }

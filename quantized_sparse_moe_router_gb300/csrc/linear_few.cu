@@ -5,19 +5,21 @@
 //
 // The weights are the tensor core's A operand: a tile is 128 outputs by one
 // block of 128 along K, so it has one scale; the tokens are B (kTok columns).
-// The inner sum over a block is made in tensor memory; four warps read it,
+// The inner sum over a block is made in tensor memory; four or eight warps read it,
 // scale it and add it to sums in registers while the next block's runs -- the
 // scales are any fp32 numbers, which the tensor core cannot apply.
 //
-// A cluster of up to eight CTAs shares one tile of 128 outputs, each with a part
-// of K: two CTAs on every SM stream weights at once whatever N is. Their sums
-// are added in the order of their ranks through distributed shared memory, so
-// results do not depend on timing.
+// Where there are fewer tiles of 128 outputs than CTAs find room, a cluster of up to
+// eight CTAs shares one, each with a part of K; their sums are added in the order of
+// their ranks through distributed shared memory, so results do not depend on timing.
+// Where there are more, a CTA takes several tiles, and its copies run on from one to
+// the next.
 //
-// Warps: 0 copies (weights, and the tokens' codes), 1 issues the products, 2-5
-// scale and add (one tensor-memory quarter each), then either four that
-// quantise bf16 tokens straight into the stage (at most 16 tokens: a launch and
-// a trip through memory less) or one that fetches scales.
+// Warps: 0 copies weights, 1 issues the products, 2 copies the tokens' codes and
+// scales, 4 on scale and add (tensor-memory quarter = warp % 4). With at most 16
+// bf16 tokens it copies those, and four more warps quantise them within the stage (a
+// launch and a trip through memory less; loaded by these warps, two blocks ahead, their
+// latency bounded them).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -32,18 +34,22 @@ using namespace dev;
 
 constexpr int kRows = 128;                           // outputs of a tile: the height of a weight block
 constexpr uint32_t kWBytes = kRows * kFp8Block;
-constexpr int kLastWarp = 6;                         // warps 2-5 scale and add; from 6 on: quantisers, or the fetcher of scales
+constexpr int kFirstEpi = 4, kQuantWarps = 4;
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kSmemHalf = 113 * 1024;           // for two CTAs on an SM
 
-template <int kTok>
+// kQuant: a stage also holds the tokens as they come, 128 bf16 values each.
+template <int kTok, bool kQuant>
 struct Few {
-  static constexpr uint32_t XBytes = kTok * kFp8Block, StageBytes = kWBytes + XBytes;
-  static constexpr int Stages = (int)((kSmemHalf - 1024 - 512) / (StageBytes + kTok * 4));
-  static constexpr int Acc = kTok <= 32 ? 4 : 2;     // buffers of sums in tensor memory
-  static constexpr uint32_t Cols = Acc * kTok < 32 ? 32 : Acc * kTok;
-  static constexpr uint32_t SmemBytes = 1024 + Stages * (StageBytes + kTok * 4);
-  static_assert(Cols <= 256, "two CTAs share tensor memory");
+  static constexpr int Ctas = kTok <= 64 ? 2 : 1;    // on an SM
+  static constexpr int EpiWarps = kTok <= 32 ? 4 : 8;
+  static constexpr int Mine = kTok * 4 / EpiWarps;   // columns of a scaling thread
+  static constexpr int Slot = kTok < 32 ? 32 : kTok; // scales of a stage (copies of them start on 128 bytes)
+  static constexpr uint32_t XBytes = kTok * kFp8Block, RawBytes = kQuant ? 2 * XBytes : 0, StageBytes = kWBytes + XBytes + RawBytes, ScaleBytes = Slot * 4;
+  static constexpr int Stages = (int)(((Ctas == 2 ? 113 : 226) * 1024 - 1024 - 512) / (StageBytes + ScaleBytes));
+  static constexpr int Acc = 4;                      // buffers of sums in tensor memory: the way round one is about 1,200 cycles, the products 480
+  static constexpr uint32_t Cols = Acc * kTok;
+  static constexpr uint32_t SmemBytes = 1024 + Stages * (StageBytes + ScaleBytes);
+  static_assert(Cols >= 32 && Cols * Ctas <= 512 && (Cols & (Cols - 1)) == 0, "an SM's CTAs share tensor memory");
   static_assert(kRows * kTok * 4 <= Stages * StageBytes, "the partial sums take the ring's place");
 };
 
@@ -79,12 +85,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// The float at this CTA's shared address `addr`, in the CTA of rank `rank` of the cluster.
-__device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
+// Four floats at this CTA's shared address `addr`, in the CTA of rank `rank` of the cluster.
+__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
   uint32_t at;
-  float v;
+  float4 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
   return v;
 }
 
@@ -96,31 +102,56 @@ __device__ __forceinline__ void store_out(const LinearArgs& a, int t, int n, flo
     static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
 }
 
+// Four neighbouring outputs of a token, n a multiple of four.
+__device__ __forceinline__ void store_four(const LinearArgs& a, int t, int n, float4 v) {
+  const int64_t at = (int64_t)t * a.out_stride + n;
+  const uintptr_t to = reinterpret_cast<uintptr_t>(a.out) + at * (a.out_fp32 ? 4 : 2);
+  if (n + 4 <= a.N && to % (a.out_fp32 ? 16 : 8) == 0) {
+    if (a.out_fp32)
+      *reinterpret_cast<float4*>(to) = v;
+    else
+      *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2_bits(v.x, v.y), bf16x2_bits(v.z, v.w));
+    return;
+  }
+  if (n < a.N) store_out(a, t, n, v.x);
+  if (n + 1 < a.N) store_out(a, t, n + 1, v.y);
+  if (n + 2 < a.N) store_out(a, t, n + 2, v.z);
+  if (n + 3 < a.N) store_out(a, t, n + 3, v.w);
+}
+
 template <int kTok, bool kQuant>
-__global__ void __launch_bounds__((kLastWarp + (kQuant ? 4 : 1)) * 32, 2)
-    linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const LinearArgs a, const int split) {
-  using F = Few<kTok>;
-  constexpr int kStages = F::Stages, kAcc = F::Acc;
+constexpr int few_threads() {
+  return (kFirstEpi + Few<kTok, kQuant>::EpiWarps + (kQuant ? kQuantWarps : 0)) * 32;
+}
+
+// tiles: of 128 outputs; split: CTAs that share one (more than one: a CTA has one tile).
+template <int kTok, bool kQuant>
+__global__ void __launch_bounds__(few_threads<kTok, kQuant>(), Few<kTok, kQuant>::Ctas)
+    linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_s,
+                      const LinearArgs a, const int tiles, const int split) {
+  using F = Few<kTok, kQuant>;
+  constexpr int kStages = F::Stages, kAcc = F::Acc, kMine = F::Mine;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], raw_full[kStages], acc_full[kAcc], acc_empty[kAcc];
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  uint8_t* ring = smem_raw + pad;                                                    // [kStages][weights 128 x 128, tokens kTok x 128]
-  float* s_scale = reinterpret_cast<float*>(ring + kStages * F::StageBytes);         // [kStages][kTok] scales, token's times weights'
-  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
-  const int n0 = tile * kRows, t0 = blockIdx.y * kTok, nt = ::min(kTok, a.T - t0);
-  const int b0 = (int)((int64_t)a.KB * rank / split), b1 = (int)((int64_t)a.KB * (rank + 1) / split);
-  const float* ws = a.w_scale + (int64_t)tile * a.KB;
+  uint8_t* ring = smem_raw + pad;                                                    // [kStages][weights 128 x 128, tokens kTok x 128, raw]
+  float* s_scale = reinterpret_cast<float*>(ring + kStages * F::StageBytes);         // [kStages][Slot] the tokens' scales
+  const int rank = blockIdx.x % split, first = blockIdx.x / split, step = gridDim.x / split;
+  const int t0 = blockIdx.y * kTok, nt = ::min(kTok, a.T - t0);
+  const int b0 = (int)((int64_t)a.KB * rank / split), nb = (int)((int64_t)a.KB * (rank + 1) / split) - b0;  // this CTA's blocks of K
+  const int blocks = first < tiles ? ((tiles - first + step - 1) / step) * nb : 0;                          // over all its tiles
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1 + (kQuant ? 4 : 1));  // the copies, and the warps that write scales
-      mbar_init(&empty[i], 1 + 4);                // the products, and the warps that have read the scales
+      mbar_init(&full[i], 1 + (kQuant ? kQuantWarps : 1));  // the weights' copies; the tokens'
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&empty[i], 1 + F::EpiWarps);                // the products, and the warps that have read the scales
     }
     for (int i = 0; i < kAcc; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], F::EpiWarps);
     }
     fence_mbar_init();
   }
@@ -132,163 +163,151 @@ __global__ void __launch_bounds__((kLastWarp + (kQuant ? 4 : 1)) * 32, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  bool ok = true;
+  // by a whole warp, which stays together
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!mbar_wait(bar, parity)) {
-      raise(a.status, FW_KV_TIMEOUT);
-      ok = false;
-    }
+    const bool ok = __all_sync(0xFFFFFFFFu, wait_inline(bar, parity));
+    if (!ok) raise(a.status, FW_KV_TIMEOUT);
     return ok;
   };
-  pdl_wait();
+  if (!a.x_alone || warp == 2) pdl_wait();
   pdl_launch_dependents();
 
-  if (warp == 0) {
-    if (lane == 0) {
-      int i = 0;
-      for (int b = b0; b < b1; ++b, ++i) {
-        const int s = i % kStages;
-        if (!wait(&empty[s], ((i / kStages) & 1) ^ 1)) break;
+  if (warp == 0 || warp == 2) {
+    bool ok = true;
+    int i = 0, s = 0, b = 0, tile = first;
+    uint32_t phase = 1;
+    for (; i < blocks; ++i) {
+      if (!(ok = wait(&empty[s], phase))) break;
+      if (elect_one()) {
         uint8_t* st = ring + s * F::StageBytes;
-        mbar_arrive_expect_tx(&full[s], kWBytes + (kQuant ? 0u : F::XBytes));
-        tma_2d(st, &map_w, b * kFp8Block, n0, &full[s]);
-        if (!kQuant) tma_2d(st + kWBytes, &map_x, b * kFp8Block, t0, &full[s]);
-      }
-      // copies still in flight after a wait that gave up land before the CTA leaves
-      if (!ok)
-        for (int j = ::max(0, i - kStages); j < i; ++j) mbar_wait(&full[j % kStages], (j / kStages) & 1);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int i = 0;
-      for (int b = b0; b < b1; ++b, ++i) {
-        const int s = i % kStages, c = i % kAcc;
-        if (!wait(&full[s], (i / kStages) & 1) || !wait(&acc_empty[c], ((i / kAcc) & 1) ^ 1)) break;
-        tc_fence_after();
-        const uint32_t w = sw128_desc_lo(smem_u32(ring + s * F::StageBytes)), x = sw128_desc_lo(smem_u32(ring + s * F::StageBytes + kWBytes));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f8(tmem + c * kTok, w + 2 * k, x + 2 * k, idesc_e4m3(kRows, kTok), k != 0);
-        mma_commit(&empty[s]);
-        mma_commit(&acc_full[c]);
-      }
-      if (i > 0) mbar_wait(&acc_full[(i - 1) % kAcc], ((i - 1) / kAcc) & 1);  // no product outlives the tensor memory
-    }
-  } else if (warp < kLastWarp) {
-    const int q = warp & 3;
-    float acc[kTok];
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) acc[j] = 0.f;
-    int i = 0;
-    for (int b = b0; b < b1; ++b, ++i) {
-      const int s = i % kStages, c = i % kAcc;
-      // (the stage's scales are there since before its products began)
-      bool fine = mbar_wait(&full[s], (i / kStages) & 1) && mbar_wait(&acc_full[c], (i / kAcc) & 1);
-      if (!__all_sync(0xFFFFFFFFu, fine)) {
-        raise(a.status, FW_KV_TIMEOUT);
-        break;
-      }
-      tc_fence_after();
-      const uint32_t from = tmem + ((uint32_t)(32 * q) << 16) + c * kTok;
-      const float4* sc = reinterpret_cast<const float4*>(s_scale + s * kTok);
-#pragma unroll
-      for (int j0 = 0; j0 < kTok; j0 += 16) {
-        uint32_t v[16];
-        tmem_load(from + j0, v);
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = sc[(j0 + j) / 4];
-          acc[j0 + j] = fmaf(__uint_as_float(v[j]), f.x, acc[j0 + j]);
-          acc[j0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y, acc[j0 + j + 1]);
-          acc[j0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z, acc[j0 + j + 2]);
-          acc[j0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w, acc[j0 + j + 3]);
+        if (warp == 0) {
+          mbar_arrive_expect_tx(&full[s], kWBytes);
+          tma_2d(st, &map_w, (b0 + b) * kFp8Block, tile * kRows, &full[s]);
+        } else if constexpr (kQuant) {
+          mbar_arrive_expect_tx(&raw_full[s], F::RawBytes);
+          tma_2d(st + kWBytes + F::XBytes, &map_x, (b0 + b) * kFp8Block, t0, &raw_full[s]);
+        } else {
+          mbar_arrive_expect_tx(&full[s], F::XBytes + F::ScaleBytes);
+          tma_2d(st + kWBytes, &map_x, (b0 + b) * kFp8Block, t0, &full[s]);
+          tma_2d(s_scale + s * F::Slot, &map_s, t0, b0 + b, &full[s]);
         }
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&acc_empty[c]);
-        mbar_arrive(&empty[s]);
-      }
+      if (++b == nb) b = 0, tile += step;
+      if (++s == kStages) s = 0, phase ^= 1;
     }
-    const int row = 32 * q + lane;
-    if (split == 1) {
-      if (n0 + row < a.N) {
+    // copies still in flight after a wait that gave up land before the CTA leaves
+    if (!ok)
+      for (int j = ::max(0, i - kStages); j < i; ++j) wait_inline(kQuant && warp == 2 ? &raw_full[j % kStages] : &full[j % kStages], (j / kStages) & 1);
+  } else if (warp == 1) {
+    // (descriptors from a value shuffled from lane 0 are uniform for the compiler)
+    const uint32_t ring_lo = __shfl_sync(0xFFFFFFFFu, sw128_desc_lo(smem_u32(ring)), 0), cols0 = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    int i = 0, s = 0;
+    uint32_t phase = 0;
+    for (; i < blocks; ++i) {
+      const int c = i % kAcc;
+      const uint32_t c_phase = ((i / kAcc) & 1) ^ 1;
+      // (both are asked at once: an answer takes some 70 cycles)
+      const bool f = mbar_test(&full[s], phase), e = mbar_test(&acc_empty[c], c_phase);
+      if (!__all_sync(0xFFFFFFFFu, f && e) && !(wait(&full[s], phase) && wait(&acc_empty[c], c_phase))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t w = ring_lo + s * (F::StageBytes >> 4), x = w + (kWBytes >> 4);
 #pragma unroll
-        for (int j = 0; j < kTok; ++j)
-          if (j < nt) store_out(a, t0 + j, n0 + row, acc[j]);
+        for (int k = 0; k < 4; ++k) mma_f8(cols0 + c * kTok, w + 2 * k, x + 2 * k, idesc_e4m3(kRows, kTok), k != 0);
+        mma_commit(&acc_full[c]);
+        mma_commit(&empty[s]);
       }
-    } else {  // (every copy has landed and every product has read it: the last block's sums are complete)
-      float* part = reinterpret_cast<float*>(ring);  // [kTok][128]
+      __syncwarp();
+      if (++s == kStages) s = 0, phase ^= 1;
+    }
+    if (i > 0) wait_inline(&acc_full[(i - 1) % kAcc], ((i - 1) / kAcc) & 1);  // no product outlives the tensor memory
+  } else if (warp >= kFirstEpi && warp < kFirstEpi + F::EpiWarps) {
+    const int q = warp & 3, part = (warp - kFirstEpi) >> 2, row = 32 * q + lane;
+    const uint32_t from0 = tmem + ((uint32_t)(32 * q) << 16) + part * kMine;
+    bool ok = true;
+    int i = 0, s = 0;
+    uint32_t phase = 0;
+    for (int tile = first; tile < tiles && ok; tile += step) {
+      const float* ws = a.w_scale + (int64_t)tile * a.KB + b0;
+      float w_now = 0.f, w_next = lane < nb ? __ldg(ws + lane) : 0.f;  // the weights' scales of 32 blocks, one a lane
+      float acc[kMine];
 #pragma unroll
-      for (int j = 0; j < kTok; ++j) part[j * kRows + row] = acc[j];
+      for (int j = 0; j < kMine; ++j) acc[j] = 0.f;
+      for (int b = 0; b < nb; ++b, ++i) {
+        if (b % 32 == 0) {
+          w_now = w_next;
+          w_next = b + 32 + lane < nb ? __ldg(ws + b + 32 + lane) : 0.f;
+        }
+        const float w = __shfl_sync(0xFFFFFFFFu, w_now, b % 32);
+        const int c = i % kAcc;
+        const uint32_t c_phase = (i / kAcc) & 1;
+        // (the stage's scales are there since before its products began)
+        const bool f = mbar_test(&full[s], phase), e = mbar_test(&acc_full[c], c_phase);
+        if (!__all_sync(0xFFFFFFFFu, f && e) && !(ok = wait(&full[s], phase) && wait(&acc_full[c], c_phase))) break;
+        tc_fence_after();
+        const uint32_t from = from0 + c * kTok;
+        const float4* sc = reinterpret_cast<const float4*>(s_scale + s * F::Slot + part * kMine);
+#pragma unroll
+        for (int j0 = 0; j0 < kMine; j0 += 16) {
+          uint32_t v[16];
+          tmem_load(from + j0, v);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 f = sc[(j0 + j) / 4];
+            acc[j0 + j] = fmaf(__uint_as_float(v[j]), f.x * w, acc[j0 + j]);
+            acc[j0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y * w, acc[j0 + j + 1]);
+            acc[j0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z * w, acc[j0 + j + 2]);
+            acc[j0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w * w, acc[j0 + j + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&acc_empty[c]);
+          mbar_arrive(&empty[s]);
+        }
+        if (++s == kStages) s = 0, phase ^= 1;
+      }
+      if (!ok) break;
+      if (split == 1) {
+        const int n = tile * kRows + row;
+        if (n < a.N) {
+#pragma unroll
+          for (int j = 0; j < kMine; ++j)
+            if (part * kMine + j < nt) store_out(a, t0 + part * kMine + j, n, acc[j]);
+        }
+      } else {  // (every copy has landed and every product has read it: the last block's sums are complete)
+        float* sums = reinterpret_cast<float*>(ring);  // [kTok][128]
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) sums[(part * kMine + j) * kRows + row] = acc[j];
+      }
     }
   } else if constexpr (kQuant) {
-    // 128 threads: rows r and r + 8 of the block, eight values each; the next block's values are fetched ahead
-    const int r = (tid - kLastWarp * 32) >> 4, ch = tid & 15;
-    auto fetch = [&](int b, uint4 (&v)[2]) {
-      const int k = b * kFp8Block + 8 * ch;
+    if (warp >= kFirstEpi + F::EpiWarps) {
+      // 128 threads: rows r, r + 8, .. of a block, eight values each
+      const int r = (tid - (kFirstEpi + F::EpiWarps) * 32) >> 4, ch = tid & 15;
+      int s = 0;
+      uint32_t phase = 0;
+      for (int i = 0; i < blocks; ++i) {
+        if (!wait(&raw_full[s], phase)) break;
+        uint8_t* x = ring + s * F::StageBytes + kWBytes;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = r + 8 * h;
-        v[h] = t < nt && k < a.K && b < b1 ? ld_nc_v4(a.x + (int64_t)(t0 + t) * a.x_stride + k) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    uint4 now[2], next[2];
-    fetch(b0, now);
-    int i = 0;
-    for (int b = b0; b < b1; ++b, ++i) {
-      const int s = i % kStages;
-      fetch(b + 1, next);
-      const float w = __ldg(ws + b);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1))) {
-        raise(a.status, FW_KV_TIMEOUT);
-        break;
-      }
-      uint8_t* x = ring + s * F::StageBytes + kWBytes;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (8 * h < nt || h == 0) {
-          const int t = r + 8 * h;
-          float scale;
-          const uint2 c = fp8_block_of_lanes(now[h], &scale);
-          // (chunk of 16 bytes j of row t lies at j ^ (t % 8): the 128-byte swizzle)
-          *reinterpret_cast<uint2*>(x + t * kFp8Block + (((ch >> 1) ^ (t & 7)) << 4) + 8 * (ch & 1)) = c;
-          if (ch == 0) s_scale[s * kTok + t] = scale * w;
+        for (int h = 0; h < kTok / 8; ++h) {
+          if (8 * h < nt) {
+            const int t = r + 8 * h;
+            float scale;
+            const uint2 c = fp8_block_of_lanes(*reinterpret_cast<const uint4*>(x + F::XBytes + t * 256 + ch * 16), &scale);
+            // (chunk of 16 bytes j of row t lies at j ^ (t % 8): the 128-byte swizzle)
+            *reinterpret_cast<uint2*>(x + t * kFp8Block + (((ch >> 1) ^ (t & 7)) << 4) + 8 * (ch & 1)) = c;
+            if (ch == 0) s_scale[s * F::Slot + t] = scale;
+          }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        if (++s == kStages) s = 0, phase ^= 1;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
-      now[0] = next[0];
-      now[1] = next[1];
-    }
-  } else {
-    // one warp: the tokens' scales times the weights', a block ahead
-    constexpr int kPer = (kTok + 31) / 32;
-    auto fetch = [&](int b, float (&v)[kPer]) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int t = lane + 32 * j;
-        v[j] = t < nt && b < b1 ? __ldg(a.x_scale + (int64_t)b * a.T + t0 + t) * __ldg(ws + b) : 0.f;
-      }
-    };
-    float now[kPer], next[kPer];
-    fetch(b0, now);
-    int i = 0;
-    for (int b = b0; b < b1; ++b, ++i) {
-      const int s = i % kStages;
-      fetch(b + 1, next);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1))) {
-        raise(a.status, FW_KV_TIMEOUT);
-        break;
-      }
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (lane + 32 * j < kTok) s_scale[s * kTok + lane + 32 * j] = now[j];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) now[j] = next[j];
     }
   }
 
@@ -298,13 +317,17 @@ __global__ void __launch_bounds__((kLastWarp + (kQuant ? 4 : 1)) * 32, 2)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F::Cols) : "memory");
   if (split > 1) {
     cluster_sync();  // every CTA's sums are in its shared memory
-    const int all = nt * kRows, i0 = all * rank / split, i1 = all * (rank + 1) / split;
-    const uint32_t part = smem_u32(ring);
+    // each its share of them, four outputs of a token a thread, all ranks' parts on their way at once
+    const int all = nt * (kRows / 4), i0 = all * rank / split, i1 = all * (rank + 1) / split;
+    const uint32_t sums = smem_u32(ring);
     for (int i = i0 + tid; i < i1; i += (int)blockDim.x) {
-      const int n = n0 + i % kRows;
-      float v = 0.f;
-      for (int r = 0; r < split; ++r) v += ld_peer(part + 4 * i, r);
-      if (n < a.N) store_out(a, t0 + i / kRows, n, v);
+      float4 p[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) p[r] = r < split ? ld_peer(sums + 16 * i, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 v = p[0];
+#pragma unroll
+      for (int r = 1; r < kMaxCluster; ++r) v.x += p[r].x, v.y += p[r].y, v.z += p[r].z, v.w += p[r].w;
+      store_four(a, t0 + i / (kRows / 4), first * kRows + i % (kRows / 4) * 4, v);
     }
     cluster_sync();  // none leaves while another still reads its sums
   }
@@ -314,26 +337,41 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 template <int kTok, bool kQuant>
 cudaError_t configure() {
-  cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<kTok, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<kTok>::SmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<kTok, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<kTok, kQuant>::SmemBytes);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(linear_few_kernel<kTok, kQuant>, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
   return e;
 }
 
+// CTAs that share a tile: as many as keep the SM with the most work shortest, in
+// blocks of K (*longest), with a few for each CTA's beginning and end. All find room at
+// once, and a part of K has two blocks.
+int split_of(int tiles, int rows, int KB, int ctas_per_sm, int sms, int64_t* longest) {
+  const int64_t all = (int64_t)tiles * rows;
+  int split = 1;
+  int64_t best = INT64_MAX;
+  for (int c = 1; c <= kMaxCluster && (c == 1 || (all * c <= (int64_t)ctas_per_sm * sms && KB >= 2 * c)); ++c) {
+    const int64_t cost = (all * c + sms - 1) / sms * ((KB + c - 1) / c + 2);
+    if (cost < best) best = cost, split = c;
+  }
+  if (longest) *longest = best;
+  return split;
+}
+
 template <int kTok, bool kQuant>
 cudaError_t launch(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s) {
-  CUtensorMap map_w, map_x = {};
+  CUtensorMap map_w, map_x = {}, map_s = {};
   cudaError_t e = encode_codes(&map_w, w, a.N, a.K, a.K, kRows);
-  if (e == cudaSuccess && !kQuant) e = encode_codes(&map_x, x_codes, a.T, a.K, codes_stride, kTok);
+  if (e == cudaSuccess) e = kQuant ? encode_values(&map_x, a.x, a.T, a.K, a.x_stride, kTok) : encode_codes(&map_x, x_codes, a.T, a.K, codes_stride, kTok);
+  if (e == cudaSuccess && !kQuant) e = encode_scales(&map_s, a.x_scale, a.T, a.KB, a.x_scale_stride, Few<kTok, kQuant>::Slot);
   if (e != cudaSuccess) return e;
-  // parts of K: as many as still find room beside each other, two CTAs an SM, with two blocks each at least
-  const int64_t tiles = (int64_t)((a.N + kRows - 1) / kRows) * ((a.T + kTok - 1) / kTok);
-  int split = 1;
-  while (split < kMaxCluster && tiles * split * 2 <= 2 * sms && a.KB >= split * 4) split *= 2;
+  const int tiles = (a.N + kRows - 1) / kRows, rows = (a.T + kTok - 1) / kTok;
+  const int split = split_of(tiles, rows, a.KB, Few<kTok, kQuant>::Ctas, sms, nullptr);
+  const int64_t room = (int64_t)Few<kTok, kQuant>::Ctas * sms;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.N + kRows - 1) / kRows * split), (unsigned)((a.T + kTok - 1) / kTok));
-  cfg.blockDim = dim3((kLastWarp + (kQuant ? 4 : 1)) * 32);
-  cfg.dynamicSmemBytes = Few<kTok>::SmemBytes;
+  cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, std::max<int64_t>(1, room / rows))), (unsigned)rows);
+  cfg.blockDim = dim3(few_threads<kTok, kQuant>());
+  cfg.dynamicSmemBytes = Few<kTok, kQuant>::SmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -342,8 +380,8 @@ cudaError_t launch(const LinearArgs& a, const void* w, const void* x_codes, int6
   attr[1].val.clusterDim.x = split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_few_kernel<kTok, kQuant>, map_w, map_x, a, split);
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_few_kernel<kTok, kQuant>, map_w, map_x, map_s, a, tiles, split);
 }
 
 }  // namespace
@@ -356,6 +394,32 @@ cudaError_t encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int6
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_rows(CUtensorMap* map, const void* out, bool fp32, int64_t rows, int64_t cols, int64_t row_bytes, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t boxes[2] = {fp32 ? 32u : 64u, (cuuint32_t)box}, steps[2] = {1, 1};
+  const CUresult r = g_encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(out), dims, strides, boxes,
+                              steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_values(CUtensorMap* map, const __nv_bfloat16* x, int64_t T, int64_t K, int64_t stride, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)T}, strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t boxes[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)box}, steps[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(x), dims, strides, boxes, steps,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_scales(CUtensorMap* map, const float* scales, int64_t T, int KB, int64_t stride, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)T, (cuuint64_t)KB}, strides[1] = {(cuuint64_t)stride * 4};
+  const cuuint32_t boxes[2] = {(cuuint32_t)box, 1}, steps[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(scales), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// (17 to 32 tokens: 12.4 us at 4096 x 4096 against 10.3 with a launch for them)
 bool linear_few_quantises(int T) { return T <= 16; }
 
 cudaError_t configure_linear_few() {
@@ -373,6 +437,12 @@ cudaError_t configure_linear_few() {
   if (e == cudaSuccess) e = configure<64, false>();
   if (e == cudaSuccess) e = configure<128, false>();
   return e;
+}
+
+int64_t linear_few_blocks(int T, int N, int KB, int sms) {
+  int64_t longest;
+  split_of((N + kRows - 1) / kRows, (T + 127) / 128, KB, Few<128, false>::Ctas, sms, &longest);
+  return longest;
 }
 
 cudaError_t launch_linear_few(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s) {

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : kMaxThreads) norm_residual_kerne
       const uint2 c = fp8_block_of_lanes(out, &scale);
       if (has) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(u.h_codes) + row * u.H + at) = c;
-        if ((l & 15) == 0) u.h_scale[(int64_t)(at / kFp8Block) * u.T + row] = scale;
+        if ((l & 15) == 0) u.h_scale[(at / kFp8Block) * u.h_scale_stride + row] = scale;
       }
     }
   }
@@ -193,12 +193,14 @@ extern "C" fw_status fw_norm_residual(const fw_norm_residual_args* u, void* stre
   if (u->y_stride < H || u->y_stride % 8 || (u->residual && (u->residual_stride < H || u->residual_stride % 8)) ||
       (u->residual_out && (u->residual_out_stride < H || u->residual_out_stride % 8)) || (u->h && (u->h_stride < H || u->h_stride % 8)))
     return set_error(FW_EINVAL, "fw_norm_residual: token strides must cover H and be multiples of 8 elements");
+  if (u->h_codes && (u->h_scale_stride < u->T || u->h_scale_stride % 4))
+    return set_error(FW_EINVAL, "fw_norm_residual: h_scale_stride must cover T and be a multiple of 4 elements");
   if (u->gate && (u->gate_per_token ? u->gate_stride < 0 : (u->gate_stride % 8 || (u->gate_stride != 0 && u->gate_stride < H))))
     return set_error(FW_EINVAL, "fw_norm_residual: gate_stride must be 0, or cover H and be a multiple of 8 (per token: not negative)");
   for (const void* p : {u->y, u->residual, u->gate_per_token ? nullptr : u->gate, (const void*)u->post_norm, (const void*)u->norm, (const void*)u->residual_out,
-                        (const void*)u->h, (const void*)u->h_codes})
+                        (const void*)u->h, (const void*)u->h_codes, (const void*)u->h_scale})
     if (!al(p, 16)) return set_error(FW_EINVAL, "fw_norm_residual: tensors need 16-byte alignment");
-  if (!al(u->gate, u->gate_fp32 ? 4 : 2) || !al(u->h_scale, 4)) return set_error(FW_EINVAL, "fw_norm_residual: gate and h_scale need the alignment of their elements");
+  if (!al(u->gate, u->gate_fp32 ? 4 : 2)) return set_error(FW_EINVAL, "fw_norm_residual: gate needs the alignment of its elements");
   if (fw_status st = check_device("fw_norm_residual: needs an sm_103 device"); st != FW_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int vecs = u->H / 8;

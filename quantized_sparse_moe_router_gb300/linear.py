@@ -16,7 +16,7 @@ from .attention import _byref, _empty, _empty_on, _fail, _i32, _i64, _f32, _not_
 
 
 class FwLinearFp8Args(ctypes.Structure):
-    _fields_ = ([(n, _i32) for n in ("T", "K", "N", "out_fp32")] + [("x", _vp), ("x_scale", _vp), ("x_stride", _i64), ("w", _vp), ("w_scale", _vp),
+    _fields_ = ([(n, _i32) for n in ("T", "K", "N", "out_fp32")] + [("x", _vp), ("x_scale", _vp), ("x_stride", _i64), ("x_scale_stride", _i64), ("w", _vp), ("w_scale", _vp),
                                                                     ("out", _vp), ("out_stride", _i64), ("status", _vp)])
 
 
@@ -24,7 +24,7 @@ class FwNormResidualArgs(ctypes.Structure):
     _fields_ = ([(n, _i32) for n in ("T", "H", "residual_fp32", "gate_fp32", "gate_per_token")] + [("eps", _f32), ("scale", _f32)]
                 + [(n, _vp) for n in ("y", "residual", "gate")] + [(n, _i64) for n in ("y_stride", "residual_stride", "gate_stride")]
                 + [(n, _vp) for n in ("post_norm", "norm", "residual_out", "h")] + [("residual_out_stride", _i64), ("h_stride", _i64)]
-                + [("h_codes", _vp), ("h_scale", _vp)])
+                + [("h_codes", _vp), ("h_scale", _vp), ("h_scale_stride", _i64)])
 
 
 _bf16, _fp32, _e4m3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
@@ -44,13 +44,19 @@ def _blocks(n):
     return (n + 127) // 128
 
 
+def _scales(new, K, T, device):
+    """fp32 [ceil(K / 128), T] with its rows apart as the library wants them, and how far."""
+    stride = (T + 3) // 4 * 4 or 4
+    return new((_blocks(K), stride), dtype=_fp32, device=device)[:, :T], stride
+
+
 def _stream_of(t, stream):
     return _raw_stream(t.get_device()) if stream is None else stream
 
 
 def quantize_fp8(x, stream=None):
-    """bf16 [T, K] -> codes float8_e4m3fn [T, K] and scales fp32 [ceil(K / 128), T]: blocks of 128
-    neighbours of a token (fw_fp8_quantize). K a multiple of 16."""
+    """bf16 [T, K] -> codes float8_e4m3fn [T, K] and scales fp32 [ceil(K / 128), T] (rows a multiple of
+    4 apart): blocks of 128 neighbours of a token (fw_fp8_quantize). K a multiple of 16."""
     w = "quantize_fp8"
     if x.dim() != 2:
         _fail(f"{w}: x must be [T, K]")
@@ -58,8 +64,9 @@ def quantize_fp8(x, stream=None):
     xs = _rows(w, "x", x, K, _bf16)
     _one_device(w, x)
     new = _empty if stream is None else functools.partial(_empty_on, stream)
-    codes, scales = new((T, K), dtype=_e4m3, device=x.device), new((_blocks(K), T), dtype=_fp32, device=x.device)
-    rc = _fw.lib().fw_fp8_quantize(x.data_ptr(), xs, T, K, codes.data_ptr(), scales.data_ptr(), _stream_of(x, stream))
+    codes = new((T, K), dtype=_e4m3, device=x.device)
+    scales, stride = _scales(new, K, T, x.device)
+    rc = _fw.lib().fw_fp8_quantize(x.data_ptr(), xs, T, K, codes.data_ptr(), scales.data_ptr(), stride, _stream_of(x, stream))
     if rc:
         _fw._check(rc, "fw_fp8_quantize")
     return codes, scales
@@ -93,9 +100,13 @@ def linear_fp8(x, w, w_scale, x_scale=None, out=None, out_dtype=None, status=Non
     if not (w.dtype is _e4m3 and w.is_cuda and w.is_contiguous() and w.shape[1] == K):
         _fail(f"{f}: w must be a contiguous float8_e4m3fn CUDA tensor [N, {K}]")
     xs = _rows(f, "x", x, K, _bf16 if x_scale is None else _e4m3)
-    for name, t, shape in (("w_scale", w_scale, (_blocks(N), _blocks(K))), ("x_scale", x_scale, (_blocks(K), T))):
-        if t is not None and not (t.dtype is _fp32 and t.is_cuda and t.is_contiguous() and t.shape == shape):
-            _fail(f"{f}: {name} must be a contiguous fp32 CUDA tensor {list(shape)}")
+    if not (w_scale.dtype is _fp32 and w_scale.is_cuda and w_scale.is_contiguous() and w_scale.shape == (_blocks(N), _blocks(K))):
+        _fail(f"{f}: w_scale must be a contiguous fp32 CUDA tensor [{_blocks(N)}, {_blocks(K)}]")
+    ss = 0
+    if x_scale is not None:
+        if not (x_scale.dtype is _fp32 and x_scale.is_cuda and x_scale.shape == (_blocks(K), T) and (x_scale.stride(1) == 1 or T <= 1)):
+            _fail(f"{f}: x_scale must be an fp32 CUDA tensor [{_blocks(K)}, {T}] with contiguous rows")
+        ss = x_scale.stride(0)
     if status is not None:
         _not_ints(f, status=status)
     _one_device(f, x, w, w_scale, x_scale, out, status)
@@ -109,7 +120,7 @@ def linear_fp8(x, w, w_scale, x_scale=None, out=None, out_dtype=None, status=Non
         if out.dim() != 2 or out.shape[0] != T or out_dtype not in (None, out.dtype):
             _fail(f"{f}: out must be [T, N] of out_dtype")
         os = _rows(f, "out", out, N, _bf16, _fp32)
-    a = FwLinearFp8Args(T, K, N, 1 if out.dtype is _fp32 else 0, x.data_ptr(), None if x_scale is None else x_scale.data_ptr(), xs, w.data_ptr(),
+    a = FwLinearFp8Args(T, K, N, 1 if out.dtype is _fp32 else 0, x.data_ptr(), None if x_scale is None else x_scale.data_ptr(), xs, ss, w.data_ptr(),
                         w_scale.data_ptr(), out.data_ptr(), os, None if status is None else status.data_ptr())
     args, L, need = _byref(a), _fw.lib(), _i64()
     rc = L.fw_linear_fp8_workspace(args, _byref(need))
@@ -165,11 +176,12 @@ def norm_residual(y, residual=None, norm=None, post_norm=None, gate=None, scale=
         ros = _rows(f, "residual_out", residual_out, H, kind)
         if residual_out.shape[0] != T:
             _fail(f"{f}: residual_out must be [T, H]")
-    h_at, hs, c_at, s_at = None, 0, None, None
+    h_at, hs, c_at, s_at, ss = None, 0, None, None, 0
     if fp8:
         if h is not None:
             _fail(f"{f}: h is bf16, fp8 gives codes and scales")
-        h = new((T, H), dtype=_e4m3, device=dev), new((_blocks(H), T), dtype=_fp32, device=dev)
+        scales, ss = _scales(new, H, T, dev)
+        h = new((T, H), dtype=_e4m3, device=dev), scales
         c_at, s_at = h[0].data_ptr(), h[1].data_ptr()
     else:
         if h is None:
@@ -181,7 +193,7 @@ def norm_residual(y, residual=None, norm=None, post_norm=None, gate=None, scale=
         h_at = h.data_ptr()
     rc = _fw.lib().fw_norm_residual(_byref(FwNormResidualArgs(
         T, H, 1 if kind is _fp32 else 0, g_fp32, g_token, eps, scale, y.data_ptr(), r_at, g_at, ys, rs, gs, None if post_norm is None else post_norm.data_ptr(),
-        None if norm is None else norm.data_ptr(), residual_out.data_ptr(), h_at, ros, hs, c_at, s_at)), _stream_of(y, stream))
+        None if norm is None else norm.data_ptr(), residual_out.data_ptr(), h_at, ros, hs, c_at, s_at, ss)), _stream_of(y, stream))
     if rc:
         _fw._check(rc, "fw_norm_residual")
     return residual_out, h

@@ -91,7 +91,8 @@ def test_blocks_of_weights(N, K, kind):
 
 SHAPES = [(1, 16, 1), (1, 128, 128), (1, 2048, 5120), (2, 4000, 129), (7, 1040, 640), (8, 2048, 256), (9, 2048, 256), (16, 7168, 384), (17, 512, 1000),
           (31, 2064, 255), (33, 144, 127), (64, 2048, 2048), (65, 1152, 130), (100, 7168, 256), (128, 256, 4096), (129, 640, 300), (257, 4096, 512),
-          (333, 4000, 2051), (512, 1024, 1024), (1000, 528, 777)]
+          (333, 4000, 2051), (512, 1024, 1024), (1000, 528, 777), (70, 7168, 128), (256, 16, 512), (257, 16, 513), (300, 2000, 5000), (2100, 384, 2304),
+          (1300, 640, 4097), (4000, 272, 136)]
 
 
 @pytest.mark.parametrize("T, K, N", SHAPES)

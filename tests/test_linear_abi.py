@@ -19,13 +19,13 @@ def built():
 
 
 def call_quantize(**over):
-    a = dict(x=4096, x_stride=256, T=3, K=256, codes=4096, scales=4096)
+    a = dict(x=4096, x_stride=256, T=3, K=256, codes=4096, scales=4096, scale_stride=4)
     a.update(over)
     return fw.lib().fw_fp8_quantize(*a.values(), None)
 
 
 @pytest.mark.parametrize("bad", [dict(T=-1), dict(K=0), dict(K=24), dict(x=None), dict(codes=None), dict(scales=None), dict(x_stride=248), dict(x_stride=260),
-                                 dict(x=4104), dict(codes=4104), dict(scales=4098)])
+                                 dict(x=4104), dict(codes=4104), dict(scales=4104), dict(scale_stride=3), dict(scale_stride=0), dict(scale_stride=6)])
 def test_quantize_refuses(bad):
     assert call_quantize(**bad) == fw.FW_EINVAL and fw.fw_moe_last_error()
 
@@ -40,7 +40,7 @@ def test_quantize_weight_refuses(bad):
 
 
 def linear_args(**over):
-    a = dict(T=40, K=256, N=64, out_fp32=0, x=4096, x_scale=None, x_stride=256, w=4096, w_scale=4096, out=4096, out_stride=64, status=None)
+    a = dict(T=40, K=256, N=64, out_fp32=0, x=4096, x_scale=None, x_stride=256, x_scale_stride=40, w=4096, w_scale=4096, out=4096, out_stride=64, status=None)
     a.update(over)
     return ctypes.byref(fw.FwLinearFp8Args(**a))
 
@@ -53,7 +53,7 @@ def test_linear_refuses_sizes(bad, status):
     assert fw.lib().fw_linear_fp8(linear_args(**bad), None, 0, None) == status and fw.fw_moe_last_error()
 
 
-@pytest.mark.parametrize("bad", [dict(x=None), dict(w=None), dict(w_scale=None), dict(out=None), dict(x=4104), dict(w=4104), dict(x_scale=4098), dict(out=4097),
+@pytest.mark.parametrize("bad", [dict(x=None), dict(w=None), dict(w_scale=None), dict(out=None), dict(x=4104), dict(w=4104), dict(x_scale=4104), dict(x_scale=4096, x_scale_stride=36), dict(x_scale=4096, x_scale_stride=42), dict(out=4097),
                                  dict(out=4098, out_fp32=1), dict(x_stride=248), dict(x_stride=260), dict(x_scale=4096, x_stride=264), dict(out_stride=63),
                                  dict(status=4098)])
 def test_linear_refuses_pointers(bad):
@@ -67,13 +67,13 @@ def test_linear_workspace():
     for at, size in ((None, 1 << 30), (4096, need.value - 1), (4104, 1 << 30)):
         assert fw.lib().fw_linear_fp8(linear_args(T=300, K=400, x_stride=400), at, size, None) == fw.FW_EINVAL
         assert "workspace" in fw.fw_moe_last_error()
-    assert fw.lib().fw_linear_fp8_workspace(linear_args(T=300, x_scale=4096), ctypes.byref(need)) == fw.FW_OK and need.value == 0
+    assert fw.lib().fw_linear_fp8_workspace(linear_args(T=300, x_scale=4096, x_scale_stride=300), ctypes.byref(need)) == fw.FW_OK and need.value == 0
     assert fw.lib().fw_linear_fp8_workspace(linear_args(), None) == fw.FW_EINVAL
 
 
 def norm_args(**over):
     a = dict(T=3, H=256, residual_fp32=0, gate_fp32=0, gate_per_token=0, eps=1e-6, scale=1.0, y=4096, residual=4096, gate=4096, y_stride=256, residual_stride=256,
-             gate_stride=256, post_norm=4096, norm=4096, residual_out=4096, h=4096, residual_out_stride=256, h_stride=256, h_codes=4096, h_scale=4096)
+             gate_stride=256, post_norm=4096, norm=4096, residual_out=4096, h=4096, residual_out_stride=256, h_stride=256, h_codes=4096, h_scale=4096, h_scale_stride=4)
     a.update(over)
     return ctypes.byref(fw.FwNormResidualArgs(**a))
 
@@ -84,7 +84,7 @@ def norm_args(**over):
     (dict(residual_out=None, h=None, h_codes=None), -1), (dict(y_stride=248), -1), (dict(y_stride=260), -1), (dict(residual_stride=8), -1),
     (dict(residual_out_stride=252), -1), (dict(h_stride=255), -1), (dict(gate_stride=128), -1), (dict(gate_stride=257), -1),
     (dict(gate_per_token=1, gate_stride=-1), -1), (dict(y=4104), -1), (dict(residual=4100), -1), (dict(gate=4104), -1), (dict(norm=4100), -1),
-    (dict(post_norm=4104), -1), (dict(residual_out=4098), -1), (dict(h=4100), -1), (dict(h_codes=4104), -1), (dict(h_scale=4098), -1),
+    (dict(post_norm=4104), -1), (dict(residual_out=4098), -1), (dict(h=4100), -1), (dict(h_codes=4104), -1), (dict(h_scale=4104), -1), (dict(h_scale_stride=2), -1), (dict(h_scale_stride=5), -1),
     (dict(gate_per_token=1, gate=4097), -1)])
 def test_norm_residual_refuses(bad, status):
     assert fw.lib().fw_norm_residual(norm_args(**bad), None) == status and fw.fw_moe_last_error()
