@@ -211,9 +211,19 @@ def fw_moe_profile_end(h):
 
 
 # ------------------------------------------------------------ torch level
+_current_stream = None  # the current stream's handle, without an object where torch can
+
+
 def _stream(stream=None) -> int:
-    import torch
-    return stream if stream is not None else torch.cuda.current_stream().cuda_stream
+    global _current_stream
+    if stream is not None:
+        return stream
+    if _current_stream is None:
+        import torch
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.init()
+        _current_stream = (lambda: torch.cuda.current_stream().cuda_stream) if raw is None or device is None else (lambda: raw(device()))
+    return _current_stream()
 
 
 def _ptr(t):
@@ -301,11 +311,11 @@ class MoELayer:
         fw_moe_set_routing(self.handle, FwMoeRouting(1 if score == "sigmoid" else 0, n_group, top_group, 1 if renorm else 0, scale, _ptr(bias)), _stream(stream))
 
     def route(self, x, expert_ids=None, gates=None, stream=None):
-        import torch
         T = x.shape[0]
         if expert_ids is None:
+            import torch
             expert_ids = torch.empty((T, self.k), dtype=torch.int32, device=x.device)
-        fw_moe_route(self.handle, _ptr(x), T, _ptr(expert_ids), _ptr(gates), _stream(stream))
+        fw_moe_route(self.handle, x.data_ptr(), T, expert_ids.data_ptr(), _ptr(gates), _stream(stream))
         return expert_ids, gates
 
     def ffn(self, x, out=None, stream=None):

@@ -7,12 +7,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 import torch
 
 import quantized_sparse_moe_router_gb300 as _fw
 
-from .attention import _byref, _empty, _empty_on, _fail, _i32, _i64, _f32, _not_ints, _one_device, _raw_stream, _vp
+from . import attention as _attention
+from .attention import _empty, _empty_on, _fail, _i32, _i64, _f32, _not_ints, _raw_stream, _vp
 
 
 class FwLinearFp8Args(ctypes.Structure):
@@ -27,7 +29,23 @@ class FwNormResidualArgs(ctypes.Structure):
                 + [("h_codes", _vp), ("h_scale", _vp), ("h_scale_stride", _i64)])
 
 
-_bf16, _fp32, _e4m3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+# The argument structs as the C compiler lays them out (a pointer is a whole number;
+# 0 for null): packing one takes a fraction of a ctypes structure's time, and small
+# calls are bound by what is done here.
+_linear_args = struct.Struct("@4i9q").pack
+_norm_args = struct.Struct("@5i2f15q").pack
+
+_bf16, _fp32, _e4m3, _uint8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8
+_byref = ctypes.byref
+# (not in every build of torch)
+_empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _new(rows, cols, dtype, like, stream):
+    """An empty [rows, cols] tensor for a call on `stream` (None: the current one)."""
+    if stream is None:
+        return _empty((rows, cols), dtype=dtype, device=like.device) if _empty_strided is None else _empty_strided((rows, cols), (cols, 1), dtype)
+    return _empty_on(stream, (rows, cols), dtype, like.device)
 
 
 def _rows(where, name, t, cols, *types):
@@ -40,14 +58,19 @@ def _rows(where, name, t, cols, *types):
     return a if t.shape[0] > 1 else cols
 
 
+def _one_device(where, *tensors):
+    if _attention._several is not False:
+        _attention._one_device(where, *tensors)
+
+
 def _blocks(n):
     return (n + 127) // 128
 
 
-def _scales(new, K, T, device):
+def _scales(K, T, like, stream):
     """fp32 [ceil(K / 128), T] with its rows apart as the library wants them, and how far."""
     stride = (T + 3) // 4 * 4 or 4
-    return new((_blocks(K), stride), dtype=_fp32, device=device)[:, :T], stride
+    return _new((K + 127) // 128, stride, _fp32, like, stream)[:, :T], stride
 
 
 def _stream_of(t, stream):
@@ -63,9 +86,8 @@ def quantize_fp8(x, stream=None):
     T, K = x.shape
     xs = _rows(w, "x", x, K, _bf16)
     _one_device(w, x)
-    new = _empty if stream is None else functools.partial(_empty_on, stream)
-    codes = new((T, K), dtype=_e4m3, device=x.device)
-    scales, stride = _scales(new, K, T, x.device)
+    codes = _new(T, K, _e4m3, x, stream)
+    scales, stride = _scales(K, T, x, stream)
     rc = _fw.lib().fw_fp8_quantize(x.data_ptr(), xs, T, K, codes.data_ptr(), scales.data_ptr(), stride, _stream_of(x, stream))
     if rc:
         _fw._check(rc, "fw_fp8_quantize")
@@ -80,60 +102,91 @@ def quantize_fp8_weight(w, stream=None):
         _fail(f"{f}: w must be a contiguous bf16 or fp32 CUDA tensor [N, K]")
     N, K = w.shape
     _one_device(f, w)
-    new = _empty if stream is None else functools.partial(_empty_on, stream)
-    codes, scales = new((N, K), dtype=_e4m3, device=w.device), new((_blocks(N), _blocks(K)), dtype=_fp32, device=w.device)
+    codes, scales = _new(N, K, _e4m3, w, stream), _new(_blocks(N), _blocks(K), _fp32, w, stream)
     rc = _fw.lib().fw_fp8_quantize_weight(w.data_ptr(), 1 if w.dtype is _fp32 else 0, N, K, codes.data_ptr(), scales.data_ptr(), _stream_of(w, stream))
     if rc:
         _fw._check(rc, "fw_fp8_quantize_weight")
     return codes, scales
 
 
+def _linear_refuses(x, w, w_scale, x_scale):
+    """Says what is wrong with linear_fp8's inputs."""
+    f = "linear_fp8"
+    if x.dim() != 2 or w.dim() != 2:
+        _fail(f"{f}: x must be [T, K] and w [N, K]")
+    (T, K), N = x.shape, w.shape[0]
+    if not (w.dtype is _e4m3 and w.is_cuda and w.is_contiguous() and w.shape[1] == K):
+        _fail(f"{f}: w must be a contiguous float8_e4m3fn CUDA tensor [N, {K}]")
+    _rows(f, "x", x, K, _bf16 if x_scale is None else _e4m3)
+    if not (w_scale.dtype is _fp32 and w_scale.is_cuda and w_scale.is_contiguous() and w_scale.shape == (_blocks(N), _blocks(K))):
+        _fail(f"{f}: w_scale must be a contiguous fp32 CUDA tensor [{_blocks(N)}, {_blocks(K)}]")
+    _fail(f"{f}: x_scale must be an fp32 CUDA tensor [{_blocks(K)}, {T}] with contiguous rows")
+
+
 def linear_fp8(x, w, w_scale, x_scale=None, out=None, out_dtype=None, status=None, stream=None):
     """x W^T in 8 bits (fw_linear_fp8): x bf16 [T, K], or codes [T, K] with x_scale as quantize_fp8 or
     norm_residual(fp8=True) give them; w codes [N, K] with w_scale as quantize_fp8_weight gives them
     -> [T, N], bf16 or (out_dtype, or out's) fp32."""
-    f = "linear_fp8"
-    if x.dim() != 2 or w.dim() != 2:
-        _fail(f"{f}: x must be [T, K] and w [N, K]")
-    T, K = x.shape
-    N = w.shape[0]
-    if not (w.dtype is _e4m3 and w.is_cuda and w.is_contiguous() and w.shape[1] == K):
-        _fail(f"{f}: w must be a contiguous float8_e4m3fn CUDA tensor [N, {K}]")
-    xs = _rows(f, "x", x, K, _bf16 if x_scale is None else _e4m3)
-    if not (w_scale.dtype is _fp32 and w_scale.is_cuda and w_scale.is_contiguous() and w_scale.shape == (_blocks(N), _blocks(K))):
-        _fail(f"{f}: w_scale must be a contiguous fp32 CUDA tensor [{_blocks(N)}, {_blocks(K)}]")
-    ss = 0
-    if x_scale is not None:
-        if not (x_scale.dtype is _fp32 and x_scale.is_cuda and x_scale.shape == (_blocks(K), T) and (x_scale.stride(1) == 1 or T <= 1)):
-            _fail(f"{f}: x_scale must be an fp32 CUDA tensor [{_blocks(K)}, {T}] with contiguous rows")
-        ss = x_scale.stride(0)
+    sx, sw, codes = x.shape, w.shape, x_scale is not None
+    if len(sx) != 2 or len(sw) != 2:
+        _linear_refuses(x, w, w_scale, x_scale)
+    T, K = sx
+    N = sw[0]
+    xs, one = x.stride()
+    if not (x.dtype is (_e4m3 if codes else _bf16) and w.dtype is _e4m3 and w_scale.dtype is _fp32 and sw[1] == K and (one == 1 or T == 0)
+            and w_scale.shape == ((N + 127) // 128, (K + 127) // 128) and w.is_contiguous() and w_scale.is_contiguous() and x.is_cuda and w.is_cuda
+            and w_scale.is_cuda):
+        _linear_refuses(x, w, w_scale, x_scale)
+    if T < 2:
+        xs = K
+    s_at = ss = 0
+    if codes:
+        if not (x_scale.dtype is _fp32 and x_scale.is_cuda and x_scale.shape == ((K + 127) // 128, T) and (x_scale.stride(1) == 1 or T < 2)):
+            _linear_refuses(x, w, w_scale, x_scale)
+        s_at, ss = x_scale.data_ptr(), x_scale.stride(0)
     if status is not None:
-        _not_ints(f, status=status)
-    _one_device(f, x, w, w_scale, x_scale, out, status)
-    dev = x.device
+        _not_ints("linear_fp8", status=status)
+    if _attention._several is not False:
+        _attention._one_device("linear_fp8", x, w, w_scale, x_scale, out, status)
     if out is None:
-        if out_dtype not in (None, _bf16, _fp32):
-            _fail(f"{f}: out_dtype must be torch.bfloat16 or torch.float32")
-        kind, os = out_dtype or _bf16, N
-        out = _empty((T, N), dtype=kind, device=dev) if stream is None else _empty_on(stream, (T, N), kind, dev)
+        if out_dtype is None:
+            out_dtype = _bf16
+        elif out_dtype is not _bf16 and out_dtype is not _fp32:
+            _fail("linear_fp8: out_dtype must be torch.bfloat16 or torch.float32")
+        out, os = _new(T, N, out_dtype, x, stream), N
     else:
         if out.dim() != 2 or out.shape[0] != T or out_dtype not in (None, out.dtype):
-            _fail(f"{f}: out must be [T, N] of out_dtype")
-        os = _rows(f, "out", out, N, _bf16, _fp32)
-    a = FwLinearFp8Args(T, K, N, 1 if out.dtype is _fp32 else 0, x.data_ptr(), None if x_scale is None else x_scale.data_ptr(), xs, ss, w.data_ptr(),
-                        w_scale.data_ptr(), out.data_ptr(), os, None if status is None else status.data_ptr())
-    args, L, need = _byref(a), _fw.lib(), _i64()
-    rc = L.fw_linear_fp8_workspace(args, _byref(need))
-    if rc:
-        _fw._check(rc, "fw_linear_fp8_workspace")
-    size, at = need.value, None
-    if size:
-        ws = _empty(size, dtype=torch.uint8, device=dev) if stream is None else _empty_on(stream, (size,), torch.uint8, dev, False)
+            _fail("linear_fp8: out must be [T, N] of out_dtype")
+        os, out_dtype = _rows("linear_fp8", "out", out, N, _bf16, _fp32), out.dtype
+    args = _linear_args(T, K, N, 1 if out_dtype is _fp32 else 0, x.data_ptr(), s_at, xs, ss, w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), os,
+                        0 if status is None else status.data_ptr())
+    L, size, at = _fw._lib or _fw.lib(), 0, None
+    if T > 16 and not codes:  # (otherwise none is needed)
+        need = _i64()
+        rc = L.fw_linear_fp8_workspace(args, _byref(need))
+        if rc:
+            _fw._check(rc, "fw_linear_fp8_workspace")
+        size = need.value
+        ws = _new(1, size, _uint8, x, None) if stream is None else _empty_on(stream, (size,), _uint8, x.device, False)
         at = ws.data_ptr()
-    rc = L.fw_linear_fp8(args, at, size, _stream_of(x, stream))
+    rc = L.fw_linear_fp8(args, at, size, _raw_stream(x.get_device()) if stream is None else stream)
     if rc:
         _fw._check(rc, "fw_linear_fp8")
     return out
+
+
+def _norm_refuses(y, residual, norm, post_norm):
+    """Says what is wrong with norm_residual's inputs."""
+    f = "norm_residual"
+    if y.dim() != 2:
+        _fail(f"{f}: y must be [T, H]")
+    T, H = y.shape
+    _rows(f, "y", y, H, _bf16)
+    if residual is not None:
+        _rows(f, "residual", residual, H, _bf16, _fp32)
+        if residual.shape[0] != T:
+            _fail(f"{f}: residual must be [T, H]")
+    _fail(f"{f}: norm and post_norm must be contiguous fp32 CUDA tensors [H]")
 
 
 def norm_residual(y, residual=None, norm=None, post_norm=None, gate=None, scale=1.0, eps=1e-6, fp8=False, residual_out=None, h=None, stream=None):
@@ -142,58 +195,67 @@ def norm_residual(y, residual=None, norm=None, post_norm=None, gate=None, scale=
     y bf16 [T, H]; residual bf16 or fp32 [T, H] or None; gate bf16 or fp32, [H], [T, 1] or [T, H], or None;
     norms fp32 [H] or None -> (r in residual's type, h bf16), or with fp8 (r, (codes, scales)) as
     linear_fp8 takes them. residual_out may be residual."""
-    f = "norm_residual"
-    if y.dim() != 2:
-        _fail(f"{f}: y must be [T, H]")
-    T, H = y.shape
-    ys = _rows(f, "y", y, H, _bf16)
-    kind, rs, r_at = _bf16, 0, None
+    f, shape = "norm_residual", y.shape
+    if len(shape) != 2 or y.dtype is not _bf16 or not y.is_cuda:
+        _norm_refuses(y, residual, norm, post_norm)
+    T, H = shape
+    ys, one = y.stride()
+    wide = rs = r_at = n_at = p_at = g_at = gs = g_fp32 = g_token = h_at = hs = c_at = s_at = ss = 0
+    kind = _bf16
     if residual is not None:
         kind = residual.dtype
-        rs, r_at = _rows(f, "residual", residual, H, _bf16, _fp32), residual.data_ptr()
-        if residual.shape[0] != T:
-            _fail(f"{f}: residual must be [T, H]")
-    for name, t in (("norm", norm), ("post_norm", post_norm)):
-        if t is not None and not (t.dtype is _fp32 and t.is_cuda and t.is_contiguous() and t.shape == (H,)):
-            _fail(f"{f}: {name} must be a contiguous fp32 CUDA tensor [H]")
-    g_at, gs, g_fp32, g_token = None, 0, 0, 0
+        rs, r_one = residual.stride() if residual.dim() == 2 else (0, 0)
+        if residual.shape != shape or kind is not _bf16 and kind is not _fp32 or r_one != 1 and T or not residual.is_cuda:
+            _norm_refuses(y, residual, norm, post_norm)
+        r_at, wide = residual.data_ptr(), 1 if kind is _fp32 else 0
+    if norm is not None:
+        if not (norm.dtype is _fp32 and norm.shape == (H,) and norm.is_contiguous() and norm.is_cuda):
+            _norm_refuses(y, residual, norm, post_norm)
+        n_at = norm.data_ptr()
+    if post_norm is not None:
+        if not (post_norm.dtype is _fp32 and post_norm.shape == (H,) and post_norm.is_contiguous() and post_norm.is_cuda):
+            _norm_refuses(y, residual, norm, post_norm)
+        p_at = post_norm.data_ptr()
+    if one != 1 and T:
+        _norm_refuses(y, residual, norm, post_norm)
+    if T < 2:
+        ys = rs = H
     if gate is not None:
-        if gate.dtype not in (_bf16, _fp32) or not gate.is_cuda or gate.shape not in ((H,), (T, 1), (T, H), (1, H)):
+        g = gate.shape
+        if gate.dtype is not _bf16 and gate.dtype is not _fp32 or not gate.is_cuda or g not in ((H,), (T, 1), shape, (1, H)):
             _fail(f"{f}: gate must be a bf16 or fp32 CUDA tensor [H], [T, 1] or [T, H]")
         g_at, g_fp32 = gate.data_ptr(), 1 if gate.dtype is _fp32 else 0
-        if gate.dim() == 2 and gate.shape[1] == 1 and H != 1:
+        if len(g) == 2 and g[1] == 1 and H != 1:
             g_token, gs = 1, gate.stride(0) if T > 1 else 0
         else:
             if gate.stride(-1) != 1:
                 _fail(f"{f}: gate's rows must be contiguous")
-            gs = gate.stride(0) if gate.dim() == 2 and gate.shape[0] > 1 else 0
-    _one_device(f, y, residual, norm, post_norm, gate, residual_out, h)
-    new = _empty if stream is None else functools.partial(_empty_on, stream)
-    dev = y.device
+            gs = gate.stride(0) if len(g) == 2 and g[0] > 1 else 0
+    if _attention._several is not False:
+        _attention._one_device(f, y, residual, norm, post_norm, gate, residual_out, h)
     if residual_out is None:
-        residual_out, ros = new((T, H), dtype=kind, device=dev), H
+        residual_out, ros = _new(T, H, kind, y, stream), H
     else:
         ros = _rows(f, "residual_out", residual_out, H, kind)
         if residual_out.shape[0] != T:
             _fail(f"{f}: residual_out must be [T, H]")
-    h_at, hs, c_at, s_at, ss = None, 0, None, None, 0
     if fp8:
         if h is not None:
             _fail(f"{f}: h is bf16, fp8 gives codes and scales")
-        scales, ss = _scales(new, H, T, dev)
-        h = new((T, H), dtype=_e4m3, device=dev), scales
-        c_at, s_at = h[0].data_ptr(), h[1].data_ptr()
-    else:
-        if h is None:
-            h, hs = new((T, H), dtype=_bf16, device=dev), H
-        else:
-            hs = _rows(f, "h", h, H, _bf16)
-            if h.shape[0] != T:
-                _fail(f"{f}: h must be [T, H]")
+        codes = _new(T, H, _e4m3, y, stream)
+        scales, ss = _scales(H, T, y, stream)
+        h, c_at, s_at = (codes, scales), codes.data_ptr(), scales.data_ptr()
+    elif h is None:
+        h, hs = _new(T, H, _bf16, y, stream), H
         h_at = h.data_ptr()
-    rc = _fw.lib().fw_norm_residual(_byref(FwNormResidualArgs(
-        T, H, 1 if kind is _fp32 else 0, g_fp32, g_token, eps, scale, y.data_ptr(), r_at, g_at, ys, rs, gs, None if post_norm is None else post_norm.data_ptr(),
-        None if norm is None else norm.data_ptr(), residual_out.data_ptr(), h_at, ros, hs, c_at, s_at, ss)), _stream_of(y, stream))
+    else:
+        hs = _rows(f, "h", h, H, _bf16)
+        if h.shape[0] != T:
+            _fail(f"{f}: h must be [T, H]")
+        h_at = h.data_ptr()
+    rc = (_fw._lib or _fw.lib()).fw_norm_residual(
+        _norm_args(T, H, wide, g_fp32, g_token, eps, scale, y.data_ptr(), r_at, g_at, ys, rs, gs, p_at, n_at, residual_out.data_ptr(), h_at, ros, hs, c_at, s_at,
+                   ss), _raw_stream(y.get_device()) if stream is None else stream)
     if rc:
         _fw._check(rc, "fw_norm_residual")
     return residual_out, h

@@ -111,6 +111,14 @@ def test_structs_match_the_header(tmp_path):
     assert [int(x) for x in got] == [v for c in by.values() for v in [getattr(c, n).offset for n, _ in c._fields_] + [ctypes.sizeof(c)]]
 
 
+def test_packed_arguments_are_the_structs():
+    """What the torch calls pack is what ctypes makes of the same values, field by field."""
+    from quantized_sparse_moe_router_gb300 import linear
+    for pack, kind in ((linear._linear_args, fw.FwLinearFp8Args), (linear._norm_args, fw.FwNormResidualArgs)):
+        values = list(range(3, 3 + len(kind._fields_)))
+        assert pack(*values) == bytes(kind(*values))
+
+
 @pytest.mark.parametrize("call", [lambda t: fw.quantize_fp8(t), lambda t: fw.quantize_fp8_weight(t), lambda t: fw.linear_fp8(t, t, t), lambda t: fw.norm_residual(t)])
 def test_torch_calls_refuse_host_tensors(call):
     with pytest.raises(ValueError):
