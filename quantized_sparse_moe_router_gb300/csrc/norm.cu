@@ -6,12 +6,13 @@
 //
 // One pass: a row's values stay in registers between the two sums over it, so
 // y and the residual are read once and r and h written once, which bounds many
-// rows by HBM. A single row is bound by latency: its loads are all issued
-// before anything waits for them.
+// rows by HBM (4096 x 7168: 6.3 TB/s). A single row is bound by latency: its loads are
+// all issued before anything waits for them. (Weights kept in shared memory with rows
+// copied ahead into a ring of it, by one CTA an SM, were slower: 46 us against 37.)
 //
 // h may leave as 8-bit codes with a scale per 128 values (the linear layers'
 // input): a thread holds eight neighbours, so a block is 16 neighbouring lanes.
-#include <algorithm>
+#include <atomic>
 
 #include "fp8.cuh"
 
@@ -56,121 +57,155 @@ __device__ __forceinline__ void floats8(const uint4 a, const uint4 b, float (&f)
 }
 
 // kVec: vectors of eight values a thread holds. kWarp: a warp a row, otherwise a
-// CTA a row. kWide: residuals are fp32.
-template <int kVec, bool kWarp, bool kWide>
-__global__ void __launch_bounds__(kWarp ? 256 : kMaxThreads) norm_residual_kernel(const __grid_constant__ fw_norm_residual_args u) {
-  __shared__ float s_sum[2][32];
+// CTA a row. kWide: residuals are fp32. kLoop: the CTA takes every gridDim.x-th row,
+// and loads the next one once it has summed the row's parts.
+template <int kVec, bool kWarp, bool kWide, bool kLoop>
+__global__ void __launch_bounds__(kWarp ? 256 : kVec <= 2 ? 512 : kMaxThreads, kWarp || kVec > 2 ? 1 : 2)
+    norm_residual_kernel(const __grid_constant__ fw_norm_residual_args u) {
+  __shared__ float s_sum[2][2][32];  // [odd turn][which sum]
   const int width = kWarp ? 32 : blockDim.x, l = kWarp ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t row = kWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  const bool in = row < u.T;  // (kWarp: a warp past the last row goes along without loads or stores)
-  pdl_wait();
-  pdl_launch_dependents();
-  const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(u.y) + row * u.y_stride;
+  int64_t row = kWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   uint4 yv[kVec], rv[kVec], rw[kWide ? kVec : 1];
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int at = 8 * (i * width + l);
-    const bool has = in && at < u.H;
-    yv[i] = has ? *reinterpret_cast<const uint4*>(y + at) : make_uint4(0u, 0u, 0u, 0u);
-    rv[i] = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (kWide) {
-      rw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (has && u.residual) {
-        const uint4* r = reinterpret_cast<const uint4*>(static_cast<const float*>(u.residual) + row * u.residual_stride + at);
-        rv[i] = r[0];
-        rw[i] = r[1];
-      }
-    } else if (has && u.residual) {
-      rv[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.residual) + row * u.residual_stride + at);
-    }
-  }
-  float by = u.scale;
-  if (u.gate && u.gate_per_token && in)
-    by *= u.gate_fp32 ? __ldg(static_cast<const float*>(u.gate) + row * u.gate_stride)
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(u.gate)[row * u.gate_stride]);
-  if (u.post_norm) {
-    float sum = 0.f;
+  auto load = [&](bool in) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      float f[8];
-      unpack8(yv[i], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
-    }
-    by *= rsqrtf(row_sum<kWarp>(sum, s_sum[0]) / (float)u.H + u.eps);
-  }
-  float r[kVec][8], sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int at = 8 * (i * width + l);
-    if (!in || at >= u.H) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
-      continue;
-    }
-    float f[8], w[8];
-    unpack8(yv[i], f);
-    if constexpr (kWide)
-      floats8(rv[i], rw[i], r[i]);
-    else
-      unpack8(rv[i], r[i]);
-    if (u.post_norm) {
-      weight8(u.post_norm, at, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= w[j];
-    }
-    if (u.gate && !u.gate_per_token) {
-      if (u.gate_fp32)
-        weight8(static_cast<const float*>(u.gate) + row * u.gate_stride, at, w);
-      else
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.gate) + row * u.gate_stride + at), w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= w[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      r[i][j] = fmaf(f[j], by, r[i][j]);
-      sum = fmaf(r[i][j], r[i][j], sum);
-    }
-    if (u.residual_out) {
+      const int at = 8 * (i * width + l);
+      const bool has = in && at < u.H;
+      yv[i] = has ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.y) + row * u.y_stride + at) : make_uint4(0u, 0u, 0u, 0u);
+      rv[i] = make_uint4(0u, 0u, 0u, 0u);
       if constexpr (kWide) {
-        float4* to = reinterpret_cast<float4*>(static_cast<float*>(u.residual_out) + row * u.residual_out_stride + at);
-        to[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
-        to[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
-      } else {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(u.residual_out) + row * u.residual_out_stride + at) = pack8(r[i]);
+        rw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (has && u.residual) {
+          const uint4* r = reinterpret_cast<const uint4*>(static_cast<const float*>(u.residual) + row * u.residual_stride + at);
+          rv[i] = r[0];
+          rw[i] = r[1];
+        }
+      } else if (has && u.residual) {
+        rv[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.residual) + row * u.residual_stride + at);
       }
     }
-  }
-  if (!u.h && !u.h_codes) return;
-  const float inv = u.norm ? rsqrtf(row_sum<kWarp>(sum, s_sum[1]) / (float)u.H + u.eps) : 1.f;
+  };
+  pdl_wait();
+  pdl_launch_dependents();
+  bool in = row < u.T;  // (kWarp: a warp past the last row goes along without loads or stores)
+  load(in);
+  for (int turn = 0;; turn ^= 1) {
+    const int64_t now = row;
+    float by = u.scale;
+    if (u.gate && u.gate_per_token && in)
+      by *= u.gate_fp32 ? __ldg(static_cast<const float*>(u.gate) + now * u.gate_stride)
+                        : __bfloat162float(static_cast<const __nv_bfloat16*>(u.gate)[now * u.gate_stride]);
+    if (u.post_norm) {
+      float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int at = 8 * (i * width + l);
-    const bool has = in && at < u.H;
-    if (u.norm && has) {
-      float w[8];
-      weight8(u.norm, at, w);
+      for (int i = 0; i < kVec; ++i) {
+        float f[8];
+        unpack8(yv[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[i][j] *= inv * w[j];
+        for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+      }
+      by *= rsqrtf(row_sum<kWarp>(sum, s_sum[turn][0]) / (float)u.H + u.eps);
     }
-    const uint4 out = pack8(r[i]);
-    if (u.h && has) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(u.h) + row * u.h_stride + at) = out;
-    if (u.h_codes) {  // (every lane takes part: past the row's end with zeros)
-      float scale;
-      const uint2 c = fp8_block_of_lanes(out, &scale);
-      if (has) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(u.h_codes) + row * u.H + at) = c;
-        if ((l & 15) == 0) u.h_scale[(at / kFp8Block) * u.h_scale_stride + row] = scale;
+    float r[kVec][8], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int at = 8 * (i * width + l);
+      if (!in || at >= u.H) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
+        continue;
+      }
+      float f[8], w[8];
+      unpack8(yv[i], f);
+      if constexpr (kWide)
+        floats8(rv[i], rw[i], r[i]);
+      else
+        unpack8(rv[i], r[i]);
+      if (u.post_norm) {
+        weight8(u.post_norm, at, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= w[j];
+      }
+      if (u.gate && !u.gate_per_token) {
+        if (u.gate_fp32)
+          weight8(static_cast<const float*>(u.gate) + now * u.gate_stride, at, w);
+        else
+          unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.gate) + now * u.gate_stride + at), w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= w[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        r[i][j] = fmaf(f[j], by, r[i][j]);
+        sum = fmaf(r[i][j], r[i][j], sum);
       }
     }
+    const bool stores = in;
+    bool more = false;
+    if constexpr (kLoop) {
+      row += gridDim.x;
+      more = in = row < u.T;
+      if (more) load(true);
+    }
+    if (u.residual_out && stores) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int at = 8 * (i * width + l);
+        if (at >= u.H) continue;
+        if constexpr (kWide) {
+          float4* to = reinterpret_cast<float4*>(static_cast<float*>(u.residual_out) + now * u.residual_out_stride + at);
+          to[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
+          to[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(u.residual_out) + now * u.residual_out_stride + at) = pack8(r[i]);
+        }
+      }
+    }
+    if (u.h || u.h_codes) {
+      const float inv = u.norm ? rsqrtf(row_sum<kWarp>(sum, s_sum[turn][1]) / (float)u.H + u.eps) : 1.f;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int at = 8 * (i * width + l);
+        const bool has = stores && at < u.H;
+        if (u.norm && has) {
+          float w[8];
+          weight8(u.norm, at, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[i][j] *= inv * w[j];
+        }
+        const uint4 out = pack8(r[i]);
+        if (u.h && has) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(u.h) + now * u.h_stride + at) = out;
+        if (u.h_codes) {  // (every lane takes part: past the row's end with zeros)
+          float scale;
+          const uint2 c = fp8_block_of_lanes(out, &scale);
+          if (has) {
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(u.h_codes) + now * u.H + at) = c;
+            if ((l & 15) == 0) u.h_scale[(at / kFp8Block) * u.h_scale_stride + now] = scale;
+          }
+        }
+      }
+    }
+    if (!more) return;
   }
 }
 
-template <int kVec, bool kWarp>
+template <int kVec, bool kWarp, bool kLoop>
 cudaError_t launch(const fw_norm_residual_args& u, unsigned grid, int threads, cudaStream_t s) {
-  return u.residual_fp32 ? launch_dependent(norm_residual_kernel<kVec, kWarp, true>, dim3(grid), dim3(threads), 0, s, u)
-                         : launch_dependent(norm_residual_kernel<kVec, kWarp, false>, dim3(grid), dim3(threads), 0, s, u);
+  return u.residual_fp32 ? launch_dependent(norm_residual_kernel<kVec, kWarp, true, kLoop>, dim3(grid), dim3(threads), 0, s, u)
+                         : launch_dependent(norm_residual_kernel<kVec, kWarp, false, kLoop>, dim3(grid), dim3(threads), 0, s, u);
+}
+
+cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];  // of each device
+  int dev = 0, n = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if ((n = known[dev].load()) == 0) {
+    if (cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev); e != cudaSuccess) return e;
+    known[dev].store(n);
+  }
+  *sms = n;
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -203,18 +238,30 @@ extern "C" fw_status fw_norm_residual(const fw_norm_residual_args* u, void* stre
   if (!al(u->gate, u->gate_fp32 ? 4 : 2)) return set_error(FW_EINVAL, "fw_norm_residual: gate needs the alignment of its elements");
   if (fw_status st = check_device("fw_norm_residual: needs an sm_103 device"); st != FW_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int vecs = u->H / 8;
+  const int vecs = u->H / 8, T = u->T;
   cudaError_t e;
-  if (vecs <= 128 && u->T > 1) {
-    const int warps = 8;
-    const unsigned grid = (unsigned)(((int64_t)u->T + warps - 1) / warps);
-    const int per = (vecs + 31) / 32;
-    e = per == 1 ? launch<1, true>(*u, grid, 32 * warps, s) : per == 2 ? launch<2, true>(*u, grid, 32 * warps, s) : launch<4, true>(*u, grid, 32 * warps, s);
+  if (vecs <= 128 && T > 1) {
+    const int warps = 8, per = (vecs + 31) / 32;
+    const unsigned grid = (unsigned)(((int64_t)T + warps - 1) / warps);
+    e = per == 1   ? launch<1, true, false>(*u, grid, 32 * warps, s)
+        : per == 2 ? launch<2, true, false>(*u, grid, 32 * warps, s)
+                   : launch<4, true, false>(*u, grid, 32 * warps, s);
   } else {
-    const int per = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+    // One vector a thread up to 2048 columns, then two (at 4096, 4096 rows: 20 us against
+    // 23), four past 8192. Rows that outnumber the SMs, and are long enough to wait for, are
+    // looped over, two CTAs an SM and, with many, two turns of them (4096 x 7168: 42 -> 37
+    // us, with norms on both sides and a gate 58 -> 48; 600 x 7168: 10 -> 8; 4096 x 2048: no
+    // gain, 12.6).
+    const int per = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : 4;
     const int threads = ((vecs + per - 1) / per + 31) / 32 * 32;
-    const unsigned grid = (unsigned)u->T;
-    e = per == 1 ? launch<1, false>(*u, grid, threads, s) : per == 2 ? launch<2, false>(*u, grid, threads, s) : launch<4, false>(*u, grid, threads, s);
+    int sms = 0;
+    if (cudaError_t err = sm_count(&sms); err != cudaSuccess) return set_cuda_error(err, "fw_norm_residual: the device's SM count");
+    if (per == 2 && T > 2 * sms)
+      e = launch<2, false, true>(*u, (unsigned)(T >= 8 * sms ? 4 * sms : 2 * sms), threads, s);
+    else
+      e = per == 1   ? launch<1, false, false>(*u, (unsigned)T, threads, s)
+          : per == 2 ? launch<2, false, false>(*u, (unsigned)T, threads, s)
+                     : launch<4, false, false>(*u, (unsigned)T, threads, s);
   }
   if (e != cudaSuccess) return set_cuda_error(e, "fw_norm_residual: launch");
   return FW_OK;

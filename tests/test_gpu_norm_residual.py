@@ -59,6 +59,33 @@ def test_gates(gate, residual, H):
     check(a, *fw.norm_residual(scale=-2.0, eps=1e-3, **a), scale=-2.0, eps=1e-3)
 
 
+@pytest.mark.parametrize("T, H", [(1000, 1032), (700, 2048), (4097, 2560), (600, 5128), (999, 7168), (400, 8192), (310, 16384), (305, 32768)])
+@pytest.mark.parametrize("residual, gate, post, norm, fp8", [(torch.bfloat16, "none", False, True, False), (torch.float32, "full32", True, True, False),
+                                                             (None, "channel16", True, True, False), (torch.float32, "token", False, False, False),
+                                                             (torch.bfloat16, "channel", False, True, True), (torch.bfloat16, "full", True, True, True)])
+def test_many_rows(T, H, residual, gate, post, norm, fp8):
+    """Rows enough for the kernel that keeps weights and a ring of rows in shared memory, in place too; the same as row by row in small calls."""
+    fp8 = fp8 and H % 16 == 0
+    a = inputs(T, H, residual, gate, post, norm, T + H)
+    r, h = fw.norm_residual(scale=0.5, **a)
+    some = [0, 1, 151, 152, 303, T - 2, T - 1]
+    check({k: v[some] if v is not None and v.dim() == 2 and v.shape[0] == T else v for k, v in a.items()}, r[some], h[some], 0.5)
+    part = {k: v[200:300] if v is not None and v.dim() == 2 and v.shape[0] == T else v for k, v in a.items()}
+    r2, h2 = fw.norm_residual(scale=0.5, **part)
+    u = ref.FP32 if residual is torch.float32 else ref.BF16
+    near = lambda x, y, u: ((x.double() - y.double()).abs() <= 2.01 * u * y.double().abs() + 1e-4 * u * y.double().abs().amax(1, keepdim=True)).all()  # noqa: E731
+    assert near(h[200:300], h2, ref.BF16) and (residual is torch.float32 or near(r[200:300], r2, u))
+    if fp8:
+        _, (codes, scales) = fw.norm_residual(scale=0.5, fp8=True, **a)
+        want_c, want_s = fw.quantize_fp8(h)
+        assert torch.equal(codes.view(torch.uint8), want_c.view(torch.uint8)) and torch.equal(scales, want_s)
+    if residual is not None:
+        into, out = a["residual"].clone(), a["y"].clone()
+        b = dict(a, residual=into, y=out)
+        fw.norm_residual(scale=0.5, residual_out=into, h=out, **b)
+        assert torch.equal(into, r) and torch.equal(out, h)
+
+
 @pytest.mark.parametrize("T, H", [(1, 16), (1, 2048), (4, 1040), (200, 144), (65, 7168), (3, 32768)])
 def test_codes_are_those_of_the_bf16_result(T, H):
     a = inputs(T, H, torch.bfloat16, "channel", True, True)
