@@ -64,7 +64,7 @@ def test_gates(gate, residual, H):
                                                              (None, "channel16", True, True, False), (torch.float32, "token", False, False, False),
                                                              (torch.bfloat16, "channel", False, True, True), (torch.bfloat16, "full", True, True, True)])
 def test_many_rows(T, H, residual, gate, post, norm, fp8):
-    """Rows enough for the kernel that keeps weights and a ring of rows in shared memory, in place too; the same as row by row in small calls."""
+    """Rows enough that a CTA loops over several, in place too; the same as row by row in small calls."""
     fp8 = fp8 and H % 16 == 0
     a = inputs(T, H, residual, gate, post, norm, T + H)
     r, h = fw.norm_residual(scale=0.5, **a)
