@@ -152,6 +152,7 @@ fw_status fw_moe_init(const fw_moe_config* cfg, const fw_moe_weights* w, void* s
     return cuda_fail(e, "fw_moe_init: decode kernel set-up");
   }
   e = configure_prefill_kernels();
+  if (e == cudaSuccess) e = configure_route_rule_kernels();
   if (e != cudaSuccess) return cuda_fail(e, "fw_moe_init: prefill kernel set-up");
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -108,10 +108,12 @@ struct LinearArgs {
 cudaError_t configure_fp8_quantize();
 cudaError_t launch_fp8_quantize(const void* x, int64_t x_stride, int T, int K, void* codes, float* scales, int64_t scale_stride, cudaStream_t s);
 
+cudaError_t configure_tensor_maps();  // before the first of the encode_* below
+
 // A tensor map of codes: rows of K bytes, `stride` apart, in boxes of 128 bytes by `box` rows, 128-byte swizzle.
 cudaError_t encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, int64_t stride, int box);
 
-// The same of results: rows of `cols` bf16 or fp32 values, in boxes of 128 bytes by `box` rows, 128-byte swizzle.
+// The same of results (or of bf16 operands): rows of `cols` bf16 or fp32 values, in boxes of 128 bytes by `box` rows, 128-byte swizzle.
 cudaError_t encode_rows(CUtensorMap* map, const void* out, bool fp32, int64_t rows, int64_t cols, int64_t row_bytes, int box);
 
 // The same of bf16 values: rows of K, `stride` elements apart, in boxes of 128 by `box` rows, no swizzle.
@@ -119,6 +121,9 @@ cudaError_t encode_values(CUtensorMap* map, const __nv_bfloat16* x, int64_t T, i
 
 // The same of tokens' scales: KB rows of T, in boxes of `box` by one row, no swizzle.
 cudaError_t encode_scales(CUtensorMap* map, const float* scales, int64_t T, int KB, int64_t stride, int box);
+
+// The same of n fp32 matrices [T][cols], one behind the other, in boxes of 32 columns by `box` rows, 128-byte swizzle.
+cudaError_t encode_parts(CUtensorMap* map, float* parts, int n, int64_t T, int64_t cols, int box);
 
 cudaError_t configure_linear_few();
 bool linear_few_quantises(int T);  // whether the kernel for few tokens takes bf16 itself

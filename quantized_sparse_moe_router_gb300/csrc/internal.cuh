@@ -222,6 +222,9 @@ bool route_prefill_mma_available(const Handle* h);
 cudaError_t launch_route_prefill_mma(Handle* h, const __nv_bfloat16* x, int T, int32_t* ids_out, float* gates_out,
                                      cudaStream_t s);
 cudaError_t launch_split_router(Handle* h, cudaStream_t s);
+// Under a rule, many tokens, the router's planes present: partial logits into h->zpart, *parts of them.
+cudaError_t configure_route_rule_kernels();
+cudaError_t launch_route_rule_logits(Handle* h, const __nv_bfloat16* x, int T, int* parts, cudaStream_t s);
 // Under a rule: the choice from `parts` partial logits in h->zpart (their sum plus zbias, if not null).
 cudaError_t launch_route_rule_select(Handle* h, int T, int parts, const float* zbias, int32_t* ids_out, float* gates_out, cudaStream_t s);
 cudaError_t launch_get_permutation(const Handle* h, int T, int32_t* offsets, int32_t* perm, int32_t* inv,

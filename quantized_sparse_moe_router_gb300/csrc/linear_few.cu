@@ -20,11 +20,11 @@
 // bf16 tokens it copies those, and four more warps quantise them within the stage (a
 // launch and a trip through memory less; loaded by these warps, two blocks ahead, their
 // latency bounded them).
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 
 #include "fp8.cuh"
+#include "pair.cuh"
 #include "tcgen05.cuh"
 
 namespace fw {
@@ -79,10 +79,6 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Four floats at this CTA's shared address `addr`, in the CTA of rank `rank` of the cluster.
@@ -333,8 +329,6 @@ __global__ void __launch_bounds__(few_threads<kTok, kQuant>(), Few<kTok, kQuant>
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-
 template <int kTok, bool kQuant>
 cudaError_t configure() {
   cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<kTok, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<kTok, kQuant>::SmemBytes);
@@ -386,52 +380,12 @@ cudaError_t launch(const LinearArgs& a, const void* w, const void* x_codes, int6
 
 }  // namespace
 
-cudaError_t encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, int64_t stride, int box) {
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
-  const cuuint32_t boxes[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)box}, steps[2] = {1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-cudaError_t encode_rows(CUtensorMap* map, const void* out, bool fp32, int64_t rows, int64_t cols, int64_t row_bytes, int box) {
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
-  const cuuint32_t boxes[2] = {fp32 ? 32u : 64u, (cuuint32_t)box}, steps[2] = {1, 1};
-  const CUresult r = g_encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(out), dims, strides, boxes,
-                              steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-cudaError_t encode_values(CUtensorMap* map, const __nv_bfloat16* x, int64_t T, int64_t K, int64_t stride, int box) {
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)T}, strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t boxes[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)box}, steps[2] = {1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(x), dims, strides, boxes, steps,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-cudaError_t encode_scales(CUtensorMap* map, const float* scales, int64_t T, int KB, int64_t stride, int box) {
-  const cuuint64_t dims[2] = {(cuuint64_t)T, (cuuint64_t)KB}, strides[1] = {(cuuint64_t)stride * 4};
-  const cuuint32_t boxes[2] = {(cuuint32_t)box, 1}, steps[2] = {1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(scales), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // (17 to 32 tokens: 12.4 us at 4096 x 4096 against 10.3 with a launch for them)
 bool linear_few_quantises(int T) { return T <= 16; }
 
 cudaError_t configure_linear_few() {
-  if (!g_encode) {
-    cudaDriverEntryPointQueryResult q;
-    void* fn = nullptr;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-    if (e != cudaSuccess) return e;
-    if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  cudaError_t e = configure<16, true>();
+  cudaError_t e = configure_tensor_maps();
+  if (e == cudaSuccess) e = configure<16, true>();
   if (e == cudaSuccess) e = configure<16, false>();
   if (e == cudaSuccess) e = configure<32, false>();
   if (e == cudaSuccess) e = configure<64, false>();

@@ -17,16 +17,13 @@
 //
 // Warps: 0, 2 and 3 copy, 1 issues the products (the first CTA's for both), 4-11
 // scale and add (tensor-memory quarter = warp % 4). Tiles are taken in turn by CTA pairs
-// that stay; where what is left for the last turn is at most half of what the
-// pairs could do, its tiles are cut into halves of 128 outputs (a half takes two
-// thirds of a tile's time). Results leave through shared memory by TMA while the
+// that stay, all 256 or all 128 outputs wide (see turns). Results leave through shared memory by TMA while the
 // next tile runs.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <type_traits>
 
 #include "fp8.cuh"
+#include "pair.cuh"
 #include "tcgen05.cuh"
 
 namespace fw {
@@ -80,33 +77,9 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_lo, uint32_
       "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kSw128DescHi)
       : "memory");
 }
-// Arrives at the barrier in both CTAs once the products issued so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "h"((uint16_t)3)
-               : "memory");
-}
-// The first CTA's copy of a shared address.
-__device__ __forceinline__ uint32_t in_first(const void* p) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
-  return r;
-}
-__device__ __forceinline__ void tma_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_out(const CUtensorMap* map, const void* src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1),
-               "r"(smem_u32(src))
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
 // (No release at cluster scope: what the arrival follows are loads from tensor
 // memory, complete by then; a fence for the rest of memory took 2000 cycles a block.)
 __device__ __forceinline__ void arrive_at(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory"); }
-__device__ __forceinline__ void cluster_sync() { asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory"); }
 
 // Columns of this thread's tensor-memory lane: on their way, and there.
 __device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&r)[16]) {

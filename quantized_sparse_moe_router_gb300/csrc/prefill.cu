@@ -934,15 +934,13 @@ cudaError_t launch_route_prefill_mma(Handle* h, const __nv_bfloat16* x, int T, i
   // pass, then a select kernel); the splits are summed in a fixed order
   int ks = std::min(std::min(h->num_sms / tiles, kRouterMaxSplit), H / kRK);
   if (ks < 2) ks = 1;
-  const bool by_rule = h->rule.score != kScoreChosen;  // the choice is then always a kernel of its own
-  a.zpart = ks > 1 || by_rule ? h->zpart : nullptr;
+  a.zpart = ks > 1 ? h->zpart : nullptr;
   const dim3 grid((unsigned)tiles, (unsigned)ks);
   if (a.k <= 8)
     route_mma_kernel<8><<<grid, kRThreads, smem, s>>>(map_x, h->maps->w3, a);
   else
     route_mma_kernel<16><<<grid, kRThreads, smem, s>>>(map_x, h->maps->w3, a);
   cudaError_t err = cudaGetLastError();
-  if (err == cudaSuccess && by_rule) return launch_route_rule_select(h, T, ks, h->bias, ids_out, gates_out, s);
   if (err == cudaSuccess && ks > 1)
     err = launch_dependent(route_select_kernel, dim3((unsigned)((T + kSelTokens - 1) / kSelTokens)),
                            dim3(kSelTokens * 32), 0, s, a, ks);

@@ -607,7 +607,13 @@ cudaError_t launch_route_prefill(Handle* h, const __nv_bfloat16* x, int T, int32
   cudaError_t err;
   if (route_prefill_mma_available(h)) {
     KernelTimer tm(h, FW_KERNEL_ROUTE_TILES, s);
-    err = launch_route_prefill_mma(h, x, T, ids_out, gates_out, s);
+    if (a.zpart) {
+      int parts = 0;
+      err = launch_route_rule_logits(h, x, T, &parts, s);
+      if (err == cudaSuccess) err = launch_route_rule_select(h, T, parts, h->bias, ids_out, gates_out, s);
+    } else {
+      err = launch_route_prefill_mma(h, x, T, ids_out, gates_out, s);
+    }
   } else {
   KernelTimer tm(h, FW_KERNEL_ROUTE_TILES, s);
   switch (EM) {

@@ -81,6 +81,21 @@ def test_choice_of_many_tokens():
     layer.close()
 
 
+@pytest.mark.parametrize("E, k, n_group", [(16, 4, 2), (48, 6, 4), (144, 8, 9), (208, 8, 8), (240, 4, 16)])
+def test_choice_of_ragged_tiles(E, k, n_group):
+    """Experts that fill a pair's tile to a half, tokens around a pair's 256."""
+    rule = dict(score="softmax", n_group=n_group, top_group=2, renorm=False, bias=bias_of(E, size=0.001))
+    w = synth.WORKLOADS["tiny"].with_(E=E, k=k, T=520, sigma_router=0.1)
+    dl = DeviceLayer(w, 0, DEV)
+    x = rule_ref.hidden(w, 0, dl.Wr, dl.bias, rule, w.T)
+    z = oracle.router_logits(x, dl.Wr, dl.bias)
+    layer = dl.make(T_max=w.T)
+    set_rule(layer, rule)
+    for T in (129, 255, 256, 257, 520):
+        route_and_check(w, layer, x[:T], z[:T], rule)
+    layer.close()
+
+
 @pytest.mark.parametrize("T", [1, 7, 50])
 @pytest.mark.parametrize("E, k, n_group, top_group", [(64, 8, 8, 2), (48, 12, 16, 4), (32, 4, 32, 4), (256, 16, 32, 3)])
 def test_ties_go_to_the_lowest(T, E, k, n_group, top_group):
