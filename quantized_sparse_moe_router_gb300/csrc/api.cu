@@ -208,7 +208,7 @@ fw_status fw_moe_init(const fw_moe_config* cfg, const fw_moe_weights* w, void* s
       {(void**)&h->hbuf, hbuf_bytes},
       {(void**)&h->yp, (size_t)(pre ? h->rows_max * H * 2 : 256)},
       {(void**)&h->partial, (size_t)(h->num_sms * T_dec * H * 4)},
-      {(void**)&h->zpart, (size_t)(pre ? kRouterMaxSplit * Tm * E * 4 : 256)},
+      {(void**)&h->zpart, (size_t)(pre ? std::max<int64_t>(kRouterMaxSplit * Tm, kRuleMaxSplit * std::min<int64_t>(Tm, kRuleSplitT)) * E * 4 : 256)},
       {(void**)&h->meta, sizeof(Meta)},
       {(void**)&h->x_dev, (size_t)(Tm * H * 2)},
       {(void**)&h->out_dev, (size_t)(Tm * H * 2)},

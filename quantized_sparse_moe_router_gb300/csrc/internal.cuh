@@ -27,6 +27,8 @@ constexpr int kTokTile = 192;      // prefill GEMM token tile (rows of one exper
 constexpr int kMidTile = 96;       // an expert's last tile of at most this many rows goes to the mid-tile GEMM
 constexpr int kSmallTile = 64;     // ... of at most this many, to the small-tile GEMM
 constexpr int kRouterMaxSplit = 8; // prefill router: K splits at most (partial logits [splits][T_max][E])
+constexpr int kRuleMaxSplit = 16;  // the same under a routing rule, up to kRuleSplitT tokens
+constexpr int kRuleSplitT = 1024;
 
 // Status bits written by kernels into the handle's device status word.
 constexpr int kStatusTimeout = 1;
@@ -148,7 +150,7 @@ struct Handle {
   __nv_bfloat16* xperm; // [rows_max][H] x gathered into grouped order (prefill)
   void* hbuf;         // [rows_max][I] fp32 (decode) or bf16 (prefill)
   __nv_bfloat16* yp;  // [rows_max][H] bf16 (prefill)
-  float* zpart;       // [kRouterMaxSplit][T_max][E] prefill router: partial logits of a K split
+  float* zpart;       // [splits][T][E] prefill router: partial logits of a K split (kRouterMaxSplit, kRuleMaxSplit)
   float* partial;     // [num_sms][min(T_max, 16)][H] decode: per-CTA partial outputs
   Meta* meta;
   int test_grid_timeouts;  // test hook (FWMOE_TEST_GRID_TIMEOUTS at init): decode calls whose grid wait must time out

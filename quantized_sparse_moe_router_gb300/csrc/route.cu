@@ -182,8 +182,13 @@ __global__ void __launch_bounds__(kNT, kNT == 128 ? 16 : 1) route_decode_kernel(
     __shared__ __align__(16) float zbuf[kMaxDecodeT * kMaxE];
     if (a.rule.score == kScoreChosen)
       route_in_smem<kNT>(a.logits, T, a.E, a.k, a.S, r, zbuf);
-    else
+    else if (T > 1)
       route_in_smem_by_rule<kNT>(a.logits, T, a.E, a.k, a.S, a.rule, r);
+    else {
+      route_one_in_smem_by_rule<kNT>(a.logits, a.E, a.k, a.S, a.rule, r);
+      route_one_tables<kNT>(a.E, a.k, a.S, r);
+      __syncthreads();
+    }
     RoutingOut o{a.ids_out, a.gates_out, a.ids,      a.gates,    a.counts, a.offsets,
                  a.perm,    a.inv,       a.row_token, a.row_gate, a.uinfo,  a.meta};
     publish_routing<kNT>(r, T, a.E, a.k, a.S, o);

@@ -216,11 +216,13 @@ cudaError_t configure_route_rule_kernels() {
 
 cudaError_t launch_route_rule_logits(Handle* h, const __nv_bfloat16* x, int T, int* parts, cudaStream_t s) {
   const int H = h->cfg.H, E = h->cfg.E, steps = H / kPairK, pairs = h->num_sms / 2, tiles = (T + 2 * kPairTok - 1) / (2 * kPairTok);
-  // H is split for the fewest steps that a pair takes, at 8 for a split's own costs
+  // H is split for the least time, in fifths of a step (0.8 us): a pair's steps, 8 more for
+  // starting and ending, and three fifths for a part that the choice then reads (16 tokens
+  // of 7168: in 8 parts 27.4 us, in 16 24.5; of 4096: 22.5 and 23.0)
   int n = 1;
   int64_t least = INT64_MAX;
-  for (int c = 1; c <= std::min(kRouterMaxSplit, steps); ++c) {
-    const int64_t cost = (((int64_t)tiles * c + pairs - 1) / pairs) * ((steps + c - 1) / c + 8);
+  for (int c = 1; c <= std::min(T <= kRuleSplitT ? kRuleMaxSplit : kRouterMaxSplit, steps); ++c) {
+    const int64_t cost = (((int64_t)tiles * c + pairs - 1) / pairs) * ((steps + c - 1) / c + 8) * 5 + 3 * c;
     if (cost < least) least = cost, n = c;
   }
   PairArgs a;
