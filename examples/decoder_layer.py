@@ -15,6 +15,13 @@ graph, and drafted tokens -- each through
 
 and at the end a second, empty cache that gets every request whole: both ways
 agree up to the roundings of bf16.
+
+Then the same with a layer of another make (EightBitLayer): its products in 8
+bits, a norm before and after each block, experts by sigmoid scores in groups:
+
+    norm_residual   (codes) -> linear_fp8 W_qkv -> qk_norm_rope -> attn_q4
+    linear_fp8 W_o  (quantises attention's rows itself) -> norm_residual
+    MoELayer        with a routing rule -> norm_residual
 """
 import os
 import sys
@@ -48,8 +55,9 @@ class DecoderLayer:
         self.norm1, self.norm2 = (1 + rand(H, sd=0.1)).bfloat16(), (1 + rand(H, sd=0.1)).bfloat16()
         self.cos_sin = rope_table(n_pos, D)
         q8 = lambda r, c: torch.stack([fw.quantize_q8_0(rand(r, c, sd=c ** -0.5)) for _ in range(E)])  # noqa: E731
+        self.router = rand(E, H, sd=H ** -0.5)
         self.moe = fw.MoELayer(H, I, E, k, T_max=T_max,
-                               weights=dict(router_w=rand(E, H, sd=H ** -0.5), w_gate=q8(I, H), w_up=q8(I, H), w_down=q8(H, I)))
+                               weights=dict(router_w=self.router, w_gate=q8(I, H), w_up=q8(I, H), w_down=q8(H, I)))
 
     def project(self, x):
         """-> q, k, v [T, heads, D]: views of one product, used as they are."""
@@ -70,6 +78,32 @@ class DecoderLayer:
         x = x + o.view(x.shape[0], -1) @ self.w_o
         h = torch.nn.functional.rms_norm(x, (x.shape[1],), self.norm2, 1e-6)
         return x + self.moe.forward(h)[1]
+
+
+class EightBitLayer(DecoderLayer):
+    """The same with linear layers in 8 bits, norms before and after each block, and experts chosen by sigmoid scores and a bias in groups."""
+
+    def __init__(self, H=512, n_q=8, n_kv=2, D=64, I=256, E=16, k=4, n_pos=4096, T_max=2048, window=0, sinks=0, seed=0):
+        super().__init__(H, n_q, n_kv, D, I, E, k, n_pos, T_max, window, sinks, seed)
+        g = torch.Generator(device="cuda").manual_seed(seed + 1)
+        norm = lambda: 1 + 0.1 * torch.randn(H, generator=g, device="cuda")  # noqa: E731
+        self.qkv8, self.o8 = fw.quantize_fp8_weight(self.w_qkv.t().contiguous()), fw.quantize_fp8_weight(self.w_o.t().contiguous())
+        self.norm1, self.norm2, self.post1, self.post2 = norm(), norm(), norm(), norm()
+        self.rule = dict(score="sigmoid", n_group=4, top_group=2, scale=2.5, bias=0.05 * torch.randn(E, generator=g, device="cuda"))
+        self.moe.set_routing(**self.rule)
+
+    def project(self, x):
+        codes, scales = fw.norm_residual(x, norm=self.norm1, fp8=True)[1]
+        y = fw.linear_fp8(codes, *self.qkv8, x_scale=scales).view(x.shape[0], -1, self.D)
+        return y.split((self.n_q, self.n_kv, self.n_kv), 1)
+
+    def join(self, x, o):
+        """x and attention's rows -> the residual stream behind them and the experts' input."""
+        return fw.norm_residual(fw.linear_fp8(o.view(x.shape[0], -1), *self.o8), x, norm=self.norm2, post_norm=self.post1)
+
+    def forward(self, x, plan, cache, block_table, max_q, status=None):
+        r, h = self.join(x, self.attend(x, plan, cache, block_table, max_q, status))
+        return fw.norm_residual(self.moe.forward(h)[1], r, post_norm=self.post2)[0]
 
 
 class Requests:
@@ -142,15 +176,16 @@ def run(layer, H=512, prompts=(37, 200, 5, 130), singles=6, drafts=(3, 1, 4, 2),
 
 def main():
     fw.build()
-    layer = DecoderLayer()
-    pieces, whole, cached = run(layer)
-    for r, (a, b) in enumerate(zip(pieces, whole)):
-        diff = (a.float() - b.float()).abs()
-        print(f"request {r}: {a.shape[0]} tokens, piece by piece against whole: mean {diff.mean():.2e}, max {diff.max():.2e} "
-              f"of values up to {b.abs().max():.1f}")
-    pages, n_kv, size = cached.cache.shape
-    print(f"pages in use: {cached.used.item()} of {pages}, {n_kv * size} bytes each ({cached.page} positions, "
-          f"{8 * size / (2 * cached.page * layer.D):.1f} bits a value)")
+    for layer in (DecoderLayer(), EightBitLayer()):
+        pieces, whole, cached = run(layer)
+        print(f"{type(layer).__name__}:")
+        for r, (a, b) in enumerate(zip(pieces, whole)):
+            diff = (a.float() - b.float()).abs()
+            print(f"request {r}: {a.shape[0]} tokens, piece by piece against whole: mean {diff.mean():.2e}, max {diff.max():.2e} "
+                  f"of values up to {b.abs().max():.1f}")
+        pages, n_kv, size = cached.cache.shape
+        print(f"pages in use: {cached.used.item()} of {pages}, {n_kv * size} bytes each ({cached.page} positions, "
+              f"{8 * size / (2 * cached.page * layer.D):.1f} bits a value)")
 
 
 if __name__ == "__main__":
