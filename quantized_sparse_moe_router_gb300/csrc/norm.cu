@@ -45,15 +45,36 @@ __device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]), bf16x2_bits(f[6], f[7]));
 }
-// (weights: read by every row, kept in L1)
-__device__ __forceinline__ void weight8(const float* w, int at, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w + at)), b = __ldg(reinterpret_cast<const float4*>(w + at) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+// Eight neighbouring floats of this lane, with one load or store where they are 32-byte
+// aligned: the two halves of a warp's kilobyte one after the other take L1 twice the time,
+// which bounded rows with weights (4096 x 7168 with norms on both sides: L1 at 74%).
+template <bool kConst>
+__device__ __forceinline__ void load8(const float* p, bool aligned, float (&f)[8]) {
+  if (aligned) {
+    if constexpr (kConst)
+      asm("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+          : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+          : "l"(p));
+    else  // (the residual, which may be written in place)
+      asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                   : "l"(p)
+                   : "memory");
+  } else {
+    const float4 a = kConst ? __ldg(reinterpret_cast<const float4*>(p)) : reinterpret_cast<const float4*>(p)[0];
+    const float4 b = kConst ? __ldg(reinterpret_cast<const float4*>(p) + 1) : reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
 }
-__device__ __forceinline__ void floats8(const uint4 a, const uint4 b, float (&f)[8]) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+__device__ __forceinline__ void store8(float* p, bool aligned, const float (&f)[8]) {
+  if (aligned) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]),
+                 "f"(f[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
 }
 
 // kVec: vectors of eight values a thread holds. kWarp: a warp a row, otherwise a
@@ -65,23 +86,24 @@ __global__ void __launch_bounds__(kWarp ? 256 : kVec <= 2 ? 512 : kMaxThreads, k
   __shared__ float s_sum[2][2][32];  // [odd turn][which sum]
   const int width = kWarp ? 32 : blockDim.x, l = kWarp ? threadIdx.x & 31 : threadIdx.x;
   int64_t row = kWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  uint4 yv[kVec], rv[kVec], rw[kWide ? kVec : 1];
+  const bool aligned = ((reinterpret_cast<uintptr_t>(u.norm) | reinterpret_cast<uintptr_t>(u.post_norm) |
+                         (u.gate_fp32 && !u.gate_per_token ? reinterpret_cast<uintptr_t>(u.gate) : 0) |
+                         (kWide ? reinterpret_cast<uintptr_t>(u.residual) | reinterpret_cast<uintptr_t>(u.residual_out) : 0)) & 31) == 0;
+  uint4 yv[kVec], rv[kWide ? 1 : kVec];
+  float rw[kWide ? kVec : 1][8];
   auto load = [&](bool in) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int at = 8 * (i * width + l);
       const bool has = in && at < u.H;
       yv[i] = has ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.y) + row * u.y_stride + at) : make_uint4(0u, 0u, 0u, 0u);
-      rv[i] = make_uint4(0u, 0u, 0u, 0u);
+      const bool adds = has && u.residual;
       if constexpr (kWide) {
-        rw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (has && u.residual) {
-          const uint4* r = reinterpret_cast<const uint4*>(static_cast<const float*>(u.residual) + row * u.residual_stride + at);
-          rv[i] = r[0];
-          rw[i] = r[1];
-        }
-      } else if (has && u.residual) {
-        rv[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.residual) + row * u.residual_stride + at);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rw[i][j] = 0.f;
+        if (adds) load8<false>(static_cast<const float*>(u.residual) + row * u.residual_stride + at, aligned, rw[i]);
+      } else {
+        rv[i] = adds ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.residual) + row * u.residual_stride + at) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
   };
@@ -117,18 +139,20 @@ __global__ void __launch_bounds__(kWarp ? 256 : kVec <= 2 ? 512 : kMaxThreads, k
       }
       float f[8], w[8];
       unpack8(yv[i], f);
-      if constexpr (kWide)
-        floats8(rv[i], rw[i], r[i]);
-      else
+      if constexpr (kWide) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] = rw[i][j];
+      } else {
         unpack8(rv[i], r[i]);
+      }
       if (u.post_norm) {
-        weight8(u.post_norm, at, w);
+        load8<true>(u.post_norm + at, aligned, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] *= w[j];
       }
       if (u.gate && !u.gate_per_token) {
         if (u.gate_fp32)
-          weight8(static_cast<const float*>(u.gate) + now * u.gate_stride, at, w);
+          load8<true>(static_cast<const float*>(u.gate) + now * u.gate_stride + at, aligned, w);
         else
           unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(u.gate) + now * u.gate_stride + at), w);
 #pragma unroll
@@ -153,9 +177,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : kVec <= 2 ? 512 : kMaxThreads, k
         const int at = 8 * (i * width + l);
         if (at >= u.H) continue;
         if constexpr (kWide) {
-          float4* to = reinterpret_cast<float4*>(static_cast<float*>(u.residual_out) + now * u.residual_out_stride + at);
-          to[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
-          to[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+          store8(static_cast<float*>(u.residual_out) + now * u.residual_out_stride + at, aligned, r[i]);
         } else {
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(u.residual_out) + now * u.residual_out_stride + at) = pack8(r[i]);
         }
@@ -169,7 +191,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : kVec <= 2 ? 512 : kMaxThreads, k
         const bool has = stores && at < u.H;
         if (u.norm && has) {
           float w[8];
-          weight8(u.norm, at, w);
+          load8<true>(u.norm + at, aligned, w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) r[i][j] *= inv * w[j];
         }
