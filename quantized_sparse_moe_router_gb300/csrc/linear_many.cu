@@ -17,8 +17,8 @@
 //
 // Warps: 0, 2 and 3 copy, 1 issues the products (the first CTA's for both), 4-11
 // scale and add (tensor-memory quarter = warp % 4). Tiles are taken in turn by CTA pairs
-// that stay, all 256 or all 128 outputs wide (see turns). Results leave through shared memory by TMA while the
-// next tile runs.
+// that stay, all 256 or all 128 outputs wide (see turns). Results leave through shared
+// memory by TMA while the next tile runs.
 #include <algorithm>
 #include <type_traits>
 
@@ -96,6 +96,13 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[16]) {
                :
                : "memory");
 }
+// (there as well: with the one that was waited for)
+__device__ __forceinline__ void tmem_ld_there(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                    "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 // acc += r * s, two columns at a time.
 template <int N>
 __device__ __forceinline__ void add_scaled(f2* acc, const uint32_t (&r)[N], f2 s) {
@@ -120,7 +127,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap map_o, const ManyArgs a) {
   using M = Many<kCols>;
   constexpr int kStages = M::Stages, kAcc = M::Acc, kMine = kCols / 2;  // kMine: columns of a thread
-  constexpr int kChunk = 16;  // columns taken out of tensor memory at once
+  // Columns that a load takes out of tensor memory, and loads at once: with 256 outputs, whose
+  // buffers come round sooner than they are read, four (1024 x 7168 x 4096 27.0 -> 26.2 us);
+  // with 128 one (four: 2048 x 2048 x 5120 22.7 -> 24.0).
+  constexpr int kChunk = 16, kLoads = kCols == 256 ? 4 : 1;
   constexpr bool kAsk = kCols == 128;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc];
@@ -263,23 +273,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
         if (b == 0) scale = s_scale[i % kSlots * kTokRows + 32 * q + lane] * __shfl_sync(0xFFFFFFFFu, w_now, 0);
         const uint32_t from = from0 + c * (2 * kMine) + half * kMine;
         const f2 s2 = f2_pack(scale, scale);
-        uint32_t v[kChunk];
+        uint32_t v[kLoads][kChunk];
 #pragma unroll
-        for (int j0 = 0; j0 < kMine; j0 += kChunk) {
-          tmem_ld_start(from + j0, v);
-          if (j0 == kMine - 2 * kChunk) {
+        for (int j0 = 0; j0 < kMine; j0 += kLoads * kChunk) {
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) tmem_ld_start(from + j0 + j * kChunk, v[j]);
+          if (j0 == (kLoads > 1 ? 0 : kMine - 2 * kChunk)) {
             const bool more = b + 1 < KB;
             if constexpr (kAsk) ready = __all_sync(0xFFFFFFFFu, more && mbar_test(&acc_full[(i + 1) % kAcc], ((i + 1) / kAcc) & 1));
             scale = more ? s_scale[(i + 1) % kSlots * kTokRows + 32 * q + lane] : 0.f;
             scale *= __shfl_sync(0xFFFFFFFFu, (b + 1) % 32 ? w_now : w_next, (b + 1) % 32);
           }
-          tmem_ld_done(v);
-          if (j0 + kChunk == kMine) {  // (all of this warp's sums are in registers)
+          tmem_ld_done(v[0]);
+#pragma unroll
+          for (int j = 1; j < kLoads; ++j) tmem_ld_there(v[j]);
+          if (j0 + kLoads * kChunk == kMine) {  // (all of this warp's sums are in registers)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_at(first_empty + c * 8);
           }
-          add_scaled(acc + j0 / 2, v, s2);
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) add_scaled(acc + (j0 + j * kChunk) / 2, v[j], s2);
         }
       }
       if (!ok) break;
@@ -373,8 +387,8 @@ cudaError_t launch(const LinearArgs& l, const void* w, const void* x_codes, int6
   return cudaLaunchKernelEx(&cfg, linear_many_kernel<kCols, kFp32>, map_w, map_x, map_s, map_o, a);
 }
 
-// The width by the turns that the pairs take: one of 128 outputs lasts 0.54 of one of
-// 256 (424 cycles a block of K and 786), and there are fewer idle pairs in the last.
+// The width by the turns that the pairs take: one of 128 outputs lasts 0.56 of one of
+// 256 (424 cycles a block of K and 755), and there are fewer idle pairs in the last.
 int64_t turns(int T, int N, int cols, int pairs) {
   return ((int64_t)((T + 2 * kTokRows - 1) / (2 * kTokRows)) * ((N + cols - 1) / cols) + pairs - 1) / pairs;
 }
@@ -382,7 +396,7 @@ int64_t turns(int T, int N, int cols, int pairs) {
 template <bool kFp32>
 cudaError_t launch_either(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s) {
   const int pairs = sms / 2;
-  return turns(l.T, l.N, 128, pairs) * 54 < turns(l.T, l.N, 256, pairs) * 100 ? launch<128, kFp32>(l, w, x_codes, codes_stride, pairs, s)
+  return turns(l.T, l.N, 128, pairs) * 56 < turns(l.T, l.N, 256, pairs) * 100 ? launch<128, kFp32>(l, w, x_codes, codes_stride, pairs, s)
                                                                              : launch<256, kFp32>(l, w, x_codes, codes_stride, pairs, s);
 }
 
@@ -408,7 +422,7 @@ cudaError_t configure_linear_many() {
 }
 
 int64_t linear_many_cycles(int T, int N, int KB, int sms) {
-  return std::min(turns(T, N, 128, sms / 2) * 424, turns(T, N, 256, sms / 2) * 786) * KB;
+  return std::min(turns(T, N, 128, sms / 2) * 424, turns(T, N, 256, sms / 2) * 755) * KB;
 }
 
 cudaError_t launch_linear_many(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s) {
