@@ -430,8 +430,8 @@ fw_status fw_fp8_quantize_weight(const void *w, int32_t w_fp32, int32_t N, int32
  * block is the tensor core's (fp32), and blocks are scaled and added in fp32; out is
  * rounded once. x may be bf16: it is then quantised by the rule above, with the same
  * result as fw_fp8_quantize before the call. out may not overlap x or w.
- * workspace: DEVICE, 16-byte aligned, at least fw_linear_fp8_workspace bytes (0 for
- * some calls); its contents mean nothing between calls, and calls that may overlap
+ * workspace: DEVICE, 16-byte aligned, at least fw_linear_fp8_workspace bytes (0 with
+ * codes, and with bf16 up to 16 tokens; it may then be NULL); its contents mean nothing between calls, and calls that may overlap
  * need one each. */
 typedef struct {
   int32_t T, K, N;           /* T >= 0; K a multiple of 16; N >= 1 */

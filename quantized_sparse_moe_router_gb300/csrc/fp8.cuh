@@ -125,14 +125,15 @@ cudaError_t encode_scales(CUtensorMap* map, const float* scales, int64_t T, int 
 // The same of n fp32 matrices [T][cols], one behind the other, in boxes of 32 columns by `box` rows, 128-byte swizzle.
 cudaError_t encode_parts(CUtensorMap* map, float* parts, int n, int64_t T, int64_t cols, int box);
 
-cudaError_t configure_linear_few();
+// (dev: the current device, below 64)
+cudaError_t configure_linear_few(int dev);
 bool linear_few_quantises(int T);  // whether the kernel for few tokens takes bf16 itself
 // Blocks of K that an SM takes one after the other at most, at more than 64 tokens.
-int64_t linear_few_blocks(int T, int N, int KB, int sms);
-cudaError_t launch_linear_few(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s);
+int64_t linear_few_blocks(int T, int N, int KB, int dev, int sms);
+cudaError_t launch_linear_few(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int dev, int sms, cudaStream_t s);
 
-cudaError_t configure_linear_many();
-int64_t linear_many_cycles(int T, int N, int KB, int sms);  // about how many its products take
-cudaError_t launch_linear_many(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s);
+cudaError_t configure_linear_many(int dev);
+int64_t linear_many_cycles(int T, int N, int KB, int dev, int sms);  // about how many its products take
+cudaError_t launch_linear_many(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int dev, int sms, cudaStream_t s);
 
 }  // namespace fw

@@ -24,8 +24,8 @@ static fw_status check_args(const fw_linear_fp8_args* a, bool pointers) {
   return FW_OK;
 }
 
-// The current device's SM count; its kernels are configured once.
-static cudaError_t device_sms(int* sms) {
+// The current device and its SM count; its kernels are configured once.
+static cudaError_t device_sms(int* device, int* sms) {
   static std::mutex mu;
   static int known[64] = {};
   int dev = 0, n = 0;
@@ -34,12 +34,13 @@ static cudaError_t device_sms(int* sms) {
   std::lock_guard<std::mutex> g(mu);
   if (!known[dev]) {
     cudaError_t e = configure_fp8_quantize();
-    if (e == cudaSuccess) e = configure_linear_few();
-    if (e == cudaSuccess) e = configure_linear_many();
+    if (e == cudaSuccess) e = configure_linear_few(dev);
+    if (e == cudaSuccess) e = configure_linear_many(dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     known[dev] = n;
   }
+  *device = dev;
   *sms = known[dev];
   return cudaSuccess;
 }
@@ -50,13 +51,14 @@ static int64_t scale_stride(const fw_linear_fp8_args* a) { return round_up(a->T,
 static int64_t codes_bytes(const fw_linear_fp8_args* a) { return round_up((int64_t)a->T * a->K, 256); }
 
 // Up to 64 tokens the weights bound the call, and the kernel for few tokens reads them
-// faster (64 x 7168 x 7168: 14.6 us against 15.7, 64 x 4096 x 4096: 8.7 against 10.0).
-// With more the other one is as fast or faster (128 x 4096 x 4096: 10.6 against 10.2,
-// 128 x 2048 x 5120: 8.8 against 7.2), but where it has so few tiles that the first one's
-// sharing of K gains more than its some 900 cycles a block and 6,000 for the sums cost.
-static bool takes_many(const fw_linear_fp8_args* a, int sms) {
+// faster (64 x 7168 x 7168: 14.6 us against 15.7, 64 x 4096 x 4096: 8.7 against 10.0). With
+// more both are estimated, by the cycles that the products of the one take and the blocks
+// of K that an SM has in the other, 970 cycles each and 2,100 for the other's longer start
+// and end (65 x 4096 x 2048: few 7.9 us, many 8.6; 130 x 7168 x 1024: 10.4 and 9.2; 257 x
+// 4096 x 4096: 20.4 and 10.7; 400 x 1024 x 1024: 6.5 and 4.9).
+static bool takes_many(const fw_linear_fp8_args* a, int dev, int sms) {
   const int KB = fp8_blocks(a->K);
-  return a->T > 64 && linear_many_cycles(a->T, a->N, KB, sms) <= linear_few_blocks(a->T, a->N, KB, sms) * 900 + 6000;
+  return a->T > 64 && linear_many_cycles(a->T, a->N, KB, dev, sms) <= linear_few_blocks(a->T, a->N, KB, dev, sms) * 970 + 2100;
 }
 
 extern "C" fw_status fw_linear_fp8_workspace(const fw_linear_fp8_args* a, int64_t* bytes) {
@@ -75,8 +77,8 @@ extern "C" fw_status fw_linear_fp8(const fw_linear_fp8_args* a, void* workspace,
   if (need && (!workspace || bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16))
     return set_error(FW_EINVAL, "fw_linear_fp8: the workspace is too small (see fw_linear_fp8_workspace) or not 16-byte aligned");
   if (fw_status st = check_device("fw_linear_fp8: needs an sm_103 device"); st != FW_OK) return st;
-  int sms = 0;
-  if (cudaError_t e = device_sms(&sms); e != cudaSuccess) return set_cuda_error(e, "fw_linear_fp8: setting the device up");
+  int dev = 0, sms = 0;
+  if (cudaError_t e = device_sms(&dev, &sms); e != cudaSuccess) return set_cuda_error(e, "fw_linear_fp8: setting the device up");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   LinearArgs l = {a->T, a->K, a->N, fp8_blocks(a->K), nullptr, 0, a->x_scale, a->x_scale_stride, a->w_scale, a->out, a->out_stride, a->out_fp32, a->status, 0};
   const void* codes = a->x;
@@ -95,8 +97,8 @@ extern "C" fw_status fw_linear_fp8(const fw_linear_fp8_args* a, void* workspace,
     l.x_stride = a->x_stride;
   }
   if (e == cudaSuccess)
-    e = takes_many(a, sms) ? launch_linear_many(l, a->w, codes, codes_stride, sms, s)
-                           : launch_linear_few(l, a->w, codes, codes_stride, sms, s);
+    e = takes_many(a, dev, sms) ? launch_linear_many(l, a->w, codes, codes_stride, dev, sms, s)
+                           : launch_linear_few(l, a->w, codes, codes_stride, dev, sms, s);
   if (e != cudaSuccess) return set_cuda_error(e, "fw_linear_fp8: launch");
   return FW_OK;
 }

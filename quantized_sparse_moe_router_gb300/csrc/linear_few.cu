@@ -22,6 +22,7 @@
 // latency bounded them).
 
 #include <algorithm>
+#include <atomic>
 
 #include "fp8.cuh"
 #include "pair.cuh"
@@ -79,15 +80,6 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
-}
-
-// Four floats at this CTA's shared address `addr`, in the CTA of rank `rank` of the cluster.
-__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
-  uint32_t at;
-  float4 v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-  return v;
 }
 
 __device__ __forceinline__ void store_out(const LinearArgs& a, int t, int n, float v) {
@@ -315,11 +307,10 @@ __global__ void __launch_bounds__(few_threads<kTok, kQuant>(), Few<kTok, kQuant>
     cluster_sync();  // every CTA's sums are in its shared memory
     // each its share of them, four outputs of a token a thread, all ranks' parts on their way at once
     const int all = nt * (kRows / 4), i0 = all * rank / split, i1 = all * (rank + 1) / split;
-    const uint32_t sums = smem_u32(ring);
     for (int i = i0 + tid; i < i1; i += (int)blockDim.x) {
       float4 p[kMaxCluster];
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) p[r] = r < split ? ld_peer(sums + 16 * i, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < kMaxCluster; ++r) p[r] = r < split ? ld_cta(in_cta(ring + 16 * i, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
       float4 v = p[0];
 #pragma unroll
       for (int r = 1; r < kMaxCluster; ++r) v.x += p[r].x, v.y += p[r].y, v.z += p[r].z, v.w += p[r].w;
@@ -329,22 +320,47 @@ __global__ void __launch_bounds__(few_threads<kTok, kQuant>(), Few<kTok, kQuant>
   }
 }
 
+// Clusters of 2 .. kMaxCluster CTAs that a device runs at once: a cluster's SMs are of one
+// group of them, so there are fewer than the SMs have places for.
+struct Room {
+  std::atomic<int> clusters[kMaxCluster + 1];
+};
 template <int kTok, bool kQuant>
-cudaError_t configure() {
+Room& room_of(int dev) {
+  static Room room[64];
+  return room[dev];
+}
+
+template <int kTok, bool kQuant>
+cudaError_t configure(int dev) {
   cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<kTok, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<kTok, kQuant>::SmemBytes);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(linear_few_kernel<kTok, kQuant>, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
+  int one[kMaxCluster + 1] = {};  // with an SM for each CTA, which is what is reported
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&one[1], cudaDevAttrMultiProcessorCount, dev);
+  for (int c = 2; c <= kMaxCluster && e == cudaSuccess; ++c)
+    e = active_clusters(linear_few_kernel<kTok, kQuant>, c, few_threads<kTok, kQuant>(), Few<kTok, kQuant>::SmemBytes, &one[c]);
+  // With two CTAs an SM: as many as have half the size; of an odd size, halfway between what
+  // is sure (twice as many, or as many as have one CTA more) and what there are places for
+  // (96 of three ran at once, 40 of seven did not: 64 x 7168 x 5120 19.0 us, with six of
+  // them to a tile 13.1).
+  int n = 0;
+  for (int c = kMaxCluster; c >= 2; --c) {
+    n = Few<kTok, kQuant>::Ctas == 1 ? one[c] : c % 2 ? (std::max(2 * one[c], n) + 2 * one[1] / c) / 2 : one[c / 2];
+    room_of<kTok, kQuant>(dev).clusters[c].store(n);
+  }
   return e;
 }
 
 // CTAs that share a tile: as many as keep the SM with the most work shortest, in
 // blocks of K (*longest), with a few for each CTA's beginning and end. All find room at
-// once, and a part of K has two blocks.
-int split_of(int tiles, int rows, int KB, int ctas_per_sm, int sms, int64_t* longest) {
+// once, and a part of K has two blocks at least.
+int split_of(int tiles, int rows, int KB, const Room& room, int sms, int64_t* longest) {
   const int64_t all = (int64_t)tiles * rows;
   int split = 1;
   int64_t best = INT64_MAX;
-  for (int c = 1; c <= kMaxCluster && (c == 1 || (all * c <= (int64_t)ctas_per_sm * sms && KB >= 2 * c)); ++c) {
+  for (int c = 1; c <= kMaxCluster && (c == 1 || KB >= 2 * c); ++c) {
+    if (c > 1 && all > room.clusters[c].load()) continue;
     const int64_t cost = (all * c + sms - 1) / sms * ((KB + c - 1) / c + 2);
     if (cost < best) best = cost, split = c;
   }
@@ -353,14 +369,14 @@ int split_of(int tiles, int rows, int KB, int ctas_per_sm, int sms, int64_t* lon
 }
 
 template <int kTok, bool kQuant>
-cudaError_t launch(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s) {
+cudaError_t launch(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int dev, int sms, cudaStream_t s) {
   CUtensorMap map_w, map_x = {}, map_s = {};
   cudaError_t e = encode_codes(&map_w, w, a.N, a.K, a.K, kRows);
   if (e == cudaSuccess) e = kQuant ? encode_values(&map_x, a.x, a.T, a.K, a.x_stride, kTok) : encode_codes(&map_x, x_codes, a.T, a.K, codes_stride, kTok);
   if (e == cudaSuccess && !kQuant) e = encode_scales(&map_s, a.x_scale, a.T, a.KB, a.x_scale_stride, Few<kTok, kQuant>::Slot);
   if (e != cudaSuccess) return e;
   const int tiles = (a.N + kRows - 1) / kRows, rows = (a.T + kTok - 1) / kTok;
-  const int split = split_of(tiles, rows, a.KB, Few<kTok, kQuant>::Ctas, sms, nullptr);
+  const int split = split_of(tiles, rows, a.KB, room_of<kTok, kQuant>(dev), sms, nullptr);
   const int64_t room = (int64_t)Few<kTok, kQuant>::Ctas * sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, std::max<int64_t>(1, room / rows))), (unsigned)rows);
@@ -383,28 +399,28 @@ cudaError_t launch(const LinearArgs& a, const void* w, const void* x_codes, int6
 // (17 to 32 tokens: 12.4 us at 4096 x 4096 against 10.3 with a launch for them)
 bool linear_few_quantises(int T) { return T <= 16; }
 
-cudaError_t configure_linear_few() {
+cudaError_t configure_linear_few(int dev) {
   cudaError_t e = configure_tensor_maps();
-  if (e == cudaSuccess) e = configure<16, true>();
-  if (e == cudaSuccess) e = configure<16, false>();
-  if (e == cudaSuccess) e = configure<32, false>();
-  if (e == cudaSuccess) e = configure<64, false>();
-  if (e == cudaSuccess) e = configure<128, false>();
+  if (e == cudaSuccess) e = configure<16, true>(dev);
+  if (e == cudaSuccess) e = configure<16, false>(dev);
+  if (e == cudaSuccess) e = configure<32, false>(dev);
+  if (e == cudaSuccess) e = configure<64, false>(dev);
+  if (e == cudaSuccess) e = configure<128, false>(dev);
   return e;
 }
 
-int64_t linear_few_blocks(int T, int N, int KB, int sms) {
+int64_t linear_few_blocks(int T, int N, int KB, int dev, int sms) {
   int64_t longest;
-  split_of((N + kRows - 1) / kRows, (T + 127) / 128, KB, Few<128, false>::Ctas, sms, &longest);
+  split_of((N + kRows - 1) / kRows, (T + 127) / 128, KB, room_of<128, false>(dev), sms, &longest);
   return longest;
 }
 
-cudaError_t launch_linear_few(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s) {
-  if (a.x) return launch<16, true>(a, w, nullptr, 0, sms, s);
-  if (a.T <= 16) return launch<16, false>(a, w, x_codes, codes_stride, sms, s);
-  if (a.T <= 32) return launch<32, false>(a, w, x_codes, codes_stride, sms, s);
-  if (a.T <= 64) return launch<64, false>(a, w, x_codes, codes_stride, sms, s);
-  return launch<128, false>(a, w, x_codes, codes_stride, sms, s);
+cudaError_t launch_linear_few(const LinearArgs& a, const void* w, const void* x_codes, int64_t codes_stride, int dev, int sms, cudaStream_t s) {
+  if (a.x) return launch<16, true>(a, w, nullptr, 0, dev, sms, s);
+  if (a.T <= 16) return launch<16, false>(a, w, x_codes, codes_stride, dev, sms, s);
+  if (a.T <= 32) return launch<32, false>(a, w, x_codes, codes_stride, dev, sms, s);
+  if (a.T <= 64) return launch<64, false>(a, w, x_codes, codes_stride, dev, sms, s);
+  return launch<128, false>(a, w, x_codes, codes_stride, dev, sms, s);
 }
 
 }  // namespace fw

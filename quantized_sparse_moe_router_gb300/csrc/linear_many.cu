@@ -15,11 +15,15 @@
 // while the next block's products run into the other buffer. That is half of
 // what the products take: one packed multiply-add for two sums.
 //
+// Where tiles are too few for the pairs, a cluster of two or four pairs takes one, each
+// with a part of K, and joins the sums in their order through distributed shared memory.
+//
 // Warps: 0, 2 and 3 copy, 1 issues the products (the first CTA's for both), 4-11
 // scale and add (tensor-memory quarter = warp % 4). Tiles are taken in turn by CTA pairs
 // that stay, all 256 or all 128 outputs wide (see turns). Results leave through shared
 // memory by TMA while the next tile runs.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -37,6 +41,7 @@ constexpr int kFirstEpi = 4;                 // warps 0-3: copies and products
 constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;
 // registers of the first warpgroup and of the other two, of 168 a thread at launch: 128 x 56 + 256 x 224 = 384 x 168
 constexpr int kFewRegs = 56, kEpiRegs = 224;
+constexpr int kJoin = 16;                    // columns that a pair joins at once, where pairs share a tile
 constexpr uint32_t kOutBytes = 32 * 128;     // a warp's staging: 32 rows of 128 bytes
 
 constexpr uint32_t kXBytes = kTokRows * kFp8Block;
@@ -65,6 +70,7 @@ struct ManyArgs {
   LinearArgs l;
   int tiles_t, tiles_n;
   int tiles;
+  int split;                                 // pairs that share a tile, each a part of K (more than one: a pair has one tile)
   int by_tma;                                // results leave by TMA (aligned rows)
 };
 
@@ -121,7 +127,48 @@ __device__ __forceinline__ void tile_at(const ManyArgs& a, int i, int* t0, int* 
   *n0 = tn * kCols;
 }
 
-template <int kCols, bool kFp32>
+// 32 rows, a lane's row in `sum`, of kJoin outputs from `col` on: 16 bytes a lane and store
+// where rows are aligned, otherwise through shared memory, two rows a store.
+template <bool kFp32>
+__device__ __forceinline__ void put_share(const LinearArgs& l, int aligned, const f2 (&sum)[kJoin / 2], int row0, int col, int lane, float* stage) {
+  float v[kJoin];
+#pragma unroll
+  for (int j = 0; j < kJoin / 2; ++j) f2_unpack(sum[j], v[2 * j], v[2 * j + 1]);
+  const int64_t size = kFp32 ? 4 : 2;
+  uint8_t* out = static_cast<uint8_t*>(l.out);
+  if (aligned && col + kJoin <= l.N) {
+    if (row0 + lane >= l.T) return;
+    uint4* to = reinterpret_cast<uint4*>(out + ((int64_t)(row0 + lane) * l.out_stride + col) * size);
+    if constexpr (kFp32) {
+#pragma unroll
+      for (int j = 0; j < kJoin / 4; ++j)
+        to[j] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kJoin / 8; ++j)
+        to[j] = make_uint4(bf16x2_bits(v[8 * j], v[8 * j + 1]), bf16x2_bits(v[8 * j + 2], v[8 * j + 3]), bf16x2_bits(v[8 * j + 4], v[8 * j + 5]),
+                           bf16x2_bits(v[8 * j + 6], v[8 * j + 7]));
+    }
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kJoin; ++j) stage[lane * (kJoin + 1) + j] = v[j];
+  __syncwarp();
+  const int c = lane % kJoin;
+#pragma unroll
+  for (int r = lane / kJoin; r < 32; r += 32 / kJoin) {
+    if (row0 + r >= l.T || col + c >= l.N) continue;
+    const int64_t to = (int64_t)(row0 + r) * l.out_stride + col + c;
+    if constexpr (kFp32)
+      static_cast<float*>(l.out)[to] = stage[r * (kJoin + 1) + c];
+    else
+      static_cast<__nv_bfloat16*>(l.out)[to] = __float2bfloat16_rn(stage[r * (kJoin + 1) + c]);
+  }
+}
+
+// kShare: a.split pairs share a tile.
+template <int kCols, bool kFp32, bool kShare>
 __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                                                                   const __grid_constant__ CUtensorMap map_s,
                                                                   const __grid_constant__ CUtensorMap map_o, const ManyArgs a) {
@@ -136,13 +183,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc];
   __shared__ uint32_t s_tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int split = kShare ? a.split : 1, rank = blockIdx.x & 1, part = kShare ? (blockIdx.x >> 1) % split : 0;
+  const int pair = (blockIdx.x >> 1) / split, pairs = (gridDim.x >> 1) / split;
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* ring = smem_raw + pad;                          // [kStages][tokens 128 x 128, weights 128 x 128]
   uint8_t* s_out = ring + kStages * M::StageBytes;           // [kEpiWarps][32 rows][128 bytes]
   float* s_scale = reinterpret_cast<float*>(s_out + kEpiWarps * kOutBytes);  // [kSlots][kTokRows]
   const LinearArgs& l = a.l;
-  const int KB = l.KB;
+  const int b0 = (int)((int64_t)l.KB * part / split), KB = (int)((int64_t)l.KB * (part + 1) / split) - b0;  // this pair's blocks of K
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -172,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     // Warp 0 copies the tokens, 2 the weights, 3 the scales: a copy takes its warp some
     // 100 cycles to start. They stay together and elect a lane for it.
-    const uint32_t first_full = in_first(full);
+    const uint32_t first_full = in_cta(full, 2 * part);
     uint32_t i = 0, s = 0, phase = 1;
     for (int tile = pair; tile < a.tiles && ok; tile += pairs) {
       int t0, n0;
@@ -189,12 +237,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
           const uint32_t bar = first_full + s * 8;
           if (warp == 0) {
             if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (M::StageBytes + kScaleBytes * ((b == 0) + (b + 1 < KB))));
-            tma_pair(st, &map_x, b * kFp8Block, t0, bar);
+            tma_pair(st, &map_x, (b0 + b) * kFp8Block, t0, bar);
           } else if (warp == 2) {
-            tma_pair(st + kXBytes, &map_w, b * kFp8Block, n0, bar);
+            tma_pair(st + kXBytes, &map_w, (b0 + b) * kFp8Block, n0, bar);
           } else {
-            if (b == 0) tma_pair(s_scale + i % kSlots * kTokRows, &map_s, t0, b, bar);
-            if (b + 1 < KB) tma_pair(s_scale + (i + 1) % kSlots * kTokRows, &map_s, t0, b + 1, bar);
+            if (b == 0) tma_pair(s_scale + i % kSlots * kTokRows, &map_s, t0, b0 + b, bar);
+            if (b + 1 < KB) tma_pair(s_scale + (i + 1) % kSlots * kTokRows, &map_s, t0, b0 + b + 1, bar);
           }
         }
         __syncwarp();
@@ -204,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
     // (after a wait that gave up) both CTAs' copies in flight land before either leaves
     if (!ok && rank == 0 && warp == 0)
       for (uint32_t j = i > kStages ? i - kStages : 0; j < i; ++j) wait_inline(&full[j % kStages], (j / kStages) & 1);
+    if constexpr (kShare) cluster_sync();  // (the parts' sums)
   } else if (warp == 1) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (rank == 0) {
@@ -229,27 +278,28 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
           const uint32_t x = ring_lo + s * (M::StageBytes >> 4), w = x + (kXBytes >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_pair(cols0 + c * kCols, x + 2 * k, w + 2 * k, idesc_e4m3(2 * kTokRows, kCols), k != 0);
-          commit_pair(&acc_full[c]);
-          commit_pair(&empty[s]);
+          commit_pair(&acc_full[c], 2 * part);
+          commit_pair(&empty[s], 2 * part);
         }
         __syncwarp();
         if (++s == kStages) s = 0, s_phase ^= 1;
       }
       if (i > 0) wait_inline(&acc_full[(i - 1) % kAcc], ((i - 1) / kAcc) & 1);  // no product outlives the tensor memory
     }
+    if constexpr (kShare) cluster_sync();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int q = warp & 3, half = (warp - kFirstEpi) >> 2;
     const uint32_t from0 = tmem + ((uint32_t)(32 * q) << 16);
     uint8_t* stage = s_out + (warp - kFirstEpi) * kOutBytes;
-    const uint32_t first_empty = in_first(acc_empty);
+    const uint32_t first_empty = in_cta(acc_empty, 2 * part);
     uint32_t i = 0;
     for (int tile = pair; tile < a.tiles && ok; tile += pairs) {
       int t0, n0;
       tile_at<kCols>(a, tile, &t0, &n0);
       const int row0 = t0 + rank * kTokRows + 32 * q, col0 = n0 + half * kMine;
       // (columns of a thread lie in one block of 128 outputs; past the last one there is nothing to scale)
-      const float* ws = l.w_scale + (int64_t)::min(col0 / kFp8Block, (l.N - 1) / kFp8Block) * KB;
+      const float* ws = l.w_scale + (int64_t)::min(col0 / kFp8Block, (l.N - 1) / kFp8Block) * l.KB + b0;
       f2 acc[kMine / 2];
 #pragma unroll
       for (int j = 0; j < kMine / 2; ++j) acc[j] = 0ull;
@@ -295,6 +345,46 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
 #pragma unroll
           for (int j = 0; j < kLoads; ++j) add_scaled(acc + (j0 + j * kChunk) / 2, v[j], s2);
         }
+      }
+      // A tile that pairs share: each leaves its sums in its ring, which nothing reads or fills
+      // any more, and joins, in the pairs' order, a share of every thread's columns.
+      if constexpr (kShare) {
+        const int at = threadIdx.x - kFirstEpi * 32, share = kMine / kJoin / split;
+        float4* mine = reinterpret_cast<float4*>(ring) + at;  // [kMine / 4][a thread]
+        if (ok) {
+#pragma unroll
+          for (int j = 0; j < kMine / 4; ++j) {
+            if (j * 4 / kJoin / share == part) continue;
+            float4 v;
+            f2_unpack(acc[2 * j], v.x, v.y);
+            f2_unpack(acc[2 * j + 1], v.z, v.w);
+            mine[j * kEpiWarps * 32] = v;
+          }
+        }
+        cluster_sync();
+        if (!ok) break;
+#pragma unroll
+        for (int j0 = 0; j0 < kMine; j0 += kJoin) {
+          if (j0 / kJoin / share != part) continue;
+          f2 sum[kJoin / 2];
+#pragma unroll
+          for (int j = 0; j < kJoin / 2; ++j) sum[j] = 0ull;
+          for (int p = 0; p < split; ++p) {
+            const uint32_t from = in_cta(mine, 2 * p + rank);
+#pragma unroll
+            for (int j = 0; j < kJoin / 4; ++j) {
+              f2 lo = acc[j0 / 2 + 2 * j], hi = acc[j0 / 2 + 2 * j + 1];
+              if (p != part) {
+                const float4 v = ld_cta(from + (j0 / 4 + j) * kEpiWarps * 32 * 16);
+                lo = f2_pack(v.x, v.y), hi = f2_pack(v.z, v.w);
+              }
+              sum[2 * j] = f2_add(sum[2 * j], lo);
+              sum[2 * j + 1] = f2_add(sum[2 * j + 1], hi);
+            }
+          }
+          put_share<kFp32>(l, a.by_tma, sum, row0, col0 + j0, lane, reinterpret_cast<float*>(stage));
+        }
+        continue;
       }
       if (!ok) break;
       // 32 rows of 128 bytes at a time, the 16-byte chunk j of a row at j ^ (row % 8): the tensor map's swizzle
@@ -354,8 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-template <int kCols, bool kFp32>
-cudaError_t launch(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int pairs, cudaStream_t s) {
+template <int kCols, bool kFp32, bool kShare>
+cudaError_t launch(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int split, int pairs, cudaStream_t s) {
   CUtensorMap map_w, map_x, map_s, map_o = {};
   cudaError_t e = encode_codes(&map_w, w, l.N, l.K, l.K, kCols / 2);
   if (e == cudaSuccess) e = encode_codes(&map_x, x_codes, l.T, l.K, codes_stride, kTokRows);
@@ -371,8 +461,9 @@ cudaError_t launch(const LinearArgs& l, const void* w, const void* x_codes, int6
   const int64_t tiles = (int64_t)a.tiles_t * a.tiles_n;
   if (tiles > 1 << 30) return cudaErrorInvalidValue;
   a.tiles = (int)tiles;
+  a.split = split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, pairs)));
+  cfg.gridDim = dim3((unsigned)(kShare ? 2 * split * tiles : 2 * std::min<int64_t>(tiles, pairs)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Many<kCols>::SmemBytes;
   cfg.stream = s;
@@ -380,53 +471,76 @@ cudaError_t launch(const LinearArgs& l, const void* w, const void* x_codes, int6
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = 2 * split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_many_kernel<kCols, kFp32>, map_w, map_x, map_s, map_o, a);
+  return cudaLaunchKernelEx(&cfg, linear_many_kernel<kCols, kFp32, kShare>, map_w, map_x, map_s, map_o, a);
 }
 
-// The width by the turns that the pairs take: one of 128 outputs lasts 0.56 of one of
-// 256 (424 cycles a block of K and 755), and there are fewer idle pairs in the last.
-int64_t turns(int T, int N, int cols, int pairs) {
-  return ((int64_t)((T + 2 * kTokRows - 1) / (2 * kTokRows)) * ((N + cols - 1) / cols) + pairs - 1) / pairs;
+// Clusters of 2 and 4 pairs that a device runs at once.
+std::atomic<int> g_room[64][2];
+
+// How the products are cut up: for the fewest cycles, by the turns that the pairs take with
+// tiles 256 or 128 outputs wide (755 cycles a block of K, 424), and, where pairs would have
+// nothing to do, with two or four of them to a tile (470), whose join takes longer the
+// more there are: 300 x 7168 x 576 14.8 -> 9.4 us with four, 500 x 7168 x 1536 15.2 -> 12.4
+// with two, 333 x 4000 x 2051 10.9 and 11.1.
+struct Cut {
+  int cols, split;
+  int64_t cycles;
+};
+Cut cut_of(int T, int N, int KB, int dev, int pairs) {
+  const int64_t rows = (T + 2 * kTokRows - 1) / (2 * kTokRows), wide = rows * ((N + 255) / 256), narrow = rows * ((N + 127) / 128);
+  Cut best = {256, 1, (wide + pairs - 1) / pairs * KB * 755};
+  if (const int64_t c = (narrow + pairs - 1) / pairs * KB * 424; c < best.cycles) best = {128, 1, c};
+  for (int split = 2; split <= 4; split *= 2)
+    if (const int64_t c = (int64_t)((KB + split - 1) / split) * 470 + (1000 + 60 * narrow) * split; c < best.cycles && KB >= 2 * split && narrow <= g_room[dev][split == 4].load())
+      best = {128, split, c};
+  return best;
 }
 
 template <bool kFp32>
-cudaError_t launch_either(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s) {
+cudaError_t launch_cut(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int dev, int sms, cudaStream_t s) {
   const int pairs = sms / 2;
-  return turns(l.T, l.N, 128, pairs) * 56 < turns(l.T, l.N, 256, pairs) * 100 ? launch<128, kFp32>(l, w, x_codes, codes_stride, pairs, s)
-                                                                             : launch<256, kFp32>(l, w, x_codes, codes_stride, pairs, s);
+  const Cut c = cut_of(l.T, l.N, l.KB, dev, pairs);
+  return c.split > 1     ? launch<128, kFp32, true>(l, w, x_codes, codes_stride, c.split, pairs, s)
+         : c.cols == 128 ? launch<128, kFp32, false>(l, w, x_codes, codes_stride, 1, pairs, s)
+                         : launch<256, kFp32, false>(l, w, x_codes, codes_stride, 1, pairs, s);
 }
 
-template <int kCols, bool kFp32>
+template <int kCols, bool kFp32, bool kShare>
 cudaError_t configure() {
   // the warps' register shares (setmaxnreg) must fit what the launch gives the
   // CTA, or the growing ones would wait for ever
   cudaFuncAttributes f;
-  cudaError_t e = cudaFuncGetAttributes(&f, linear_many_kernel<kCols, kFp32>);
+  cudaError_t e = cudaFuncGetAttributes(&f, linear_many_kernel<kCols, kFp32, kShare>);
   if (e == cudaSuccess && f.numRegs * kThreads < kFewRegs * 32 * kFirstEpi + kEpiRegs * 32 * kEpiWarps) e = cudaErrorInvalidConfiguration;
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_many_kernel<kCols, kFp32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Many<kCols>::SmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_many_kernel<kCols, kFp32, kShare>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Many<kCols>::SmemBytes);
   return e;
 }
 
 }  // namespace
 
-cudaError_t configure_linear_many() {
-  cudaError_t e = configure<256, false>();
-  if (e == cudaSuccess) e = configure<256, true>();
-  if (e == cudaSuccess) e = configure<128, false>();
-  if (e == cudaSuccess) e = configure<128, true>();
+cudaError_t configure_linear_many(int dev) {
+  cudaError_t e = configure<256, false, false>();
+  if (e == cudaSuccess) e = configure<256, true, false>();
+  if (e == cudaSuccess) e = configure<128, false, false>();
+  if (e == cudaSuccess) e = configure<128, true, false>();
+  if (e == cudaSuccess) e = configure<128, false, true>();
+  if (e == cudaSuccess) e = configure<128, true, true>();
+  for (int split = 2; split <= 4 && e == cudaSuccess; split *= 2) {
+    int n = 0;
+    e = active_clusters(linear_many_kernel<128, false, true>, 2 * split, kThreads, Many<128>::SmemBytes, &n);
+    g_room[dev][split == 4].store(n);
+  }
   return e;
 }
 
-int64_t linear_many_cycles(int T, int N, int KB, int sms) {
-  return std::min(turns(T, N, 128, sms / 2) * 424, turns(T, N, 256, sms / 2) * 755) * KB;
-}
+int64_t linear_many_cycles(int T, int N, int KB, int dev, int sms) { return cut_of(T, N, KB, dev, sms / 2).cycles; }
 
-cudaError_t launch_linear_many(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int sms, cudaStream_t s) {
-  return l.out_fp32 ? launch_either<true>(l, w, x_codes, codes_stride, sms, s) : launch_either<false>(l, w, x_codes, codes_stride, sms, s);
+cudaError_t launch_linear_many(const LinearArgs& l, const void* w, const void* x_codes, int64_t codes_stride, int dev, int sms, cudaStream_t s) {
+  return l.out_fp32 ? launch_cut<true>(l, w, x_codes, codes_stride, dev, sms, s) : launch_cut<false>(l, w, x_codes, codes_stride, dev, sms, s);
 }
 
 }  // namespace fw

@@ -5,18 +5,41 @@
 #include "internal.cuh"
 
 namespace fw {
+
+// Clusters of `size` CTAs that the current device runs at once.
+template <typename... Args>
+cudaError_t active_clusters(void (*kernel)(Args...), int size, int threads, size_t smem, int* n) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+}
+
 namespace dev {
 
-// Arrives at the barrier in both CTAs once the products issued so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+// Arrives at the barrier in both CTAs of the pair once the products issued so far are
+// done. (first: the rank in the cluster of the pair's first CTA.)
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t first = 0) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "h"((uint16_t)(3u << first))
                : "memory");
 }
-// The first CTA's copy of a shared address.
-__device__ __forceinline__ uint32_t in_first(const void* p) {
+// A shared address in the CTA of rank `rank` of the cluster (the pair's first one).
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank = 0) {
   uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
+}
+__device__ __forceinline__ float4 ld_cta(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void tma_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) route_logits_kernel(const __g
   pdl_launch_dependents();
 
   if (warp == 0 || warp == 2) {
-    const uint32_t first_full = in_first(full);
+    const uint32_t first_full = in_cta(full);
     int i = 0, s = 0;
     uint32_t phase = 1;
     for (; i < steps; ++i) {

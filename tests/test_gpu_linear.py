@@ -108,6 +108,18 @@ def test_products(T, K, N, kind):
     assert status.item() == 0
 
 
+@pytest.mark.parametrize("T, K, N", [(300, 7168, 576), (300, 7168, 577), (130, 7168, 1024), (500, 7168, 1536), (257, 7168, 2047), (200, 7088, 1500), (513, 16400, 200)])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_products_of_shared_tiles(T, K, N, kind):
+    """Few tiles and a long K, which pairs of SMs then share; rows apart, and of no alignment."""
+    x, (w, ws) = tokens(T, K, 1), fw.quantize_fp8_weight(weights(N, K, 2))
+    out = fw.linear_fp8(x, w, ws, out_dtype=kind)
+    check(out, x, w, ws)
+    big = torch.full((T, N + 37), 7.0, dtype=kind, device=DEV)
+    assert torch.equal(fw.linear_fp8(x, w, ws, out=big[:, 5:5 + N]), out)
+    assert (big[:, :5] == 7).all() and (big[:, 5 + N:] == 7).all()
+
+
 @pytest.mark.parametrize("T", [1, 5, 40, 300])
 def test_scales_far_apart(T):
     """Blocks whose scales differ by many powers of two, along K and over tokens and outputs."""
