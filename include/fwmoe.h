@@ -431,10 +431,10 @@ fw_status fw_fp8_quantize_weight(const void *w, int32_t w_fp32, int32_t N, int32
  * rounded once. x may be bf16: it is then quantised by the rule above, with the same
  * result as fw_fp8_quantize before the call. out may not overlap x or w.
  * workspace: DEVICE, 16-byte aligned, at least fw_linear_fp8_workspace bytes (0 with
- * codes, and with bf16 up to 16 tokens; it may then be NULL); its contents mean nothing between calls, and calls that may overlap
- * need one each. */
+ * codes, and with bf16 up to 16 tokens; it may then be NULL); its contents mean nothing
+ * between calls, and calls that may overlap need one each. */
 typedef struct {
-  int32_t T, K, N;           /* T >= 0; K a multiple of 16; N >= 1 */
+  int32_t T, K, N;           /* 0 <= T <= 2^22; K a multiple of 16; 1 <= N <= 2^26 */
   int32_t out_fp32;          /* 0: out is bf16, 1: fp32 */
   const void *x;             /* DEVICE, 16-byte aligned: bf16 [T][K], or with x_scale e4m3 codes */
   const float *x_scale;      /* DEVICE fp32 [ceil(K / 128)] rows of T, 16-byte aligned, or NULL */

@@ -5,7 +5,7 @@
 //   of their best two c; of these groups' experts the k with the largest c (ties to
 //   the lower group, the lower expert); gates = scale * s, over their sum or not
 //
-// (The bias only moves the choice: DeepSeek-style balance without an auxiliary
+// (The bias only moves the choice, as for balance without an auxiliary
 // loss. A NaN among the logits ranks below every number.)
 #pragma once
 
