@@ -42,6 +42,7 @@ constexpr int kMaxCluster = 8;
 template <int kTok, bool kQuant>
 struct Few {
   static constexpr int Ctas = kTok <= 64 ? 2 : 1;    // on an SM
+  static constexpr int Both = kTok <= 16 ? 120 : Ctas == 2 ? 175 : 200;  // (see split_of)
   static constexpr int EpiWarps = kTok <= 32 ? 4 : 8;
   static constexpr int Mine = kTok * 4 / EpiWarps;   // columns of a scaling thread
   static constexpr int Slot = kTok < 32 ? 32 : kTok; // scales of a stage (copies of them start on 128 bytes)
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(few_threads<kTok, kQuant>(), Few<kTok, kQuant>
 // group of them, so there are fewer than the SMs have places for.
 struct Room {
   std::atomic<int> clusters[kMaxCluster + 1];
+  std::atomic<int> alone[kMaxCluster + 1];  // with an SM for each CTA
 };
 template <int kTok, bool kQuant>
 Room& room_of(int dev) {
@@ -348,23 +350,27 @@ cudaError_t configure(int dev) {
   for (int c = kMaxCluster; c >= 2; --c) {
     n = Few<kTok, kQuant>::Ctas == 1 ? one[c] : c % 2 ? (std::max(2 * one[c], n) + 2 * one[1] / c) / 2 : one[c / 2];
     room_of<kTok, kQuant>(dev).clusters[c].store(n);
+    room_of<kTok, kQuant>(dev).alone[c].store(one[c]);
   }
   return e;
 }
 
 // CTAs that share a tile: as many as keep the SM with the most work shortest, in
-// blocks of K (*longest), with a few for each CTA's beginning and end. All find room at
-// once, and a part of K has two blocks at least.
-int split_of(int tiles, int rows, int KB, const Room& room, int sms, int64_t* longest) {
+// blocks of K (*longest), with two for each CTA's beginning and end. All find room at
+// once, and a part of K has two blocks at least. Two CTAs on an SM take `both` / 100 of what
+// one takes by itself: 120 with up to 16 tokens, whose blocks are mostly latency (16 x 2048 x
+// 5120 in 3 parts 7.4 us, in 6 6.7; 16 x 4096 x 4096 in 4 8.9, in 8 7.9), 175 with more
+// (64 x 4096 x 2560 in 6 parts 7.0 us, in 8 8.2; 64 x 4096 x 4096 in 4 8.7, in 8 9.8).
+int split_of(int tiles, int rows, int KB, const Room& room, int both, int sms, int64_t* longest) {
   const int64_t all = (int64_t)tiles * rows;
   int split = 1;
-  int64_t best = INT64_MAX;
-  for (int c = 1; c <= kMaxCluster && (c == 1 || KB >= 2 * c); ++c) {
-    if (c > 1 && all > room.clusters[c].load()) continue;
-    const int64_t cost = (all * c + sms - 1) / sms * ((KB + c - 1) / c + 2);
+  int64_t best = (all + sms - 1) / sms * (KB + 2) * (all > sms ? both / 2 : 100);
+  for (int c = 2; c <= kMaxCluster && KB >= 2 * c; ++c) {
+    if (all > room.clusters[c].load()) continue;
+    const int64_t cost = ((KB + c - 1) / c + 2) * (all > room.alone[c].load() ? both : 100);
     if (cost < best) best = cost, split = c;
   }
-  if (longest) *longest = best;
+  if (longest) *longest = best / 100;
   return split;
 }
 
@@ -376,7 +382,7 @@ cudaError_t launch(const LinearArgs& a, const void* w, const void* x_codes, int6
   if (e == cudaSuccess && !kQuant) e = encode_scales(&map_s, a.x_scale, a.T, a.KB, a.x_scale_stride, Few<kTok, kQuant>::Slot);
   if (e != cudaSuccess) return e;
   const int tiles = (a.N + kRows - 1) / kRows, rows = (a.T + kTok - 1) / kTok;
-  const int split = split_of(tiles, rows, a.KB, room_of<kTok, kQuant>(dev), sms, nullptr);
+  const int split = split_of(tiles, rows, a.KB, room_of<kTok, kQuant>(dev), Few<kTok, kQuant>::Both, sms, nullptr);
   const int64_t room = (int64_t)Few<kTok, kQuant>::Ctas * sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, std::max<int64_t>(1, room / rows))), (unsigned)rows);
@@ -411,7 +417,7 @@ cudaError_t configure_linear_few(int dev) {
 
 int64_t linear_few_blocks(int T, int N, int KB, int dev, int sms) {
   int64_t longest;
-  split_of((N + kRows - 1) / kRows, (T + 127) / 128, KB, room_of<128, false>(dev), sms, &longest);
+  split_of((N + kRows - 1) / kRows, (T + 127) / 128, KB, room_of<128, false>(dev), Few<128, false>::Both, sms, &longest);
   return longest;
 }
 
