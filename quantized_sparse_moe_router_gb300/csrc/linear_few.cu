@@ -50,7 +50,11 @@ struct Few {
   static constexpr int Stages = (int)(((Ctas == 2 ? 113 : 226) * 1024 - 1024 - 512) / (StageBytes + ScaleBytes));
   static constexpr int Acc = 4;                      // buffers of sums in tensor memory: the way round one is about 1,200 cycles, the products 480
   static constexpr uint32_t Cols = Acc * kTok;
-  static constexpr uint32_t SmemBytes = 1024 + Stages * (StageBytes + ScaleBytes);
+  // Not less than 110 KB: the fused expert kernel (122 KB or more) lets its dependents start
+  // before it takes its tensor memory. Beside it on an SM this one would take some first, and
+  // hold it until that kernel's end, for which it waits; so there must be no room beside it.
+  static constexpr uint32_t LeastSmem = 110 * 1024, UsedSmem = 1024 + Stages * (StageBytes + ScaleBytes);
+  static constexpr uint32_t SmemBytes = UsedSmem < LeastSmem ? LeastSmem : UsedSmem;
   static_assert(Cols >= 32 && Cols * Ctas <= 512 && (Cols & (Cols - 1)) == 0, "an SM's CTAs share tensor memory");
   static_assert(kRows * kTok * 4 <= Stages * StageBytes, "the partial sums take the ring's place");
 };

@@ -129,6 +129,23 @@ def test_two_graphs_at_once(T):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("T", [1, 16, 40, 64, 200])
+def test_behind_the_experts(T):
+    """Linear layers that follow a step of the fused experts at once, and the other way round: each has the tensor memory it needs."""
+    H, I, E, k = 512, 128, 16, 2
+    q8 = lambda r, c, s: torch.stack([fw.quantize_q8_0(rand(r, c, seed=s + e) * c ** -0.5) for e in range(E)])  # noqa: E731
+    moe = fw.MoELayer(H, I, E, k, T_max=16, weights=dict(router_w=rand(E, H) * H ** -0.5, w_gate=q8(I, H, 10), w_up=q8(I, H, 40), w_down=q8(H, I, 70)))
+    x16 = rand(16, H, seed=3).bfloat16()
+    x, w, ws = layer(T, H, 1024)
+    codes, scales = fw.quantize_fp8(x)
+    want, want_moe = fw.linear_fp8(codes, w, ws, x_scale=scales), moe.forward(x16)[1].clone()
+    got = [(moe.forward(x16)[1].clone() if i % 10 == 9 else moe.forward(x16)[1], fw.linear_fp8(codes, w, ws, x_scale=scales)) for i in range(100)]
+    torch.cuda.synchronize()
+    moe.status()
+    assert all(torch.equal(b, want) for _, b in got) and torch.equal(got[99][0], want_moe)
+    moe.close()
+
+
 def check_products(x, w, rows, cols, out, codes, scales):
     """The products of some tokens and some outputs (whole blocks of them)."""
     want, tol = ref.linear(bits(codes[rows]), f64(scales[:, rows]).T, bits(w[0][cols]), f64(w[1][cols.start // 128:(cols.stop + 127) // 128]))
