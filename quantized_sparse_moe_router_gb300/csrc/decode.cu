@@ -239,6 +239,14 @@ __device__ __forceinline__ void x_block_to_q8(const uint4 a, const uint4 b, cons
   i1 = make_int2(__float_as_int(d), 128 * s1);
 }
 
+// A scaled value as a 16-bit number. An fp32 value of the largest exponent may round up to
+// 32768, one more than 16 bits hold (a bf16 one ends at 32640); this conversion ends at 32767.
+__device__ __forceinline__ int to_16_bits(float v) {
+  int16_t r;
+  asm("cvt.rni.s16.f32 %0, %1;" : "=h"(r) : "f"(v));
+  return r;
+}
+
 // The chunk's h of one token (16 fp32 values in shared memory) -> the same
 // 16-bit fixed point at its largest exponent as x (byte planes, 2^(e - 14),
 // 128 * sum): the down codes then multiply it with dp4a. Two passes over the
@@ -264,8 +272,7 @@ __device__ __forceinline__ void h16_to_planes(const float* h, uint4& hi, uint4& 
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float4 v = h4[j];
-    const int x0 = __float2int_rn(v.x * mult), x1 = __float2int_rn(v.y * mult), x2 = __float2int_rn(v.z * mult),
-              x3 = __float2int_rn(v.w * mult);
+    const int x0 = to_16_bits(v.x * mult), x1 = to_16_bits(v.y * mult), x2 = to_16_bits(v.z * mult), x3 = to_16_bits(v.w * mult);
     sum += x0 + x1 + x2 + x3;
     hw[j] = ((uint32_t)(x0 >> 8) & 0xFFu) | (((uint32_t)(x1 >> 8) & 0xFFu) << 8) | (((uint32_t)(x2 >> 8) & 0xFFu) << 16) |
             (((uint32_t)(x3 >> 8) & 0xFFu) << 24);
@@ -284,7 +291,7 @@ __device__ __forceinline__ void h16_to_planes_warp(const float* h, HPlanes* out,
   const float v = lane < 16 ? h[lane] : 0.f;
   const uint32_t emax = __reduce_max_sync(0xFFFFFFFFu, (__float_as_uint(v) >> 23) & 0xFFu);
   int xi = 0;
-  if (emax >= 15u) xi = __float2int_rn(v * __uint_as_float((268u - emax) << 23));  // 2^(14 - e)
+  if (emax >= 15u) xi = to_16_bits(v * __uint_as_float((268u - emax) << 23));  // 2^(14 - e)
   const int sum = __reduce_add_sync(0xFFFFFFFFu, xi);
   uint32_t hw = ((uint32_t)(xi >> 8) & 0xFFu) << ((lane & 3) * 8), lw = ((uint32_t)xi & 0xFFu) << ((lane & 3) * 8);
   hw |= __shfl_xor_sync(0xFFFFFFFFu, hw, 1);
