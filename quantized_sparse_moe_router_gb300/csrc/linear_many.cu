@@ -20,7 +20,7 @@
 //
 // Warps: 0, 2 and 3 copy, 1 issues the products (the first CTA's for both), 4-11
 // scale and add (tensor-memory quarter = warp % 4). Tiles are taken in turn by CTA pairs
-// that stay, all 256 or all 128 outputs wide (see turns). Results leave through shared
+// that stay, all 256 or all 128 outputs wide (see cut_of). Results leave through shared
 // memory by TMA while the next tile runs.
 #include <algorithm>
 #include <atomic>

@@ -123,6 +123,14 @@ def _linear_refuses(x, w, w_scale, x_scale):
     _fail(f"{f}: x_scale must be an fp32 CUDA tensor [{_blocks(K)}, {T}] with contiguous rows")
 
 
+@functools.lru_cache(maxsize=1024)
+def _linear_workspace(T, K):
+    """fw_linear_fp8_workspace's answer for bf16 tokens, which does not depend on N."""
+    need = _i64()
+    _fw._check(_fw.lib().fw_linear_fp8_workspace(_linear_args(T, K, 1, 0, 0, 0, K, 0, 0, 0, 0, 1, 0), _byref(need)), "fw_linear_fp8_workspace")
+    return need.value
+
+
 def linear_fp8(x, w, w_scale, x_scale=None, out=None, out_dtype=None, status=None, stream=None):
     """x W^T in 8 bits (fw_linear_fp8): x bf16 [T, K], or codes [T, K] with x_scale as quantize_fp8 or
     norm_residual(fp8=True) give them; w codes [N, K] with w_scale as quantize_fp8_weight gives them
@@ -162,11 +170,7 @@ def linear_fp8(x, w, w_scale, x_scale=None, out=None, out_dtype=None, status=Non
                         0 if status is None else status.data_ptr())
     L, size, at = _fw._lib or _fw.lib(), 0, None
     if T > 16 and not codes:  # (otherwise none is needed)
-        need = _i64()
-        rc = L.fw_linear_fp8_workspace(args, _byref(need))
-        if rc:
-            _fw._check(rc, "fw_linear_fp8_workspace")
-        size = need.value
+        size = _linear_workspace(T, K)
         ws = _new(1, size, _uint8, x, None) if stream is None else _empty_on(stream, (size,), _uint8, x.device, False)
         at = ws.data_ptr()
     rc = L.fw_linear_fp8(args, at, size, _raw_stream(x.get_device()) if stream is None else stream)
