@@ -101,7 +101,10 @@ typedef struct { /* all DEVICE pointers, read only during fw_moe_init */
  *   gates    = scale * s[t,ids], divided by (their sum of s + 1e-20) when renorm
  * (The vOOM README speaks of DeepSeek-shaped experts and routers, the Flyweight
  * README's served families name that MoE too; the pages print no formula, and this
- * is the reading used.) A NaN among the logits ranks below every number. */
+ * is the reading used.) A NaN among a token's logits is no score: the softmax is over the
+ * others, a group's score is made of the others' c, and its expert ranks below every number;
+ * where it is chosen all the same, its gate is NaN, and under renorm all of the token's. Infinite
+ * logits have the scores' limits (several of +infinity share a softmax evenly). */
 typedef struct {
   int32_t score;               /* 0 softmax over all experts, 1 sigmoid */
   int32_t n_group, top_group;  /* 1..32, dividing E; 1..n_group, with k experts at least in that many groups. 1, 1: no groups */

@@ -6,7 +6,8 @@
 //   the lower group, the lower expert); gates = scale * s, over their sum or not
 //
 // (The bias only moves the choice, as for balance without an auxiliary
-// loss. A NaN among the logits ranks below every number.)
+// loss. A NaN among the logits ranks below every number and counts in neither a
+// softmax nor a group's sum; infinite logits have the scores' limits.)
 #pragma once
 
 #include "routing.cuh"
@@ -35,16 +36,18 @@ __device__ __forceinline__ void rule_scores(const float (&zl)[MPL], int E, int l
   float sum = 0.f;
 #pragma unroll
   for (int m = 0; m < MPL; ++m) {
-    s[m] = MPL * lane + m < E ? expf(zl[m] - top) : 0.f;
-    sum += s[m];
+    // (e^0, also where the difference of infinite logits is none; a NaN stays one, and out of the sum)
+    s[m] = MPL * lane + m < E ? zl[m] == top ? 1.f : expf(zl[m] - top) : 0.f;
+    sum += s[m] == s[m] ? s[m] : 0.f;
   }
   sum = warp_sum(sum);
 #pragma unroll
   for (int m = 0; m < MPL; ++m) s[m] = s[m] / sum;
 }
 
+// (second: 0 where there is none, 1 where it is a NaN)
 __device__ __forceinline__ uint32_t group_key(uint32_t top, uint32_t second) {
-  return topk_key(second ? topk_value(top) + topk_value(second) : topk_value(top));
+  return topk_key(second > 1u ? topk_value(top) + topk_value(second) : topk_value(top));
 }
 
 // The groups' choice: keys of experts in groups left out become 0. A group's best two
