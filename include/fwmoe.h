@@ -430,8 +430,10 @@ fw_status fw_fp8_quantize_weight(const void *w, int32_t w_fp32, int32_t N, int32
 
 /* A linear layer: out[t][n] = sum over k of x[t][k] w[n][k], both as their codes and
  * scales stand for. Products of codes are exact, the sum over the at most 128 of a
- * block is the tensor core's (fp32), and blocks are scaled and added in fp32; out is
- * rounded once. x may be bf16: it is then quantised by the rule above, with the same
+ * block is the tensor core's (fp32), and blocks are scaled and added in fp32, also where the
+ * product of the two scales would leave fp32's range (of scales that the rule gives, from
+ * 2^-105 to 2^120, and of weights to 2^103; smaller ones may cost precision, larger ones of
+ * weights may overflow before a token's small scale is applied); out is rounded once. x may be bf16: it is then quantised by the rule above, with the same
  * result as fw_fp8_quantize before the call. out may not overlap x or w.
  * workspace: DEVICE, 16-byte aligned, at least fw_linear_fp8_workspace bytes (0 with
  * codes, and with bf16 up to 16 tokens; it may then be NULL); its contents mean nothing

@@ -85,6 +85,15 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+// Whether a weight scale's product with a token's is a normal fp32 number whatever the
+// token's: those the rule gives lie between 2^-104.9 and 2^119.2. Where it need not be (a
+// block of weights all below 2^-12, so also one of zeros, or one above 2^16) a block's sum, 0
+// or of 2^-18 to 2^24.6, is multiplied by the weights' scale and then by the token's: what is
+// between is above 2^-123, and below 2^128 for weights' scales up to 2^103. Asked for 32
+// blocks at a time, with a loop for each way: a branch for each block's additions took 4096 x
+// 7168 x 4096 from 91 us to 118, two multiplications for all to 110.
+__device__ __forceinline__ bool scales_join(float w) { return fabsf(w) >= 4.76837158203125e-7f && fabsf(w) <= 256.f; }
+
 }  // namespace dev
 
 // What the linear kernels take: codes of the tokens with their scales, or (few

@@ -23,6 +23,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "fp8.cuh"
 #include "pair.cuh"
@@ -85,6 +86,12 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+// acc += v f w (kJoined: see scales_join).
+template <bool kJoined>
+__device__ __forceinline__ void add_scaled(float& acc, uint32_t v, float f, float w) {
+  acc = kJoined ? fmaf(__uint_as_float(v), f * w, acc) : fmaf(__uint_as_float(v) * w, f, acc);
 }
 
 __device__ __forceinline__ void store_out(const LinearArgs& a, int t, int n, float v) {
@@ -227,40 +234,46 @@ __global__ void __launch_bounds__(few_threads<kTok, kQuant>(), Few<kTok, kQuant>
       float acc[kMine];
 #pragma unroll
       for (int j = 0; j < kMine; ++j) acc[j] = 0.f;
-      for (int b = 0; b < nb; ++b, ++i) {
-        if (b % 32 == 0) {
-          w_now = w_next;
-          w_next = b + 32 + lane < nb ? __ldg(ws + b + 32 + lane) : 0.f;
-        }
-        const float w = __shfl_sync(0xFFFFFFFFu, w_now, b % 32);
-        const int c = i % kAcc;
-        const uint32_t c_phase = (i / kAcc) & 1;
-        // (the stage's scales are there since before its products began)
-        const bool f = mbar_test(&full[s], phase), e = mbar_test(&acc_full[c], c_phase);
-        if (!__all_sync(0xFFFFFFFFu, f && e) && !(ok = wait(&full[s], phase) && wait(&acc_full[c], c_phase))) break;
-        tc_fence_after();
-        const uint32_t from = from0 + c * kTok;
-        const float4* sc = reinterpret_cast<const float4*>(s_scale + s * F::Slot + part * kMine);
+      const auto add_blocks = [&](auto joined, int b, int end) {
+        for (; b < end; ++b, ++i) {
+          const float w = __shfl_sync(0xFFFFFFFFu, w_now, b % 32);
+          const int c = i % kAcc;
+          const uint32_t c_phase = (i / kAcc) & 1;
+          // (the stage's scales are there since before its products began)
+          const bool f = mbar_test(&full[s], phase), e = mbar_test(&acc_full[c], c_phase);
+          if (!__all_sync(0xFFFFFFFFu, f && e) && !(ok = wait(&full[s], phase) && wait(&acc_full[c], c_phase))) break;
+          tc_fence_after();
+          const uint32_t from = from0 + c * kTok;
+          const float4* sc = reinterpret_cast<const float4*>(s_scale + s * F::Slot + part * kMine);
 #pragma unroll
-        for (int j0 = 0; j0 < kMine; j0 += 16) {
-          uint32_t v[16];
-          tmem_load(from + j0, v);
+          for (int j0 = 0; j0 < kMine; j0 += 16) {
+            uint32_t v[16];
+            tmem_load(from + j0, v);
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 f = sc[(j0 + j) / 4];
-            acc[j0 + j] = fmaf(__uint_as_float(v[j]), f.x * w, acc[j0 + j]);
-            acc[j0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y * w, acc[j0 + j + 1]);
-            acc[j0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z * w, acc[j0 + j + 2]);
-            acc[j0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w * w, acc[j0 + j + 3]);
+            for (int j = 0; j < 16; j += 4) {
+              const float4 f = sc[(j0 + j) / 4];
+              add_scaled<joined>(acc[j0 + j], v[j], f.x, w);
+              add_scaled<joined>(acc[j0 + j + 1], v[j + 1], f.y, w);
+              add_scaled<joined>(acc[j0 + j + 2], v[j + 2], f.z, w);
+              add_scaled<joined>(acc[j0 + j + 3], v[j + 3], f.w, w);
+            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&acc_empty[c]);
+            mbar_arrive(&empty[s]);
+          }
+          if (++s == kStages) s = 0, phase ^= 1;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&acc_empty[c]);
-          mbar_arrive(&empty[s]);
-        }
-        if (++s == kStages) s = 0, phase ^= 1;
+      };
+      for (int b = 0; b < nb && ok; b += 32) {
+        w_now = w_next;
+        w_next = b + 32 + lane < nb ? __ldg(ws + b + 32 + lane) : 0.f;
+        if (__all_sync(0xFFFFFFFFu, b + lane >= nb || scales_join(w_now)))
+          add_blocks(std::true_type(), b, ::min(nb, b + 32));
+        else
+          add_blocks(std::false_type(), b, ::min(nb, b + 32));
       }
       if (!ok) break;
       if (split == 1) {

@@ -116,6 +116,18 @@ __device__ __forceinline__ void add_scaled(f2* acc, const uint32_t (&r)[N], f2 s
   for (int j = 0; j < N; j += 2) acc[j / 2] = f2_fma(f2_pack_bits(r[j], r[j + 1]), s, acc[j / 2]);
 }
 
+// The same by two scales one after the other.
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void add_scaled(f2* acc, const uint32_t (&r)[N], f2 first, f2 then) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) acc[j / 2] = f2_fma(f2_mul(f2_pack_bits(r[j], r[j + 1]), first), then, acc[j / 2]);
+}
+
 // Tile i of 256 tokens and kCols outputs: neighbours share tokens in runs of kRun
 // token tiles, whose weights are then read close together.
 constexpr int kRun = 8;
@@ -308,43 +320,60 @@ __global__ void __launch_bounds__(kThreads, 1) linear_many_kernel(const __grid_c
       // is being added: its barrier, its scale. (Done in turn that took a third of the time.)
       bool ready = false;
       float scale = 0.f;
-      for (int b = 0; b < KB; ++b, ++i) {
-        const uint32_t c = i % kAcc;
-        if (!ready && !__all_sync(0xFFFFFFFFu, wait_inline(&acc_full[c], (i / kAcc) & 1))) {
-          raise(l.status, FW_KV_TIMEOUT);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (b % 32 == 0) {
-          w_now = w_next;
-          w_next = b + 32 + lane < KB ? __ldg(ws + b + 32 + lane) : 0.f;
-        }
-        if (b == 0) scale = s_scale[i % kSlots * kTokRows + 32 * q + lane] * __shfl_sync(0xFFFFFFFFu, w_now, 0);
-        const uint32_t from = from0 + c * (2 * kMine) + half * kMine;
-        const f2 s2 = f2_pack(scale, scale);
-        uint32_t v[kLoads][kChunk];
-#pragma unroll
-        for (int j0 = 0; j0 < kMine; j0 += kLoads * kChunk) {
-#pragma unroll
-          for (int j = 0; j < kLoads; ++j) tmem_ld_start(from + j0 + j * kChunk, v[j]);
-          if (j0 == (kLoads > 1 ? 0 : kMine - 2 * kChunk)) {
-            const bool more = b + 1 < KB;
-            if constexpr (kAsk) ready = __all_sync(0xFFFFFFFFu, more && mbar_test(&acc_full[(i + 1) % kAcc], ((i + 1) / kAcc) & 1));
-            scale = more ? s_scale[(i + 1) % kSlots * kTokRows + 32 * q + lane] : 0.f;
-            scale *= __shfl_sync(0xFFFFFFFFu, (b + 1) % 32 ? w_now : w_next, (b + 1) % 32);
+      const auto add_blocks = [&](auto joined, int b, int end) {
+        for (; b < end; ++b, ++i) {
+          const uint32_t c = i % kAcc;
+          if (!ready && !__all_sync(0xFFFFFFFFu, wait_inline(&acc_full[c], (i / kAcc) & 1))) {
+            raise(l.status, FW_KV_TIMEOUT);
+            ok = false;
+            break;
           }
-          tmem_ld_done(v[0]);
+          tc_fence_after();
+          if (b == 0) scale = s_scale[i % kSlots * kTokRows + 32 * q + lane] * __shfl_sync(0xFFFFFFFFu, w_now, 0);
+          const uint32_t from = from0 + c * (2 * kMine) + half * kMine;
+          const f2 s2 = f2_pack(scale, scale);
+          uint32_t v[kLoads][kChunk];
 #pragma unroll
-          for (int j = 1; j < kLoads; ++j) tmem_ld_there(v[j]);
-          if (j0 + kLoads * kChunk == kMine) {  // (all of this warp's sums are in registers)
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(first_empty + c * 8);
+          for (int j0 = 0; j0 < kMine; j0 += kLoads * kChunk) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) tmem_ld_start(from + j0 + j * kChunk, v[j]);
+            if (j0 == (kLoads > 1 ? 0 : kMine - 2 * kChunk)) {
+              const bool more = b + 1 < KB;
+              if constexpr (kAsk) ready = __all_sync(0xFFFFFFFFu, more && mbar_test(&acc_full[(i + 1) % kAcc], ((i + 1) / kAcc) & 1));
+              scale = more ? s_scale[(i + 1) % kSlots * kTokRows + 32 * q + lane] : 0.f;
+              scale *= __shfl_sync(0xFFFFFFFFu, (b + 1) % 32 ? w_now : w_next, (b + 1) % 32);
+            }
+            tmem_ld_done(v[0]);
+#pragma unroll
+            for (int j = 1; j < kLoads; ++j) tmem_ld_there(v[j]);
+            if (j0 + kLoads * kChunk == kMine) {  // (all of this warp's sums are in registers)
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_at(first_empty + c * 8);
+            }
+            if (joined) {
+#pragma unroll
+              for (int j = 0; j < kLoads; ++j) add_scaled(acc + (j0 + j * kChunk) / 2, v[j], s2);
+            } else {  // (the block's own scale is still in its slot, see kSlots)
+              const float f = s_scale[i % kSlots * kTokRows + 32 * q + lane], w = __shfl_sync(0xFFFFFFFFu, w_now, b % 32);
+#pragma unroll
+              for (int j = 0; j < kLoads; ++j) add_scaled(acc + (j0 + j * kChunk) / 2, v[j], f2_pack(w, w), f2_pack(f, f));
+            }
           }
-#pragma unroll
-          for (int j = 0; j < kLoads; ++j) add_scaled(acc + (j0 + j * kChunk) / 2, v[j], s2);
         }
+      };
+      for (int b = 0; b < KB && ok; b += 32) {
+        w_now = w_next;
+        w_next = b + 32 + lane < KB ? __ldg(ws + b + 32 + lane) : 0.f;
+        // (see scales_join; 256 wide, with 64 columns to a branch, one loop is faster: 1500 x 5120 x
+        // 5120 35.8 us against 43.9, 8192 x 4096 x 4096 97 against 114; 128 wide it is the slower)
+        const bool joined = __all_sync(0xFFFFFFFFu, b + lane >= KB || scales_join(w_now));
+        if constexpr (kLoads > 1)
+          add_blocks(joined, b, ::min(KB, b + 32));
+        else if (joined)
+          add_blocks(std::true_type(), b, ::min(KB, b + 32));
+        else
+          add_blocks(std::false_type(), b, ::min(KB, b + 32));
       }
       // A tile that pairs share: each leaves its sums in its ring, which nothing reads or fills
       // any more, and joins, in the pairs' order, a share of every thread's columns.
