@@ -309,7 +309,9 @@ class MoELayer:
             if not (bias.dtype is torch.float32 and bias.is_cuda and bias.is_contiguous() and bias.shape == (self.E,)):
                 raise ValueError("set_routing: bias must be a contiguous fp32 CUDA tensor [E]")
         fw_moe_set_routing(self.handle, FwMoeRouting(1 if score == "sigmoid" else 0, n_group, top_group, 1 if renorm else 0, scale, _ptr(bias)), _stream(stream))
-        self._bias = bias  # (read in the stream's order, which may be later)
+        if bias is not None:  # read in the stream's order, which may be later than this layer's next rule and the caller's last use
+            bias.record_stream(torch.cuda.current_stream(bias.device) if stream is None else torch.cuda.ExternalStream(stream, device=bias.device))
+        self._bias = bias  # (a captured copy reads it at each replay)
 
     def route(self, x, expert_ids=None, gates=None, stream=None):
         T = x.shape[0]
