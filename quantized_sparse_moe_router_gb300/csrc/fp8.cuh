@@ -17,7 +17,7 @@ namespace fw {
 
 constexpr int kFp8Block = 128;  // values along K that share a scale
 
-__host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+__host__ __device__ inline int fp8_blocks(int n) { return n / kFp8Block + (n % kFp8Block != 0); }  // (n + 127 may not fit)
 
 namespace dev {
 
