@@ -48,6 +48,10 @@ def _new(rows, cols, dtype, like, stream):
     return _empty_on(stream, (rows, cols), dtype, like.device)
 
 
+def _not_sizes(where):
+    _fail(f"{where}: sizes must be below 2^31")
+
+
 def _rows(where, name, t, cols, *types):
     """Elements between rows of a [T, cols] CUDA tensor whose rows are contiguous."""
     if t.dtype not in types or not t.is_cuda or t.dim() != 2 or t.shape[1] != cols:
@@ -84,6 +88,8 @@ def quantize_fp8(x, stream=None):
     if x.dim() != 2:
         _fail(f"{w}: x must be [T, K]")
     T, K = x.shape
+    if T > 0x7FFFFFFF or K > 0x7FFFFFFF:  # (ctypes would cut them to 32 bits)
+        _not_sizes(w)
     xs = _rows(w, "x", x, K, _bf16)
     _one_device(w, x)
     codes = _new(T, K, _e4m3, x, stream)
@@ -101,6 +107,8 @@ def quantize_fp8_weight(w, stream=None):
     if not (w.dtype in (_bf16, _fp32) and w.is_cuda and w.dim() == 2 and w.is_contiguous()):
         _fail(f"{f}: w must be a contiguous bf16 or fp32 CUDA tensor [N, K]")
     N, K = w.shape
+    if N > 0x7FFFFFFF or K > 0x7FFFFFFF:
+        _not_sizes(f)
     _one_device(f, w)
     codes, scales = _new(N, K, _e4m3, w, stream), _new(_blocks(N), _blocks(K), _fp32, w, stream)
     rc = _fw.lib().fw_fp8_quantize_weight(w.data_ptr(), 1 if w.dtype is _fp32 else 0, N, K, codes.data_ptr(), scales.data_ptr(), _stream_of(w, stream))
