@@ -37,15 +37,22 @@ _norm_args = struct.Struct("@5i2f15q").pack
 
 _bf16, _fp32, _e4m3, _uint8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8
 _byref = ctypes.byref
-# (not in every build of torch)
+# An empty tensor of these sizes, strides and type on the current device, quicker than torch.empty;
+# a name of torch's own, so one that may be missing or change.
 _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
 def _new(rows, cols, dtype, like, stream):
     """An empty [rows, cols] tensor for a call on `stream` (None: the current one)."""
-    if stream is None:
-        return _empty((rows, cols), dtype=dtype, device=like.device) if _empty_strided is None else _empty_strided((rows, cols), (cols, 1), dtype)
-    return _empty_on(stream, (rows, cols), dtype, like.device)
+    global _empty_strided
+    if stream is not None:
+        return _empty_on(stream, (rows, cols), dtype, like.device)
+    if _empty_strided is not None:
+        try:
+            return _empty_strided((rows, cols), (cols, 1), dtype)
+        except TypeError:  # (not the arguments that this torch's takes)
+            _empty_strided = None
+    return _empty((rows, cols), dtype=dtype, device=like.device)
 
 
 def _not_sizes(where):
