@@ -51,7 +51,7 @@ static int64_t scale_stride(const fw_linear_fp8_args* a) { return round_up(a->T,
 static int64_t codes_bytes(const fw_linear_fp8_args* a) { return round_up((int64_t)a->T * a->K, 256); }
 
 // Up to 64 tokens the weights bound the call, and the kernel for few tokens reads them
-// faster (64 x 7168 x 7168: 14.6 us against 15.7, 64 x 4096 x 4096: 8.7 against 10.0). With
+// faster (64 x 7168 x 7168: 14.8 us against 15.7, 64 x 4096 x 4096: 8.7 against 10.0). With
 // more both are estimated, by the cycles that the products of the one take and the blocks
 // of K that an SM has in the other, 970 cycles each and 2,100 for the other's longer start
 // and end (65 x 4096 x 2048: few 7.9 us, many 8.6; 130 x 7168 x 1024: 10.4 and 9.2; 257 x

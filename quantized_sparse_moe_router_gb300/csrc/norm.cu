@@ -80,6 +80,8 @@ __device__ __forceinline__ void store8(float* p, bool aligned, const float (&f)[
 // kVec: vectors of eight values a thread holds. kWarp: a warp a row, otherwise a
 // CTA a row. kWide: residuals are fp32. kLoop: the CTA takes every gridDim.x-th row,
 // and loads the next one once it has summed the row's parts.
+// (1024 threads of four vectors with fp32 residuals, rows past 8192, have 64 registers
+// each and keep 68 bytes of them in local memory.)
 template <int kVec, bool kWarp, bool kWide, bool kLoop>
 __global__ void __launch_bounds__(kWarp ? 256 : kVec <= 2 ? 512 : kMaxThreads, kWarp || kVec > 2 ? 1 : 2)
     norm_residual_kernel(const __grid_constant__ fw_norm_residual_args u) {

@@ -610,6 +610,9 @@ cudaError_t launch_route_prefill(Handle* h, const __nv_bfloat16* x, int T, int32
   const int n_tiles = (T + kRouteTileM - 1) / kRouteTileM;
   const int EM = (h->cfg.E + 31) / 32;
   cudaError_t err;
+  // Under a rule the tensor cores are taken by the default step's condition (E a multiple of 16);
+  // with other E a CTA of the tile kernel walks all of H for its 32 tokens (64 tokens of 7168, 8
+  // experts: 159 us; of 1024: 34; 64 experts of 2048 on the tensor cores: 16).
   if (route_prefill_mma_available(h)) {
     KernelTimer tm(h, FW_KERNEL_ROUTE_TILES, s);
     if (a.zpart) {
