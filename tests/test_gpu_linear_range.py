@@ -13,8 +13,10 @@ import quantized_sparse_moe_router_gb300 as fw
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
 
-# bf16 quantised in the kernel; codes of up to 16, 32, 64 and 128 tokens; pairs of SMs, 128 and 256 wide and sharing a tile
-SHAPES = [(1, 1024, 384), (16, 2048, 300), (24, 1024, 384), (50, 1024, 256), (100, 512, 384), (300, 1024, 384), (300, 7168, 576), (2100, 384, 2304)]
+# bf16 quantised in the kernel, codes of up to 16, 32, 64 and 128 tokens; pairs of SMs 128 wide, sharing a
+# tile, and 256 wide; the last of few tokens with more than 32 blocks in a part of K
+SHAPES = [(1, 1024, 384), (16, 2048, 300), (24, 1024, 384), (50, 1024, 256), (100, 512, 384), (300, 1024, 384), (300, 7168, 576), (2100, 384, 2304),
+          (100, 7168, 256), (500, 7168, 1536), (2048, 4224, 2304), (40, 4224, 20000)]
 
 
 def f64(t):
